@@ -2,7 +2,8 @@
 
 The decode kernels are instantiated once per activation-row count in separate
 objects (csrc/inst.hip compiled with -DW4K_M=1..8), the prefill kernels and
-the C ABI in two more, all compiled in parallel and linked into one library.
+the C ABI in two more, the key/value cache and its attention (once per head
+size) in four, all compiled in parallel and linked into one library.
 """
 import concurrent.futures as cf
 import os
@@ -36,7 +37,9 @@ UNITS = [(f"inst_m{m}", "inst.hip", [f"-DW4K_M={m}"]) for m in range(1, 9)] + [
     # every one back before its scaling fma (80 extra VALU per wave and step)
     ("prefill", "prefill.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
     ("abi", "w4a16.hip", []),
-]
+    # the paged 8-bit key/value cache (include/w4a16_kv.h); its attention once per head size
+    ("kv", "kv.hip", []),
+] + [(f"kv_attention_d{d}", "kv_attention.hip", [f"-DW4K_D={d}"]) for d in (64, 128, 256)]
 
 _NOISE = "not a recognized feature for this target"
 

@@ -1,0 +1,458 @@
+// C ABI of the paged 8-bit key/value cache (include/w4a16_kv.h), and the plan,
+// append and dequant kernels.  The attention is in kv_attention.hip.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kv_device.hpp"
+
+namespace w4k {
+
+namespace {
+
+constexpr int kKvThreads = 256;
+constexpr int kKvWaves = kKvThreads / kWave;
+constexpr int kKvMaxLen = 1 << 29;
+
+__device__ __forceinline__ int kv_length(int n) { return min(max(n, 0), kKvMaxLen); }
+
+// ---------------------------------------------------------------------------
+// plan.  A block takes kKvWaves requests, one a wave; the grid's y axis shares
+// the columns and tokens of each.  The exclusive sums up to the block's first
+// request are a reduction over all earlier lengths (a few strided loads a
+// thread, from L2), so one launch does everything and no block waits for
+// another.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(kKvThreads) void kv_plan_kernel(const int32_t* __restrict__ ctx_lens,
+                                                             const int32_t* __restrict__ new_lens,
+                                                             const int32_t* __restrict__ free_pages, int num_free,
+                                                             int32_t* __restrict__ table, int width,
+                                                             int32_t* __restrict__ seq_lens,
+                                                             int32_t* __restrict__ token_start,
+                                                             int32_t* __restrict__ slot_map,
+                                                             int32_t* __restrict__ pages_used, int requests,
+                                                             int tokens, int page_shift) {
+  __shared__ int s_new[kKvWaves], s_need[kKvWaves];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int P = 1 << page_shift;
+  const int r0 = blockIdx.x * kKvWaves;
+  auto pages_of = [&](int n) { return (n + P - 1) >> page_shift; };
+  int sum_new = 0, sum_need = 0;
+  for (int r = threadIdx.x; r < r0; r += kKvThreads) {
+    const int c = kv_length(ctx_lens[r]), n = kv_length(new_lens[r]);
+    sum_new += n;
+    sum_need += pages_of(c + n) - pages_of(c);
+  }
+#pragma unroll
+  for (int off = kWave / 2; off > 0; off >>= 1) {
+    sum_new += __shfl_xor(sum_new, off);
+    sum_need += __shfl_xor(sum_need, off);
+  }
+  if (lane == 0) {
+    s_new[wave] = sum_new;
+    s_need[wave] = sum_need;
+  }
+  __syncthreads();
+  int start = 0, first = 0;
+#pragma unroll
+  for (int w = 0; w < kKvWaves; ++w) {
+    start += s_new[w];
+    first += s_need[w];
+  }
+  int c = 0, n = 0, held = 0, need = 0;
+  const int r = r0 + wave;
+  for (int x = r0; x <= r && x < requests; ++x) {   // this block's earlier requests
+    start += n;
+    first += need;
+    c = kv_length(ctx_lens[x]);
+    n = kv_length(new_lens[x]);
+    held = pages_of(c);
+    need = pages_of(c + n) - held;
+  }
+  const int step = gridDim.y * kWave, at = blockIdx.y * kWave + lane;
+  if (r < requests) {
+    if (at == 0) {
+      seq_lens[r] = c + n;
+      token_start[r] = start;
+    }
+    // entry b of the request's row: its own, the next free page, or none
+    auto fresh = [&](int b) {
+      const long long f = (long long)first + (b - held);
+      return b < held + need && f < num_free ? free_pages[f] : -1;
+    };
+    int32_t* row = table + (size_t)r * width;
+    for (int b = held + at; b < width; b += step) row[b] = fresh(b);
+    for (int i = at; i < n; i += step) {
+      const long long t = (long long)start + i;
+      if (t >= tokens) break;
+      const int b = (c + i) >> page_shift;
+      const int page = b >= width ? -1 : b < held ? row[b] : fresh(b);
+      slot_map[t] = page >= 0 ? (page << page_shift) + ((c + i) & (P - 1)) : -1;
+    }
+  }
+  // the wave of the last request knows the totals
+  if (r == requests - 1 || (requests == 0 && wave == 0)) {
+    const int total = start + n;
+    if (at == 0) {
+      token_start[requests] = total;
+      pages_used[0] = first + need;
+    }
+    for (long long t = (long long)total + at; t < tokens; t += step) slot_map[t] = -1;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// append.  A block looks at `span` consecutive tokens for one cache head, keys
+// or values (grid y), and quantizes every run that begins among them: the
+// largest magnitude of the run (an integer maximum of bf16 bits), the scale,
+// then the codes.  A run lies in one page, so its block alone writes that page
+// and head.
+// ---------------------------------------------------------------------------
+template <int TYPE>
+__device__ __forceinline__ uint32_t kv_pack4(float a, float b, float c, float d, float s) {
+  return kv_code_of<TYPE>(a, s) | kv_code_of<TYPE>(b, s) << 8 | kv_code_of<TYPE>(c, s) << 16 |
+         kv_code_of<TYPE>(d, s) << 24;
+}
+
+// the four codes of a word encoded again for a larger scale
+template <int TYPE>
+__device__ __forceinline__ uint32_t kv_again4(uint32_t w, float old_s, float s) {
+  return kv_pack4<TYPE>(kv_decode<TYPE, 0>(w) * old_s, kv_decode<TYPE, 1>(w) * old_s, kv_decode<TYPE, 2>(w) * old_s,
+                        kv_decode<TYPE, 3>(w) * old_s, s);
+}
+
+template <int D, int TYPE>
+__global__ __launch_bounds__(kKvThreads) void kv_append_kernel(const uint16_t* __restrict__ k, int64_t k_stride,
+                                                               const uint16_t* __restrict__ v, int64_t v_stride,
+                                                               const int32_t* __restrict__ slot_map, KvCache c,
+                                                               int tokens, int span) {
+  __shared__ uint32_t s_max[kKvWaves];
+  __shared__ int s_len[kKvWaves];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int head = blockIdx.y >> 1;
+  const bool is_v = blockIdx.y & 1;
+  const uint16_t* x = (is_v ? v : k) + (size_t)head * D;
+  const int64_t stride = is_v ? v_stride : k_stride;
+  const int P = 1 << c.page_shift;
+  const long long slots = (long long)c.pages << c.page_shift;
+  const long long t_end = min((long long)(blockIdx.x + 1) * span, (long long)tokens);
+  for (long long t0 = (long long)blockIdx.x * span; t0 < t_end; ++t0) {
+    const int slot = slot_map[t0];
+    if (slot < 0 || slot >= slots) continue;
+    const int off = slot & (P - 1);
+    if (off != 0 && t0 > 0 && slot_map[t0 - 1] == slot - 1) continue;    // not the first of its run
+    // run length: thread i looks at token t0 + i
+    bool in_run = off + (int)threadIdx.x < P && t0 + threadIdx.x < tokens;
+    if (in_run) in_run = slot_map[t0 + threadIdx.x] == slot + (int)threadIdx.x;
+    const uint64_t no = ~__ballot(in_run);
+    if (lane == 0) s_len[wave] = no ? __builtin_ctzll(no) : kWave;
+    __syncthreads();
+    int n = 0;
+    for (int w = 0; w < kKvWaves; ++w) {
+      n += s_len[w];
+      if (s_len[w] < kWave) break;
+    }
+    const uint16_t* xr = x + t0 * stride;
+    uint32_t big = 0;
+    for (int e = threadIdx.x; e < n * (D / 8); e += kKvThreads) {
+      const uint4 u = *reinterpret_cast<const uint4*>(xr + (e / (D / 8)) * stride + (e % (D / 8)) * 8);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) big = max(big, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+    }
+#pragma unroll
+    for (int o = kWave / 2; o > 0; o >>= 1) big = max(big, (uint32_t)__shfl_xor((int)big, o));
+    if (lane == 0) s_max[wave] = big;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kKvWaves; ++w) big = max(big, s_max[w]);
+    const size_t ph = (size_t)(slot >> c.page_shift) * c.heads + head;
+    uint16_t* scale_at = (is_v ? c.vs : c.ks) + ph;
+    float s = kv_scale_of<TYPE>(big), old_s = 0.0f;
+    bool grown = false;
+    if (off > 0) {
+      old_s = bf16_lo(*scale_at);
+      if (!(s <= old_s))        // larger, or either is NaN
+        grown = old_s == old_s;
+      else
+        s = old_s;
+      if (!(old_s == old_s)) s = old_s;
+    }
+    __syncthreads();            // every thread has read the old scale and the shared words
+    if (threadIdx.x == 0) *scale_at = (uint16_t)(__float_as_uint(s) >> 16);
+    if (!is_v) {
+      uint8_t* page = c.k + ph * P * D;
+      if (grown)
+        for (int e = threadIdx.x; e < off * (D / 4); e += kKvThreads) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(page) + e;
+          *w = kv_again4<TYPE>(*w, old_s, s);
+        }
+      for (int e = threadIdx.x; e < n * (D / 8); e += kKvThreads) {
+        const uint4 u = *reinterpret_cast<const uint4*>(xr + (e / (D / 8)) * stride + (e % (D / 8)) * 8);
+        uint2 o;
+        o.x = kv_pack4<TYPE>(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y), s);
+        o.y = kv_pack4<TYPE>(bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w), s);
+        *reinterpret_cast<uint2*>(page + (size_t)off * D + (size_t)e * 8) = o;
+      }
+    } else {
+      // words of four tokens: [first, last) are touched; a word on the run's
+      // border keeps its other bytes (encoded again if the scale grew)
+      uint8_t* page = c.v + ph * P * D;
+      const int first = grown ? 0 : off >> 2, words = ((off + n + 3) >> 2) - first;
+      for (int e = threadIdx.x; e < words * D; e += kKvThreads) {
+        const int d = e / words, tok = 4 * (first + e % words);     // tok: offset in the page
+        uint32_t* w = reinterpret_cast<uint32_t*>(page + (size_t)d * P + tok);
+        uint32_t old = 0;
+        if (tok < off || tok + 4 > off + n) old = *w;
+        uint32_t o = 0;
+        const uint32_t again = grown && tok < off ? kv_again4<TYPE>(old, old_s, s) : old;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = tok + i - off;
+          const uint32_t byte = j < 0 ? again >> (8 * i) & 0xFFu
+                              : j >= n ? old >> (8 * i) & 0xFFu
+                                       : kv_code_of<TYPE>(bf16_lo(xr[j * stride + d]), s);
+          o |= byte << (8 * i);
+        }
+        *w = o;
+      }
+    }
+    __syncthreads();            // the shared words are free for the next run
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dequant: block (page, head, keys or values); four codes a thread and step.
+// ---------------------------------------------------------------------------
+template <int D, int TYPE>
+__global__ __launch_bounds__(kKvThreads) void kv_dequant_kernel(KvCache c, const int32_t* __restrict__ pages,
+                                                                float* __restrict__ k_out,
+                                                                float* __restrict__ v_out) {
+  const int P = 1 << c.page_shift;
+  const int head = blockIdx.y >> 1;
+  const bool is_v = blockIdx.y & 1;
+  const int page = pages[blockIdx.x];
+  const bool ok = page >= 0 && page < c.pages;
+  const size_t ph = ok ? (size_t)page * c.heads + head : 0;
+  const float s = ok ? bf16_lo((is_v ? c.vs : c.ks)[ph]) : __builtin_nanf("");
+  float* out = (is_v ? v_out : k_out) + ((size_t)blockIdx.x * c.heads + head) * P * D;
+  if (!is_v) {
+    const uint32_t* in = reinterpret_cast<const uint32_t*>(c.k + ph * P * D);
+    for (int e = threadIdx.x; e < P * D / 4; e += kKvThreads) {
+      const uint32_t w = ok ? in[e] : 0;
+      reinterpret_cast<float4*>(out)[e] = make_float4(kv_decode<TYPE, 0>(w) * s, kv_decode<TYPE, 1>(w) * s,
+                                                      kv_decode<TYPE, 2>(w) * s, kv_decode<TYPE, 3>(w) * s);
+    }
+  } else {
+    // 4 x 4 pieces: four rows' words of four tokens in, four tokens' float4 of four rows out
+    const uint8_t* in = c.v + ph * P * D;
+    for (int e = threadIdx.x; e < P * D / 16; e += kKvThreads) {
+      const int d = 4 * (e % (D / 4)), tok = 4 * (e / (D / 4));
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = ok ? *reinterpret_cast<const uint32_t*>(in + (size_t)(d + i) * P + tok) : 0;
+      auto put = [&](auto bc) {
+        constexpr int B = decltype(bc)::value;
+        *reinterpret_cast<float4*>(out + (size_t)(tok + B) * D + d) =
+            make_float4(kv_decode<TYPE, B>(w[0]) * s, kv_decode<TYPE, B>(w[1]) * s, kv_decode<TYPE, B>(w[2]) * s,
+                        kv_decode<TYPE, B>(w[3]) * s);
+      };
+      put(std::integral_constant<int, 0>{});
+      put(std::integral_constant<int, 1>{});
+      put(std::integral_constant<int, 2>{});
+      put(std::integral_constant<int, 3>{});
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+bool kv_aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+w4a16_status_t kv_launched(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_HIP; }
+
+bool page_supported(int page) { return page == 16 || page == 32 || page == 64 || page == 128 || page == 256; }
+
+// sizes of a cache, without its pointers
+w4a16_status_t check_cache(const w4a16_kv_cache_t* c) {
+  if (!c) return W4A16_ERR_NULL;
+  if (c->type != W4A16_KV_INT8 && c->type != W4A16_KV_FP8) return W4A16_ERR_UNSUPPORTED;
+  if (c->dim != 64 && c->dim != 128 && c->dim != 256) return W4A16_ERR_UNSUPPORTED;
+  if (!page_supported(c->page)) return W4A16_ERR_UNSUPPORTED;
+  if (c->heads < 1 || c->heads > W4A16_KV_MAX_HEADS || c->pages < 0) return W4A16_ERR_SHAPE;
+  if ((int64_t)c->pages * c->page > 0x7FFFFFFFLL) return W4A16_ERR_SHAPE;
+  return W4A16_OK;
+}
+
+w4a16_status_t check_cache_pointers(const w4a16_kv_cache_t* c) {
+  if (!c->k || !c->v || !c->k_scales || !c->v_scales) return W4A16_ERR_NULL;
+  if (!kv_aligned(c->k, 16) || !kv_aligned(c->v, 16) || !kv_aligned(c->k_scales, 2) || !kv_aligned(c->v_scales, 2))
+    return W4A16_ERR_ALIGN;
+  return W4A16_OK;
+}
+
+KvCache device_cache(const w4a16_kv_cache_t* c) {
+  return KvCache{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->k_scales, c->v_scales, c->pages,
+                 c->heads, __builtin_ctz((unsigned)c->page)};
+}
+
+// calls f with the cache's head size and type as constants
+template <class F>
+void with_cache_form(const w4a16_kv_cache_t* c, F&& f) {
+  using std::integral_constant;
+  auto typed = [&](auto d) {
+    if (c->type == W4A16_KV_INT8)
+      f(d, integral_constant<int, W4A16_KV_INT8>{});
+    else
+      f(d, integral_constant<int, W4A16_KV_FP8>{});
+  };
+  if (c->dim == 64)
+    typed(integral_constant<int, 64>{});
+  else if (c->dim == 128)
+    typed(integral_constant<int, 128>{});
+  else
+    typed(integral_constant<int, 256>{});
+}
+
+w4a16_status_t check_attention(const w4a16_kv_cache_t* cache, int tokens, int requests, int max_new, int max_len,
+                               int window, int q_heads) {
+  const w4a16_status_t st = check_cache(cache);
+  if (st != W4A16_OK) return st;
+  if (tokens < 0 || requests < 0 || max_new < 0 || max_len < 0 || window < 0 || q_heads < 1) return W4A16_ERR_SHAPE;
+  if (tokens > W4A16_KV_MAX_TOKENS || requests > W4A16_KV_MAX_REQUESTS || max_len > kKvMaxLen) return W4A16_ERR_SHAPE;
+  if (q_heads % cache->heads) return W4A16_ERR_SHAPE;
+  if (q_heads / cache->heads > W4A16_KV_MAX_GROUP) return W4A16_ERR_UNSUPPORTED;
+  return W4A16_OK;
+}
+
+}  // namespace
+
+size_t kv_attention_workspace(int, int, int, int, int, int, int, int) { return 0; }
+
+}  // namespace w4k
+
+using namespace w4k;
+
+extern "C" {
+
+w4a16_status_t w4a16_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* free_pages,
+                             int num_free, int32_t* block_table, int width, int32_t* seq_lens, int32_t* token_start,
+                             int32_t* slot_map, int32_t* pages_used, int requests, int tokens, int page,
+                             void* stream) {
+  if (!page_supported(page)) return W4A16_ERR_UNSUPPORTED;
+  if (requests < 0 || requests > W4A16_KV_MAX_REQUESTS || tokens < 0 || tokens > W4A16_KV_MAX_TOKENS ||
+      num_free < 0 || width < 0 || width > W4A16_KV_MAX_WIDTH)
+    return W4A16_ERR_SHAPE;
+  if (!token_start || !pages_used) return W4A16_ERR_NULL;
+  if (requests > 0 && (!ctx_lens || !new_lens || !seq_lens)) return W4A16_ERR_NULL;
+  if ((num_free > 0 && !free_pages) || (tokens > 0 && !slot_map) || (requests > 0 && width > 0 && !block_table))
+    return W4A16_ERR_NULL;
+  for (const void* p : {(const void*)ctx_lens, (const void*)new_lens, (const void*)free_pages,
+                        (const void*)block_table, (const void*)seq_lens, (const void*)token_start,
+                        (const void*)slot_map, (const void*)pages_used})
+    if (!kv_aligned(p, 4)) return W4A16_ERR_ALIGN;
+  // enough blocks a request for the longest row of columns or (as far as the
+  // host can tell) tokens, 16 a lane; the whole grid bounded
+  const int gx = requests > 0 ? (requests + kKvWaves - 1) / kKvWaves : 1;
+  int gy = (int)(((long long)(tokens > width ? tokens : width) + kWave * 16 - 1) / (kWave * 16));
+  const int most = 4096 / gx;
+  gy = gy > most ? most : gy;
+  gy = gy < 1 ? 1 : gy;
+  hipLaunchKernelGGL(kv_plan_kernel, dim3(gx, gy), dim3(kKvThreads), 0, (hipStream_t)stream, ctx_lens, new_lens,
+                     free_pages, num_free, block_table, width, seq_lens, token_start, slot_map, pages_used, requests,
+                     tokens, __builtin_ctz((unsigned)page));
+  return kv_launched(hipGetLastError());
+}
+
+w4a16_status_t w4a16_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                               const int32_t* slot_map, const w4a16_kv_cache_t* cache, int tokens, void* stream) {
+  w4a16_status_t st = check_cache(cache);
+  if (st != W4A16_OK) return st;
+  if (tokens < 0 || tokens > W4A16_KV_MAX_TOKENS) return W4A16_ERR_SHAPE;
+  const int64_t row = (int64_t)cache->heads * cache->dim;
+  if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8 || k_stride > (1LL << 40) ||
+      v_stride > (1LL << 40))
+    return W4A16_ERR_SHAPE;
+  if (tokens == 0 || cache->pages == 0) return W4A16_OK;
+  st = check_cache_pointers(cache);
+  if (st != W4A16_OK) return st;
+  if (!k || !v || !slot_map) return W4A16_ERR_NULL;
+  if (!kv_aligned(k, 16) || !kv_aligned(v, 16) || !kv_aligned(slot_map, 4)) return W4A16_ERR_ALIGN;
+  const int span = tokens <= 1024 ? 1 : 16;
+  with_cache_form(cache, [&](auto d, auto type) {
+    hipLaunchKernelGGL((kv_append_kernel<decltype(d)::value, decltype(type)::value>),
+                       dim3((unsigned)((tokens + span - 1) / span), 2 * cache->heads), dim3(kKvThreads), 0,
+                       (hipStream_t)stream, k, k_stride, v, v_stride, slot_map, device_cache(cache), tokens, span);
+  });
+  return kv_launched(hipGetLastError());
+}
+
+size_t w4a16_kv_attention_workspace_bytes(int tokens, int requests, int max_new, int max_len, int window, int q_heads,
+                                          const w4a16_kv_cache_t* cache) {
+  if (check_attention(cache, tokens, requests, max_new, max_len, window, q_heads) != W4A16_OK) return 0;
+  return kv_attention_workspace(tokens, requests, max_new, max_len, window, q_heads, cache->heads, cache->dim);
+}
+
+w4a16_status_t w4a16_kv_attention(const uint16_t* q, int64_t q_stride, const w4a16_kv_cache_t* cache,
+                                  const int32_t* block_table, int width, const int32_t* seq_lens,
+                                  const int32_t* token_start, uint16_t* out, float scale, int window, int tokens,
+                                  int requests, int max_new, int max_len, int q_heads, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  w4a16_status_t st = check_attention(cache, tokens, requests, max_new, max_len, window, q_heads);
+  if (st != W4A16_OK) return st;
+  if (width < 0 || width > W4A16_KV_MAX_WIDTH || q_stride < (int64_t)q_heads * cache->dim || q_stride % 8 || q_stride > (1LL << 40))
+    return W4A16_ERR_SHAPE;
+  if (tokens == 0 || requests == 0 || max_new == 0) return W4A16_OK;
+  st = check_cache_pointers(cache);
+  if (st != W4A16_OK) return st;
+  if (!q || !out || !seq_lens || !token_start || (width > 0 && !block_table)) return W4A16_ERR_NULL;
+  if (!kv_aligned(q, 16) || !kv_aligned(out, 16) || !kv_aligned(block_table, 4) || !kv_aligned(seq_lens, 4) ||
+      !kv_aligned(token_start, 4))
+    return W4A16_ERR_ALIGN;
+  const size_t need =
+      kv_attention_workspace(tokens, requests, max_new, max_len, window, q_heads, cache->heads, cache->dim);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  if (!kv_aligned(workspace, 16)) return W4A16_ERR_ALIGN;
+  KvAttnArgs a;
+  a.c = device_cache(cache);
+  a.q = q;
+  a.q_stride = q_stride;
+  a.table = block_table;
+  a.seq_lens = seq_lens;
+  a.token_start = token_start;
+  a.out = out;
+  a.scale_log2 = scale * 1.44269504088896340736f;
+  a.width = width;
+  a.window = window;
+  a.tokens = tokens;
+  a.requests = requests;
+  a.max_new = max_new;
+  a.max_len = max_len;
+  a.q_heads = q_heads;
+  a.group = q_heads / cache->heads;
+  hipStream_t s = (hipStream_t)stream;
+  switch (cache->dim) {
+    case 64: return kv_launched(kv_attention_d64(cache->type, a, workspace, s));
+    case 128: return kv_launched(kv_attention_d128(cache->type, a, workspace, s));
+    default: return kv_launched(kv_attention_d256(cache->type, a, workspace, s));
+  }
+}
+
+w4a16_status_t w4a16_kv_dequant(const w4a16_kv_cache_t* cache, const int32_t* pages, int count, float* k_out,
+                                float* v_out, void* stream) {
+  w4a16_status_t st = check_cache(cache);
+  if (st != W4A16_OK) return st;
+  if (count < 0) return W4A16_ERR_SHAPE;
+  if (count == 0) return W4A16_OK;
+  st = check_cache_pointers(cache);
+  if (st != W4A16_OK) return st;
+  if (!pages || !k_out || !v_out) return W4A16_ERR_NULL;
+  if (!kv_aligned(pages, 4) || !kv_aligned(k_out, 16) || !kv_aligned(v_out, 16)) return W4A16_ERR_ALIGN;
+  with_cache_form(cache, [&](auto d, auto type) {
+    hipLaunchKernelGGL((kv_dequant_kernel<decltype(d)::value, decltype(type)::value>),
+                       dim3((unsigned)count, 2 * cache->heads), dim3(kKvThreads), 0, (hipStream_t)stream,
+                       device_cache(cache), pages, k_out, v_out);
+  });
+  return kv_launched(hipGetLastError());
+}
+
+}  // extern "C"

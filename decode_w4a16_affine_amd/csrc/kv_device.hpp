@@ -1,0 +1,90 @@
+// Device helpers of the paged 8-bit key/value cache (include/w4a16_kv.h): the
+// scale rule, encoding and decoding of codes, and the argument structs.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "qmm_device.hpp"
+#include "w4a16_kv.h"
+
+namespace w4k {
+
+constexpr float kKvMinScale = 0x1p-100f;
+
+// Scale of a page and head from the bit pattern of its largest magnitude (bf16
+// bits without sign, so integer order is the order of magnitudes with
+// infinity and NaN on top), as fp32.  a / 127 resp. a / 448 in fp32 (correctly
+// rounded), then up to the next bf16 number resp. power of two.  The exact
+// quotient lies on the same side of every bf16 number b as its fp32 rounding:
+// a and 127 b are multiples of one ulp of b's 8 significant bits, so where
+// they differ they differ by over 2^-16 of a.  Non-finite magnitudes give NaN.
+template <int TYPE>
+__device__ __forceinline__ float kv_scale_of(uint32_t amax_bits) {
+  if (amax_bits >= 0x7F80u) return __builtin_nanf("");
+  const float a = bf16_lo(amax_bits);
+  uint32_t u;
+  if constexpr (TYPE == W4A16_KV_INT8)
+    u = (__float_as_uint(a / 127.0f) + 0xFFFFu) & 0xFFFF0000u;
+  else
+    u = (__float_as_uint(a / 448.0f) + 0x7FFFFFu) & 0x7F800000u;
+  return fmaxf(__uint_as_float(u), kKvMinScale);
+}
+
+// Nearest code of y (|y| <= 127 resp. 448 up to rounding), ties to even.
+template <int TYPE>
+__device__ __forceinline__ uint32_t kv_encode(float y) {
+  if constexpr (TYPE == W4A16_KV_INT8)
+    return (uint32_t)(int)rintf(y) & 0xFFu;
+  else
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, 0.0f, 0, false) & 0xFFu;
+}
+
+// Code in byte B of a word as fp32 (exact).
+template <int TYPE, int B>
+__device__ __forceinline__ float kv_decode(uint32_t w) {
+  if constexpr (TYPE == W4A16_KV_INT8)
+    return (float)(int8_t)(w >> (8 * B));
+  else
+    return __builtin_amdgcn_cvt_f32_fp8((int)w, B);
+}
+
+// A page and head's scale is NaN: its codes are 0 (int8 has no other answer).
+template <int TYPE>
+__device__ __forceinline__ uint32_t kv_code_of(float x, float scale) {
+  return scale == scale ? kv_encode<TYPE>(x / scale) : 0u;
+}
+
+struct KvCache {
+  uint8_t* k;
+  uint8_t* v;
+  uint16_t* ks;
+  uint16_t* vs;
+  int pages, heads, page_shift;
+};
+
+struct KvAttnArgs {
+  KvCache c;
+  const uint16_t* q;
+  int64_t q_stride;
+  const int32_t* table;
+  const int32_t* seq_lens;
+  const int32_t* token_start;
+  uint16_t* out;
+  float scale_log2;      // scale * log2(e): softmax in base 2
+  int width, window, tokens, requests, max_new, max_len, q_heads, group;
+};
+
+// Launchers (kv_attention.hip, once per head size).
+#define W4K_DECLARE_KV(D)                                                                     \
+  hipError_t kv_attention_d##D(int type, const KvAttnArgs& a, void* workspace, hipStream_t st);
+W4K_DECLARE_KV(64)
+W4K_DECLARE_KV(128)
+W4K_DECLARE_KV(256)
+#undef W4K_DECLARE_KV
+
+// Workspace of the attention (kv.hip uses it for validation and the query).
+size_t kv_attention_workspace(int tokens, int requests, int max_new, int max_len, int window, int q_heads, int heads,
+                              int dim);
+
+}  // namespace w4k

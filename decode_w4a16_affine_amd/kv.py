@@ -1,0 +1,244 @@
+"""Python binding of the paged 8-bit key/value cache (include/w4a16_kv.h).
+
+Same conventions as the package's other functions: C-ABI names, tensors in,
+dtype and shape checks before any pointer reaches the library, the current
+stream of torch unless one is given, no fallback.
+
+Tensor conventions (all on the same GPU; contiguous unless said otherwise):
+  q, k, v, out            : torch.bfloat16; q, k, v may be parts of wider token
+                            rows (only their last two dimensions are dense)
+  k_cache, v_cache        : torch.int8 or torch.float8_e4m3fn, [pages, H, P, D] and [pages, H, D, P]
+  k_scales, v_scales      : torch.bfloat16 [pages, H]
+  lengths, tables, slots  : torch.int32
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import _check, _dtype, _on_device, _ptr, _shape, _stream
+from . import lib as _base_lib
+
+KV_INT8 = 0               # W4A16_KV_INT8
+KV_FP8 = 1                # W4A16_KV_FP8
+KV_DIMS = (64, 128, 256)
+KV_PAGES = (16, 32, 64, 128, 256)
+KV_MAX_REQUESTS = 1 << 20   # W4A16_KV_MAX_REQUESTS
+KV_MAX_TOKENS = 1 << 20     # W4A16_KV_MAX_TOKENS
+KV_MAX_HEADS = 1024         # W4A16_KV_MAX_HEADS
+KV_MAX_GROUP = 64           # W4A16_KV_MAX_GROUP
+KV_MAX_WIDTH = 1 << 22      # W4A16_KV_MAX_WIDTH
+
+KV_EXPORTS = ("w4a16_kv_plan", "w4a16_kv_append", "w4a16_kv_attention_workspace_bytes", "w4a16_kv_attention",
+              "w4a16_kv_dequant")
+
+_TYPES = {torch.int8: KV_INT8, torch.float8_e4m3fn: KV_FP8}
+_vp = ctypes.c_void_p
+_int = ctypes.c_int
+_i64 = ctypes.c_int64
+
+
+class KVCache(ctypes.Structure):
+    """w4a16_kv_cache_t"""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scales", _vp), ("v_scales", _vp), ("type", _int), ("pages", _int),
+                ("heads", _int), ("page", _int), ("dim", _int)]
+
+
+_lib = None
+
+
+def kv_lib() -> ctypes.CDLL:
+    """libw4a16.so with the prototypes of the key/value cache."""
+    global _lib
+    if _lib is None:
+        L = _base_lib()
+        cache = ctypes.POINTER(KVCache)
+        L.w4a16_kv_plan.restype = _int
+        L.w4a16_kv_plan.argtypes = [_vp, _vp, _vp, _int, _vp, _int, _vp, _vp, _vp, _vp, _int, _int, _int, _vp]
+        L.w4a16_kv_append.restype = _int
+        L.w4a16_kv_append.argtypes = [_vp, _i64, _vp, _i64, _vp, cache, _int, _vp]
+        L.w4a16_kv_attention_workspace_bytes.restype = ctypes.c_size_t
+        L.w4a16_kv_attention_workspace_bytes.argtypes = [_int, _int, _int, _int, _int, _int, cache]
+        L.w4a16_kv_attention.restype = _int
+        L.w4a16_kv_attention.argtypes = [_vp, _i64, cache, _vp, _int, _vp, _vp, _vp, ctypes.c_float, _int, _int, _int,
+                                         _int, _int, _int, _vp, ctypes.c_size_t, _vp]
+        L.w4a16_kv_dequant.restype = _int
+        L.w4a16_kv_dequant.argtypes = [cache, _vp, _int, _vp, _vp, _vp]
+        _lib = L
+    return _lib
+
+
+def _cache(k_cache, v_cache, k_scales, v_scales) -> KVCache:
+    """The checked C struct of a cache's tensors."""
+    kind = _TYPES.get(k_cache.dtype)
+    if kind is None:
+        raise TypeError(f"k_cache must be torch.int8 or torch.float8_e4m3fn, got {k_cache.dtype}")
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache must be 4-D [pages, heads, page, D], got {list(k_cache.shape)}")
+    _dtype(v_cache, k_cache.dtype, "v_cache")
+    _dtype(k_scales, torch.bfloat16, "k_scales")
+    _dtype(v_scales, torch.bfloat16, "v_scales")
+    pages, heads, page, dim = k_cache.shape
+    _shape(v_cache, (pages, heads, dim, page), "v_cache")
+    _shape(k_scales, (pages, heads), "k_scales")
+    _shape(v_scales, (pages, heads), "v_scales")
+    return KVCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), kind, pages,
+                   heads, page, dim)
+
+
+def _vector(t, name):
+    _dtype(t, torch.int32, name)
+    if t.dim() != 1:
+        raise ValueError(f"{name} must be 1-D, got {list(t.shape)}")
+    return t.shape[0]
+
+
+def _rows(t, heads, dim, name):
+    """Token count and token stride of a [T, heads, D] tensor whose token rows are dense."""
+    _dtype(t, torch.bfloat16, name)
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != dim:
+        raise ValueError(f"{name} must have shape [T, {'heads' if heads is None else heads}, {dim}], got {list(t.shape)}")
+    tokens, stride, head_stride, unit = t.shape[0], *t.stride()
+    row = t.shape[1] * dim
+    if tokens <= 1:
+        stride = -(-max(stride, row) // 8) * 8      # no second row: any valid stride
+    if (unit != 1 and dim > 1) or (head_stride != dim and t.shape[1] > 1) or stride < row:
+        raise ValueError(f"{name} must be dense within a token (strides [>= {row}, {dim}, 1]), got {list(t.stride())}")
+    return tokens, stride
+
+
+# ---- C-ABI entry points ---------------------------------------------------------
+
+def w4a16_kv_plan(ctx_lens, new_lens, free_pages, block_table, seq_lens, token_start, slot_map, pages_used, page: int,
+                  stream=None) -> None:
+    """Block tables and slot maps of a step from request lengths (block_table [R, width] is updated in place)."""
+    R = _vector(ctx_lens, "ctx_lens")
+    _dtype(new_lens, torch.int32, "new_lens")
+    _shape(new_lens, (R,), "new_lens")
+    num_free = _vector(free_pages, "free_pages")
+    _dtype(block_table, torch.int32, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError(f"block_table must have shape [{R}, width], got {list(block_table.shape)}")
+    _dtype(seq_lens, torch.int32, "seq_lens")
+    _shape(seq_lens, (R,), "seq_lens")
+    _dtype(token_start, torch.int32, "token_start")
+    _shape(token_start, (R + 1,), "token_start")
+    tokens = _vector(slot_map, "slot_map")
+    _dtype(pages_used, torch.int32, "pages_used")
+    _shape(pages_used, (1,), "pages_used")
+    _on_device(ctx_lens, new_lens, free_pages, block_table, seq_lens, token_start, slot_map, pages_used)
+    _check(kv_lib().w4a16_kv_plan(_ptr(ctx_lens), _ptr(new_lens), _ptr(free_pages), num_free, _ptr(block_table),
+                                  block_table.shape[1], _ptr(seq_lens), _ptr(token_start), _ptr(slot_map),
+                                  _ptr(pages_used), R, tokens, page, _stream(stream)), "w4a16_kv_plan")
+
+
+def w4a16_kv_append(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, stream=None) -> None:
+    """Quantizes k, v [T, H, D] into the cache at slot_map [T] (slots outside the cache are skipped)."""
+    c = _cache(k_cache, v_cache, k_scales, v_scales)
+    tokens, k_stride = _rows(k, c.heads, c.dim, "k")
+    v_tokens, v_stride = _rows(v, c.heads, c.dim, "v")
+    _dtype(slot_map, torch.int32, "slot_map")
+    _shape(slot_map, (tokens,), "slot_map")
+    if v_tokens != tokens:
+        raise ValueError(f"k and v must have the same tokens, got {tokens} and {v_tokens}")
+    _on_device(k_cache, v_cache, k_scales, v_scales, slot_map)
+    _on_device(k_cache, k, v, contiguous=False)
+    _check(kv_lib().w4a16_kv_append(_ptr(k), k_stride, _ptr(v), v_stride, _ptr(slot_map), ctypes.byref(c), tokens,
+                                    _stream(stream)), "w4a16_kv_append")
+
+
+def w4a16_kv_attention_workspace_bytes(tokens: int, requests: int, max_new: int, max_len: int, window: int,
+                                       q_heads: int, k_cache, v_cache, k_scales, v_scales) -> int:
+    c = _cache(k_cache, v_cache, k_scales, v_scales)
+    return int(kv_lib().w4a16_kv_attention_workspace_bytes(tokens, requests, max_new, max_len, window, q_heads,
+                                                           ctypes.byref(c)))
+
+
+def w4a16_kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, out, workspace,
+                       max_new: int, max_len: int = None, scale: float = None, window: int = 0, stream=None) -> None:
+    """out [T, HQ, D] = causal attention of q [T, HQ, D] over the cache.
+
+    token_start [R + 1] and seq_lens [R] as w4a16_kv_plan writes them; max_new
+    and max_len bound the requests' new tokens and lengths (max_len None: what
+    the block table's columns hold); scale None: 1 / sqrt(D); window 0: no
+    window; workspace: a uint8 device tensor of at least
+    w4a16_kv_attention_workspace_bytes bytes, or None where that is 0."""
+    c = _cache(k_cache, v_cache, k_scales, v_scales)
+    tokens, q_stride = _rows(q, None, c.dim, "q")
+    R = _vector(seq_lens, "seq_lens")
+    _dtype(token_start, torch.int32, "token_start")
+    _shape(token_start, (R + 1,), "token_start")
+    _dtype(block_table, torch.int32, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError(f"block_table must have shape [{R}, width], got {list(block_table.shape)}")
+    _dtype(out, torch.bfloat16, "out")
+    _shape(out, q.shape, "out")
+    if workspace is not None:
+        _dtype(workspace, torch.uint8, "workspace")
+    if max_len is None:
+        max_len = block_table.shape[1] * c.page
+    if scale is None:
+        scale = 1.0 / math.sqrt(c.dim)
+    _on_device(k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, out, workspace)
+    _on_device(k_cache, q, contiguous=False)
+    _check(kv_lib().w4a16_kv_attention(_ptr(q), q_stride, ctypes.byref(c), _ptr(block_table), block_table.shape[1],
+                                       _ptr(seq_lens), _ptr(token_start), _ptr(out), scale, window, tokens, R, max_new,
+                                       max_len, q.shape[1], _ptr(workspace),
+                                       0 if workspace is None else workspace.numel(), _stream(stream)),
+           "w4a16_kv_attention")
+
+
+def w4a16_kv_dequant(k_cache, v_cache, k_scales, v_scales, pages, k_out, v_out, stream=None) -> None:
+    """k_out, v_out [n, H, P, D] (fp32) = the values of pages [n]."""
+    c = _cache(k_cache, v_cache, k_scales, v_scales)
+    n = _vector(pages, "pages")
+    _dtype(k_out, torch.float32, "k_out")
+    _dtype(v_out, torch.float32, "v_out")
+    _shape(k_out, (n, c.heads, c.page, c.dim), "k_out")
+    _shape(v_out, (n, c.heads, c.page, c.dim), "v_out")
+    _on_device(k_cache, v_cache, k_scales, v_scales, pages, k_out, v_out)
+    _check(kv_lib().w4a16_kv_dequant(ctypes.byref(c), _ptr(pages), n, _ptr(k_out), _ptr(v_out), _stream(stream)),
+           "w4a16_kv_dequant")
+
+
+# ---- allocating conveniences (torch allocates; the library computes) ------------
+
+def kv_cache(pages: int, heads: int, dim: int, page: int = 64, dtype=torch.int8, device="cuda"):
+    """An empty cache: (k_cache, v_cache, k_scales, v_scales)."""
+    return (torch.zeros((pages, heads, page, dim), dtype=dtype, device=device),
+            torch.zeros((pages, heads, dim, page), dtype=dtype, device=device),
+            torch.zeros((pages, heads), dtype=torch.bfloat16, device=device),
+            torch.zeros((pages, heads), dtype=torch.bfloat16, device=device))
+
+
+def kv_plan(ctx_lens, new_lens, free_pages, block_table, tokens: int, page: int, stream=None):
+    """(seq_lens, token_start, slot_map [tokens], pages_used); block_table is updated in place."""
+    R = ctx_lens.shape[0]
+    seq_lens, token_start, slot_map, pages_used = (
+        torch.empty((n,), dtype=torch.int32, device=ctx_lens.device) for n in (R, R + 1, tokens, 1))
+    w4a16_kv_plan(ctx_lens, new_lens, free_pages, block_table, seq_lens, token_start, slot_map, pages_used, page,
+                  stream=stream)
+    return seq_lens, token_start, slot_map, pages_used
+
+
+def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, max_new: int,
+                 max_len: int = None, scale: float = None, window: int = 0, stream=None):
+    out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if max_len is None:
+        max_len = block_table.shape[1] * k_cache.shape[2]
+    need = w4a16_kv_attention_workspace_bytes(q.shape[0], seq_lens.shape[0], max_new, max_len, window, q.shape[1],
+                                              k_cache, v_cache, k_scales, v_scales)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    w4a16_kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, out, ws, max_new,
+                       max_len=max_len, scale=scale, window=window, stream=stream)
+    return out
+
+
+def kv_dequant(k_cache, v_cache, k_scales, v_scales, pages, stream=None):
+    pages_heads, (page, dim) = (pages.shape[0], k_cache.shape[1]), k_cache.shape[2:]
+    k_out = torch.empty((*pages_heads, page, dim), dtype=torch.float32, device=k_cache.device)
+    v_out = torch.empty_like(k_out)
+    w4a16_kv_dequant(k_cache, v_cache, k_scales, v_scales, pages, k_out, v_out, stream=stream)
+    return k_out, v_out
