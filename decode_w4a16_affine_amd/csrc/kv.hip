@@ -324,9 +324,40 @@ w4a16_status_t check_attention(const w4a16_kv_cache_t* cache, int tokens, int re
   return W4A16_OK;
 }
 
-}  // namespace
+// The launch parameters of an attention call from its (checked) sizes.  Chunks
+// of 512 entries, doubled until max_len holds at most 128: short enough that
+// one request's chunks fill the chip, long enough that the partial results
+// (D + 2 floats a row and chunk) stay small beside the codes.  They depend on
+// max_len alone, so a row's sums do not depend on the batch.
+KvAttnArgs attention_args(const w4a16_kv_cache_t* cache, int tokens, int requests, int max_new, int max_len,
+                          int window, int q_heads) {
+  KvAttnArgs a{};
+  a.c = device_cache(cache);
+  a.window = window;
+  a.tokens = tokens;
+  a.requests = requests;
+  a.max_new = max_new;
+  a.max_len = max_len;
+  a.q_heads = q_heads;
+  a.group = q_heads / cache->heads;
+  a.split_tokens = max_new < kKvSplitRows / a.group ? max_new : kKvSplitRows / a.group;
+  const int rows = a.split_tokens * a.group;
+  a.row_groups = rows <= 16 ? 1 : (rows + 31) / 32;
+  a.chunk = 512;
+  while ((max_len + (long long)a.chunk - 1) / a.chunk > 128) a.chunk *= 2;
+  long long chunks = (max_len + (long long)a.chunk - 1) / a.chunk;
+  // a window's rows attend window + split_tokens - 1 entries at most
+  const long long in_window = ((long long)window + a.split_tokens - 1 + a.chunk - 2) / a.chunk + 1;
+  if (window > 0 && in_window < chunks) chunks = in_window;
+  a.chunks = chunks > 1 ? (int)chunks : 1;
+  return a;
+}
 
-size_t kv_attention_workspace(int, int, int, int, int, int, int, int) { return 0; }
+size_t attention_workspace(const KvAttnArgs& a, int dim) {
+  return a.chunks > 1 ? kv_partials(a) * (dim + 2) * sizeof(float) : 0;
+}
+
+}  // namespace
 
 }  // namespace w4k
 
@@ -389,7 +420,8 @@ w4a16_status_t w4a16_kv_append(const uint16_t* k, int64_t k_stride, const uint16
 size_t w4a16_kv_attention_workspace_bytes(int tokens, int requests, int max_new, int max_len, int window, int q_heads,
                                           const w4a16_kv_cache_t* cache) {
   if (check_attention(cache, tokens, requests, max_new, max_len, window, q_heads) != W4A16_OK) return 0;
-  return kv_attention_workspace(tokens, requests, max_new, max_len, window, q_heads, cache->heads, cache->dim);
+  if (tokens == 0 || requests == 0 || max_new == 0) return 0;
+  return attention_workspace(attention_args(cache, tokens, requests, max_new, max_len, window, q_heads), cache->dim);
 }
 
 w4a16_status_t w4a16_kv_attention(const uint16_t* q, int64_t q_stride, const w4a16_kv_cache_t* cache,
@@ -408,27 +440,18 @@ w4a16_status_t w4a16_kv_attention(const uint16_t* q, int64_t q_stride, const w4a
   if (!kv_aligned(q, 16) || !kv_aligned(out, 16) || !kv_aligned(block_table, 4) || !kv_aligned(seq_lens, 4) ||
       !kv_aligned(token_start, 4))
     return W4A16_ERR_ALIGN;
-  const size_t need =
-      kv_attention_workspace(tokens, requests, max_new, max_len, window, q_heads, cache->heads, cache->dim);
+  KvAttnArgs a = attention_args(cache, tokens, requests, max_new, max_len, window, q_heads);
+  const size_t need = attention_workspace(a, cache->dim);
   if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
   if (!kv_aligned(workspace, 16)) return W4A16_ERR_ALIGN;
-  KvAttnArgs a;
-  a.c = device_cache(cache);
   a.q = q;
   a.q_stride = q_stride;
   a.table = block_table;
+  a.width = width;
   a.seq_lens = seq_lens;
   a.token_start = token_start;
   a.out = out;
   a.scale_log2 = scale * 1.44269504088896340736f;
-  a.width = width;
-  a.window = window;
-  a.tokens = tokens;
-  a.requests = requests;
-  a.max_new = max_new;
-  a.max_len = max_len;
-  a.q_heads = q_heads;
-  a.group = q_heads / cache->heads;
   hipStream_t s = (hipStream_t)stream;
   switch (cache->dim) {
     case 64: return kv_launched(kv_attention_d64(cache->type, a, workspace, s));

@@ -1,5 +1,6 @@
 // Attention over the paged 8-bit cache (include/w4a16_kv.h).  Compiled once per
 // head size (W4K_D = 64, 128, 256).
+#include "kv_attn_split.hpp"
 #include "kv_device.hpp"
 
 namespace w4k {
@@ -38,7 +39,7 @@ __global__ __launch_bounds__(kWave) void kv_attention_row_kernel(KvAttnArgs a) {
   if (r < 0) return;
   const int n = a.token_start[r + 1] - a.token_start[r];
   const int i = t - a.token_start[r];
-  if (i >= a.max_new) return;
+  if (i >= a.max_new || n * a.group <= kKvSplitRows) return;
   const int kh = h / a.group;
   const int pos = a.seq_lens[r] - n + i;
   const int end = (int)min((long long)min(pos + 1, a.max_len), (long long)a.width << a.c.page_shift);
@@ -102,19 +103,38 @@ __global__ __launch_bounds__(kWave) void kv_attention_row_kernel(KvAttnArgs a) {
     a.out[((size_t)t * a.q_heads + h) * D + lane + e * kWave] = (uint16_t)f32_to_bf16(l != 0.0f ? o[e] / l : 0.0f);
 }
 
+template <int TYPE>
+hipError_t kv_attention_typed(const KvAttnArgs& a, void* workspace, hipStream_t st) {
+  constexpr int D = W4K_D;
+  float* part_o = static_cast<float*>(workspace);
+  float* part_ml = part_o + kv_partials(a) * D;
+  const dim3 grid(a.requests, a.c.heads * a.row_groups, a.chunks);
+  const int rows = a.split_tokens * a.group;
+  auto split = [&](auto nc) {
+    constexpr int NC = decltype(nc)::value;
+    hipLaunchKernelGGL((kv_split_kernel<D, TYPE, NC>), grid, dim3(kKvSplitWaves * kWave), 0, st, a, part_o, part_ml);
+    if (a.chunks > 1)
+      hipLaunchKernelGGL((kv_join_kernel<D, NC>), dim3(a.requests, a.c.heads, rows), dim3(kKvJoinThreads), 0, st, a,
+                         part_o, part_ml);
+  };
+  if (rows <= 16)
+    split(std::integral_constant<int, 1>{});
+  else
+    split(std::integral_constant<int, 2>{});
+  if ((int64_t)a.max_new * a.group > kKvSplitRows)
+    hipLaunchKernelGGL((kv_attention_row_kernel<D, TYPE>), dim3((unsigned)((size_t)a.tokens * a.q_heads)), dim3(kWave),
+                       0, st, a);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 #define W4K_CAT_(a, b) a##b
 #define W4K_CAT(a, b) W4K_CAT_(a, b)
 
 hipError_t W4K_CAT(kv_attention_d, W4K_D)(int type, const KvAttnArgs& a, void* workspace, hipStream_t st) {
-  (void)workspace;
-  const dim3 grid((unsigned)((size_t)a.tokens * a.q_heads));
-  if (type == W4A16_KV_INT8)
-    hipLaunchKernelGGL((kv_attention_row_kernel<W4K_D, W4A16_KV_INT8>), grid, dim3(kWave), 0, st, a);
-  else
-    hipLaunchKernelGGL((kv_attention_row_kernel<W4K_D, W4A16_KV_FP8>), grid, dim3(kWave), 0, st, a);
-  return hipGetLastError();
+  return type == W4A16_KV_INT8 ? kv_attention_typed<W4A16_KV_INT8>(a, workspace, st)
+                               : kv_attention_typed<W4A16_KV_FP8>(a, workspace, st);
 }
 
 }  // namespace w4k

@@ -73,6 +73,9 @@ struct KvAttnArgs {
   uint16_t* out;
   float scale_log2;      // scale * log2(e): softmax in base 2
   int width, window, tokens, requests, max_new, max_len, q_heads, group;
+  // requests of few rows: entries a chunk, chunks a row at most, row groups a
+  // cache head, new tokens a request at most
+  int chunk, chunks, row_groups, split_tokens;
 };
 
 // Launchers (kv_attention.hip, once per head size).
@@ -83,8 +86,11 @@ W4K_DECLARE_KV(128)
 W4K_DECLARE_KV(256)
 #undef W4K_DECLARE_KV
 
-// Workspace of the attention (kv.hip uses it for validation and the query).
-size_t kv_attention_workspace(int tokens, int requests, int max_new, int max_len, int window, int q_heads, int heads,
-                              int dim);
+constexpr int kKvSplitRows = 64;      // requests of at most this many rows a cache head take the split form
+
+// Floats of one row and chunk's partial result: the output, maximum and sum.
+inline size_t kv_partials(const KvAttnArgs& a) {
+  return (size_t)a.requests * a.c.heads * a.split_tokens * a.group * a.chunks;
+}
 
 }  // namespace w4k
