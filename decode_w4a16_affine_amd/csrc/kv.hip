@@ -451,7 +451,8 @@ w4a16_status_t w4a16_kv_attention(const uint16_t* q, int64_t q_stride, const w4a
   a.seq_lens = seq_lens;
   a.token_start = token_start;
   a.out = out;
-  a.scale_log2 = scale * 1.44269504088896340736f;
+  a.scale_log2 = __builtin_fabsf(scale) * 1.44269504088896340736f;
+  a.q_sign = scale < 0.0f ? 0x80008000u : 0u;
   hipStream_t s = (hipStream_t)stream;
   switch (cache->dim) {
     case 64: return kv_launched(kv_attention_d64(cache->type, a, workspace, s));

@@ -42,86 +42,11 @@
 // any batch and for any number of candidates.
 #pragma once
 
-#include "kv_device.hpp"
+#include "kv_attn_common.hpp"
 
 namespace w4k {
 
-typedef __bf16 kv_bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 kv_bf16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 kv_f16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 kv_f16x2 __attribute__((ext_vector_type(2)));
-typedef float kv_f32x4 __attribute__((ext_vector_type(4)));
-typedef float kv_f32x2 __attribute__((ext_vector_type(2)));
-
-constexpr int kKvTile = 64;           // cache entries a wave takes at once
 constexpr int kKvSplitWaves = 4;
-constexpr float kKvNone = -3e38f;     // running maximum before any entry
-
-// Four codes as two words of two bf16 (exact).
-template <int TYPE>
-__device__ __forceinline__ uint2 kv_bf16_of4(uint32_t w) {
-  uint2 o;
-  if constexpr (TYPE == W4A16_KV_INT8) {
-    // integers up to 128 have 8 significant bits: the upper halves of their fp32 form
-    o.x = __builtin_amdgcn_perm(__float_as_uint(kv_decode<TYPE, 1>(w)), __float_as_uint(kv_decode<TYPE, 0>(w)),
-                                0x07060302u);
-    o.y = __builtin_amdgcn_perm(__float_as_uint(kv_decode<TYPE, 3>(w)), __float_as_uint(kv_decode<TYPE, 2>(w)),
-                                0x07060302u);
-  } else {
-    o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
-    o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
-  }
-  return o;
-}
-
-// Four codes as two words of two fp16 (exact).
-template <int TYPE>
-__device__ __forceinline__ uint2 kv_f16_of4(uint32_t w) {
-  uint2 o;
-  if constexpr (TYPE == W4A16_KV_INT8) {
-    // code + 128 in the low byte of the fp16 number 1024, then minus 1152
-    const uint32_t u = w ^ 0x80808080u;
-    const kv_f16x2 bias = {(_Float16)-1152.0f, (_Float16)-1152.0f};
-    o.x = __builtin_bit_cast(uint32_t, __builtin_bit_cast(kv_f16x2, __builtin_amdgcn_perm(u, 0x64646464u, 0x00050004u)) + bias);
-    o.y = __builtin_bit_cast(uint32_t, __builtin_bit_cast(kv_f16x2, __builtin_amdgcn_perm(u, 0x64646464u, 0x00070006u)) + bias);
-  } else {
-    o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
-    o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true));
-  }
-  return o;
-}
-
-template <int TYPE>
-__device__ __forceinline__ kv_bf16x8 kv_bf16_of8(uint32_t a, uint32_t b) {
-  const uint2 x = kv_bf16_of4<TYPE>(a), y = kv_bf16_of4<TYPE>(b);
-  return __builtin_bit_cast(kv_bf16x8, make_uint4(x.x, x.y, y.x, y.y));
-}
-
-template <int TYPE>
-__device__ __forceinline__ kv_f16x8 kv_f16_of8(uint32_t a, uint32_t b) {
-  const uint2 x = kv_f16_of4<TYPE>(a), y = kv_f16_of4<TYPE>(b);
-  return __builtin_bit_cast(kv_f16x8, make_uint4(x.x, x.y, y.x, y.y));
-}
-
-// Where the rows of one workgroup lie: shared by the split kernel and the join.
-struct KvRows {
-  int n, first, seq;      // new tokens, first token row, length of the request
-  int begin, end;         // cache entries any of the group's rows attends
-};
-
-// Rows [row0, row0 + rows) of request r (rows counted token by token, G a token).
-__device__ __forceinline__ KvRows kv_rows_of(const KvAttnArgs& a, int r, int row0, int rows) {
-  KvRows k;
-  k.first = a.token_start[r];
-  k.n = a.token_start[r + 1] - k.first;
-  k.seq = a.seq_lens[r];
-  const int last = min(row0 + rows, min(k.n, a.max_new) * a.group) - 1;
-  const long long held = (long long)a.width << a.c.page_shift;
-  const int lo = k.seq - k.n + row0 / a.group, hi = k.seq - k.n + last / a.group;
-  k.end = (int)min((long long)min(hi + 1, a.max_len), held);
-  k.begin = a.window > 0 ? max(0, lo - a.window + 1) : 0;
-  return k;
-}
 
 template <int D, int TYPE, int NC>
 __global__ __launch_bounds__(kKvSplitWaves * kWave) void kv_split_kernel(KvAttnArgs a, float* part_o, float* part_ml) {
@@ -143,23 +68,21 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave) void kv_split_kernel(KvAttnA
   if (c_begin >= c_end && (blockIdx.z > 0 || rows.end > rows.begin)) return;
   const int shift = a.c.page_shift, P = 1 << shift;
 
-  // this lane's rows: queries (in the keys' order), positions, where they go
+  // this lane's rows: queries (in the keys' order) and positions
   kv_bf16x8 q[NC][2 * KC];
-  int hi[NC], lo[NC];
-  int64_t out_at[NC];
+  KvLaneRows<NC> lr;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int row = min(row0 + 16 * c + x, live - 1);
     const int i = row / a.group, t = rows.first + i, h = kh * a.group + row % a.group;
     const bool ok = row0 + 16 * c + x < live && t >= 0 && t < a.tokens;
-    hi[c] = ok ? min(rows.seq - rows.n + i, rows.end - 1) : -1;
-    lo[c] = a.window > 0 ? rows.seq - rows.n + i - a.window + 1 : 0;
-    out_at[c] = ok ? ((int64_t)t * a.q_heads + h) * D : -1;
+    lr.hi[c] = ok ? min(rows.seq - rows.n + i, rows.end - 1) : -1;
+    lr.lo[c] = a.window > 0 ? rows.seq - rows.n + i - a.window + 1 : 0;
     const uint16_t* qp = a.q + (ok ? (size_t)t * a.q_stride + (size_t)h * D : 0) + 16 * g;
 #pragma unroll
     for (int k = 0; k < KC; ++k) {
-      q[c][2 * k] = *reinterpret_cast<const kv_bf16x8*>(qp + 64 * k);
-      q[c][2 * k + 1] = *reinterpret_cast<const kv_bf16x8*>(qp + 64 * k + 8);
+      q[c][2 * k] = kv_query8(qp + 64 * k, a.q_sign);
+      q[c][2 * k + 1] = kv_query8(qp + 64 * k + 8, a.q_sign);
     }
   }
   // positions that every row of the group attends need no mask
@@ -219,77 +142,18 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave) void kv_split_kernel(KvAttnA
         }
       }
     }
-    // logits in base 2 with the value scale inside, the running maximum, the weights
-    const float lv = __builtin_amdgcn_logf(vs), rv = __builtin_amdgcn_rcpf(vs);
+    float fade[NC];
     kv_f16x8 w[NC][2];
+    kv_softmax_step<NC>(s, lr, j0 + 16 * g, ks, vs, whole, vp >= 0, m, l, fade, w);
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      float top = kKvNone;
+    for (int c = 0; c < NC; ++c)
+      if (__any(fade[c] != 1.0f))
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float u = __builtin_fmaf(s[c][t][i], ks, lv);
-          if (!whole) {
-            const int j = j0 + 16 * g + 4 * t + i;
-            u = vp >= 0 && j >= lo[c] && j <= hi[c] ? u : -__builtin_inff();
-          }
-          s[c][t][i] = u;
-          top = fmaxf(top, u);
-        }
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float m_new = fmaxf(m[c], top);
-      const float fade = __builtin_amdgcn_exp2f(m[c] - m_new);
-      m[c] = m_new;
-      float sum = 0.0f;
-      float p[16];
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[4 * t + i] = __builtin_amdgcn_exp2f(s[c][t][i] - m_new);
-          sum += p[4 * t + i];
-        }
-      // a row's masked entries are exactly 0 also where the page's scales are NaN
-      if (!whole) {
-        float keep = 0.0f;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = j0 + 16 * g + 4 * t + i;
-            p[4 * t + i] = vp >= 0 && j >= lo[c] && j <= hi[c] ? p[4 * t + i] : 0.0f;
-            keep += p[4 * t + i];
-          }
-        sum = keep;
-      }
-      const bool any = whole || (vp >= 0 && j0 + 16 * g + 15 >= lo[c] && j0 + 16 * g <= hi[c]);
-      l[c] = l[c] * fade + (any ? sum * rv : 0.0f);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const kv_f32x2 pair = {p[8 * h + 2 * i], p[8 * h + 2 * i + 1]};
-          pk[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, kv_f16x2));
-        }
-        w[c][h] = __builtin_bit_cast(kv_f16x8, make_uint4(pk[0], pk[1], pk[2], pk[3]));
-      }
-#pragma unroll
-      for (int d = 0; d < DT; ++d) o[c][d] *= fade;
-    }
-    // E4M3 codes of entries that hold nothing may be NaN: 0 * NaN must not enter the sums
+        for (int d = 0; d < DT; ++d) o[c][d] *= fade[c];
     if (TYPE == W4A16_KV_FP8 && !whole) {
-      const int left = vp >= 0 ? rows.end - (j0 + 16 * g) : 0;     // entries of this lane's 16 that exist
-      auto bytes = [&](int b) {
-        const int k = left - 4 * b;
-        return k >= 4 ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
-      };
-      const uint4 mask = make_uint4(bytes(0), bytes(1), bytes(2), bytes(3));
+      const uint4 mask = kv_existing_bytes(vp >= 0 ? rows.end - (j0 + 16 * g) : 0);
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
-        vc[d] = make_uint4(vc[d].x & mask.x, vc[d].y & mask.y, vc[d].z & mask.z, vc[d].w & mask.w);
+      for (int d = 0; d < DT; ++d) vc[d] = kv_and(vc[d], mask);
     }
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
@@ -341,11 +205,7 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave) void kv_split_kernel(KvAttnA
       if (single) {
         const int t = rows.first + row / a.group;
         if (t < 0 || t >= a.tokens) continue;
-        uint16_t* out = a.out + ((size_t)t * a.q_heads + kh * a.group + row % a.group) * D + d;
-        uint32_t b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = f32_to_bf16(ll != 0.0f ? sum[i] / ll : 0.0f);
-        *reinterpret_cast<uint2*>(out) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+        kv_store4(a.out + ((size_t)t * a.q_heads + kh * a.group + row % a.group) * D + d, sum, ll);
       } else {
         const size_t at = (((size_t)r * a.c.heads + kh) * max_rows + row) * a.chunks + blockIdx.z;
         *reinterpret_cast<kv_f32x4*>(part_o + at * D + d) = sum;
@@ -420,11 +280,7 @@ __global__ __launch_bounds__(kKvJoinThreads) void kv_join_kernel(KvAttnArgs a, c
   for (int s = 1; s < S; ++s) sum += s_o[s * (D / 4) + threadIdx.x];
   const int t = rows.first + row / a.group;
   if (t < 0 || t >= a.tokens) return;
-  uint32_t b[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) b[i] = f32_to_bf16(ll != 0.0f ? sum[i] / ll : 0.0f);
-  *reinterpret_cast<uint2*>(a.out + ((size_t)t * a.q_heads + kh * a.group + row % a.group) * D + d) =
-      make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+  kv_store4(a.out + ((size_t)t * a.q_heads + kh * a.group + row % a.group) * D + d, sum, ll);
 }
 
 }  // namespace w4k

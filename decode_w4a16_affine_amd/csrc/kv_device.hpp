@@ -71,7 +71,8 @@ struct KvAttnArgs {
   const int32_t* seq_lens;
   const int32_t* token_start;
   uint16_t* out;
-  float scale_log2;      // scale * log2(e): softmax in base 2
+  float scale_log2;      // |scale| * log2(e): softmax in base 2
+  uint32_t q_sign;       // sign bits of two bf16 if scale < 0, else 0
   int width, window, tokens, requests, max_new, max_len, q_heads, group;
   // requests of few rows: entries a chunk, chunks a row at most, row groups a
   // cache head, new tokens a request at most
