@@ -39,7 +39,9 @@ UNITS = [(f"inst_m{m}", "inst.hip", [f"-DW4K_M={m}"]) for m in range(1, 9)] + [
     ("abi", "w4a16.hip", []),
     # the paged 8-bit key/value cache (include/w4a16_kv.h); its attention once per head size
     ("kv", "kv.hip", []),
-] + [(f"kv_attention_d{d}", "kv_attention.hip", [f"-DW4K_D={d}"]) for d in (64, 128, 256)]
+    # (matrix results in VGPRs here too: the softmax works on them between the products)
+] + [(f"kv_attention_d{d}", "kv_attention.hip", [f"-DW4K_D={d}", "-mllvm", "-amdgpu-mfma-vgpr-form"])
+     for d in (64, 128, 256)]
 
 _NOISE = "not a recognized feature for this target"
 

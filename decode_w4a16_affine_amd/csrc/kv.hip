@@ -279,7 +279,8 @@ w4a16_status_t check_cache(const w4a16_kv_cache_t* c) {
   if (c->dim != 64 && c->dim != 128 && c->dim != 256) return W4A16_ERR_UNSUPPORTED;
   if (!page_supported(c->page)) return W4A16_ERR_UNSUPPORTED;
   if (c->heads < 1 || c->heads > W4A16_KV_MAX_HEADS || c->pages < 0) return W4A16_ERR_SHAPE;
-  if ((int64_t)c->pages * c->page > 0x7FFFFFFFLL) return W4A16_ERR_SHAPE;
+  if ((int64_t)c->pages * c->page > 0x7FFFFFFFLL || (int64_t)c->pages * c->heads > 0x7FFFFFFFLL)
+    return W4A16_ERR_SHAPE;
   return W4A16_OK;
 }
 
@@ -319,16 +320,21 @@ w4a16_status_t check_attention(const w4a16_kv_cache_t* cache, int tokens, int re
   if (st != W4A16_OK) return st;
   if (tokens < 0 || requests < 0 || max_new < 0 || max_len < 0 || window < 0 || q_heads < 1) return W4A16_ERR_SHAPE;
   if (tokens > W4A16_KV_MAX_TOKENS || requests > W4A16_KV_MAX_REQUESTS || max_len > kKvMaxLen) return W4A16_ERR_SHAPE;
-  if (q_heads % cache->heads) return W4A16_ERR_SHAPE;
+  if (q_heads % cache->heads || (int64_t)tokens * q_heads > 0x7FFFFFFFLL) return W4A16_ERR_SHAPE;
   if (q_heads / cache->heads > W4A16_KV_MAX_GROUP) return W4A16_ERR_UNSUPPORTED;
   return W4A16_OK;
 }
 
-// The launch parameters of an attention call from its (checked) sizes.  Chunks
-// of 512 entries, doubled until max_len holds at most 128: short enough that
-// one request's chunks fill the chip, long enough that the partial results
-// (D + 2 floats a row and chunk) stay small beside the codes.  They depend on
-// max_len alone, so a row's sums do not depend on the batch.
+// The launch parameters of an attention call from its (checked) sizes.
+// Chunks of the cache (one workgroup each): they depend on max_len alone, so a
+// row's sums do not depend on the batch.  A workgroup needs 3 us to begin and
+// about 1 us for each step of 128 entries, and a row and chunk costs D + 5
+// floats written and read again: short chunks answer sooner, long ones stream
+// better.  Measured (us, chunks of 128 / 256 / 512 / 1024): one request of 717
+// entries 9.1 / 12.0 / 17.6 / 20.3; 96 with a window of 512 in up to 3101
+// 16.7 / 16.2 / 16.4 / 18.4; 48 of up to 6001 88.7 / 73.5 / 65.5 / 62.8; 16
+// verify batches of up to 9006 39.1 / 34.8 / 32.2 / 45.4; 3 of up to 120002
+// 178 / 145 / 126 / 117.
 KvAttnArgs attention_args(const w4a16_kv_cache_t* cache, int tokens, int requests, int max_new, int max_len,
                           int window, int q_heads) {
   KvAttnArgs a{};
@@ -340,21 +346,23 @@ KvAttnArgs attention_args(const w4a16_kv_cache_t* cache, int tokens, int request
   a.max_len = max_len;
   a.q_heads = q_heads;
   a.group = q_heads / cache->heads;
+  a.group_inverse = (65536u + a.group - 1) / a.group;
   a.split_tokens = max_new < kKvSplitRows / a.group ? max_new : kKvSplitRows / a.group;
   const int rows = a.split_tokens * a.group;
   a.row_groups = rows <= 16 ? 1 : (rows + 31) / 32;
-  a.chunk = 512;
-  while ((max_len + (long long)a.chunk - 1) / a.chunk > 128) a.chunk *= 2;
-  long long chunks = (max_len + (long long)a.chunk - 1) / a.chunk;
+  a.chunk_shift = max_len <= 1024 ? 7 : max_len <= 4096 ? 8 : max_len <= 16384 ? 9 : 10;
+  auto in_chunks = [&](long long n) { return (n + (1LL << a.chunk_shift) - 1) >> a.chunk_shift; };
+  while (in_chunks(max_len) > kKvMaxChunks - 1) ++a.chunk_shift;     // (a window may add one)
+  long long chunks = in_chunks(max_len);
   // a window's rows attend window + split_tokens - 1 entries at most
-  const long long in_window = ((long long)window + a.split_tokens - 1 + a.chunk - 2) / a.chunk + 1;
+  const long long in_window = in_chunks((long long)window + a.split_tokens - 2) + 1;
   if (window > 0 && in_window < chunks) chunks = in_window;
   a.chunks = chunks > 1 ? (int)chunks : 1;
   return a;
 }
 
 size_t attention_workspace(const KvAttnArgs& a, int dim) {
-  return a.chunks > 1 ? kv_partials(a) * (dim + 2) * sizeof(float) : 0;
+  return a.chunks > 1 ? kv_partials(a) * (dim + kKvPartStats) * sizeof(float) : 0;
 }
 
 }  // namespace
@@ -434,6 +442,7 @@ w4a16_status_t w4a16_kv_attention(const uint16_t* q, int64_t q_stride, const w4a
   if (width < 0 || width > W4A16_KV_MAX_WIDTH || q_stride < (int64_t)q_heads * cache->dim || q_stride % 8 || q_stride > (1LL << 40))
     return W4A16_ERR_SHAPE;
   if (tokens == 0 || requests == 0 || max_new == 0) return W4A16_OK;
+  if (cache->pages == 0) return W4A16_ERR_SHAPE;      // masked entries are read from page 0
   st = check_cache_pointers(cache);
   if (st != W4A16_OK) return st;
   if (!q || !out || !seq_lens || !token_start || (width > 0 && !block_table)) return W4A16_ERR_NULL;

@@ -13,13 +13,15 @@ hipError_t kv_attention_typed(const KvAttnArgs& a, void* workspace, hipStream_t 
   constexpr int D = W4K_D;
   float* part_o = static_cast<float*>(workspace);
   float* part_ml = part_o + kv_partials(a) * D;
-  const dim3 grid(a.requests, a.c.heads * a.row_groups, a.chunks);
   const int rows = a.split_tokens * a.group;
+  const unsigned ry = a.requests < kKvGridRequests ? a.requests : kKvGridRequests;
+  const unsigned rz = (a.requests + kKvGridRequests - 1) / kKvGridRequests;
   auto split = [&](auto nc) {
     constexpr int NC = decltype(nc)::value;
-    hipLaunchKernelGGL((kv_split_kernel<D, TYPE, NC>), grid, dim3(kKvSplitWaves * kWave), 0, st, a, part_o, part_ml);
+    hipLaunchKernelGGL((kv_split_kernel<D, TYPE, NC>), dim3(a.c.heads * a.row_groups * a.chunks, ry, rz),
+                       dim3(kKvSplitWaves * kWave), 0, st, a, part_o, part_ml);
     if (a.chunks > 1)
-      hipLaunchKernelGGL((kv_join_kernel<D, NC>), dim3(a.requests, a.c.heads, rows), dim3(kKvJoinThreads), 0, st, a,
+      hipLaunchKernelGGL((kv_join_kernel<D, NC>), dim3(a.c.heads * rows, ry, rz), dim3(kKvJoinThreads), 0, st, a,
                          part_o, part_ml);
   };
   if (rows <= 16)
@@ -27,7 +29,7 @@ hipError_t kv_attention_typed(const KvAttnArgs& a, void* workspace, hipStream_t 
   else
     split(std::integral_constant<int, 2>{});
   if ((int64_t)a.max_new * a.group > kKvSplitRows) {
-    const int64_t tiles = a.tokens / kv_tile_tokens(a.group) + a.requests;
+    const int64_t tiles = a.tokens / (kKvTileRows / a.group) + a.requests;
     hipLaunchKernelGGL((kv_tile_kernel<D, TYPE>), dim3((unsigned)tiles, a.c.heads), dim3(kKvTileWaves * kWave), 0, st,
                        a);
   }

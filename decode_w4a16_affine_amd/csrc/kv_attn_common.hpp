@@ -12,9 +12,18 @@ typedef _Float16 kv_f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 kv_f16x2 __attribute__((ext_vector_type(2)));
 typedef float kv_f32x4 __attribute__((ext_vector_type(4)));
 typedef float kv_f32x2 __attribute__((ext_vector_type(2)));
+// 16 codes; a plain vector: arrays of the HIP struct type end up in scratch memory
+typedef uint32_t kv_u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t kv_u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kKvTile = 64;           // cache entries a wave takes at once
 constexpr float kKvNone = -3e38f;     // running maximum before any entry
+
+// 16 codes from the cache, past the caches' reuse order: the cache streams
+// through once, and whole lines fetched this way reach 5.9 TB/s where ordinary
+// loads reach 5.4 (12 x 105k entries, 8 heads of 128, loads alone).
+__device__ __forceinline__ kv_u32x4 kv_load(const uint8_t* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const kv_u32x4*>(p));
+}
 
 // Four codes as two words of two bf16 (exact).
 template <int TYPE>
@@ -68,15 +77,14 @@ struct KvRows {
   int begin, end;         // cache entries any of the group's rows attends
 };
 
-// Rows [row0, row0 + rows) of request r (rows counted token by token, G a token).
-__device__ __forceinline__ KvRows kv_rows_of(const KvAttnArgs& a, int r, int row0, int rows) {
+// The rows of tokens i0 .. i1 of request r (the last one clipped to its tokens).
+__device__ __forceinline__ KvRows kv_rows_of(const KvAttnArgs& a, int r, int i0, int i1) {
   KvRows k;
   k.first = a.token_start[r];
   k.n = a.token_start[r + 1] - k.first;
   k.seq = a.seq_lens[r];
-  const int last = min(row0 + rows, min(k.n, a.max_new) * a.group) - 1;
   const long long held = (long long)a.width << a.c.page_shift;
-  const int lo = k.seq - k.n + row0 / a.group, hi = k.seq - k.n + last / a.group;
+  const int lo = k.seq - k.n + i0, hi = k.seq - k.n + min(i1, min(k.n, a.max_new) - 1);
   k.end = (int)min((long long)min(hi + 1, a.max_len), held);
   k.begin = a.window > 0 ? max(0, lo - a.window + 1) : 0;
   return k;
@@ -88,59 +96,70 @@ struct KvLaneRows {
   int hi[NC], lo[NC];
 };
 
-// One tile's softmax step for a lane: scores s of its 16 entries (first entry
-// j) and NC rows become fp16 weights; the running maximum m, sum l and the
-// factor `fade` for what was summed before are updated.  ks: key scale times
-// the logits' scale (>= 0), vs: value scale; whole: no entry of the tile is
-// masked for any row; page_ok: this lane's entries have a page.
-//
-// The maximum moves only when a row's logits exceed it by 2^3: weights then stay
-// below 2^8, far inside fp16, and most tiles leave the sums as they are (a
-// factor of exactly 1, also for the rows beside one that moves).
-constexpr float kKvSlack = 8.0f;
+// At the head of a block that few waves enter: without it the compiler runs the
+// block's selects for every tile instead of branching (a third of a tile's
+// vector instructions).
+__device__ __forceinline__ void kv_keep_branch() { asm volatile(""); }
 
-template <int NC>
-__device__ __forceinline__ void kv_softmax_step(kv_f32x4 (&s)[NC][4], const KvLaneRows<NC>& rows, int j, float ks,
-                                                float vs, bool whole, bool page_ok, float (&m)[NC], float (&l)[NC],
-                                                float (&fade)[NC], kv_f16x8 (&w)[NC][2]) {
-  const float lv = __builtin_amdgcn_logf(vs), rv = __builtin_amdgcn_rcpf(vs);
+// One tile's softmax step for a lane, in two parts: the scores s of its 4 NP
+// entries (first entry j) for NC rows become the tile's largest logit of each row
+// (kv_tile_max) and, once the running maximum is known, fp16 weights
+// (kv_weights).  ks: key scale times the logits' scale (>= 0); vs: value
+// scale; whole: no entry of the tile is masked for any row; page_ok: this
+// lane's entries have a page.
+template <int NC, int NP>
+__device__ __forceinline__ void kv_tile_max(kv_f32x4 (&s)[NC][NP], const KvLaneRows<NC>& rows, int j, float ks,
+                                            float lv, bool whole, bool page_ok, float (&tile_top)[NC]) {
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    // entry e of the 16 is attended by row c iff first <= e <= last
+    // entry e of the lane's 4 NP is attended by row c iff first <= e <= last
     const int first = rows.lo[c] - j, last = page_ok ? rows.hi[c] - j : -1;
     if (!whole) {
+      kv_keep_branch();
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
+      for (int e = 0; e < 4 * NP; ++e)
         s[c][e / 4][e % 4] = e >= first && e <= last ? s[c][e / 4][e % 4] : -__builtin_inff();
     }
-    float top = fmaxf(fmaxf(s[c][0][0], s[c][0][1]), s[c][0][2]);
-    top = fmaxf(fmaxf(top, s[c][0][3]), s[c][1][0]);
-    top = fmaxf(fmaxf(top, s[c][1][1]), s[c][1][2]);
-    top = fmaxf(fmaxf(top, s[c][1][3]), s[c][2][0]);
-    top = fmaxf(fmaxf(top, s[c][2][1]), s[c][2][2]);
-    top = fmaxf(fmaxf(top, s[c][2][3]), s[c][3][0]);
-    top = fmaxf(fmaxf(top, s[c][3][1]), fmaxf(s[c][3][2], s[c][3][3]));
+    float top = s[c][0][0];
+#pragma unroll
+    for (int e = 1; e + 1 < 4 * NP; e += 2)      // maxima of three
+      top = fmaxf(fmaxf(top, s[c][e / 4][e % 4]), s[c][(e + 1) / 4][(e + 1) % 4]);
+    top = fmaxf(top, s[c][NP - 1][3]);
     top = top > kKvNone ? __builtin_fmaf(top, ks, lv) : kKvNone;
     top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const float m_new = top > m[c] + kKvSlack ? top : m[c];
-    fade[c] = __builtin_amdgcn_exp2f(m[c] - m_new);
-    m[c] = m_new;
-    const float shift = lv - m_new;
-    float p[16], sum = 0.0f;
+    tile_top[c] = fmaxf(top, __shfl_xor(top, 32));
+  }
+}
+
+// The running maximum moves only when a row's logits exceed it by 8: weights
+// then stay at or below 2^8, far inside fp16, and most tiles leave the sums as
+// they are (a factor of exactly 1, also for the rows beside one that moves).
+__device__ __forceinline__ float kv_new_max(float m, float top) { return top > m + 8.0f ? top : m; }
+
+// Weights under the maxima m (already the new ones); l *= fade, += the tile's sum.
+template <int NC, int NP>
+__device__ __forceinline__ void kv_weights(kv_f32x4 (&s)[NC][NP], const KvLaneRows<NC>& rows, int j, float ks, float lv,
+                                           float rv, bool whole, bool page_ok, const float (&m)[NC],
+                                           const float (&fade)[NC], float (&l)[NC], kv_f16x8 (&w)[NC][NP / 2]) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][e / 4][e % 4], ks, shift));
+  for (int c = 0; c < NC; ++c) {
+    const int first = rows.lo[c] - j, last = page_ok ? rows.hi[c] - j : -1;
+    const float shift = lv - m[c];
+    float p[4 * NP], sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4 * NP; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][e / 4][e % 4], ks, shift));
     // masked entries are exactly 0 also where the page's scales are 0 or NaN
     if (!whole) {
+      kv_keep_branch();
 #pragma unroll
-      for (int e = 0; e < 16; ++e) p[e] = e >= first && e <= last ? p[e] : 0.0f;
+      for (int e = 0; e < 4 * NP; ++e) p[e] = e >= first && e <= last ? p[e] : 0.0f;
     }
 #pragma unroll
-    for (int e = 0; e < 16; ++e) sum += p[e];
-    const bool any = whole || (first <= 15 && last >= 0 && first <= last);
+    for (int e = 0; e < 4 * NP; ++e) sum += p[e];
+    const bool any = whole || (first < 4 * NP && last >= 0 && first <= last);
     l[c] = l[c] * fade[c] + (any ? sum * rv : 0.0f);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < NP / 2; ++h) {
       uint32_t pk[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -154,15 +173,12 @@ __device__ __forceinline__ void kv_softmax_step(kv_f32x4 (&s)[NC][4], const KvLa
 
 // E4M3 codes of entries that hold nothing may be NaN, and 0 * NaN must not
 // enter the sums: the bytes of 16 value codes that stand for existing entries.
-__device__ __forceinline__ uint4 kv_existing_bytes(int left) {
+__device__ __forceinline__ kv_u32x4 kv_existing_bytes(int left) {
   auto bytes = [&](int b) {
     const int k = left - 4 * b;
     return k >= 4 ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
   };
-  return make_uint4(bytes(0), bytes(1), bytes(2), bytes(3));
-}
-__device__ __forceinline__ uint4 kv_and(uint4 a, uint4 b) {
-  return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w);
+  return kv_u32x4{bytes(0), bytes(1), bytes(2), bytes(3)};
 }
 
 // 16 queries' elements with the sign of the logits' scale (so that ks >= 0)
@@ -172,11 +188,13 @@ __device__ __forceinline__ kv_bf16x8 kv_query8(const uint16_t* p, uint32_t sign)
   return __builtin_bit_cast(kv_bf16x8, u);
 }
 
-__device__ __forceinline__ void kv_store4(uint16_t* out, kv_f32x4 v, float l) {
-  uint32_t b[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) b[i] = f32_to_bf16(l != 0.0f ? v[i] / l : 0.0f);
-  *reinterpret_cast<uint2*>(out) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+// What the sums are multiplied with at the end: 1 / l, and 0 for a row that
+// attends nothing (one more fp32 rounding than a division, far below bf16's).
+__device__ __forceinline__ float kv_inverse(float l) { return l != 0.0f ? 1.0f / l : 0.0f; }
+
+__device__ __forceinline__ void kv_store4(uint16_t* out, kv_f32x4 v, float inverse) {
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  *reinterpret_cast<bf16x4*>(out) = __builtin_convertvector(v * inverse, bf16x4);
 }
 
 }  // namespace w4k

@@ -17,12 +17,10 @@
 
 namespace w4k {
 
+constexpr int kKvTile = 64;           // cache entries at once
 constexpr int kKvTileWaves = 4;
 constexpr int kKvTileCols = 2;                                     // 16-row pieces a wave
 constexpr int kKvTileRows = kKvTileWaves * kKvTileCols * 16;
-
-// Tokens of a workgroup's rows.
-__host__ __device__ __forceinline__ int kv_tile_tokens(int group) { return kKvTileRows / group; }
 
 // Workgroup u -> request and first token.  Request r owns the numbers from
 // floor(token_start[r] / TT) + r on: at least ceil(n / TT) of them, and they
@@ -49,11 +47,11 @@ __global__ __launch_bounds__(kKvTileWaves * kWave) void kv_tile_kernel(KvAttnArg
   constexpr int KC = D / 64;          // 16-byte pieces of a key a lane holds
   constexpr int DT = D / 16;          // 16-row pieces of the output
   constexpr int VW = DT / kKvTileWaves;   // of which a wave loads
-  __shared__ uint4 s_k[2][4 * 2 * KC * kWave];      // [piece t][sum step][lane]
-  __shared__ uint4 s_v[2][DT * 2 * kWave];          // [piece d][sum step][lane]
+  __shared__ kv_u32x4 s_k[2][4 * 2 * KC * kWave];      // [piece t][sum step][lane]
+  __shared__ kv_u32x4 s_v[2][DT * 2 * kWave];          // [piece d][sum step][lane]
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int x = lane & 15, g = lane >> 4;
-  const int tt = kv_tile_tokens(a.group);
+  const int tt = kv_token_of(a, kKvTileRows);
   const int u = gridDim.x - 1 - blockIdx.x;        // later tokens attend more: they go first
   const int kh = blockIdx.y;
   const int r = __builtin_amdgcn_readfirstlane(kv_tile_owner(a.token_start, a.requests, tt, u));
@@ -62,22 +60,27 @@ __global__ __launch_bounds__(kKvTileWaves * kWave) void kv_tile_kernel(KvAttnArg
   const int n = a.token_start[r + 1] - a.token_start[r];
   const int live_tokens = min(min(n, a.max_new), a.tokens - a.token_start[r]);
   if ((long long)n * a.group <= kKvSplitRows || i0 < 0 || i0 >= live_tokens || a.token_start[r] < 0) return;
-  const int row0 = i0 * a.group, live = min(i0 + tt, live_tokens) * a.group;
-  const KvRows rows = kv_rows_of(a, r, row0, live - row0);
+  const int here = min(tt, live_tokens - i0);       // the workgroup's tokens
+  const int live = here * a.group;                  // and rows
+  const KvRows rows = kv_rows_of(a, r, i0, i0 + here - 1);
   const int shift = a.c.page_shift, P = 1 << shift;
 
   // this wave's rows
-  const int wrow = row0 + wave * NC * 16;
+  const int wrow = wave * NC * 16;
   kv_bf16x8 q[NC][2 * KC];
   KvLaneRows<NC> lr;
+  int64_t out_at[NC];
+  const int pos0 = rows.seq - rows.n + i0;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int row = min(wrow + 16 * c + x, live - 1);
-    const int i = row / a.group, h = kh * a.group + row % a.group;
+    const int i = kv_token_of(a, row), h = kh * a.group + row - i * a.group;
+    const int64_t t = rows.first + i0 + i;
     const bool ok = wrow + 16 * c + x < live;
-    lr.hi[c] = ok ? min(rows.seq - rows.n + i, rows.end - 1) : -1;
-    lr.lo[c] = a.window > 0 ? rows.seq - rows.n + i - a.window + 1 : 0;
-    const uint16_t* qp = a.q + (size_t)(rows.first + i) * a.q_stride + (size_t)h * D + 16 * g;
+    lr.hi[c] = ok ? min(pos0 + i, rows.end - 1) : -1;
+    lr.lo[c] = a.window > 0 ? pos0 + i - a.window + 1 : 0;
+    out_at[c] = ok ? (t * a.q_heads + h) * D : -1;
+    const uint16_t* qp = a.q + t * a.q_stride + (size_t)h * D + 16 * g;
 #pragma unroll
     for (int k = 0; k < KC; ++k) {
       q[c][2 * k] = kv_query8(qp + 64 * k, a.q_sign);
@@ -85,8 +88,8 @@ __global__ __launch_bounds__(kKvTileWaves * kWave) void kv_tile_kernel(KvAttnArg
     }
   }
   // entries that some row of the wave attends, and those that every row does
-  const int first_pos = rows.seq - rows.n + min(wrow, live - 1) / a.group;
-  const int last_pos = rows.seq - rows.n + (min(wrow + NC * 16, live) - 1) / a.group;
+  const int first_pos = pos0 + kv_token_of(a, min(wrow, live - 1));
+  const int last_pos = pos0 + kv_token_of(a, min(wrow + NC * 16, live) - 1);
   const int any_hi = wrow < live ? min(last_pos, rows.end - 1) : -1;
   const int any_lo = a.window > 0 ? first_pos - a.window + 1 : 0;
   const int all_hi = min(first_pos, rows.end - 1);
@@ -104,7 +107,7 @@ __global__ __launch_bounds__(kKvTileWaves * kWave) void kv_tile_kernel(KvAttnArg
 
   // the codes, scales and page of a tile that this thread loads
   const int32_t* table = a.table + (size_t)r * a.width;
-  uint4 kc[KC], vc[VW];
+  kv_u32x4 kc[KC], vc[VW];
   float ks, vs;
   bool page_ok;
   auto load = [&](int j0) {
@@ -118,32 +121,32 @@ __global__ __launch_bounds__(kKvTileWaves * kWave) void kv_tile_kernel(KvAttnArg
     const uint8_t* ka = a.c.k + (kph * P + ((j0 + 16 * (x >> 2)) & (P - 1)) + 4 * wave + (x & 3)) * D + 16 * g;
     const uint8_t* va = a.c.v + (vph * D + 16 * VW * wave + x) * P + ((j0 + 16 * g) & (P - 1));
 #pragma unroll
-    for (int k = 0; k < KC; ++k) kc[k] = *reinterpret_cast<const uint4*>(ka + 64 * k);
+    for (int k = 0; k < KC; ++k) kc[k] = *reinterpret_cast<const kv_u32x4*>(ka + 64 * k);
 #pragma unroll
-    for (int d = 0; d < VW; ++d) vc[d] = *reinterpret_cast<const uint4*>(va + (size_t)d * 16 * P);
+    for (int d = 0; d < VW; ++d) vc[d] = *reinterpret_cast<const kv_u32x4*>(va + (size_t)d * 16 * P);
     ks = bf16_lo(a.c.ks[vph]) * a.scale_log2;
     vs = bf16_lo(a.c.vs[vph]);
     vs = vs < kKvMinScale ? kKvMinScale : vs;     // 0 in a page that was never begun; NaN stays
     page_ok = vp >= 0;
     if (TYPE == W4A16_KV_FP8 && (j0 + kKvTile > rows.end || !__all(page_ok))) {
-      const uint4 mask = kv_existing_bytes(page_ok ? rows.end - (j0 + 16 * g) : 0);
+      const kv_u32x4 mask = kv_existing_bytes(page_ok ? rows.end - (j0 + 16 * g) : 0);
 #pragma unroll
-      for (int d = 0; d < VW; ++d) vc[d] = kv_and(vc[d], mask);
+      for (int d = 0; d < VW; ++d) vc[d] = vc[d] & mask;
     }
   };
   auto store = [&](int b) {
 #pragma unroll
     for (int k = 0; k < KC; ++k) {
       s_k[b][((wave * KC + k) * 2) * kWave + lane] =
-          __builtin_bit_cast(uint4, kv_bf16_of8<TYPE>(kc[k].x, kc[k].y));
+          __builtin_bit_cast(kv_u32x4, kv_bf16_of8<TYPE>(kc[k].x, kc[k].y));
       s_k[b][((wave * KC + k) * 2 + 1) * kWave + lane] =
-          __builtin_bit_cast(uint4, kv_bf16_of8<TYPE>(kc[k].z, kc[k].w));
+          __builtin_bit_cast(kv_u32x4, kv_bf16_of8<TYPE>(kc[k].z, kc[k].w));
     }
 #pragma unroll
     for (int d = 0; d < VW; ++d) {
-      s_v[b][((wave * VW + d) * 2) * kWave + lane] = __builtin_bit_cast(uint4, kv_f16_of8<TYPE>(vc[d].x, vc[d].y));
+      s_v[b][((wave * VW + d) * 2) * kWave + lane] = __builtin_bit_cast(kv_u32x4, kv_f16_of8<TYPE>(vc[d].x, vc[d].y));
       s_v[b][((wave * VW + d) * 2 + 1) * kWave + lane] =
-          __builtin_bit_cast(uint4, kv_f16_of8<TYPE>(vc[d].z, vc[d].w));
+          __builtin_bit_cast(kv_u32x4, kv_f16_of8<TYPE>(vc[d].z, vc[d].w));
     }
   };
 
@@ -172,9 +175,17 @@ __global__ __launch_bounds__(kKvTileWaves * kWave) void kv_tile_kernel(KvAttnArg
           for (int c = 0; c < NC; ++c) s[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, q[c][k], s[c][t], 0, 0, 0);
         }
       }
-      float fade[NC];
+      float fade[NC], top[NC];
       kv_f16x8 w[NC][2];
-      kv_softmax_step<NC>(s, lr, j0 + 16 * g, ks_now, vs_now, whole, ok_now, m, l, fade, w);
+      const float lv = __builtin_amdgcn_logf(vs_now), rv = __builtin_amdgcn_rcpf(vs_now);
+      kv_tile_max<NC, 4>(s, lr, j0 + 16 * g, ks_now, lv, whole, ok_now, top);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const float m_new = kv_new_max(m[c], top[c]);
+        fade[c] = __builtin_amdgcn_exp2f(m[c] - m_new);
+        m[c] = m_new;
+      }
+      kv_weights<NC, 4>(s, lr, j0 + 16 * g, ks_now, lv, rv, whole, ok_now, m, fade, l, w);
 #pragma unroll
       for (int c = 0; c < NC; ++c)
         if (__any(fade[c] != 1.0f))
@@ -197,11 +208,10 @@ __global__ __launch_bounds__(kKvTileWaves * kWave) void kv_tile_kernel(KvAttnArg
   for (int c = 0; c < NC; ++c) {
     l[c] += __shfl_xor(l[c], 16);
     l[c] += __shfl_xor(l[c], 32);
-    const int row = wrow + 16 * c + x;
-    if (row >= live) continue;
-    uint16_t* out = a.out + ((size_t)(rows.first + row / a.group) * a.q_heads + kh * a.group + row % a.group) * D;
+    if (out_at[c] < 0) continue;
+    const float inverse = kv_inverse(l[c]);
 #pragma unroll
-    for (int d = 0; d < DT; ++d) kv_store4(out + 16 * d + 4 * g, o[c][d], l[c]);
+    for (int d = 0; d < DT; ++d) kv_store4(a.out + out_at[c] + 16 * d + 4 * g, o[c][d], inverse);
   }
 }
 

@@ -74,9 +74,10 @@ struct KvAttnArgs {
   float scale_log2;      // |scale| * log2(e): softmax in base 2
   uint32_t q_sign;       // sign bits of two bf16 if scale < 0, else 0
   int width, window, tokens, requests, max_new, max_len, q_heads, group;
-  // requests of few rows: entries a chunk, chunks a row at most, row groups a
-  // cache head, new tokens a request at most
-  int chunk, chunks, row_groups, split_tokens;
+  uint32_t group_inverse;      // ceil(2^16 / group): see kv_token_of
+  // requests of few rows: log2 of the entries a chunk, chunks a row at most, row
+  // groups a cache head, new tokens a request at most
+  int chunk_shift, chunks, row_groups, split_tokens;
 };
 
 // Launchers (kv_attention.hip, once per head size).
@@ -87,9 +88,18 @@ W4K_DECLARE_KV(128)
 W4K_DECLARE_KV(256)
 #undef W4K_DECLARE_KV
 
+// Row / group for 0 <= row < 1024 (group <= 64): the product exceeds the
+// quotient by less than row / 2^16 < 1 / group.
+__device__ __forceinline__ int kv_token_of(const KvAttnArgs& a, int row) {
+  return (int)((uint32_t)row * a.group_inverse >> 16);
+}
+
+constexpr int kKvMaxChunks = 128;     // chunks of a row at most
 constexpr int kKvSplitRows = 64;      // requests of at most this many rows a cache head take the split form
 
-// Floats of one row and chunk's partial result: the output, maximum and sum.
+// A row and chunk's partial result: D floats of output, then these (the
+// maximum and four waves' sums).
+constexpr int kKvPartStats = 5;
 inline size_t kv_partials(const KvAttnArgs& a) {
   return (size_t)a.requests * a.c.heads * a.split_tokens * a.group * a.chunks;
 }

@@ -32,8 +32,8 @@
  * lengths, tables and slots on the device, so they can be captured in a graph
  * and replayed as these change.
  * Limits: D 64, 128 or 256; P 16, 32, 64, 128 or 256; HQ / H <= 64;
- * pages * P < 2^31; H <= 1024; R and T <= 2^20; block tables of at most 2^22
- * columns; max_len <= 2^29.  Sizes 0 succeed without work.
+ * pages * P, pages * H and T * HQ < 2^31; H <= 1024; R and T <= 2^20; block
+ * tables of at most 2^22 columns; max_len <= 2^29.  Sizes 0 succeed without work.
  * Alignment: q, k, v, out and the codes 16 bytes, strides multiples of 8
  * elements; scales 2; int32 arrays 4; workspace 16; fp32 outputs 16 bytes.
  */
@@ -123,7 +123,7 @@ size_t w4a16_kv_attention_workspace_bytes(int tokens, int requests, int max_new,
  * the cache entries 0 <= j <= pos and, with window > 0, j > pos - window.
  * Entry j lies in page block_table[r][j / P]; entries whose page is outside
  * the cache, or past the table's `width` columns, are not attended.  A row
- * without entries is 0.  Rows of q and out outside every request are not
+ * without entries is 0.  (The cache needs at least one page.)  Rows of q and out outside every request are not
  * touched.
  *   q    bf16 [T][HQ][D], token rows q_stride elements apart
  *   out  bf16 [T][HQ][D], dense

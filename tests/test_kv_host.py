@@ -107,6 +107,9 @@ def test_attention_refuses_bad_arguments(L):
                 dict(width=2 ** 22 + 1), dict(qs=1023), dict(qs=1016), dict(qs=1028), dict(qs=2 ** 41)):
         assert att(**bad) == ESHAPE, bad
     assert att(HQ=130, qs=130 * 128) == EUNSUP          # 65 query heads a cache head
+    assert att(pages=0) == ESHAPE
+    assert att(T=2 ** 20, HQ=2048, heads=1024, qs=2048 * 128) == ESHAPE        # T * HQ = 2^31
+    assert att(pages=2 ** 21, page=16, heads=1024) == ESHAPE                  # pages * heads = 2^31
     for name in ("q", "table", "seq", "start", "out"):
         assert att(**{name: None}) == ENULL, name
     assert att(q=A4) == EALIGN and att(out=A16 + 8) == EALIGN and att(table=A16 + 2) == EALIGN
