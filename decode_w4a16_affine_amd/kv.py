@@ -18,7 +18,7 @@ import math
 
 import torch
 
-from . import _check, _dtype, _on_device, _ptr, _shape, _stream
+from . import _check, _dtype, _shape
 from . import lib as _base_lib
 
 KV_INT8 = 0               # W4A16_KV_INT8
@@ -70,8 +70,36 @@ def kv_lib() -> ctypes.CDLL:
     return _lib
 
 
+# The checks below run on every call of a decode step, so each is one cheap
+# test a tensor (get_device() is -1 for host tensors; pointers go to ctypes as
+# plain numbers).
+
+def _same_gpu(first, *ts) -> int:
+    """The GPU that all tensors are on."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on the GPU")
+    for t in ts:
+        if t.get_device() != dev:
+            raise ValueError("tensors must be on the GPU" if t.get_device() < 0 else
+                             f"tensors must be on one device ({first.device} and {t.device})")
+    return dev
+
+
+def _dense(*ts) -> None:
+    for t in ts:
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+
+
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _cache(k_cache, v_cache, k_scales, v_scales) -> KVCache:
-    """The checked C struct of a cache's tensors."""
+    """The C struct of a cache's tensors, their types and shapes checked."""
     kind = _TYPES.get(k_cache.dtype)
     if kind is None:
         raise TypeError(f"k_cache must be torch.int8 or torch.float8_e4m3fn, got {k_cache.dtype}")
@@ -81,30 +109,49 @@ def _cache(k_cache, v_cache, k_scales, v_scales) -> KVCache:
     _dtype(k_scales, torch.bfloat16, "k_scales")
     _dtype(v_scales, torch.bfloat16, "v_scales")
     pages, heads, page, dim = k_cache.shape
-    _shape(v_cache, (pages, heads, dim, page), "v_cache")
-    _shape(k_scales, (pages, heads), "k_scales")
-    _shape(v_scales, (pages, heads), "v_scales")
+    if v_cache.shape != (pages, heads, dim, page):
+        _shape(v_cache, (pages, heads, dim, page), "v_cache")
+    if k_scales.shape != (pages, heads):
+        _shape(k_scales, (pages, heads), "k_scales")
+    if v_scales.shape != (pages, heads):
+        _shape(v_scales, (pages, heads), "v_scales")
     return KVCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), kind, pages,
                    heads, page, dim)
 
 
-def _vector(t, name):
-    _dtype(t, torch.int32, name)
-    if t.dim() != 1:
+def _vector(t, name, n=None):
+    """The length of an int32 vector (checked against n where given)."""
+    if t.dtype != torch.int32:
+        _dtype(t, torch.int32, name)
+    if n is not None:
+        if t.shape != (n,):
+            _shape(t, (n,), name)
+    elif t.dim() != 1:
         raise ValueError(f"{name} must be 1-D, got {list(t.shape)}")
     return t.shape[0]
 
 
+def _table(t, R):
+    """The width of a block table [R, width]."""
+    if t.dtype != torch.int32:
+        _dtype(t, torch.int32, "block_table")
+    if t.dim() != 2 or t.shape[0] != R:
+        raise ValueError(f"block_table must have shape [{R}, width], got {list(t.shape)}")
+    return t.shape[1]
+
+
 def _rows(t, heads, dim, name):
     """Token count and token stride of a [T, heads, D] tensor whose token rows are dense."""
-    _dtype(t, torch.bfloat16, name)
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != dim:
-        raise ValueError(f"{name} must have shape [T, {'heads' if heads is None else heads}, {dim}], got {list(t.shape)}")
-    tokens, stride, head_stride, unit = t.shape[0], *t.stride()
-    row = t.shape[1] * dim
+    if t.dtype != torch.bfloat16:
+        _dtype(t, torch.bfloat16, name)
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != dim:
+        raise ValueError(f"{name} must have shape [T, {'heads' if heads is None else heads}, {dim}], got {list(shape)}")
+    tokens, row = shape[0], shape[1] * dim
+    stride, head_stride, unit = t.stride()
     if tokens <= 1:
-        stride = -(-max(stride, row) // 8) * 8      # no second row: any valid stride
-    if (unit != 1 and dim > 1) or (head_stride != dim and t.shape[1] > 1) or stride < row:
+        stride = row                    # no second row: any valid stride
+    if unit != 1 or (head_stride != dim and shape[1] > 1) or stride < row:
         raise ValueError(f"{name} must be dense within a token (strides [>= {row}, {dim}, 1]), got {list(t.stride())}")
     return tokens, stride
 
@@ -115,23 +162,19 @@ def w4a16_kv_plan(ctx_lens, new_lens, free_pages, block_table, seq_lens, token_s
                   stream=None) -> None:
     """Block tables and slot maps of a step from request lengths (block_table [R, width] is updated in place)."""
     R = _vector(ctx_lens, "ctx_lens")
-    _dtype(new_lens, torch.int32, "new_lens")
-    _shape(new_lens, (R,), "new_lens")
+    _vector(new_lens, "new_lens", R)
     num_free = _vector(free_pages, "free_pages")
-    _dtype(block_table, torch.int32, "block_table")
-    if block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError(f"block_table must have shape [{R}, width], got {list(block_table.shape)}")
-    _dtype(seq_lens, torch.int32, "seq_lens")
-    _shape(seq_lens, (R,), "seq_lens")
-    _dtype(token_start, torch.int32, "token_start")
-    _shape(token_start, (R + 1,), "token_start")
+    width = _table(block_table, R)
+    _vector(seq_lens, "seq_lens", R)
+    _vector(token_start, "token_start", R + 1)
     tokens = _vector(slot_map, "slot_map")
-    _dtype(pages_used, torch.int32, "pages_used")
-    _shape(pages_used, (1,), "pages_used")
-    _on_device(ctx_lens, new_lens, free_pages, block_table, seq_lens, token_start, slot_map, pages_used)
-    _check(kv_lib().w4a16_kv_plan(_ptr(ctx_lens), _ptr(new_lens), _ptr(free_pages), num_free, _ptr(block_table),
-                                  block_table.shape[1], _ptr(seq_lens), _ptr(token_start), _ptr(slot_map),
-                                  _ptr(pages_used), R, tokens, page, _stream(stream)), "w4a16_kv_plan")
+    _vector(pages_used, "pages_used", 1)
+    dev = _same_gpu(ctx_lens, new_lens, free_pages, block_table, seq_lens, token_start, slot_map, pages_used)
+    _dense(ctx_lens, new_lens, free_pages, block_table, seq_lens, token_start, slot_map, pages_used)
+    _check(kv_lib().w4a16_kv_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), num_free,
+                                  block_table.data_ptr(), width, seq_lens.data_ptr(), token_start.data_ptr(),
+                                  slot_map.data_ptr(), pages_used.data_ptr(), R, tokens, page,
+                                  _raw_stream(stream, dev)), "w4a16_kv_plan")
 
 
 def w4a16_kv_append(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, stream=None) -> None:
@@ -139,14 +182,13 @@ def w4a16_kv_append(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, stream
     c = _cache(k_cache, v_cache, k_scales, v_scales)
     tokens, k_stride = _rows(k, c.heads, c.dim, "k")
     v_tokens, v_stride = _rows(v, c.heads, c.dim, "v")
-    _dtype(slot_map, torch.int32, "slot_map")
-    _shape(slot_map, (tokens,), "slot_map")
+    _vector(slot_map, "slot_map", tokens)
     if v_tokens != tokens:
         raise ValueError(f"k and v must have the same tokens, got {tokens} and {v_tokens}")
-    _on_device(k_cache, v_cache, k_scales, v_scales, slot_map)
-    _on_device(k_cache, k, v, contiguous=False)
-    _check(kv_lib().w4a16_kv_append(_ptr(k), k_stride, _ptr(v), v_stride, _ptr(slot_map), ctypes.byref(c), tokens,
-                                    _stream(stream)), "w4a16_kv_append")
+    dev = _same_gpu(k_cache, v_cache, k_scales, v_scales, slot_map, k, v)
+    _dense(k_cache, v_cache, k_scales, v_scales, slot_map)
+    _check(kv_lib().w4a16_kv_append(k.data_ptr(), k_stride, v.data_ptr(), v_stride, slot_map.data_ptr(),
+                                    ctypes.byref(c), tokens, _raw_stream(stream, dev)), "w4a16_kv_append")
 
 
 def w4a16_kv_attention_workspace_bytes(tokens: int, requests: int, max_new: int, max_len: int, window: int,
@@ -165,29 +207,35 @@ def w4a16_kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq
     the block table's columns hold); scale None: 1 / sqrt(D); window 0: no
     window; workspace: a uint8 device tensor of at least
     w4a16_kv_attention_workspace_bytes bytes, or None where that is 0."""
-    c = _cache(k_cache, v_cache, k_scales, v_scales)
+    _attention(_cache(k_cache, v_cache, k_scales, v_scales), (k_cache, v_cache, k_scales, v_scales), q, block_table,
+               seq_lens, token_start, out, workspace, max_new, max_len, scale, window, stream)
+
+
+def _attention(c, cache, q, block_table, seq_lens, token_start, out, workspace, max_new, max_len, scale, window, stream):
     tokens, q_stride = _rows(q, None, c.dim, "q")
     R = _vector(seq_lens, "seq_lens")
-    _dtype(token_start, torch.int32, "token_start")
-    _shape(token_start, (R + 1,), "token_start")
-    _dtype(block_table, torch.int32, "block_table")
-    if block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError(f"block_table must have shape [{R}, width], got {list(block_table.shape)}")
-    _dtype(out, torch.bfloat16, "out")
-    _shape(out, q.shape, "out")
-    if workspace is not None:
-        _dtype(workspace, torch.uint8, "workspace")
+    _vector(token_start, "token_start", R + 1)
+    width = _table(block_table, R)
+    if out.dtype != torch.bfloat16:
+        _dtype(out, torch.bfloat16, "out")
+    if out.shape != q.shape:
+        _shape(out, q.shape, "out")
     if max_len is None:
-        max_len = block_table.shape[1] * c.page
+        max_len = width * c.page
     if scale is None:
         scale = 1.0 / math.sqrt(c.dim)
-    _on_device(k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, out, workspace)
-    _on_device(k_cache, q, contiguous=False)
-    _check(kv_lib().w4a16_kv_attention(_ptr(q), q_stride, ctypes.byref(c), _ptr(block_table), block_table.shape[1],
-                                       _ptr(seq_lens), _ptr(token_start), _ptr(out), scale, window, tokens, R, max_new,
-                                       max_len, q.shape[1], _ptr(workspace),
-                                       0 if workspace is None else workspace.numel(), _stream(stream)),
-           "w4a16_kv_attention")
+    ws = bytes_ = 0
+    if workspace is not None:
+        _dtype(workspace, torch.uint8, "workspace")
+        _same_gpu(out, workspace)
+        _dense(workspace)
+        ws, bytes_ = workspace.data_ptr(), workspace.numel()
+    dev = _same_gpu(*cache, block_table, seq_lens, token_start, out, q)
+    _dense(*cache, block_table, seq_lens, token_start, out)
+    _check(kv_lib().w4a16_kv_attention(q.data_ptr(), q_stride, ctypes.byref(c), block_table.data_ptr(), width,
+                                       seq_lens.data_ptr(), token_start.data_ptr(), out.data_ptr(), scale, window,
+                                       tokens, R, max_new, max_len, q.shape[1], ws, bytes_,
+                                       _raw_stream(stream, dev)), "w4a16_kv_attention")
 
 
 def w4a16_kv_dequant(k_cache, v_cache, k_scales, v_scales, pages, k_out, v_out, stream=None) -> None:
@@ -198,9 +246,10 @@ def w4a16_kv_dequant(k_cache, v_cache, k_scales, v_scales, pages, k_out, v_out, 
     _dtype(v_out, torch.float32, "v_out")
     _shape(k_out, (n, c.heads, c.page, c.dim), "k_out")
     _shape(v_out, (n, c.heads, c.page, c.dim), "v_out")
-    _on_device(k_cache, v_cache, k_scales, v_scales, pages, k_out, v_out)
-    _check(kv_lib().w4a16_kv_dequant(ctypes.byref(c), _ptr(pages), n, _ptr(k_out), _ptr(v_out), _stream(stream)),
-           "w4a16_kv_dequant")
+    dev = _same_gpu(k_cache, v_cache, k_scales, v_scales, pages, k_out, v_out)
+    _dense(k_cache, v_cache, k_scales, v_scales, pages, k_out, v_out)
+    _check(kv_lib().w4a16_kv_dequant(ctypes.byref(c), pages.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(),
+                                     _raw_stream(stream, dev)), "w4a16_kv_dequant")
 
 
 # ---- allocating conveniences (torch allocates; the library computes) ------------
@@ -216,8 +265,8 @@ def kv_cache(pages: int, heads: int, dim: int, page: int = 64, dtype=torch.int8,
 def kv_plan(ctx_lens, new_lens, free_pages, block_table, tokens: int, page: int, stream=None):
     """(seq_lens, token_start, slot_map [tokens], pages_used); block_table is updated in place."""
     R = ctx_lens.shape[0]
-    seq_lens, token_start, slot_map, pages_used = (
-        torch.empty((n,), dtype=torch.int32, device=ctx_lens.device) for n in (R, R + 1, tokens, 1))
+    seq_lens, token_start, slot_map, pages_used = torch.empty(
+        (2 * R + tokens + 2,), dtype=torch.int32, device=ctx_lens.device).split((R, R + 1, tokens, 1))
     w4a16_kv_plan(ctx_lens, new_lens, free_pages, block_table, seq_lens, token_start, slot_map, pages_used, page,
                   stream=stream)
     return seq_lens, token_start, slot_map, pages_used
@@ -225,14 +274,15 @@ def kv_plan(ctx_lens, new_lens, free_pages, block_table, tokens: int, page: int,
 
 def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, max_new: int,
                  max_len: int = None, scale: float = None, window: int = 0, stream=None):
-    out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    c = _cache(k_cache, v_cache, k_scales, v_scales)
+    out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if max_len is None:
-        max_len = block_table.shape[1] * k_cache.shape[2]
-    need = w4a16_kv_attention_workspace_bytes(q.shape[0], seq_lens.shape[0], max_new, max_len, window, q.shape[1],
-                                              k_cache, v_cache, k_scales, v_scales)
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    w4a16_kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, out, ws, max_new,
-                       max_len=max_len, scale=scale, window=window, stream=stream)
+        max_len = block_table.shape[1] * c.page
+    need = kv_lib().w4a16_kv_attention_workspace_bytes(q.shape[0], seq_lens.shape[0], max_new, max_len, window,
+                                                       q.shape[1], ctypes.byref(c))
+    ws = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
+    _attention(c, (k_cache, v_cache, k_scales, v_scales), q, block_table, seq_lens, token_start, out, ws, max_new,
+               max_len, scale, window, stream)
     return out
 
 
