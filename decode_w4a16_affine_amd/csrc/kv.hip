@@ -322,6 +322,9 @@ w4a16_status_t check_attention(const w4a16_kv_cache_t* cache, int tokens, int re
   if (tokens > W4A16_KV_MAX_TOKENS || requests > W4A16_KV_MAX_REQUESTS || max_len > kKvMaxLen) return W4A16_ERR_SHAPE;
   if (q_heads % cache->heads || (int64_t)tokens * q_heads > 0x7FFFFFFFLL) return W4A16_ERR_SHAPE;
   if (q_heads / cache->heads > W4A16_KV_MAX_GROUP) return W4A16_ERR_UNSUPPORTED;
+  // the tiles' grid (at least 64 rows each) within the launch limit of 2^32 threads
+  const int64_t tiles = tokens / (64 / (q_heads / cache->heads)) + requests;
+  if (tiles * cache->heads > (1 << 22)) return W4A16_ERR_SHAPE;
   return W4A16_OK;
 }
 
@@ -348,6 +351,9 @@ KvAttnArgs attention_args(const w4a16_kv_cache_t* cache, int tokens, int request
   a.group = q_heads / cache->heads;
   a.group_inverse = (65536u + a.group - 1) / a.group;
   a.split_tokens = max_new < kKvSplitRows / a.group ? max_new : kKvSplitRows / a.group;
+  // A call of one request of many new tokens is a prompt: without the launches
+  // for requests of few it is 9 us shorter (it may still bring few, as tiles).
+  a.split = requests > 1 || (int64_t)max_new * a.group <= kKvSplitRows;
   const int rows = a.split_tokens * a.group;
   a.row_groups = rows <= 16 ? 1 : (rows + 31) / 32;
   a.chunk_shift = max_len <= 1024 ? 7 : max_len <= 4096 ? 8 : max_len <= 16384 ? 9 : 10;
@@ -362,7 +368,7 @@ KvAttnArgs attention_args(const w4a16_kv_cache_t* cache, int tokens, int request
 }
 
 size_t attention_workspace(const KvAttnArgs& a, int dim) {
-  return a.chunks > 1 ? kv_partials(a) * (dim + kKvPartStats) * sizeof(float) : 0;
+  return a.split && a.chunks > 1 ? kv_partials(a) * (dim + kKvPartStats) * sizeof(float) : 0;
 }
 
 }  // namespace

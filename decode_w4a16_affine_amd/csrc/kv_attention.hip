@@ -24,14 +24,16 @@ hipError_t kv_attention_typed(const KvAttnArgs& a, void* workspace, hipStream_t 
       hipLaunchKernelGGL((kv_join_kernel<D, NC>), dim3(a.c.heads * rows, ry, rz), dim3(kKvJoinThreads), 0, st, a,
                          part_o, part_ml);
   };
-  if (rows <= 16)
-    split(std::integral_constant<int, 1>{});
-  else
-    split(std::integral_constant<int, 2>{});
+  if (a.split) {
+    if (rows <= 16)
+      split(std::integral_constant<int, 1>{});
+    else
+      split(std::integral_constant<int, 2>{});
+  }
   if ((int64_t)a.max_new * a.group > kKvSplitRows) {
-    const int64_t tiles = a.tokens / (kKvTileRows / a.group) + a.requests;
-    hipLaunchKernelGGL((kv_tile_kernel<D, TYPE>), dim3((unsigned)tiles, a.c.heads), dim3(kKvTileWaves * kWave), 0, st,
-                       a);
+    const int64_t tiles = a.tokens / (kv_tile_rows(D, TYPE) / a.group) + a.requests;
+    hipLaunchKernelGGL((kv_tile_kernel<D, TYPE>), dim3((unsigned)(tiles * a.c.heads)),
+                       dim3(kv_tile_waves(D, TYPE) * kWave), 0, st, a);
   }
   return hipGetLastError();
 }

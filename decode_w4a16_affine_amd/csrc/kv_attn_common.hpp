@@ -16,6 +16,9 @@ typedef float kv_f32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t kv_u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t kv_u32x2 __attribute__((ext_vector_type(2)));
 
+// lambdas over register arrays must be inlined for these to stay in registers
+#define W4K_INLINE __attribute__((always_inline))
+
 constexpr float kKvNone = -3e38f;     // running maximum before any entry
 
 // 16 codes from the cache, past the caches' reuse order: the cache streams
@@ -96,10 +99,14 @@ struct KvLaneRows {
   int hi[NC], lo[NC];
 };
 
-// At the head of a block that few waves enter: without it the compiler runs the
-// block's selects for every tile instead of branching (a third of a tile's
-// vector instructions).
-__device__ __forceinline__ void kv_keep_branch() { asm volatile(""); }
+// For a number that a block entered by few waves computes with: made opaque
+// inside the block, so that the compiler cannot move the block's selects in
+// front of the branch (it did, and they were over a third of a tile's vector
+// instructions).
+__device__ __forceinline__ int kv_opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
 
 // One tile's softmax step for a lane, in two parts: the scores s of its 4 NP
 // entries (first entry j) for NC rows become the tile's largest logit of each row
@@ -113,9 +120,8 @@ __device__ __forceinline__ void kv_tile_max(kv_f32x4 (&s)[NC][NP], const KvLaneR
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     // entry e of the lane's 4 NP is attended by row c iff first <= e <= last
-    const int first = rows.lo[c] - j, last = page_ok ? rows.hi[c] - j : -1;
     if (!whole) {
-      kv_keep_branch();
+      const int first = kv_opaque(rows.lo[c] - j), last = kv_opaque(page_ok ? rows.hi[c] - j : -1);
 #pragma unroll
       for (int e = 0; e < 4 * NP; ++e)
         s[c][e / 4][e % 4] = e >= first && e <= last ? s[c][e / 4][e % 4] : -__builtin_inff();
@@ -143,21 +149,21 @@ __device__ __forceinline__ void kv_weights(kv_f32x4 (&s)[NC][NP], const KvLaneRo
                                            const float (&fade)[NC], float (&l)[NC], kv_f16x8 (&w)[NC][NP / 2]) {
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int first = rows.lo[c] - j, last = page_ok ? rows.hi[c] - j : -1;
     const float shift = lv - m[c];
     float p[4 * NP], sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4 * NP; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][e / 4][e % 4], ks, shift));
     // masked entries are exactly 0 also where the page's scales are 0 or NaN
+    float value_inverse = rv;
     if (!whole) {
-      kv_keep_branch();
+      const int first = kv_opaque(rows.lo[c] - j), last = kv_opaque(page_ok ? rows.hi[c] - j : -1);
 #pragma unroll
       for (int e = 0; e < 4 * NP; ++e) p[e] = e >= first && e <= last ? p[e] : 0.0f;
+      value_inverse = first < 4 * NP && last >= 0 && first <= last ? rv : 0.0f;
     }
 #pragma unroll
     for (int e = 0; e < 4 * NP; ++e) sum += p[e];
-    const bool any = whole || (first < 4 * NP && last >= 0 && first <= last);
-    l[c] = l[c] * fade[c] + (any ? sum * rv : 0.0f);
+    l[c] = __builtin_fmaf(l[c], fade[c], sum * value_inverse);
 #pragma unroll
     for (int h = 0; h < NP / 2; ++h) {
       uint32_t pk[4];

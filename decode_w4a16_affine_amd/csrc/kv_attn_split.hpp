@@ -61,9 +61,6 @@
 
 namespace w4k {
 
-// lambdas over register arrays must be inlined for these to stay in registers
-#define W4K_INLINE __attribute__((always_inline))
-
 constexpr int kKvSplitWaves = 4;
 constexpr int kKvSplitTile = 32;                   // entries a wave takes at once (T above)
 constexpr int kKvGridRequests = 32768;             // requests on the grid's y axis (more go to z)
@@ -122,12 +119,8 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
   // No load stands under a condition: entries without a page read page 0 instead
   // (in the L2 after the first) and are masked, so the waits for loads count
   // exactly and the next step's stay in flight through this one.
-  // (what the loops below derive from an opaque number is computed anew each
-  // step; kept over the steps it would take thirty registers)
-  auto opaque = [](int v) W4K_INLINE {
-    asm volatile("" : "+v"(v));
-    return v;
-  };
+  // (What the loops below derive from an opaque number is computed anew each
+  // step; kept over the steps it would take thirty registers.)
   constexpr int KP = D / 16, KR = kWave / KP;      // 16-byte pieces a key, keys an instruction
   constexpr int VR = D / W;                        // rows of values a wave owns
   const uint32_t page_head_bytes = (uint32_t)D << shift;      // one head's codes of a page, keys or values
@@ -178,7 +171,7 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
         vc[i] = kv_load(v0 + lane_value(off, (i * kWave >> pps) << bs) + ((i * kWave & in_page) >> bs << shift) +
                         value_lane);
     } else {
-      const int lane_page = opaque(lane >> pps);
+      const int lane_page = kv_opaque(lane >> pps);
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
         const int at = ((i * kWave >> pps) + lane_page) << bs;
@@ -215,14 +208,14 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
     // E4M3 codes of entries that hold nothing may be NaN, which weights of 0
     // would not hide: where entries of the step are missing, their codes become 0
     if (TYPE == W4A16_KV_FP8 && !(j0 + STEP <= rows.end && __all(page >= 0 || x >= STEP / 16))) {
-      kv_keep_branch();
+      const int lane_first = kv_opaque(lane_block);
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
-        const int block = (i * kWave >> pps << bs) + lane_block;
+        const int block = (i * kWave >> pps << bs) + lane_first;
         vc[i] = vc[i] & kv_existing_bytes(__shfl(page, block) >= 0 ? rows.end - (j0 + 16 * block) : 0);
       }
     }
-    const int value_put = opaque(value_put_0);
+    const int value_put = kv_opaque(value_put_0);
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
       const int block = i * kWave >> pps << bs, row = (i * kWave & in_page) >> bs;

@@ -1,26 +1,45 @@
 // Attention over the paged 8-bit cache for requests of many new tokens
 // (prompts and prompt chunks).
 //
-// A workgroup of four waves takes 128 rows of one request and cache head (as
-// many whole tokens' query heads as fit), 32 a wave, and walks the cache in
-// tiles of 64 entries.  The products, the order of a lane's entries, the
-// softmax and the arithmetic are those of the split form (kv_attn_split.hpp);
-// what differs is where the operands come from: here a tile's codes serve 128
-// rows, so each is loaded and converted once, by the thread whose place in a
-// matrix operand it has, and put into LDS as a finished 16-bit operand (16
-// bytes a lane, in lane order: reads and writes are free of bank conflicts).
-// Two LDS buffers: the codes of the next tile are loaded into registers before
-// the current one is multiplied and converted after it, one barrier a tile.
+// A workgroup takes 128 rows of one request and cache head (64 for D = 256 with
+// E4M3 codes; as many whole tokens' query heads as fit) and walks the cache in
+// tiles of 64 entries.  The products, the softmax and the arithmetic are those of
+// the split form (kv_attn_split.hpp); what differs is how the work is cut.  Here
+// a tile's codes serve all rows, so each is loaded and converted once, by the
+// thread whose place in a matrix operand it has, and put into LDS as a finished
+// 16-bit operand (16 bytes a lane, in lane order: reads and writes are free of
+// bank conflicts).  Lane (x, g) = (l % 16, l / 16) scores entries 16 g .. + 15 of the
+// tile: rows 4 b + i of piece t of the key operand are entries 16 b + 4 t + i.
+//
+// D = 64, 128: a wave has 32 rows.  Keys and values have two buffers; the next
+// tile's codes are loaded before this one is multiplied and converted after it,
+// one barrier a tile.  (One buffer and two barriers: 686 us instead of 634 for
+// four prompt chunks of 200 to 2000 tokens behind up to 12000, 32 heads of 128.)
+// D = 256: the output of 32 rows would take 128 registers of a wave, so two waves
+// share them: each scores half of the entries (pieces t = 2 h, 2 h + 1, whose
+// weights are operand h of the second product), they agree on the maxima and
+// exchange weights through LDS, and each multiplies all 64 weights with the
+// values of its half of the head's elements.  One buffer and two barriers: before
+// the first, the waves score and publish maxima; between them they write
+// weights, this tile's values and the next tile's keys.  (One wave for 32 rows:
+// 246 us instead of 166 for a prompt of 4099 tokens, 10 heads of 256.)  With int8
+// codes the conversions need registers that only eight waves (two pieces each
+// to convert instead of four) leave; four reloaded the queries from scratch
+// memory every tile (515 us instead of 207).
+//
 #pragma once
 
 #include "kv_attn_common.hpp"
 
 namespace w4k {
 
-constexpr int kKvTile = 64;           // cache entries at once
-constexpr int kKvTileWaves = 4;
-constexpr int kKvTileCols = 2;                                     // 16-row pieces a wave
-constexpr int kKvTileRows = kKvTileWaves * kKvTileCols * 16;
+constexpr int kKvTile = 64;                                        // cache entries at once
+constexpr int kKvTileCols = 2;                                     // 16-row pieces a pair of waves
+// Waves that share 32 rows: two for D = 256, where the output of 32 rows alone
+// would take 128 registers of a wave.
+constexpr int kv_tile_share(int D) { return D == 256 ? 2 : 1; }
+constexpr int kv_tile_waves(int D, int type) { return D == 256 && type == W4A16_KV_INT8 ? 8 : 4; }
+constexpr int kv_tile_rows(int D, int type) { return kv_tile_waves(D, type) / kv_tile_share(D) * kKvTileCols * 16; }
 
 // Workgroup u -> request and first token.  Request r owns the numbers from
 // floor(token_start[r] / TT) + r on: at least ceil(n / TT) of them, and they
@@ -42,52 +61,58 @@ __device__ __forceinline__ int kv_tile_owner(const int32_t* token_start, int req
 }
 
 template <int D, int TYPE>
-__global__ __launch_bounds__(kKvTileWaves * kWave) void kv_tile_kernel(KvAttnArgs a) {
-  constexpr int NC = kKvTileCols;
-  constexpr int KC = D / 64;          // 16-byte pieces of a key a lane holds
-  constexpr int DT = D / 16;          // 16-row pieces of the output
-  constexpr int VW = DT / kKvTileWaves;   // of which a wave loads
-  __shared__ kv_u32x4 s_k[2][4 * 2 * KC * kWave];      // [piece t][sum step][lane]
-  __shared__ kv_u32x4 s_v[2][DT * 2 * kWave];          // [piece d][sum step][lane]
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+__global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_kernel(KvAttnArgs a) {
+  constexpr int NC = kKvTileCols, W = kv_tile_waves(D, TYPE), HS = kv_tile_share(D);
+  constexpr int KC = D / 64;              // 16-byte pieces of a key a lane multiplies
+  constexpr int NP = 4 / HS;              // 16-entry pieces of a tile that a wave scores
+  constexpr int DT = D / 16, DH = DT / HS;  // 16-row pieces of the output, and those a wave owns
+  constexpr int KU = 4 * KC, VU = DT;     // 64-lane pieces of a tile's keys and values
+  constexpr int KL = (KU + W - 1) / W, VL = (VU + W - 1) / W;   // of which a wave loads
+  constexpr int NB = HS == 1 ? 2 : 1;       // buffers
+  __shared__ kv_u32x4 s_k[NB][KU * 2 * kWave];      // [piece t][sum step][lane]
+  __shared__ kv_u32x4 s_v[NB][VU * 2 * kWave];      // [piece d][sum step][lane]
+  __shared__ kv_u32x4 s_p[HS == 2 ? W : 1][NC][kWave];      // a wave's weights as an operand
+  __shared__ float s_m[W][NC * 16];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int x = lane & 15, g = lane >> 4;
-  const int tt = kv_token_of(a, kKvTileRows);
-  const int u = gridDim.x - 1 - blockIdx.x;        // later tokens attend more: they go first
-  const int kh = blockIdx.y;
+  const int half = HS == 2 ? wave & 1 : 0;
+  const int tt = kv_token_of(a, kv_tile_rows(D, TYPE));
+  // Heads run fastest: a head's workgroups share an XCD's L2 (eight heads), and
+  // the last tokens, which attend most, go first for every head (with a head's
+  // tiles together, the last head's long ones began late: 770 us instead of 638).
+  const int kh = blockIdx.x % a.c.heads;
+  const int u = (gridDim.x - 1 - blockIdx.x) / a.c.heads;
   const int r = __builtin_amdgcn_readfirstlane(kv_tile_owner(a.token_start, a.requests, tt, u));
   if (r < 0) return;
   const int i0 = (u - a.token_start[r] / tt - r) * tt;
   const int n = a.token_start[r + 1] - a.token_start[r];
   const int live_tokens = min(min(n, a.max_new), a.tokens - a.token_start[r]);
-  if ((long long)n * a.group <= kKvSplitRows || i0 < 0 || i0 >= live_tokens || a.token_start[r] < 0) return;
+  if ((a.split && n * a.group <= kKvSplitRows) || i0 < 0 || i0 >= live_tokens || a.token_start[r] < 0) return;
   const int here = min(tt, live_tokens - i0);       // the workgroup's tokens
   const int live = here * a.group;                  // and rows
   const KvRows rows = kv_rows_of(a, r, i0, i0 + here - 1);
   const int shift = a.c.page_shift, P = 1 << shift;
 
-  // this wave's rows
-  const int wrow = wave * NC * 16;
+  // this pair of waves' rows
+  const int wrow = wave / HS * NC * 16;
   kv_bf16x8 q[NC][2 * KC];
   KvLaneRows<NC> lr;
-  int64_t out_at[NC];
+  int out_at[NC];
   const int pos0 = rows.seq - rows.n + i0;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int row = min(wrow + 16 * c + x, live - 1);
     const int i = kv_token_of(a, row), h = kh * a.group + row - i * a.group;
-    const int64_t t = rows.first + i0 + i;
+    const int t = rows.first + i0 + i;
     const bool ok = wrow + 16 * c + x < live;
     lr.hi[c] = ok ? min(pos0 + i, rows.end - 1) : -1;
     lr.lo[c] = a.window > 0 ? pos0 + i - a.window + 1 : 0;
-    out_at[c] = ok ? (t * a.q_heads + h) * D : -1;
+    out_at[c] = ok ? t * a.q_heads + h : -1;
     const uint16_t* qp = a.q + t * a.q_stride + (size_t)h * D + 16 * g;
 #pragma unroll
-    for (int k = 0; k < KC; ++k) {
-      q[c][2 * k] = kv_query8(qp + 64 * k, a.q_sign);
-      q[c][2 * k + 1] = kv_query8(qp + 64 * k + 8, a.q_sign);
-    }
+    for (int k = 0; k < 2 * KC; ++k) q[c][k] = kv_query8(qp + 64 * (k >> 1) + 8 * (k & 1), a.q_sign);
   }
-  // entries that some row of the wave attends, and those that every row does
+  // entries that some row of the pair attends, and those that every row does
   const int first_pos = pos0 + kv_token_of(a, min(wrow, live - 1));
   const int last_pos = pos0 + kv_token_of(a, min(wrow + NC * 16, live) - 1);
   const int any_hi = wrow < live ? min(last_pos, rows.end - 1) : -1;
@@ -95,123 +120,196 @@ __global__ __launch_bounds__(kKvTileWaves * kWave) void kv_tile_kernel(KvAttnArg
   const int all_hi = min(first_pos, rows.end - 1);
   const int all_lo = a.window > 0 ? last_pos - a.window + 1 : 0;
 
-  kv_f32x4 o[NC][DT];
+  kv_f32x4 o[NC][DH];
   float m[NC], l[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     m[c] = kKvNone;
     l[c] = 0.0f;
 #pragma unroll
-    for (int d = 0; d < DT; ++d) o[c][d] = kv_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int d = 0; d < DH; ++d) o[c][d] = kv_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  // the codes, scales and page of a tile that this thread loads
+  // Pages of a tile: lane (x, g) needs that of block x / 4 for its keys and of
+  // block g for its values and scores; lane b holds block b's, others fetch it.
   const int32_t* table = a.table + (size_t)r * a.width;
-  kv_u32x4 kc[KC], vc[VW];
-  float ks, vs;
-  bool page_ok;
-  auto load = [&](int j0) {
-    auto page_of = [&](int b) {
-      const int j = j0 + 16 * b;
-      const int page = j < rows.end ? table[j >> shift] : -1;
-      return page >= 0 && page < a.c.pages ? page : -1;
-    };
-    const int kp = page_of(x >> 2), vp = page_of(g);
-    const size_t kph = (size_t)max(kp, 0) * a.c.heads + kh, vph = (size_t)max(vp, 0) * a.c.heads + kh;
-    const uint8_t* ka = a.c.k + (kph * P + ((j0 + 16 * (x >> 2)) & (P - 1)) + 4 * wave + (x & 3)) * D + 16 * g;
-    const uint8_t* va = a.c.v + (vph * D + 16 * VW * wave + x) * P + ((j0 + 16 * g) & (P - 1));
+  auto pages = [&](int j0) W4K_INLINE {
+    const int j = j0 + 16 * (lane & 3), col = j >> shift;
+    const int page = table[min(col, a.width - 1)];
+    return j < rows.end && page >= 0 && page < a.c.pages ? page : -1;
+  };
+  const uint32_t head_bytes = (uint32_t)D << shift;      // one head's codes of a page
+  const uint64_t page_bytes = (uint64_t)a.c.heads * head_bytes;
+  kv_u32x4 kc[KL], vc[VL];
+  auto load_keys = [&](int j0, int page) W4K_INLINE {
+    const int kp = max(__shfl(page, x >> 2), 0);
+    const uint8_t* ka = a.c.k + (size_t)kh * head_bytes + kp * page_bytes +
+                        (((j0 + 16 * (x >> 2)) & (P - 1)) + (x & 3)) * D + 16 * g;
 #pragma unroll
-    for (int k = 0; k < KC; ++k) kc[k] = *reinterpret_cast<const kv_u32x4*>(ka + 64 * k);
-#pragma unroll
-    for (int d = 0; d < VW; ++d) vc[d] = *reinterpret_cast<const kv_u32x4*>(va + (size_t)d * 16 * P);
-    ks = bf16_lo(a.c.ks[vph]) * a.scale_log2;
-    vs = bf16_lo(a.c.vs[vph]);
-    vs = vs < kKvMinScale ? kKvMinScale : vs;     // 0 in a page that was never begun; NaN stays
-    page_ok = vp >= 0;
-    if (TYPE == W4A16_KV_FP8 && (j0 + kKvTile > rows.end || !__all(page_ok))) {
-      const kv_u32x4 mask = kv_existing_bytes(page_ok ? rows.end - (j0 + 16 * g) : 0);
-#pragma unroll
-      for (int d = 0; d < VW; ++d) vc[d] = vc[d] & mask;
+    for (int i = 0; i < KL; ++i) {
+      const int unit = KU < W ? wave & (KU - 1) : wave * KL + i;       // (few units: two waves load the same)
+      kc[i] = *reinterpret_cast<const kv_u32x4*>(ka + 4 * (unit / KC) * D + 64 * (unit % KC));
     }
   };
-  auto store = [&](int b) {
+  auto load_values = [&](int j0, int page) W4K_INLINE {
+    const int vp = __shfl(page, g);
+    const uint8_t* va = a.c.v + (size_t)kh * head_bytes + max(vp, 0) * page_bytes + ((j0 + 16 * g) & (P - 1));
 #pragma unroll
-    for (int k = 0; k < KC; ++k) {
-      s_k[b][((wave * KC + k) * 2) * kWave + lane] =
-          __builtin_bit_cast(kv_u32x4, kv_bf16_of8<TYPE>(kc[k].x, kc[k].y));
-      s_k[b][((wave * KC + k) * 2 + 1) * kWave + lane] =
-          __builtin_bit_cast(kv_u32x4, kv_bf16_of8<TYPE>(kc[k].z, kc[k].w));
+    for (int i = 0; i < VL; ++i) {
+      const int unit = VU < W ? wave & (VU - 1) : wave * VL + i;
+      vc[i] = *reinterpret_cast<const kv_u32x4*>(va + (size_t)(16 * unit + x) * P);
+    }
+  };
+  float ks, vs;
+  auto load_scales = [&](int page) W4K_INLINE {
+    const uint32_t at = (uint32_t)max(__shfl(page, g), 0) * (uint32_t)a.c.heads + kh;
+    ks = bf16_lo(a.c.ks[at]) * a.scale_log2;
+    vs = bf16_lo(a.c.vs[at]);
+  };
+  auto put_keys = [&](int b) W4K_INLINE {
+#pragma unroll
+    for (int i = 0; i < KL; ++i) {
+      const int unit = KU < W ? wave & (KU - 1) : wave * KL + i;
+      s_k[b][unit * 2 * kWave + lane] = __builtin_bit_cast(kv_u32x4, kv_bf16_of8<TYPE>(kc[i].x, kc[i].y));
+      s_k[b][(unit * 2 + 1) * kWave + lane] = __builtin_bit_cast(kv_u32x4, kv_bf16_of8<TYPE>(kc[i].z, kc[i].w));
+    }
+  };
+  auto put_values = [&](int b, int j0, int page) W4K_INLINE {
+    // E4M3 codes of entries that hold nothing may be NaN, which weights of 0
+    // would not hide: where entries of the tile are missing, their codes become 0
+    if (TYPE == W4A16_KV_FP8 && !(j0 + kKvTile <= rows.end && __all(page >= 0))) {
+      const int first = kv_opaque(j0 + 16 * g);
+      const kv_u32x4 exist = kv_existing_bytes(__shfl(page, g) >= 0 ? rows.end - first : 0);
+#pragma unroll
+      for (int i = 0; i < VL; ++i) vc[i] = vc[i] & exist;
     }
 #pragma unroll
-    for (int d = 0; d < VW; ++d) {
-      s_v[b][((wave * VW + d) * 2) * kWave + lane] = __builtin_bit_cast(kv_u32x4, kv_f16_of8<TYPE>(vc[d].x, vc[d].y));
-      s_v[b][((wave * VW + d) * 2 + 1) * kWave + lane] =
-          __builtin_bit_cast(kv_u32x4, kv_f16_of8<TYPE>(vc[d].z, vc[d].w));
+    for (int i = 0; i < VL; ++i) {
+      const int unit = VU < W ? wave & (VU - 1) : wave * VL + i;
+      s_v[b][unit * 2 * kWave + lane] = __builtin_bit_cast(kv_u32x4, kv_f16_of8<TYPE>(vc[i].x, vc[i].y));
+      s_v[b][(unit * 2 + 1) * kWave + lane] = __builtin_bit_cast(kv_u32x4, kv_f16_of8<TYPE>(vc[i].z, vc[i].w));
     }
   };
 
   int j0 = rows.begin & ~(kKvTile - 1);
+  int page = -1, page_next = -1;
   if (j0 < rows.end) {
-    load(j0);
-    store(0);
+    page = pages(j0);
+    page_next = pages(j0 + kKvTile);
+    load_keys(j0, page);
+    load_values(j0, page);
+    load_scales(page);
+    put_keys(0);
+    if constexpr (HS == 1)
+      put_values(0, j0, page);
+    else
+      load_keys(j0 + kKvTile, page_next);
   }
   __syncthreads();
-  for (int b = 0; j0 < rows.end; j0 += kKvTile, b ^= 1) {
-    const float ks_now = ks, vs_now = vs;
-    const bool ok_now = page_ok;
-    const bool more = j0 + kKvTile < rows.end;
-    if (more) load(j0 + kKvTile);
-    if (j0 <= any_hi && j0 + kKvTile > any_lo) {
-      const bool whole = __all(ok_now) && j0 + kKvTile - 1 <= all_hi && j0 >= all_lo;
-      kv_f32x4 s[NC][4];
+  for (int b = 0; j0 < rows.end; j0 += kKvTile, b ^= NB - 1) {
+    const bool active = j0 <= any_hi && j0 + kKvTile > any_lo;      // of this pair's rows
+    const int jl = j0 + 16 * g + 8 * half;       // this lane's first entry
+    const bool ok = __shfl(page, g) >= 0;
+    const bool whole = __all(page >= 0) && j0 + kKvTile - 1 <= all_hi && j0 >= all_lo;
+    const float vs_now = vs < kKvMinScale ? kKvMinScale : vs;       // 0 in a page never begun; NaN stays
+    const float ks_now = ks, lv = __builtin_amdgcn_logf(vs_now), rv = __builtin_amdgcn_rcpf(vs_now);
+    int page_after = -1;
+    if constexpr (HS == 1) {
+      page_after = pages(j0 + 2 * kKvTile);
+      load_keys(j0 + kKvTile, page_next);
+      load_values(j0 + kKvTile, page_next);
+      load_scales(page_next);
+    }
+    kv_f32x4 s[NC][NP];
+    float top[NC];
+    if (active) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < NP; ++t) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) s[c][t] = kv_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < 2 * KC; ++k) {
-          const kv_bf16x8 f = __builtin_bit_cast(kv_bf16x8, s_k[b][(t * 2 * KC + k) * kWave + lane]);
+          const kv_bf16x8 f = __builtin_bit_cast(kv_bf16x8, s_k[b][((2 * half + t) * 2 * KC + k) * kWave + lane]);
 #pragma unroll
           for (int c = 0; c < NC; ++c) s[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, q[c][k], s[c][t], 0, 0, 0);
         }
       }
-      float fade[NC], top[NC];
-      kv_f16x8 w[NC][2];
-      const float lv = __builtin_amdgcn_logf(vs_now), rv = __builtin_amdgcn_rcpf(vs_now);
-      kv_tile_max<NC, 4>(s, lr, j0 + 16 * g, ks_now, lv, whole, ok_now, top);
+      kv_tile_max<NC, NP>(s, lr, jl, ks_now, lv, whole, ok, top);
+      if constexpr (HS == 2) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          if (g == 0) s_m[wave][16 * c + x] = top[c];
+      }
+    }
+    if constexpr (HS == 2) __syncthreads();
+    kv_f16x8 w[NC][NP / 2];
+    if (active) {
+      float fade[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
+        if constexpr (HS == 2) top[c] = fmaxf(top[c], s_m[wave ^ 1][16 * c + x]);
         const float m_new = kv_new_max(m[c], top[c]);
         fade[c] = __builtin_amdgcn_exp2f(m[c] - m_new);
         m[c] = m_new;
       }
-      kv_weights<NC, 4>(s, lr, j0 + 16 * g, ks_now, lv, rv, whole, ok_now, m, fade, l, w);
+      kv_weights<NC, NP>(s, lr, jl, ks_now, lv, rv, whole, ok, m, fade, l, w);
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
+      for (int c = 0; c < NC; ++c) {
+        if constexpr (HS == 2) s_p[wave][c][lane] = __builtin_bit_cast(kv_u32x4, w[c][0]);
         if (__any(fade[c] != 1.0f))
 #pragma unroll
-          for (int d = 0; d < DT; ++d) o[c][d] *= fade[c];
+          for (int d = 0; d < DH; ++d) o[c][d] *= fade[c];
+      }
+    }
+    if constexpr (HS == 2) {
+      put_values(0, j0, page);
+      put_keys(0);                               // of the next tile
+      page_after = pages(j0 + 2 * kKvTile);
+      load_values(j0 + kKvTile, page_next);
+      load_scales(page_next);
+      __syncthreads();
+      load_keys(j0 + 2 * kKvTile, page_after);
+    }
+    if (active) {
+      kv_f16x8 p[NC][2];
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          p[c][h] = HS == 1 ? w[c][h % (NP / 2)] : __builtin_bit_cast(kv_f16x8, s_p[(wave & ~1) + h][c][lane]);
+#pragma unroll
+      for (int d = 0; d < DH; ++d)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const kv_f16x8 f = __builtin_bit_cast(kv_f16x8, s_v[b][(d * 2 + h) * kWave + lane]);
+          const kv_f16x8 f = __builtin_bit_cast(kv_f16x8, s_v[b][((half * DH + d) * 2 + h) * kWave + lane]);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, w[c][h], o[c][d], 0, 0, 0);
+          for (int c = 0; c < NC; ++c) o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, p[c][h], o[c][d], 0, 0, 0);
         }
     }
-    if (more) store(b ^ 1);
-    __syncthreads();
+    if constexpr (HS == 1) {
+      put_keys(b ^ 1);
+      put_values(b ^ 1, j0 + kKvTile, page_next);
+      __syncthreads();
+    }
+    page = page_next;
+    page_next = page_after;
   }
 
+  // a row's sum over both waves
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     l[c] += __shfl_xor(l[c], 16);
     l[c] += __shfl_xor(l[c], 32);
-    if (out_at[c] < 0) continue;
-    const float inverse = kv_inverse(l[c]);
+    if (HS == 2 && g == 0) s_m[wave][16 * c + x] = l[c];
+  }
+  if constexpr (HS == 2) __syncthreads();
 #pragma unroll
-    for (int d = 0; d < DT; ++d) kv_store4(a.out + out_at[c] + 16 * d + 4 * g, o[c][d], inverse);
+  for (int c = 0; c < NC; ++c) {
+    if (out_at[c] < 0) continue;
+    const float inverse = kv_inverse(HS == 1 ? l[c] : s_m[wave & ~1][16 * c + x] + s_m[wave | 1][16 * c + x]);
+    uint16_t* out = a.out + (size_t)out_at[c] * D + 16 * DH * half + 4 * g;
+#pragma unroll
+    for (int d = 0; d < DH; ++d) kv_store4(out + 16 * d, o[c][d], inverse);
   }
 }
 

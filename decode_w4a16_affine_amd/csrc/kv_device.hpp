@@ -75,6 +75,7 @@ struct KvAttnArgs {
   uint32_t q_sign;       // sign bits of two bf16 if scale < 0, else 0
   int width, window, tokens, requests, max_new, max_len, q_heads, group;
   uint32_t group_inverse;      // ceil(2^16 / group): see kv_token_of
+  bool split;                  // requests of few rows take the split form (else all take tiles)
   // requests of few rows: log2 of the entries a chunk, chunks a row at most, row
   // groups a cache head, new tokens a request at most
   int chunk_shift, chunks, row_groups, split_tokens;

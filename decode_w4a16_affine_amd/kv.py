@@ -148,8 +148,10 @@ def _rows(t, heads, dim, name):
     if len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != dim:
         raise ValueError(f"{name} must have shape [T, {'heads' if heads is None else heads}, {dim}], got {list(shape)}")
     tokens, row = shape[0], shape[1] * dim
+    if t.numel() == 0:
+        return tokens, row
     stride, head_stride, unit = t.stride()
-    if tokens <= 1:
+    if tokens == 1:
         stride = row                    # no second row: any valid stride
     if unit != 1 or (head_stride != dim and shape[1] > 1) or stride < row:
         raise ValueError(f"{name} must be dense within a token (strides [>= {row}, {dim}, 1]), got {list(t.stride())}")

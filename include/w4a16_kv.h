@@ -129,11 +129,13 @@ size_t w4a16_kv_attention_workspace_bytes(int tokens, int requests, int max_new,
  *   out  bf16 [T][HQ][D], dense
  * max_new and max_len bound the requests' n and seq_lens (the launch is sized
  * by them; rows past max_new stay unwritten and entries past max_len unread).
- * Softmax statistics and sums in fp32.  The result of a row depends on its
- * own query, position and entries, on max_len and on the form its request
- * takes, not on the other requests; requests of n * HQ / H up to a bound
- * (64 rows) share one form, whose rows are bitwise equal to those of calls
- * with fewer new tokens.
+ * Softmax statistics and sums in fp32, weights rounded to fp16, keys, values
+ * and queries exact.  Requests of n * HQ / H <= 64 rows take one form, whose rows
+ * depend on their own query, position and entries and on max_len alone: they
+ * are bitwise equal in any batch and for any number of new tokens up to that
+ * bound (a verify batch gives the rows of single-token calls).  Requests of more
+ * take another, as does a call of one request with max_new * HQ / H > 64.
+ * (T / (64 / (HQ / H)) + R) * H must not exceed 2^22 (the launch's size).
  */
 w4a16_status_t w4a16_kv_attention(const uint16_t *q, int64_t q_stride, const w4a16_kv_cache_t *cache,
                                   const int32_t *block_table, int width, const int32_t *seq_lens,

@@ -357,6 +357,18 @@ def test_attention_bounds_of_the_step_are_respected():
 
 
 @pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("D,G", [(64, 2), (128, 4), (256, 5)])
+def test_one_request_of_fewer_tokens_than_its_bound(kind, D, G):
+    """A call sized for a prompt that brings one or a few tokens only."""
+    for n, length in ((1, 130), (3, 67), (0, 20)):
+        p = Problem(37, kind, 2, G, D, 32, [length], [n])
+        if n:
+            p.check(max_new=500)
+        else:
+            assert p.run(max_new=500).numel() == 0
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
 def test_offsets_past_32_bits(kind):
     """A cache of over 4 GiB a tensor, the request's pages at its far end."""
     H, D, page, pages = 8, 128, 128, 40000       # 5.2 GB of codes in each tensor

@@ -108,6 +108,7 @@ def test_attention_refuses_bad_arguments(L):
         assert att(**bad) == ESHAPE, bad
     assert att(HQ=130, qs=130 * 128) == EUNSUP          # 65 query heads a cache head
     assert att(pages=0) == ESHAPE
+    assert att(T=2 ** 19, HQ=512, heads=512, qs=512 * 128) == ESHAPE           # a launch of over 2^22 workgroups
     assert att(T=2 ** 20, HQ=2048, heads=1024, qs=2048 * 128) == ESHAPE        # T * HQ = 2^31
     assert att(pages=2 ** 21, page=16, heads=1024) == ESHAPE                  # pages * heads = 2^31
     for name in ("q", "table", "seq", "start", "out"):
