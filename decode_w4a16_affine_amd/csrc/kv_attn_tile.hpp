@@ -69,6 +69,7 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
   constexpr int KU = 4 * KC, VU = DT;     // 64-lane pieces of a tile's keys and values
   constexpr int KL = (KU + W - 1) / W, VL = (VU + W - 1) / W;   // of which a wave loads
   constexpr int NB = HS == 1 ? 2 : 1;       // buffers
+  constexpr int AHEAD = D == 256 ? 3 : 4;   // operands read ahead of their products, as registers allow
   __shared__ kv_u32x4 s_k[NB][KU * 2 * kWave];      // [piece t][sum step][lane]
   __shared__ kv_u32x4 s_v[NB][VU * 2 * kWave];      // [piece d][sum step][lane]
   __shared__ kv_u32x4 s_p[HS == 2 ? W : 1][NC][kWave];      // a wave's weights as an operand
@@ -130,20 +131,25 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
     for (int d = 0; d < DH; ++d) o[c][d] = kv_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  // Pages of a tile: lane (x, g) needs that of block x / 4 for its keys and of
-  // block g for its values and scores; lane b holds block b's, others fetch it.
+  // Pages of a tile: lane (x, g) needs that of 16-entry block x / 4 for its keys
+  // and of block g for its values and scores.  They are read two tiles ahead of
+  // their use and checked only there, so that nothing waits for them.
   const int32_t* table = a.table + (size_t)r * a.width;
+  struct Pages {
+    int k, v;
+  };
   auto pages = [&](int j0) W4K_INLINE {
-    const int j = j0 + 16 * (lane & 3), col = j >> shift;
-    const int page = table[min(col, a.width - 1)];
-    return j < rows.end && page >= 0 && page < a.c.pages ? page : -1;
+    return Pages{table[min((j0 + 16 * (x >> 2)) >> shift, a.width - 1)], table[min((j0 + 16 * g) >> shift, a.width - 1)]};
+  };
+  auto checked = [&](int j0, Pages p) W4K_INLINE {
+    return Pages{j0 + 16 * (x >> 2) < rows.end && p.k >= 0 && p.k < a.c.pages ? p.k : -1,
+                 j0 + 16 * g < rows.end && p.v >= 0 && p.v < a.c.pages ? p.v : -1};
   };
   const uint32_t head_bytes = (uint32_t)D << shift;      // one head's codes of a page
   const uint64_t page_bytes = (uint64_t)a.c.heads * head_bytes;
   kv_u32x4 kc[KL], vc[VL];
   auto load_keys = [&](int j0, int page) W4K_INLINE {
-    const int kp = max(__shfl(page, x >> 2), 0);
-    const uint8_t* ka = a.c.k + (size_t)kh * head_bytes + kp * page_bytes +
+    const uint8_t* ka = a.c.k + (size_t)kh * head_bytes + max(page, 0) * page_bytes +
                         (((j0 + 16 * (x >> 2)) & (P - 1)) + (x & 3)) * D + 16 * g;
 #pragma unroll
     for (int i = 0; i < KL; ++i) {
@@ -152,8 +158,7 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
     }
   };
   auto load_values = [&](int j0, int page) W4K_INLINE {
-    const int vp = __shfl(page, g);
-    const uint8_t* va = a.c.v + (size_t)kh * head_bytes + max(vp, 0) * page_bytes + ((j0 + 16 * g) & (P - 1));
+    const uint8_t* va = a.c.v + (size_t)kh * head_bytes + max(page, 0) * page_bytes + ((j0 + 16 * g) & (P - 1));
 #pragma unroll
     for (int i = 0; i < VL; ++i) {
       const int unit = VU < W ? wave & (VU - 1) : wave * VL + i;
@@ -162,7 +167,7 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
   };
   float ks, vs;
   auto load_scales = [&](int page) W4K_INLINE {
-    const uint32_t at = (uint32_t)max(__shfl(page, g), 0) * (uint32_t)a.c.heads + kh;
+    const uint32_t at = (uint32_t)max(page, 0) * (uint32_t)a.c.heads + kh;
     ks = bf16_lo(a.c.ks[at]) * a.scale_log2;
     vs = bf16_lo(a.c.vs[at]);
   };
@@ -179,7 +184,7 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
     // would not hide: where entries of the tile are missing, their codes become 0
     if (TYPE == W4A16_KV_FP8 && !(j0 + kKvTile <= rows.end && __all(page >= 0))) {
       const int first = kv_opaque(j0 + 16 * g);
-      const kv_u32x4 exist = kv_existing_bytes(__shfl(page, g) >= 0 ? rows.end - first : 0);
+      const kv_u32x4 exist = kv_existing_bytes(page >= 0 ? rows.end - first : 0);
 #pragma unroll
       for (int i = 0; i < VL; ++i) vc[i] = vc[i] & exist;
     }
@@ -192,48 +197,52 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
   };
 
   int j0 = rows.begin & ~(kKvTile - 1);
-  int page = -1, page_next = -1;
+  int page = -1;                  // of this tile's values
+  Pages next = {-1, -1}, after = {-1, -1};
   if (j0 < rows.end) {
-    page = pages(j0);
-    page_next = pages(j0 + kKvTile);
-    load_keys(j0, page);
+    const Pages first = checked(j0, pages(j0));
+    next = checked(j0 + kKvTile, pages(j0 + kKvTile));
+    after = pages(j0 + 2 * kKvTile);
+    page = first.v;
+    load_keys(j0, first.k);
     load_values(j0, page);
     load_scales(page);
     put_keys(0);
     if constexpr (HS == 1)
       put_values(0, j0, page);
     else
-      load_keys(j0 + kKvTile, page_next);
+      load_keys(j0 + kKvTile, next.k);
   }
   __syncthreads();
   for (int b = 0; j0 < rows.end; j0 += kKvTile, b ^= NB - 1) {
     const bool active = j0 <= any_hi && j0 + kKvTile > any_lo;      // of this pair's rows
     const int jl = j0 + 16 * g + 8 * half;       // this lane's first entry
-    const bool ok = __shfl(page, g) >= 0;
+    const bool ok = page >= 0;
     const bool whole = __all(page >= 0) && j0 + kKvTile - 1 <= all_hi && j0 >= all_lo;
     const float vs_now = vs < kKvMinScale ? kKvMinScale : vs;       // 0 in a page never begun; NaN stays
     const float ks_now = ks, lv = __builtin_amdgcn_logf(vs_now), rv = __builtin_amdgcn_rcpf(vs_now);
-    int page_after = -1;
+    const Pages second = checked(j0 + 2 * kKvTile, after);
+    after = pages(j0 + 3 * kKvTile);
     if constexpr (HS == 1) {
-      page_after = pages(j0 + 2 * kKvTile);
-      load_keys(j0 + kKvTile, page_next);
-      load_values(j0 + kKvTile, page_next);
-      load_scales(page_next);
+      load_keys(j0 + kKvTile, next.k);
+      load_values(j0 + kKvTile, next.v);
+      load_scales(next.v);
     }
     kv_f32x4 s[NC][NP];
     float top[NC];
     if (active) {
 #pragma unroll
-      for (int t = 0; t < NP; ++t) {
+      for (int t = 0; t < NP; ++t)
 #pragma unroll
         for (int c = 0; c < NC; ++c) s[c][t] = kv_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      kv_stream_operands<AHEAD, NP * 2 * KC>(
+          [&](int i) W4K_INLINE { return s_k[b][(2 * half * 2 * KC + i) * kWave + lane]; },
+          [&](int i, kv_u32x4 f) W4K_INLINE {
 #pragma unroll
-        for (int k = 0; k < 2 * KC; ++k) {
-          const kv_bf16x8 f = __builtin_bit_cast(kv_bf16x8, s_k[b][((2 * half + t) * 2 * KC + k) * kWave + lane]);
-#pragma unroll
-          for (int c = 0; c < NC; ++c) s[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, q[c][k], s[c][t], 0, 0, 0);
-        }
-      }
+            for (int c = 0; c < NC; ++c)
+              s[c][i / (2 * KC)] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(kv_bf16x8, f), q[c][i % (2 * KC)], s[c][i / (2 * KC)], 0, 0, 0);
+          });
       kv_tile_max<NC, NP>(s, lr, jl, ks_now, lv, whole, ok, top);
       if constexpr (HS == 2) {
 #pragma unroll
@@ -264,11 +273,10 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
     if constexpr (HS == 2) {
       put_values(0, j0, page);
       put_keys(0);                               // of the next tile
-      page_after = pages(j0 + 2 * kKvTile);
-      load_values(j0 + kKvTile, page_next);
-      load_scales(page_next);
+      load_values(j0 + kKvTile, next.v);
+      load_scales(next.v);
       __syncthreads();
-      load_keys(j0 + 2 * kKvTile, page_after);
+      load_keys(j0 + 2 * kKvTile, second.k);
     }
     if (active) {
       kv_f16x8 p[NC][2];
@@ -277,22 +285,22 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           p[c][h] = HS == 1 ? w[c][h % (NP / 2)] : __builtin_bit_cast(kv_f16x8, s_p[(wave & ~1) + h][c][lane]);
+      kv_stream_operands<AHEAD, DH * 2>(
+          [&](int i) W4K_INLINE { return s_v[b][(half * DH * 2 + i) * kWave + lane]; },
+          [&](int i, kv_u32x4 f) W4K_INLINE {
 #pragma unroll
-      for (int d = 0; d < DH; ++d)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const kv_f16x8 f = __builtin_bit_cast(kv_f16x8, s_v[b][((half * DH + d) * 2 + h) * kWave + lane]);
-#pragma unroll
-          for (int c = 0; c < NC; ++c) o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, p[c][h], o[c][d], 0, 0, 0);
-        }
+            for (int c = 0; c < NC; ++c)
+              o[c][i / 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(kv_f16x8, f), p[c][i % 2],
+                                                                   o[c][i / 2], 0, 0, 0);
+          });
     }
     if constexpr (HS == 1) {
       put_keys(b ^ 1);
-      put_values(b ^ 1, j0 + kKvTile, page_next);
+      put_values(b ^ 1, j0 + kKvTile, next.v);
       __syncthreads();
     }
-    page = page_next;
-    page_next = page_after;
+    page = next.v;
+    next = second;
   }
 
   // a row's sum over both waves
