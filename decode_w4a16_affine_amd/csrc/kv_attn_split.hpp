@@ -63,6 +63,7 @@ namespace w4k {
 
 constexpr int kKvSplitWaves = 4;
 constexpr int kKvSplitTile = 32;                   // entries a wave takes at once (T above)
+constexpr int kKvSplitAhead = 2;                    // operands read from LDS ahead of their products
 constexpr int kKvGridRequests = 32768;             // requests on the grid's y axis (more go to z)
 
 // Waves per SIMD that the registers have to allow: what they do without spilling
@@ -101,11 +102,12 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
   // from there.  They are looked up whatever the request's length (beyond it
   // they are masked), so the first step's do not wait for the length.
   auto pages = [&](int j0) W4K_INLINE {
-    const int col = (j0 + 16 * x) >> shift;
-    const int page = table[min(col, a.width - 1)];
-    return col < a.width && page >= 0 && page < a.c.pages ? page : -1;
+    return table[min((j0 + 16 * x) >> shift, a.width - 1)];
   };
-  int page = 0, page_next = 0;
+  auto checked = [&](int j0, int page) W4K_INLINE {
+    return (j0 + 16 * x) >> shift < a.width && page >= 0 && page < a.c.pages ? page : -1;
+  };
+  int page = 0, page_after = 0;
   if (a.window == 0 && a.width > 0) page = pages(block << a.chunk_shift);
   const int i_first = kv_token_of(a, row0), i_last = kv_token_of(a, row0 + NC * 16 - 1);
   const KvRows rows = kv_rows_of(a, r, i_first, i_last);
@@ -134,7 +136,7 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
   const uint8_t* const k_head = a.c.k + (size_t)kh * page_head_bytes;
   const uint8_t* const v_head = a.c.v + (size_t)kh * page_head_bytes + (size_t)(VR * wave << shift);
   kv_u32x4 kc[LD], vc[LD];
-  float ks, vs;
+  uint16_t ks, vs;      // bits, converted where used: a conversion here would wait for the loads
   bool page_ok;
   const int my_block = (T * wave + E * g) >> 4;    // of this lane's scores
   // keys: piece 64 i + lane of the wave's T keys is lane's i-th
@@ -150,8 +152,8 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
     const int sp = __shfl(page, my_block);
     page_ok = sp >= 0;
     const uint32_t sph = (uint32_t)max(sp, 0) * (uint32_t)a.c.heads + kh;      // pages * heads < 2^32: see the host's check
-    ks = bf16_lo(a.c.ks[sph]) * a.scale_log2;
-    vs = bf16_lo(a.c.vs[sph]);
+    ks = a.c.ks[sph];
+    vs = a.c.vs[sph];
   };
   // Values: a wave's VR rows of the step, page by page, each row of a page a
   // power of two of pieces (16-entry blocks).  The bits of a piece's number
@@ -224,6 +226,7 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
   };
   int j0 = max(at_begin, rows.begin & ~(STEP - 1));
   if (a.window > 0 && rows.begin < rows.end) page = pages(j0);
+  page = checked(j0, page);
 
   // this lane's rows: queries (in the keys' order) and positions
   kv_bf16x8 q[Q_LDS ? 1 : NC][2 * KC];
@@ -269,7 +272,7 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
   if (j0 < at_end) {
     load_keys(j0, page);
     load_values(j0, page);
-    page_next = pages(j0 + STEP);
+    page_after = pages(j0 + STEP);
   }
   // one step; more: another one follows in this block
   auto step = [&](auto more_c) W4K_INLINE {
@@ -277,33 +280,42 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
     const int jw = j0 + T * wave, jl = jw + E * g;      // the wave's and this lane's first entry
     const bool whole = __all(page_ok) && jw + T - 1 <= all_hi && jw >= all_lo;
     const bool ok_now = page_ok;
-    const float ks_now = ks, vs_now = vs < kKvMinScale ? kKvMinScale : vs;   // 0 in a page never begun; NaN stays
     put_keys();
-    if constexpr (more) load_keys(j0 + STEP, page_next);
+    const float ks_now = bf16_lo(ks) * a.scale_log2, vs_page = bf16_lo(vs);
+    const float vs_now = vs_page < kKvMinScale ? kKvMinScale : vs_page;      // 0 in a page never begun; NaN stays
+    int page_next = 0;
+    if constexpr (more) {
+      page_next = checked(j0 + STEP, page_after);
+      page_after = pages(j0 + 2 * STEP);
+      load_keys(j0 + STEP, page_next);
+    }
     kv_f32x4 s[NC][NP];
 #pragma unroll
-    for (int t = 0; t < NP; ++t) {
+    for (int t = 0; t < NP; ++t)
 #pragma unroll
       for (int c = 0; c < NC; ++c) s[c][t] = kv_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    kv_bf16x8 qk[Q_LDS ? 2 : 1][NC][2];      // queries of two pieces: the next one's are read ahead
+    auto read_queries = [&](int k) W4K_INLINE {
 #pragma unroll
-      for (int k = 0; k < KC; ++k) {
-        const kv_u32x4 kk = stage[key_get[k] + 4 * t * KP];
-        const kv_bf16x8 a0 = kv_bf16_of8<TYPE>(kk.x, kk.y), a1 = kv_bf16_of8<TYPE>(kk.z, kk.w);
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          kv_bf16x8 b0, b1;
-          if constexpr (Q_LDS) {
-            b0 = __builtin_bit_cast(kv_bf16x8, s_q[c * 2 * KC + 2 * k][lane]);
-            b1 = __builtin_bit_cast(kv_bf16x8, s_q[c * 2 * KC + 2 * k + 1][lane]);
-          } else {
-            b0 = q[c][2 * k];
-            b1 = q[c][2 * k + 1];
+        for (int h = 0; h < 2; ++h)
+          qk[k % 2][c][h] = __builtin_bit_cast(kv_bf16x8, s_q[c * 2 * KC + 2 * k + h][lane]);
+    };
+    if constexpr (Q_LDS) read_queries(0);
+    kv_stream_operands<kKvSplitAhead, KC * NP>(
+        [&](int i) W4K_INLINE { return stage[key_get[i / NP] + 4 * (i % NP) * KP]; },
+        [&](int i, kv_u32x4 kk) W4K_INLINE {
+          const int k = i / NP, t = i % NP;
+          if constexpr (Q_LDS)
+            if (t == 0 && k + 1 < KC) read_queries(k + 1);
+          const kv_bf16x8 a0 = kv_bf16_of8<TYPE>(kk.x, kk.y), a1 = kv_bf16_of8<TYPE>(kk.z, kk.w);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            s[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, Q_LDS ? qk[k % 2][c][0] : q[c][2 * k], s[c][t], 0, 0, 0);
+            s[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, Q_LDS ? qk[k % 2][c][1] : q[c][2 * k + 1], s[c][t], 0, 0, 0);
           }
-          s[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, b0, s[c][t], 0, 0, 0);
-          s[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b1, s[c][t], 0, 0, 0);
-        }
-      }
-    }
+        });
     const float lv = __builtin_amdgcn_logf(vs_now), rv = __builtin_amdgcn_rcpf(vs_now);
     float top[NC], fade[NC];
     kv_tile_max<NC, NP>(s, lr, jl, ks_now, lv, whole, ok_now, top);
@@ -334,26 +346,28 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
     if constexpr (more) {
       load_values(j0 + STEP, page_next);
       page = page_next;
-      page_next = pages(j0 + 2 * STEP);
     }
     __syncthreads();
+    constexpr int VB = T / 16;               // blocks a tile
+    kv_f16x8 p[2][NC];                       // weights of two tiles: the next one's are read ahead
 #pragma unroll
-    for (int v = 0; v < W; ++v) {
-      __builtin_amdgcn_sched_barrier(0);      // operands of one tile at a time
-      kv_f16x8 p[NC];
+    for (int c = 0; c < NC; ++c) p[0][c] = __builtin_bit_cast(kv_f16x8, s_p[0][c][lane]);
+    kv_stream_operands<kKvSplitAhead, W * DW>(
+        [&](int i) W4K_INLINE {             // this lane's 8 entries of the row: half of a 16-byte unit
+          const int v = i / DW, d = i % DW;
+          return reinterpret_cast<const kv_u32x2*>(
+              &stage[(value_get ^ value_turn(VB * v)) + VB * v * VR + 16 * d])[g & 1];
+        },
+        [&](int i, kv_u32x2 vv) W4K_INLINE {
+          const int v = i / DW, d = i % DW;
+          if (d == 0 && v + 1 < W)
 #pragma unroll
-      for (int c = 0; c < NC; ++c) p[c] = __builtin_bit_cast(kv_f16x8, s_p[v][c][lane]);
-      constexpr int VB = T / 16;               // blocks a tile
+            for (int c = 0; c < NC; ++c) p[(v + 1) % 2][c] = __builtin_bit_cast(kv_f16x8, s_p[v + 1][c][lane]);
+          const kv_f16x8 av = kv_f16_of8<TYPE>(vv.x, vv.y);
 #pragma unroll
-      for (int d = 0; d < DW; ++d) {
-        // this lane's 8 entries of the row: half of a 16-byte unit
-        const kv_u32x2 vv = reinterpret_cast<const kv_u32x2*>(
-            &stage[(value_get ^ value_turn(VB * v)) + VB * v * VR + 16 * d])[g & 1];
-        const kv_f16x8 av = kv_f16_of8<TYPE>(vv.x, vv.y);
-#pragma unroll
-        for (int c = 0; c < NC; ++c) o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, p[c], o[c][d], 0, 0, 0);
-      }
-    }
+          for (int c = 0; c < NC; ++c)
+            o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, p[v % 2][c], o[c][d], 0, 0, 0);
+        });
   };
   for (; j0 + STEP < at_end; j0 += STEP) step(std::true_type{});
   if (j0 < at_end) step(std::false_type{});      // (none where nothing is attended: zeros)
