@@ -20,7 +20,8 @@ __device__ __forceinline__ int kv_length(int n) { return min(max(n, 0), kKvMaxLe
 // the columns and tokens of each.  The exclusive sums up to the block's first
 // request are a reduction over all earlier lengths (a few strided loads a
 // thread, from L2), so one launch does everything and no block waits for
-// another.
+// another.  Bound by its one launch and three dependent loads: 40 requests of
+// 248 columns 3.5 us, 701 of 956 columns with 13k new tokens 5.1 (2.7 MB).
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(kKvThreads) void kv_plan_kernel(const int32_t* __restrict__ ctx_lens,
                                                              const int32_t* __restrict__ new_lens,
@@ -101,12 +102,18 @@ __global__ __launch_bounds__(kKvThreads) void kv_plan_kernel(const int32_t* __re
 }
 
 // ---------------------------------------------------------------------------
-// append.  A block looks at `span` consecutive tokens for one cache head, keys
+// append.  Codes are nearest(x / scale), the scale a rule on the largest |x| of
+// the run (see kv_device.hpp), so a run is read for its maximum and then encoded;
+// a thread keeps the first four tokens it read, and short runs are read once.  A
+// block looks at `span` consecutive tokens for one cache head, keys
 // or values (grid y), and quantizes every run that begins among them: the
 // largest magnitude of the run (an integer maximum of bf16 bits), the scale,
 // then the codes.  A run lies in one page, so its threads alone write that page
 // and head.  A single run is the whole block's; several (single tokens of
 // many requests) go to the block's waves in turn, without barriers.
+// Bound: HBM for prompts, 3 bytes a number: 11.8k tokens, 8 heads of 128, 72 MB,
+// 23 us, 3.1 TB/s (a block waits for its maximum before it writes); the launch and
+// two dependent loads for tokens: 64 requests 5.9 us, 24 verify batches 5.1.
 // ---------------------------------------------------------------------------
 
 // Codes of four bf16 entries under factor f = 1 / scale (0 where the scale is NaN).

@@ -149,9 +149,13 @@ __device__ __forceinline__ void kv_tile_max(kv_f32x4 (&s)[NC][NP], const KvLaneR
   }
 }
 
-// The running maximum moves only when a row's logits exceed it by 8: weights
-// then stay at or below 2^8, far inside fp16, and most tiles leave the sums as
-// they are (a factor of exactly 1, also for the rows beside one that moves).
+// The running maximum moves only when a row's logits exceed it by 8, and most
+// tiles leave the sums as they are (a factor of exactly 1, also for the rows
+// beside one that moves).  Weights are held times 2^6 (sums and output alike, so
+// it divides out): at most 2^14, inside fp16's 65504, while entries of 2^-30 of the
+// largest weight still count (without the factor those below 2^-25 vanished:
+// a million of them beside one large entry are 3% of the answer).
+constexpr float kKvWeightLog2 = 6.0f;
 __device__ __forceinline__ float kv_new_max(float m, float top) { return top > m + 8.0f ? top : m; }
 
 // Weights under the maxima m (already the new ones); l *= fade, += the tile's sum.
@@ -161,7 +165,7 @@ __device__ __forceinline__ void kv_weights(kv_f32x4 (&s)[NC][NP], const KvLaneRo
                                            const float (&fade)[NC], float (&l)[NC], kv_f16x8 (&w)[NC][NP / 2]) {
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const float shift = lv - m[c];
+    const float shift = lv + kKvWeightLog2 - m[c];
     float p[4 * NP], sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4 * NP; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][e / 4][e % 4], ks, shift));

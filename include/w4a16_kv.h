@@ -123,14 +123,16 @@ size_t w4a16_kv_attention_workspace_bytes(int tokens, int requests, int max_new,
  * the cache entries 0 <= j <= pos and, with window > 0, j > pos - window.
  * Entry j lies in page block_table[r][j / P]; entries whose page is outside
  * the cache, or past the table's `width` columns, are not attended.  A row
- * without entries is 0.  (The cache needs at least one page.)  Rows of q and out outside every request are not
- * touched.
+ * without entries is 0.  Rows of q and out outside every request are not
+ * touched.  The cache needs at least one page.
  *   q    bf16 [T][HQ][D], token rows q_stride elements apart
  *   out  bf16 [T][HQ][D], dense
  * max_new and max_len bound the requests' n and seq_lens (the launch is sized
  * by them; rows past max_new stay unwritten and entries past max_len unread).
  * Softmax statistics and sums in fp32, weights rounded to fp16, keys, values
- * and queries exact.  Requests of n * HQ / H <= 64 rows take one form, whose rows
+ * and queries exact.  A weight is held times its page's value scale: beside
+ * values beyond about 10^6 the weights of a page of zeros (scale 2^-100) can
+ * underflow.  Requests of n * HQ / H <= 64 rows take one form, whose rows
  * depend on their own query, position and entries and on max_len alone: they
  * are bitwise equal in any batch and for any number of new tokens up to that
  * bound (a verify batch gives the rows of single-token calls).  Requests of more

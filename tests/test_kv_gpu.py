@@ -369,6 +369,40 @@ def test_one_request_of_fewer_tokens_than_its_bound(kind, D, G):
 
 
 @pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("D,G", [(64, 2), (128, 2), (256, 2)])
+@pytest.mark.parametrize("new", [1, 40])
+def test_many_small_weights_beside_a_large_one_count(kind, D, G, new):
+    """200000 entries of weight 1.3 * 2^-27 beside one of weight 1 whose value is 0: the answer is theirs alone.
+
+    A weight is rounded to fp16 as a multiple of 2^-24 after a factor of 2^6, so it is off by at most 2^-31, which is
+    2^-4 / 1.3 of these; the logits' own error ((D + 16) 2^-24 of 18.5) and the output's rounding add less than 2^-7."""
+    say(f"small weights {kind} D={D} G={G} new={new}")
+    n, page = 200001, 256
+    w = 1.3 * 2.0 ** -27
+    pages = -(-n // page)
+    k, v, ks, vs = w4.kv_cache(pages, 1, D, page, dtype=ref.TORCH[kind])
+    kv = torch.zeros((pages, 1, page, D))
+    kv[0, 0, 0, 0] = 64.0
+    k.copy_(kv.to(ref.TORCH[kind]))
+    kv.fill_(64.0)
+    kv[0, 0, 0] = 0.0
+    v.copy_(kv.swapaxes(2, 3).to(ref.TORCH[kind]))
+    ks.fill_(1.0 / 64), vs.fill_(1.0 / 64)
+    q = torch.zeros((new, G, D), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1.0
+    table = i32(np.random.default_rng(1).permutation(pages).reshape(1, pages)[:, :])
+    # (page 0 holds the large entry: it has to come first)
+    t = table.cpu().numpy()
+    t[0, int(np.argwhere(t[0] == 0)[0, 0])], t[0, 0] = t[0, 0], 0
+    out = w4.kv_attention(q, k, v, ks, vs, i32(t), i32([n]), i32([0, new]), new, max_len=n, scale=-math.log(w))
+    torch.cuda.synchronize()
+    others = n - new + np.arange(new, dtype=np.float64)         # entries beside the first that row i attends
+    want = np.broadcast_to((others * w / (1.0 + others * w))[:, None, None], (new, G, D))
+    err = np.abs(out.double().cpu().numpy() / want - 1.0).max()
+    assert err < 2.0 ** -4 / 1.3 + 2.0 ** -7, err
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
 def test_offsets_past_32_bits(kind):
     """A cache of over 4 GiB a tensor, the request's pages at its far end."""
     H, D, page, pages = 8, 128, 128, 40000       # 5.2 GB of codes in each tensor
