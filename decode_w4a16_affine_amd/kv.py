@@ -92,9 +92,14 @@ def _dense(*ts) -> None:
             raise ValueError("tensors must be contiguous")
 
 
+# the current stream's handle without a Stream object around it (0.1 us a call instead of 1.1), where torch has it
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _raw_stream(stream, dev: int) -> int:
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _current_stream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
