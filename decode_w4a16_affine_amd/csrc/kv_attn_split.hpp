@@ -79,7 +79,7 @@ constexpr int kKvGridRequests = 32768;             // requests on the grid's y a
 
 // Waves per SIMD that the registers have to allow: what they do without spilling
 // (a reload of a spilled register would wait for the loads in flight).
-constexpr int kv_split_occupancy(int D, int NC) { return D == 256 || NC == 2 ? 2 : D == 128 ? 3 : 4; }
+constexpr int kv_split_occupancy(int D, int NC) { return D == 256 ? 2 : D == 128 || NC == 2 ? 3 : 4; }
 
 template <int D, int TYPE, int NC>
 __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) void kv_split_kernel(
@@ -87,7 +87,11 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
   constexpr int W = kKvSplitWaves;
   constexpr int T = kKvSplitTile, E = T / 4, STEP = W * T;
   constexpr int NP = T / 16;                       // pieces of scores
-  constexpr bool Q_LDS = NC * D >= 512;            // queries that would take 64 registers stay in LDS
+  // Queries stay in LDS where a third wave a SIMD, or the products' operands, need
+  // their registers (16 requests of 16 tokens, 4 query heads of 128: 71 us instead of
+  // 79); with D = 256 there is room to read those of the next piece ahead.
+  constexpr bool Q_LDS = NC == 2 && D >= 128;
+  constexpr int QB = D == 256 ? 2 : 1;             // pieces of queries in registers
   constexpr int KC = D / 64;                       // 16-byte pieces of a key a lane multiplies
   constexpr int DW = D / 16 / W;                   // 16-row pieces of the output a wave owns
   constexpr int LD = T * D / (16 * kWave);         // 16-byte loads a lane and step, keys and values each
@@ -305,26 +309,26 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
     for (int t = 0; t < NP; ++t)
 #pragma unroll
       for (int c = 0; c < NC; ++c) s[c][t] = kv_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    kv_bf16x8 qk[Q_LDS ? 2 : 1][NC][2];      // queries of two pieces: the next one's are read ahead
+    kv_bf16x8 qk[Q_LDS ? QB : 1][NC][2];
     auto read_queries = [&](int k) W4K_INLINE {
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          qk[k % 2][c][h] = __builtin_bit_cast(kv_bf16x8, s_q[c * 2 * KC + 2 * k + h][lane]);
+          qk[k % QB][c][h] = __builtin_bit_cast(kv_bf16x8, s_q[c * 2 * KC + 2 * k + h][lane]);
     };
-    if constexpr (Q_LDS) read_queries(0);
+    if constexpr (Q_LDS && QB == 2) read_queries(0);
     kv_stream_operands<kKvSplitAhead, KC * NP>(
         [&](int i) W4K_INLINE { return stage[key_get[i / NP] + 4 * (i % NP) * KP]; },
         [&](int i, kv_u32x4 kk) W4K_INLINE {
           const int k = i / NP, t = i % NP;
           if constexpr (Q_LDS)
-            if (t == 0 && k + 1 < KC) read_queries(k + 1);
+            if (t == 0 && k + QB - 1 < KC) read_queries(k + QB - 1);
           const kv_bf16x8 a0 = kv_bf16_of8<TYPE>(kk.x, kk.y), a1 = kv_bf16_of8<TYPE>(kk.z, kk.w);
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            s[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, Q_LDS ? qk[k % 2][c][0] : q[c][2 * k], s[c][t], 0, 0, 0);
-            s[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, Q_LDS ? qk[k % 2][c][1] : q[c][2 * k + 1], s[c][t], 0, 0, 0);
+            s[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, Q_LDS ? qk[k % QB][c][0] : q[c][2 * k], s[c][t], 0, 0, 0);
+            s[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, Q_LDS ? qk[k % QB][c][1] : q[c][2 * k + 1], s[c][t], 0, 0, 0);
           }
         });
     const float lv = __builtin_amdgcn_logf(vs_now), rv = __builtin_amdgcn_rcpf(vs_now);
