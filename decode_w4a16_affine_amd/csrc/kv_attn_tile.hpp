@@ -77,7 +77,8 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
   constexpr int NP = 4 / HS;              // 16-entry pieces of a tile that a wave scores
   constexpr int DT = D / 16, DH = DT / HS;  // 16-row pieces of the output, and those a wave owns
   constexpr int KU = 4 * KC, VU = DT;     // 64-lane pieces of a tile's keys and values
-  constexpr int KL = (KU + W - 1) / W, VL = (VU + W - 1) / W;   // of which a wave loads
+  constexpr int KL = KU / W, VL = VU / W;   // of which a wave loads
+  static_assert(KU % W == 0 && VU % W == 0 && KC % KL == 0, "each wave loads the same");
   constexpr int NB = HS == 1 ? 2 : 1;       // buffers
   constexpr int AHEAD = D == 256 ? 3 : 4;   // operands read ahead of their products, as registers allow
   __shared__ kv_u32x4 s_k[NB][KU * 2 * kWave];      // [piece t][sum step][lane]
@@ -155,25 +156,23 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
     return Pages{j0 + 16 * (x >> 2) < rows.end && p.k >= 0 && p.k < a.c.pages ? p.k : -1,
                  j0 + 16 * g < rows.end && p.v >= 0 && p.v < a.c.pages ? p.v : -1};
   };
+  // What of an address does not change over the tiles is one number a lane; a
+  // wave's units of keys lie within one piece of 16 entries (KL divides KC)
   const uint32_t head_bytes = (uint32_t)D << shift;      // one head's codes of a page
-  const uint64_t page_bytes = (uint64_t)a.c.heads * head_bytes;
+  const uint32_t page_bytes = (uint32_t)a.c.heads * head_bytes;      // <= 2^10 * 2^16
+  const uint8_t* const k_lane = a.c.k + (size_t)kh * head_bytes + 4 * (wave * KL / KC) * D + 64 * (wave * KL % KC) +
+                                (x & 3) * D + 16 * g;
+  const uint8_t* const v_lane = a.c.v + (size_t)kh * head_bytes + ((16 * wave * VL + x) << shift);
   kv_u32x4 kc[KL], vc[VL];
   auto load_keys = [&](int j0, int page) W4K_INLINE {
-    const uint8_t* ka = a.c.k + (size_t)kh * head_bytes + max(page, 0) * page_bytes +
-                        (((j0 + 16 * (x >> 2)) & (P - 1)) + (x & 3)) * D + 16 * g;
+    const uint8_t* ka = k_lane + (uint64_t)(uint32_t)max(page, 0) * page_bytes + ((j0 + 16 * (x >> 2)) & (P - 1)) * D;
 #pragma unroll
-    for (int i = 0; i < KL; ++i) {
-      const int unit = KU < W ? wave & (KU - 1) : wave * KL + i;       // (few units: two waves load the same)
-      kc[i] = *reinterpret_cast<const kv_u32x4*>(ka + 4 * (unit / KC) * D + 64 * (unit % KC));
-    }
+    for (int i = 0; i < KL; ++i) kc[i] = *reinterpret_cast<const kv_u32x4*>(ka + 64 * i);
   };
   auto load_values = [&](int j0, int page) W4K_INLINE {
-    const uint8_t* va = a.c.v + (size_t)kh * head_bytes + max(page, 0) * page_bytes + ((j0 + 16 * g) & (P - 1));
+    const uint8_t* va = v_lane + (uint64_t)(uint32_t)max(page, 0) * page_bytes + ((j0 + 16 * g) & (P - 1));
 #pragma unroll
-    for (int i = 0; i < VL; ++i) {
-      const int unit = VU < W ? wave & (VU - 1) : wave * VL + i;
-      vc[i] = *reinterpret_cast<const kv_u32x4*>(va + (size_t)(16 * unit + x) * P);
-    }
+    for (int i = 0; i < VL; ++i) vc[i] = *reinterpret_cast<const kv_u32x4*>(va + (16 * i << shift));
   };
   float ks, vs;
   auto load_scales = [&](int page) W4K_INLINE {
@@ -184,7 +183,7 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
   auto put_keys = [&](int b) W4K_INLINE {
 #pragma unroll
     for (int i = 0; i < KL; ++i) {
-      const int unit = KU < W ? wave & (KU - 1) : wave * KL + i;
+      const int unit = wave * KL + i;
       s_k[b][unit * 2 * kWave + lane] = __builtin_bit_cast(kv_u32x4, kv_bf16_of8<TYPE>(kc[i].x, kc[i].y));
       s_k[b][(unit * 2 + 1) * kWave + lane] = __builtin_bit_cast(kv_u32x4, kv_bf16_of8<TYPE>(kc[i].z, kc[i].w));
     }
@@ -200,7 +199,7 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
     }
 #pragma unroll
     for (int i = 0; i < VL; ++i) {
-      const int unit = VU < W ? wave & (VU - 1) : wave * VL + i;
+      const int unit = wave * VL + i;
       s_v[b][unit * 2 * kWave + lane] = __builtin_bit_cast(kv_u32x4, kv_f16_of8<TYPE>(vc[i].x, vc[i].y));
       s_v[b][(unit * 2 + 1) * kWave + lane] = __builtin_bit_cast(kv_u32x4, kv_f16_of8<TYPE>(vc[i].z, vc[i].w));
     }

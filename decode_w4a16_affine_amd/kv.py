@@ -168,10 +168,7 @@ def _rows(t, heads, dim, name):
 def w4a16_kv_plan(ctx_lens, new_lens, free_pages, block_table, seq_lens, token_start, slot_map, pages_used, page: int,
                   stream=None) -> None:
     """Block tables and slot maps of a step from request lengths (block_table [R, width] is updated in place)."""
-    R = _vector(ctx_lens, "ctx_lens")
-    _vector(new_lens, "new_lens", R)
-    num_free = _vector(free_pages, "free_pages")
-    width = _table(block_table, R)
+    R, num_free, width = _plan_inputs(ctx_lens, new_lens, free_pages, block_table)
     _vector(seq_lens, "seq_lens", R)
     _vector(token_start, "token_start", R + 1)
     tokens = _vector(slot_map, "slot_map")
@@ -182,6 +179,14 @@ def w4a16_kv_plan(ctx_lens, new_lens, free_pages, block_table, seq_lens, token_s
                                   block_table.data_ptr(), width, seq_lens.data_ptr(), token_start.data_ptr(),
                                   slot_map.data_ptr(), pages_used.data_ptr(), R, tokens, page,
                                   _raw_stream(stream, dev)), "w4a16_kv_plan")
+
+
+def _plan_inputs(ctx_lens, new_lens, free_pages, block_table):
+    """Requests, free pages and table width of a plan's inputs, types and shapes checked."""
+    R = _vector(ctx_lens, "ctx_lens")
+    _vector(new_lens, "new_lens", R)
+    num_free = _vector(free_pages, "free_pages")
+    return R, num_free, _table(block_table, R)
 
 
 def w4a16_kv_append(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, stream=None) -> None:
@@ -253,9 +258,15 @@ def w4a16_kv_dequant(k_cache, v_cache, k_scales, v_scales, pages, k_out, v_out, 
     _dtype(v_out, torch.float32, "v_out")
     _shape(k_out, (n, c.heads, c.page, c.dim), "k_out")
     _shape(v_out, (n, c.heads, c.page, c.dim), "v_out")
-    dev = _same_gpu(k_cache, v_cache, k_scales, v_scales, pages, k_out, v_out)
-    _dense(k_cache, v_cache, k_scales, v_scales, pages, k_out, v_out)
-    _check(kv_lib().w4a16_kv_dequant(ctypes.byref(c), pages.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(),
+    _same_gpu(k_cache, k_out, v_out)
+    _dense(k_out, v_out)
+    _dequant(c, (k_cache, v_cache, k_scales, v_scales, pages), n, k_out, v_out, stream)
+
+
+def _dequant(c, inputs, n, k_out, v_out, stream):
+    dev = _same_gpu(*inputs)
+    _dense(*inputs)
+    _check(kv_lib().w4a16_kv_dequant(ctypes.byref(c), inputs[4].data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(),
                                      _raw_stream(stream, dev)), "w4a16_kv_dequant")
 
 
@@ -271,12 +282,16 @@ def kv_cache(pages: int, heads: int, dim: int, page: int = 64, dtype=torch.int8,
 
 def kv_plan(ctx_lens, new_lens, free_pages, block_table, tokens: int, page: int, stream=None):
     """(seq_lens, token_start, slot_map [tokens], pages_used); block_table is updated in place."""
-    R = ctx_lens.shape[0]
-    seq_lens, token_start, slot_map, pages_used = torch.empty(
-        (2 * R + tokens + 2,), dtype=torch.int32, device=ctx_lens.device).split((R, R + 1, tokens, 1))
-    w4a16_kv_plan(ctx_lens, new_lens, free_pages, block_table, seq_lens, token_start, slot_map, pages_used, page,
-                  stream=stream)
-    return seq_lens, token_start, slot_map, pages_used
+    R, num_free, width = _plan_inputs(ctx_lens, new_lens, free_pages, block_table)
+    dev = _same_gpu(ctx_lens, new_lens, free_pages, block_table)
+    _dense(ctx_lens, new_lens, free_pages, block_table)
+    out = ctx_lens.new_empty(2 * R + tokens + 2)      # (one allocation: its parts need no checks of their own)
+    at = out.data_ptr()
+    _check(kv_lib().w4a16_kv_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), num_free,
+                                  block_table.data_ptr(), width, at, at + 4 * R, at + 4 * (2 * R + 1),
+                                  at + 4 * (2 * R + 1 + tokens), R, tokens, page, _raw_stream(stream, dev)),
+           "w4a16_kv_plan")
+    return out.split((R, R + 1, tokens, 1))
 
 
 def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, max_new: int,
@@ -287,15 +302,16 @@ def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens,
         max_len = block_table.shape[1] * c.page
     need = kv_lib().w4a16_kv_attention_workspace_bytes(q.shape[0], seq_lens.shape[0], max_new, max_len, window,
                                                        q.shape[1], ctypes.byref(c))
-    ws = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
+    ws = q.new_empty(need, dtype=torch.uint8) if need else None
     _attention(c, (k_cache, v_cache, k_scales, v_scales), q, block_table, seq_lens, token_start, out, ws, max_new,
                max_len, scale, window, stream)
     return out
 
 
 def kv_dequant(k_cache, v_cache, k_scales, v_scales, pages, stream=None):
-    pages_heads, (page, dim) = (pages.shape[0], k_cache.shape[1]), k_cache.shape[2:]
-    k_out = torch.empty((*pages_heads, page, dim), dtype=torch.float32, device=k_cache.device)
+    c = _cache(k_cache, v_cache, k_scales, v_scales)
+    n = _vector(pages, "pages")
+    k_out = k_scales.new_empty((n, c.heads, c.page, c.dim), dtype=torch.float32)
     v_out = torch.empty_like(k_out)
-    w4a16_kv_dequant(k_cache, v_cache, k_scales, v_scales, pages, k_out, v_out, stream=stream)
+    _dequant(c, (k_cache, v_cache, k_scales, v_scales, pages), n, k_out, v_out, stream)
     return k_out, v_out
