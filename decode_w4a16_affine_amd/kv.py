@@ -219,35 +219,38 @@ def w4a16_kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq
     the block table's columns hold); scale None: 1 / sqrt(D); window 0: no
     window; workspace: a uint8 device tensor of at least
     w4a16_kv_attention_workspace_bytes bytes, or None where that is 0."""
-    _attention(_cache(k_cache, v_cache, k_scales, v_scales), (k_cache, v_cache, k_scales, v_scales), q, block_table,
-               seq_lens, token_start, out, workspace, max_new, max_len, scale, window, stream)
-
-
-def _attention(c, cache, q, block_table, seq_lens, token_start, out, workspace, max_new, max_len, scale, window, stream):
-    tokens, q_stride = _rows(q, None, c.dim, "q")
-    R = _vector(seq_lens, "seq_lens")
-    _vector(token_start, "token_start", R + 1)
-    width = _table(block_table, R)
+    c = _cache(k_cache, v_cache, k_scales, v_scales)
+    inputs = _attention_inputs(c, q, block_table, seq_lens, token_start)
     if out.dtype != torch.bfloat16:
         _dtype(out, torch.bfloat16, "out")
     if out.shape != q.shape:
         _shape(out, q.shape, "out")
-    if max_len is None:
-        max_len = width * c.page
-    if scale is None:
-        scale = 1.0 / math.sqrt(c.dim)
-    ws = bytes_ = 0
     if workspace is not None:
         _dtype(workspace, torch.uint8, "workspace")
         _same_gpu(out, workspace)
         _dense(workspace)
-        ws, bytes_ = workspace.data_ptr(), workspace.numel()
-    dev = _same_gpu(*cache, block_table, seq_lens, token_start, out, q)
-    _dense(*cache, block_table, seq_lens, token_start, out)
-    _check(kv_lib().w4a16_kv_attention(q.data_ptr(), q_stride, ctypes.byref(c), block_table.data_ptr(), width,
-                                       seq_lens.data_ptr(), token_start.data_ptr(), out.data_ptr(), scale, window,
-                                       tokens, R, max_new, max_len, q.shape[1], ws, bytes_,
-                                       _raw_stream(stream, dev)), "w4a16_kv_attention")
+    dev = _same_gpu(k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, out, q)
+    _dense(k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, out)
+    if max_len is None:
+        max_len = inputs[3] * c.page
+    _attention(ctypes.byref(c), inputs, q, block_table, seq_lens, token_start, out, workspace, max_new, max_len,
+               1.0 / math.sqrt(c.dim) if scale is None else scale, window, _raw_stream(stream, dev))
+
+
+def _attention_inputs(c, q, block_table, seq_lens, token_start):
+    """Tokens, their stride, requests and table width of an attention's inputs, types and shapes checked."""
+    tokens, q_stride = _rows(q, None, c.dim, "q")
+    R = _vector(seq_lens, "seq_lens")
+    _vector(token_start, "token_start", R + 1)
+    return tokens, q_stride, R, _table(block_table, R)
+
+
+def _attention(c, inputs, q, block_table, seq_lens, token_start, out, workspace, max_new, max_len, scale, window, stream):
+    tokens, q_stride, R, width = inputs
+    ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    _check(kv_lib().w4a16_kv_attention(q.data_ptr(), q_stride, c, block_table.data_ptr(), width, seq_lens.data_ptr(),
+                                       token_start.data_ptr(), out.data_ptr(), scale, window, tokens, R, max_new,
+                                       max_len, q.shape[1], ws, ws_bytes, stream), "w4a16_kv_attention")
 
 
 def w4a16_kv_dequant(k_cache, v_cache, k_scales, v_scales, pages, k_out, v_out, stream=None) -> None:
@@ -296,15 +299,19 @@ def kv_plan(ctx_lens, new_lens, free_pages, block_table, tokens: int, page: int,
 
 def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, max_new: int,
                  max_len: int = None, scale: float = None, window: int = 0, stream=None):
+    """Attention of the step's queries: a new out [T, HQ, D] (see w4a16_kv_attention)."""
     c = _cache(k_cache, v_cache, k_scales, v_scales)
-    out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    inputs = tokens, _, R, width = _attention_inputs(c, q, block_table, seq_lens, token_start)
+    dev = _same_gpu(k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, q)
+    _dense(k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start)
     if max_len is None:
-        max_len = block_table.shape[1] * c.page
-    need = kv_lib().w4a16_kv_attention_workspace_bytes(q.shape[0], seq_lens.shape[0], max_new, max_len, window,
-                                                       q.shape[1], ctypes.byref(c))
-    ws = q.new_empty(need, dtype=torch.uint8) if need else None
-    _attention(c, (k_cache, v_cache, k_scales, v_scales), q, block_table, seq_lens, token_start, out, ws, max_new,
-               max_len, scale, window, stream)
+        max_len = width * c.page
+    ref = ctypes.byref(c)
+    out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    need = kv_lib().w4a16_kv_attention_workspace_bytes(tokens, R, max_new, max_len, window, q.shape[1], ref)
+    _attention(ref, inputs, q, block_table, seq_lens, token_start, out,
+               q.new_empty(need, dtype=torch.uint8) if need else None, max_new, max_len,
+               1.0 / math.sqrt(c.dim) if scale is None else scale, window, _raw_stream(stream, dev))
     return out
 
 
