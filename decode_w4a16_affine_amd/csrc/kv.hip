@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "kv_device.hpp"
 
 namespace w4k {
@@ -510,11 +512,29 @@ KvAttnArgs attention_args(const w4a16_kv_cache_t* cache, int tokens, int request
   const long long in_window = in_chunks((long long)window + a.split_tokens - 2) + 1;
   if (window > 0 && in_window < chunks) chunks = in_window;
   a.chunks = chunks > 1 ? (int)chunks : 1;
+  // Where prompts bring fewer workgroups than the card holds (512, two a CU), the
+  // cache is cut into parts that share their rows: their tiles run side by side, and
+  // a join adds the parts.  A part has 8 tiles at least: each row and part costs
+  // D + 2 floats written and read again, and the join 4 us.
+  a.parts = 1;
+  a.part = kKvMaxLen + kKvTile;      // all
+  if (requests > 0 && (int64_t)max_new * a.group > kKvSplitRows) {
+    const int tile_tokens = kv_tile_rows(cache->dim, cache->type) / a.group;
+    const int64_t workgroups = (int64_t)(tokens / tile_tokens + requests) * cache->heads;
+    const int64_t reach = (int64_t)window + tile_tokens - 1;      // entries of a window's workgroup
+    const int64_t span = window > 0 && reach < max_len ? reach : max_len;
+    const int64_t wanted = std::min<int64_t>(512 / workgroups, span / (8 * kKvTile));
+    if (wanted > 1) {
+      a.part = (int)((span + wanted * kKvTile - 1) / (wanted * kKvTile)) * kKvTile;
+      // (a window's entries may begin inside a part)
+      a.parts = (int)std::min<int64_t>((max_len + a.part - 1) / a.part, (span + a.part - 2) / a.part + 1);
+    }
+  }
   return a;
 }
 
 size_t attention_workspace(const KvAttnArgs& a, int dim) {
-  return a.split && a.chunks > 1 ? kv_partials(a) * (dim + kKvPartStats) * sizeof(float) : 0;
+  return kv_workspace_floats(a, dim) * sizeof(float);
 }
 
 }  // namespace

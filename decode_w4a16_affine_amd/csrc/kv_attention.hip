@@ -13,6 +13,8 @@ hipError_t kv_attention_typed(const KvAttnArgs& a, void* workspace, hipStream_t 
   constexpr int D = W4K_D;
   float* part_o = static_cast<float*>(workspace);
   float* part_ml = part_o + kv_partials(a) * D;
+  float* tile_o = part_o + kv_split_floats(a, D);
+  float* tile_ml = tile_o + kv_tile_partials(a) * D;
   const int rows = a.split_tokens * a.group;
   const unsigned ry = a.requests < kKvGridRequests ? a.requests : kKvGridRequests;
   const unsigned rz = (a.requests + kKvGridRequests - 1) / kKvGridRequests;
@@ -32,8 +34,14 @@ hipError_t kv_attention_typed(const KvAttnArgs& a, void* workspace, hipStream_t 
   }
   if ((int64_t)a.max_new * a.group > kKvSplitRows) {
     const int64_t tiles = a.tokens / (kv_tile_rows(D, TYPE) / a.group) + a.requests;
-    hipLaunchKernelGGL((kv_tile_kernel<D, TYPE>), dim3((unsigned)(tiles * a.c.heads)),
-                       dim3(kv_tile_waves(D, TYPE) * kWave), 0, st, a);
+    hipLaunchKernelGGL((kv_tile_kernel<D, TYPE>), dim3((unsigned)(tiles * a.c.heads), a.parts),
+                       dim3(kv_tile_waves(D, TYPE) * kWave), 0, st, a, tile_o, tile_ml);
+    if (a.parts > 1) {
+      constexpr int rows_a_block = kKvJoinThreads / (D / 4);
+      hipLaunchKernelGGL((kv_tile_join_kernel<D, TYPE>),
+                         dim3((unsigned)(((int64_t)a.tokens * a.q_heads + rows_a_block - 1) / rows_a_block)),
+                         dim3(kKvJoinThreads), 0, st, a, tile_o, tile_ml);
+    }
   }
   return hipGetLastError();
 }

@@ -20,6 +20,7 @@ typedef uint32_t kv_u32x2 __attribute__((ext_vector_type(2)));
 #define W4K_INLINE __attribute__((always_inline))
 
 constexpr float kKvNone = -3e38f;     // running maximum before any entry
+constexpr int kKvJoinThreads = 256;   // of the kernels that join partial results
 
 // 16 codes from the cache, past the caches' reuse order: the cache streams
 // through once, and whole lines fetched this way reach 5.9 TB/s where ordinary
@@ -91,6 +92,16 @@ __device__ __forceinline__ KvRows kv_rows_of(const KvAttnArgs& a, int r, int i0,
   k.end = (int)min((long long)min(hi + 1, a.max_len), held);
   k.begin = a.window > 0 ? max(0, lo - a.window + 1) : 0;
   return k;
+}
+
+// The parts of the cache (a.part entries each) that rows of the tile form attend.
+struct KvParts {
+  int first, count;
+};
+__device__ __forceinline__ KvParts kv_parts_of(const KvAttnArgs& a, const KvRows& rows) {
+  if (a.parts <= 1) return KvParts{0, 1};
+  const int first = rows.begin / a.part;
+  return KvParts{first, max(rows.end - 1, rows.begin) / a.part - first + 1};
 }
 
 // One lane's part of the rows it shares: entries lo .. hi of the cache.

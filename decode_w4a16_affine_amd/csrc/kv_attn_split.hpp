@@ -426,8 +426,6 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
 // D / 4 threads hold four elements each of one slice of the chunks, the slices'
 // sums are added in slice order.  Rows whose group lies in one chunk are
 // already written.
-constexpr int kKvJoinThreads = 256;
-
 template <int D, int NC>
 __global__ __launch_bounds__(kKvJoinThreads) void kv_join_kernel(KvAttnArgs a, const float* part_o,
                                                                  const float* part_ml) {

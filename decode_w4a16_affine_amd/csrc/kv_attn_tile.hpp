@@ -43,14 +43,6 @@
 
 namespace w4k {
 
-constexpr int kKvTile = 64;                                        // cache entries at once
-constexpr int kKvTileCols = 2;                                     // 16-row pieces a pair of waves
-// Waves that share 32 rows: two for D = 256, where the output of 32 rows alone
-// would take 128 registers of a wave.
-constexpr int kv_tile_share(int D) { return D == 256 ? 2 : 1; }
-constexpr int kv_tile_waves(int D, int type) { return D == 256 && type == W4A16_KV_INT8 ? 8 : 4; }
-constexpr int kv_tile_rows(int D, int type) { return kv_tile_waves(D, type) / kv_tile_share(D) * kKvTileCols * 16; }
-
 // Workgroup u -> request and first token.  Request r owns the numbers from
 // floor(token_start[r] / TT) + r on: at least ceil(n / TT) of them, and they
 // grow with r, so a search finds the owner without a prefix sum of tiles.
@@ -71,7 +63,9 @@ __device__ __forceinline__ int kv_tile_owner(const int32_t* token_start, int req
 }
 
 template <int D, int TYPE>
-__global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_kernel(KvAttnArgs a) {
+__global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_kernel(KvAttnArgs a,
+                                                                                             float* part_o,
+                                                                                             float* part_ml) {
   constexpr int NC = kKvTileCols, W = kv_tile_waves(D, TYPE), HS = kv_tile_share(D);
   constexpr int KC = D / 64;              // 16-byte pieces of a key a lane multiplies
   constexpr int NP = 4 / HS;              // 16-entry pieces of a tile that a wave scores
@@ -104,6 +98,12 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
   const int live = here * a.group;                  // and rows
   const KvRows rows = kv_rows_of(a, r, i0, i0 + here - 1);
   const int shift = a.c.page_shift, P = 1 << shift;
+  // the part of the cache (all of it if a.parts is 1) that this workgroup walks
+  const KvParts parts = kv_parts_of(a, rows);
+  const int part = blockIdx.y;
+  if (part >= parts.count) return;
+  const int part_begin = (parts.first + part) * a.part;
+  const int part_end = (int)min((long long)part_begin + a.part, (long long)rows.end);
 
   // this pair of waves' rows
   const int wrow = wave / HS * NC * 16;
@@ -205,10 +205,10 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
     }
   };
 
-  int j0 = rows.begin & ~(kKvTile - 1);
+  int j0 = max(part_begin, rows.begin & ~(kKvTile - 1));
   int page = -1;                  // of this tile's values
   Pages next = {-1, -1}, after = {-1, -1};
-  if (j0 < rows.end) {
+  if (j0 < part_end) {
     const Pages first = checked(j0, pages(j0));
     next = checked(j0 + kKvTile, pages(j0 + kKvTile));
     after = pages(j0 + 2 * kKvTile);
@@ -223,7 +223,7 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
       load_keys(j0 + kKvTile, next.k);
   }
   __syncthreads();
-  for (int b = 0; j0 < rows.end; j0 += kKvTile, b ^= NB - 1) {
+  for (int b = 0; j0 < part_end; j0 += kKvTile, b ^= NB - 1) {
     const bool active = j0 <= any_hi && j0 + kKvTile > any_lo;      // of this pair's rows
     const int jl = j0 + 16 * g + 8 * half;       // this lane's first entry
     const bool ok = page >= 0;
@@ -323,11 +323,61 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     if (out_at[c] < 0) continue;
-    const float inverse = kv_inverse(HS == 1 ? l[c] : s_m[wave & ~1][16 * c + x] + s_m[wave | 1][16 * c + x]);
-    uint16_t* out = a.out + (size_t)out_at[c] * D + 16 * DH * half + 4 * g;
+    const float sum = HS == 1 ? l[c] : s_m[wave & ~1][16 * c + x] + s_m[wave | 1][16 * c + x];
+    const int d0 = 16 * DH * half + 4 * g;
+    if (parts.count == 1) {
+      const float inverse = kv_inverse(sum);
+      uint16_t* out = a.out + (size_t)out_at[c] * D + d0;
 #pragma unroll
-    for (int d = 0; d < DH; ++d) kv_store4(out + 16 * d, o[c][d], inverse);
+      for (int d = 0; d < DH; ++d) kv_store4(out + 16 * d, o[c][d], inverse);
+    } else {
+      const size_t at = (size_t)out_at[c] * a.parts + part;
+#pragma unroll
+      for (int d = 0; d < DH; ++d) *reinterpret_cast<kv_f32x4*>(part_o + at * D + d0 + 16 * d) = o[c][d];
+      if (g == 0 && half == 0) {
+        part_ml[kKvTileStats * at] = m[c];
+        part_ml[kKvTileStats * at + 1] = sum;
+      }
+    }
   }
+}
+
+// Joins the parts of a row in their order: D / 4 threads a row.  Rows that lie
+// in one part are written already, those of requests of few rows are not the
+// tiles'.
+template <int D, int TYPE>
+__global__ __launch_bounds__(kKvJoinThreads) void kv_tile_join_kernel(KvAttnArgs a, const float* part_o,
+                                                                      const float* part_ml) {
+  const int row = blockIdx.x * (kKvJoinThreads / (D / 4)) + threadIdx.x / (D / 4);      // of `out`
+  const int d = 4 * (threadIdx.x % (D / 4));
+  const int t = row / a.q_heads;
+  if (t >= a.tokens || t < a.token_start[0]) return;
+  int r = 0;                                                    // the last request that begins at or before t
+  for (int count = a.requests; count > 1;) {
+    const int step = count >> 1;
+    if (a.token_start[r + step] <= t) r += step;
+    count -= step;
+  }
+  const int n = a.token_start[r + 1] - a.token_start[r], i = t - a.token_start[r];
+  if (a.token_start[r] < 0 || i >= min(n, a.max_new) || (a.split && n * a.group <= kKvSplitRows)) return;
+  // the rows of its workgroup
+  const int tt = kv_token_of(a, kv_tile_rows(D, TYPE)), i0 = i / tt * tt;
+  const int here = min(tt, min(min(n, a.max_new), a.tokens - a.token_start[r]) - i0);
+  const KvParts parts = kv_parts_of(a, kv_rows_of(a, r, i0, i0 + here - 1));
+  if (parts.count <= 1) return;
+  const size_t at = (size_t)row * a.parts;
+  float top = kKvNone;
+  for (int p = 0; p < parts.count; ++p) top = fmaxf(top, part_ml[kKvTileStats * (at + p)]);
+  float sum_l = 0.0f;
+  kv_f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int p = 0; p < parts.count; ++p) {
+    const float f = __builtin_amdgcn_exp2f(part_ml[kKvTileStats * (at + p)] - top);
+    const kv_f32x4 v = *reinterpret_cast<const kv_f32x4*>(part_o + (at + p) * D + d);
+    sum_l = __builtin_fmaf(part_ml[kKvTileStats * (at + p) + 1], f, sum_l);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(v[e], f, sum[e]);
+  }
+  kv_store4(a.out + (size_t)row * D + d, sum, kv_inverse(sum_l));
 }
 
 }  // namespace w4k

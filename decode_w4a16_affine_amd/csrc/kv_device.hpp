@@ -79,6 +79,8 @@ struct KvAttnArgs {
   // requests of few rows: log2 of the entries a chunk, chunks a row at most, row
   // groups a cache head, new tokens a request at most
   int chunk_shift, chunks, row_groups, split_tokens;
+  // requests of many: parts of the cache that a row's workgroups share, entries a part
+  int parts, part;
 };
 
 // Launchers (kv_attention.hip, once per head size).
@@ -102,7 +104,29 @@ constexpr int kKvSplitRows = 64;      // requests of at most this many rows a ca
 // maximum and four waves' sums).
 constexpr int kKvPartStats = 5;
 inline size_t kv_partials(const KvAttnArgs& a) {
-  return (size_t)a.requests * a.c.heads * a.split_tokens * a.group * a.chunks;
+  return a.split && a.chunks > 1 ? (size_t)a.requests * a.c.heads * a.split_tokens * a.group * a.chunks : 0;
+}
+
+// The tile form: waves of a workgroup, of which `share` take the same 32 rows
+// (two for D = 256, where the output of 32 rows alone would take 128 registers of a
+// wave), and its rows.  A row and part's partial result: D floats, maximum, sum.
+constexpr int kKvTile = 64;           // cache entries at once
+constexpr int kKvTileCols = 2;        // 16-row pieces a wave (or the waves that share rows)
+constexpr int kKvTileStats = 2;
+constexpr int kv_tile_share(int D) { return D == 256 ? 2 : 1; }
+constexpr int kv_tile_waves(int D, int type) { return D == 256 && type == W4A16_KV_INT8 ? 8 : 4; }
+constexpr int kv_tile_rows(int D, int type) { return kv_tile_waves(D, type) / kv_tile_share(D) * kKvTileCols * 16; }
+inline size_t kv_tile_partials(const KvAttnArgs& a) {
+  return a.parts > 1 ? (size_t)a.tokens * a.q_heads * a.parts : 0;
+}
+
+// The workspace, in floats: the split form's results, their statistics (up to a
+// multiple of 16 bytes), the tile form's results and statistics.
+inline size_t kv_split_floats(const KvAttnArgs& a, int D) {
+  return kv_partials(a) * D + (kv_partials(a) * kKvPartStats + 3) / 4 * 4;
+}
+inline size_t kv_workspace_floats(const KvAttnArgs& a, int D) {
+  return kv_split_floats(a, D) + kv_tile_partials(a) * (D + kKvTileStats);
 }
 
 }  // namespace w4k

@@ -288,6 +288,27 @@ def test_attention_with_a_window(kind, H, G, D, page, lens, news, window):
 
 
 @pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("H,G,D,page,lens,news,window,gone", [
+    (1, 8, 64, 64, [3000], [70], 0, None),                  # few tokens behind a long cache
+    (2, 4, 128, 32, [2100, 1500, 40, 0, 1999], [40, 300, 3, 0, 17], 0, None),      # beside rows of the other form
+    (1, 5, 256, 64, [2511], [33], 0, None),
+    (1, 2, 64, 16, [1301], [1301], 0, None),                # first rows lie in one part, last ones in several
+    (1, 8, 128, 64, [3000, 1100], [100, 9], 700, None),     # a window that begins inside a part
+    (1, 8, 128, 16, [2600], [50], 0, (40, 150)),            # no page in a whole part
+    (1, 8, 256, 128, [2600], [50], 0, (0, 21)),             # no page at all
+])
+def test_attention_of_prompts_in_parts(kind, H, G, D, page, lens, news, window, gone):
+    say("attention in parts", kind, H, G, D, lens, news, window)
+    p = Problem(19, kind, H, G, D, page, lens, news)
+    if gone:
+        p.table[0, gone[0]:gone[1]] = -1
+    one = p.run(window=window)
+    p.check(window=window, max_len=max(lens))
+    p.check(window=window, max_len=4 * max(lens), strided=True)
+    assert torch.equal(p.run(window=window), one)
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
 def test_attention_skips_missing_pages_and_leaves_empty_rows_zero(kind):
     p = Problem(17, kind, 2, 4, 128, 16, [90, 200, 33, 120], [1, 4, 33, 70])
     p.table[0, 2] = -1
