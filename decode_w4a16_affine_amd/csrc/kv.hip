@@ -514,8 +514,12 @@ KvAttnArgs attention_args(const w4a16_kv_cache_t* cache, int tokens, int request
   a.chunks = chunks > 1 ? (int)chunks : 1;
   // Where prompts bring fewer workgroups than the card holds (512, two a CU), the
   // cache is cut into parts that share their rows: their tiles run side by side, and
-  // a join adds the parts.  A part has 8 tiles at least: each row and part costs
-  // D + 2 floats written and read again, and the join 4 us.
+  // a join adds the parts (uncut, 100 tokens behind 8000 entries, 32 heads of 128 over
+  // 8: 211 us instead of 44).  Each row and part costs D + 2 floats written and read
+  // again, so a part has six tiles at least.  Measured (us, at least 4 / 6 / 8): 64
+  // tokens behind 8000, 10 heads of 256 over 2, 41.6 / 34.9 / 36.8; two of 103 behind
+  // 1373, 16 heads of 128 over 2, 27.1 / 29.2 / 34.7.  For 1024 workgroups instead of
+  // 512: 1000 behind 8000, 32 heads of 128 over 8, 199 instead of 187.
   a.parts = 1;
   a.part = kKvMaxLen + kKvTile;      // all
   if (requests > 0 && (int64_t)max_new * a.group > kKvSplitRows) {
@@ -523,7 +527,7 @@ KvAttnArgs attention_args(const w4a16_kv_cache_t* cache, int tokens, int request
     const int64_t workgroups = (int64_t)(tokens / tile_tokens + requests) * cache->heads;
     const int64_t reach = (int64_t)window + tile_tokens - 1;      // entries of a window's workgroup
     const int64_t span = window > 0 && reach < max_len ? reach : max_len;
-    const int64_t wanted = std::min<int64_t>(512 / workgroups, span / (8 * kKvTile));
+    const int64_t wanted = std::min<int64_t>(512 / workgroups, span / (6 * kKvTile));
     if (wanted > 1) {
       a.part = (int)((span + wanted * kKvTile - 1) / (wanted * kKvTile)) * kKvTile;
       // (a window's entries may begin inside a part)

@@ -342,7 +342,8 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
   }
 }
 
-// Joins the parts of a row in their order: D / 4 threads a row.  Rows that lie
+// Joins the parts of a row in their order: D / 4 threads a row (bound by two reads
+// from L2, one after the other: 4 us).  Rows that lie
 // in one part are written already, those of requests of few rows are not the
 // tiles'.
 template <int D, int TYPE>
@@ -366,16 +367,33 @@ __global__ __launch_bounds__(kKvJoinThreads) void kv_tile_join_kernel(KvAttnArgs
   const KvParts parts = kv_parts_of(a, kv_rows_of(a, r, i0, i0 + here - 1));
   if (parts.count <= 1) return;
   const size_t at = (size_t)row * a.parts;
+  // eight parts at a time, so that their loads do not wait for each other (the
+  // last one's are repeated, with factor 0)
+  constexpr int U = 8;
+  const kv_f32x2* ml = reinterpret_cast<const kv_f32x2*>(part_ml) + at;
   float top = kKvNone;
-  for (int p = 0; p < parts.count; ++p) top = fmaxf(top, part_ml[kKvTileStats * (at + p)]);
+  for (int p0 = 0; p0 < parts.count; p0 += U)
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = fmaxf(top, ml[min(p0 + u, parts.count - 1)][0]);
   float sum_l = 0.0f;
   kv_f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int p = 0; p < parts.count; ++p) {
-    const float f = __builtin_amdgcn_exp2f(part_ml[kKvTileStats * (at + p)] - top);
-    const kv_f32x4 v = *reinterpret_cast<const kv_f32x4*>(part_o + (at + p) * D + d);
-    sum_l = __builtin_fmaf(part_ml[kKvTileStats * (at + p) + 1], f, sum_l);
+  for (int p0 = 0; p0 < parts.count; p0 += U) {
+    kv_f32x2 s[U];
+    kv_f32x4 v[U];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(v[e], f, sum[e]);
+    for (int u = 0; u < U; ++u) {
+      const int p = min(p0 + u, parts.count - 1);
+      s[u] = ml[p];
+      v[u] = *reinterpret_cast<const kv_f32x4*>(part_o + (at + p) * D + d);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (p0 + u >= parts.count) break;
+      const float f = __builtin_amdgcn_exp2f(s[u][0] - top);
+      sum_l = __builtin_fmaf(s[u][1], f, sum_l);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(v[u][e], f, sum[e]);
+    }
   }
   kv_store4(a.out + (size_t)row * D + d, sum, kv_inverse(sum_l));
 }

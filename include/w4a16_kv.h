@@ -136,7 +136,8 @@ size_t w4a16_kv_attention_workspace_bytes(int tokens, int requests, int max_new,
  * depend on their own query, position and entries and on max_len alone: they
  * are bitwise equal in any batch and for any number of new tokens up to that
  * bound (a verify batch gives the rows of single-token calls).  Requests of more
- * take another, as does a call of one request with max_new * HQ / H > 64.
+ * take another, as does a call of one request with max_new * HQ / H > 64 (the
+ * order of whose sums may depend on the call's sizes, never on chance).
  * (T / (64 / (HQ / H)) + R) * H must not exceed 2^22 (the launch's size).
  */
 w4a16_status_t w4a16_kv_attention(const uint16_t *q, int64_t q_stride, const w4a16_kv_cache_t *cache,
