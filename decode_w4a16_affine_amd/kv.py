@@ -274,6 +274,16 @@ def _dequant(c, inputs, n, k_out, v_out, stream):
 
 
 # ---- allocating conveniences (torch allocates; the library computes) ------------
+# On a stream of the caller's they run as its current stream, so that what they
+# allocate is not given to others before the call has run.
+
+def _current(stream, t):
+    """A context with `stream` (a torch stream or a handle) current on t's GPU."""
+    dev = _same_gpu(t)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
+
 
 def kv_cache(pages: int, heads: int, dim: int, page: int = 64, dtype=torch.int8, device="cuda"):
     """An empty cache: (k_cache, v_cache, k_scales, v_scales)."""
@@ -285,6 +295,9 @@ def kv_cache(pages: int, heads: int, dim: int, page: int = 64, dtype=torch.int8,
 
 def kv_plan(ctx_lens, new_lens, free_pages, block_table, tokens: int, page: int, stream=None):
     """(seq_lens, token_start, slot_map [tokens], pages_used); block_table is updated in place."""
+    if stream is not None:
+        with _current(stream, ctx_lens):
+            return kv_plan(ctx_lens, new_lens, free_pages, block_table, tokens, page)
     R, num_free, width = _plan_inputs(ctx_lens, new_lens, free_pages, block_table)
     dev = _same_gpu(ctx_lens, new_lens, free_pages, block_table)
     _dense(ctx_lens, new_lens, free_pages, block_table)
@@ -292,7 +305,7 @@ def kv_plan(ctx_lens, new_lens, free_pages, block_table, tokens: int, page: int,
     at = out.data_ptr()
     _check(kv_lib().w4a16_kv_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), num_free,
                                   block_table.data_ptr(), width, at, at + 4 * R, at + 4 * (2 * R + 1),
-                                  at + 4 * (2 * R + 1 + tokens), R, tokens, page, _raw_stream(stream, dev)),
+                                  at + 4 * (2 * R + 1 + tokens), R, tokens, page, _current_stream(dev)),
            "w4a16_kv_plan")
     return out.split((R, R + 1, tokens, 1))
 
@@ -300,6 +313,10 @@ def kv_plan(ctx_lens, new_lens, free_pages, block_table, tokens: int, page: int,
 def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, max_new: int,
                  max_len: int = None, scale: float = None, window: int = 0, stream=None):
     """Attention of the step's queries: a new out [T, HQ, D] (see w4a16_kv_attention)."""
+    if stream is not None:
+        with _current(stream, q):
+            return kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, max_new,
+                                max_len, scale, window)
     c = _cache(k_cache, v_cache, k_scales, v_scales)
     inputs = tokens, _, R, width = _attention_inputs(c, q, block_table, seq_lens, token_start)
     dev = _same_gpu(k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, q)
@@ -307,18 +324,22 @@ def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens,
     if max_len is None:
         max_len = width * c.page
     ref = ctypes.byref(c)
-    out = torch.empty_like(q, memory_format=torch.contiguous_format)
     need = kv_lib().w4a16_kv_attention_workspace_bytes(tokens, R, max_new, max_len, window, q.shape[1], ref)
-    _attention(ref, inputs, q, block_table, seq_lens, token_start, out,
-               q.new_empty(need, dtype=torch.uint8) if need else None, max_new, max_len,
-               1.0 / math.sqrt(c.dim) if scale is None else scale, window, _raw_stream(stream, dev))
+    out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    ws = q.new_empty(need, dtype=torch.uint8) if need else None
+    _attention(ref, inputs, q, block_table, seq_lens, token_start, out, ws, max_new, max_len,
+               1.0 / math.sqrt(c.dim) if scale is None else scale, window, _current_stream(dev))
     return out
 
 
 def kv_dequant(k_cache, v_cache, k_scales, v_scales, pages, stream=None):
+    """(k_out, v_out) fp32 [n, H, P, D]: the values of pages [n]."""
+    if stream is not None:
+        with _current(stream, k_scales):
+            return kv_dequant(k_cache, v_cache, k_scales, v_scales, pages)
     c = _cache(k_cache, v_cache, k_scales, v_scales)
     n = _vector(pages, "pages")
     k_out = k_scales.new_empty((n, c.heads, c.page, c.dim), dtype=torch.float32)
     v_out = torch.empty_like(k_out)
-    _dequant(c, (k_cache, v_cache, k_scales, v_scales, pages), n, k_out, v_out, stream)
+    _dequant(c, (k_cache, v_cache, k_scales, v_scales, pages), n, k_out, v_out, None)
     return k_out, v_out

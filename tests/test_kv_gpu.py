@@ -549,3 +549,28 @@ def test_two_streams_match_one():
         torch.cuda.synchronize()
         for x, y in zip(a.snapshot() + b.snapshot(), ref_a + ref_b):
             assert torch.equal(x, y), rep
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_call_on_another_stream_keeps_its_memory(raw):
+    """Workspaces and outputs of calls on a stream of the caller's are not given to the current one before they ran."""
+    p = Problem(23, "int8", 2, 4, 128, 64, [3000, 2500, 1800], [1, 2, 1])
+    cache, args = p.device(), (i32(p.table), i32(p.lens), i32(p.start))
+    q = p.q.cuda()
+    want = w4.kv_attention(q, *cache, *args, 2)
+    values = w4.kv_dequant(*cache, i32([1, 0]))
+    s = torch.cuda.Stream()
+    busy = torch.randn((4096, 4096), device="cuda")
+    torch.cuda.synchronize()
+    for rep in range(3):
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                busy @ busy              # (the calls wait behind these)
+        stream = s.cuda_stream if raw else s
+        out = w4.kv_attention(q, *cache, *args, 2, stream=stream)
+        got = w4.kv_dequant(*cache, i32([1, 0]), stream=stream)
+        others = [torch.full((n,), math.nan, device="cuda") for n in (1 << 16, 1 << 18, 1 << 20, 1 << 22) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), rep
+        assert torch.equal(got[0], values[0]) and torch.equal(got[1], values[1]), rep
+        del others
