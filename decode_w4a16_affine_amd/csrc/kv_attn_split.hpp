@@ -425,7 +425,8 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
 // Joins the chunks of one row (grid: cache head and row, request) in chunk order:
 // D / 4 threads hold four elements each of one slice of the chunks, the slices'
 // sums are added in slice order.  Rows whose group lies in one chunk are
-// already written.
+// already written.  Bound by the launch and three reads that wait for each other:
+// 2.7 to 4.8 us in the cases above, 6.9 for 96 rows of up to 118 chunks.
 template <int D, int NC>
 __global__ __launch_bounds__(kKvJoinThreads) void kv_join_kernel(KvAttnArgs a, const float* part_o,
                                                                  const float* part_ml) {
