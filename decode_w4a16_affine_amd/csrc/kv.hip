@@ -482,10 +482,9 @@ w4a16_status_t check_attention(const w4a16_kv_cache_t* cache, int tokens, int re
 // about 1 us for each step of 128 entries, and a row and chunk costs D + 5
 // floats written and read again: short chunks answer sooner, long ones stream
 // better.  Measured (us, chunks of 128 / 256 / 512 / 1024): one request of 717
-// entries 9.1 / 12.0 / 17.6 / 20.3; 96 with a window of 512 in up to 3101
-// 16.7 / 16.2 / 16.4 / 18.4; 48 of up to 6001 88.7 / 73.5 / 65.5 / 62.8; 16
-// verify batches of up to 9006 39.1 / 34.8 / 32.2 / 45.4; 3 of up to 120002
-// 178 / 145 / 126 / 117.
+// entries 8.8 / 11.2 / 15.7 / 17.6; 96 with a window of 512 in up to 3101
+// 16.1 / 15.1 / 15.2 / 17.4; 48 of up to 6001 84.2 / 70.2 / 63.3 / 63.3; 16
+// verify batches of up to 9006 37.4 / 33.4 / 31.0 / 42.8.
 KvAttnArgs attention_args(const w4a16_kv_cache_t* cache, int tokens, int requests, int max_new, int max_len,
                           int window, int q_heads) {
   KvAttnArgs a{};
