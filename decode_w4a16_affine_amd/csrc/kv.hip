@@ -489,7 +489,9 @@ KvAttnArgs attention_args(const w4a16_kv_cache_t* cache, int tokens, int request
                           int window, int q_heads) {
   KvAttnArgs a{};
   a.c = device_cache(cache);
-  a.window = window;
+  // (a window of 2^30 hides nothing from lengths up to 2^29, and leaves room for what is
+  // subtracted from it)
+  a.window = window < 1 << 30 ? window : 1 << 30;
   a.tokens = tokens;
   a.requests = requests;
   a.max_new = max_new;
@@ -508,7 +510,7 @@ KvAttnArgs attention_args(const w4a16_kv_cache_t* cache, int tokens, int request
   while (in_chunks(max_len) > kKvMaxChunks - 1) ++a.chunk_shift;     // (a window may add one)
   long long chunks = in_chunks(max_len);
   // a window's rows attend window + split_tokens - 1 entries at most
-  const long long in_window = in_chunks((long long)window + a.split_tokens - 2) + 1;
+  const long long in_window = in_chunks((long long)a.window + a.split_tokens - 2) + 1;
   if (window > 0 && in_window < chunks) chunks = in_window;
   a.chunks = chunks > 1 ? (int)chunks : 1;
   // Where prompts bring fewer workgroups than the card holds (512, two a CU), the
@@ -524,7 +526,7 @@ KvAttnArgs attention_args(const w4a16_kv_cache_t* cache, int tokens, int request
   if (requests > 0 && (int64_t)max_new * a.group > kKvSplitRows) {
     const int tile_tokens = kv_tile_rows(cache->dim, cache->type) / a.group;
     const int64_t workgroups = (int64_t)(tokens / tile_tokens + requests) * cache->heads;
-    const int64_t reach = (int64_t)window + tile_tokens - 1;      // entries of a window's workgroup
+    const int64_t reach = (int64_t)a.window + tile_tokens - 1;      // entries of a window's workgroup
     const int64_t span = window > 0 && reach < max_len ? reach : max_len;
     const int64_t wanted = std::min<int64_t>(512 / workgroups, span / (6 * kKvTile));
     if (wanted > 1) {

@@ -88,9 +88,13 @@ __device__ __forceinline__ KvRows kv_rows_of(const KvAttnArgs& a, int r, int i0,
   k.n = a.token_start[r + 1] - k.first;
   k.seq = a.seq_lens[r];
   const long long held = (long long)a.width << a.c.page_shift;
-  const int lo = k.seq - k.n + i0, hi = k.seq - k.n + min(i1, min(k.n, a.max_new) - 1);
-  k.end = (int)min((long long)min(hi + 1, a.max_len), held);
-  k.begin = a.window > 0 ? max(0, lo - a.window + 1) : 0;
+  const long long pos0 = (long long)k.seq - k.n;      // of token 0
+  const long long hi = pos0 + min(i1, min(k.n, a.max_new) - 1);
+  // 0 <= begin <= end <= max_len where anything is attended, and begin = max(end, 0) where
+  // nothing is: whatever the lengths and the window, tiles are counted from a number
+  // that a few of them more do not carry past 32 bits
+  k.end = (int)max(min(min(hi + 1, (long long)a.max_len), held), 0LL);
+  k.begin = a.window > 0 ? (int)min(max(pos0 + i0 - a.window + 1, 0LL), (long long)k.end) : 0;
   return k;
 }
 

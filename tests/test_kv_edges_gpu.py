@@ -1,0 +1,70 @@
+"""GPU tests of the key/value cache at the edges of its contract: steps with more
+tokens than their bounds, entries that no row attends, windows and chunks that
+candidates cross, launches and appends beyond the common sizes.
+
+The oracle, its bounds and the random problems are those of test_kv_gpu.py.
+"""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import decode_w4a16_affine_amd as w4
+import kv_reference as ref
+from parity import say
+from test_kv_gpu import Problem, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    w4.kv_lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def run_into(p, q, out, max_new, max_len=None, window=0, cache=None):
+    """The C-ABI call on the caller's q and out (max_len None: what the table's columns hold)."""
+    cache = cache or p.device()
+    bound = p.width * p.page if max_len is None else max_len
+    need = w4.w4a16_kv_attention_workspace_bytes(q.shape[0], len(p.lens), max_new, bound, window, q.shape[1], *cache)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+    w4.w4a16_kv_attention(q, *cache, i32(p.table), i32(p.lens), i32(p.start), out, ws, max_new, max_len=max_len,
+                          window=window)
+    torch.cuda.synchronize()
+    return out
+
+
+def close(got, want, tol):
+    """Within the oracle's bound of each element (NaN is not)."""
+    got = got.cpu().double().numpy()
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[0], got[bad][0], want[bad][0], tol[bad][0])
+
+
+@pytest.mark.parametrize("H,G,D,lens,news", [(1, 2, 64, [2, 0, 3], [5, 2, 3]), (1, 4, 128, [10, 3], [40, 6]),
+                                             (1, 5, 256, [33, 9], [33, 12])])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30 + 5])
+def test_the_widest_windows_hide_nothing(H, G, D, lens, news, window):
+    say("attention window", window, H, G, D, lens, news)
+    Problem(53, "int8", H, G, D, 16, lens, news).check(window=window)
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("D,G", [(64, 4), (256, 5)])
+def test_lengths_far_past_the_bound_read_nothing_of_a_window(kind, D, G):
+    """Positions near 2^31: no entry below max_len lies in their window, and the rows are 0; others are as ever."""
+    say("attention, lengths past the bound", kind, D, G)
+    p = Problem(57, kind, 2, G, D, 16, [64, 64, 50], [3, 40, 1])
+    want, tol = p.want(1 / math.sqrt(D), 100)
+    cache = p.device()
+    p.lens[:2] = [2 ** 31 - 1, 2 ** 31 - 30]
+    out = p.run(window=100, cache=cache)
+    assert (out[:43] == 0).all()
+    close(out[43:], want[43:], tol[43:])
