@@ -75,6 +75,13 @@ __device__ __forceinline__ kv_f16x8 kv_f16_of8(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(kv_f16x8, make_uint4(x.x, x.y, y.x, y.y));
 }
 
+// Requests whose rows within the step's bound (max_new tokens, which is what the
+// launch is sized by) are few take the split form, the others tiles: one rule for
+// the kernels of both forms and for their joins.
+__device__ __forceinline__ bool kv_few_rows(const KvAttnArgs& a, int n) {
+  return a.split && min(n, a.max_new) * a.group <= kKvSplitRows;
+}
+
 // Where the rows of one workgroup lie: shared by the split kernel and the join.
 struct KvRows {
   int n, first, seq;      // new tokens, first token row, length of the request

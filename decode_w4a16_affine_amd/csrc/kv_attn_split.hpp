@@ -127,7 +127,7 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
   const int i_first = kv_token_of(a, row0), i_last = kv_token_of(a, row0 + NC * 16 - 1);
   const KvRows rows = kv_rows_of(a, r, i_first, i_last);
   const int live = min(rows.n, a.max_new) * a.group;       // rows of the request
-  if (rows.n * a.group > kKvSplitRows || row0 >= live) return;
+  if (!kv_few_rows(a, rows.n) || row0 >= live) return;
   const int first = rows.begin >> a.chunk_shift;            // the group's first chunk
   const int at_begin = (first + block) << a.chunk_shift;
   const int at_end = (int)min((long long)at_begin + (1LL << a.chunk_shift), (long long)rows.end);
@@ -441,7 +441,7 @@ __global__ __launch_bounds__(kKvJoinThreads) void kv_join_kernel(KvAttnArgs a, c
   const int kh = blockIdx.x / max_rows, row = blockIdx.x % max_rows;
   const int row0 = row / (NC * 16) * (NC * 16);
   const KvRows rows = kv_rows_of(a, r, kv_token_of(a, row0), kv_token_of(a, row0 + NC * 16 - 1));
-  if (rows.n * a.group > kKvSplitRows || row >= min(rows.n, a.max_new) * a.group) return;
+  if (!kv_few_rows(a, rows.n) || row >= min(rows.n, a.max_new) * a.group) return;
   const int first = rows.begin >> a.chunk_shift;
   const int count = (max(rows.end - 1, rows.begin) >> a.chunk_shift) - first + 1;
   if (count <= 1) return;

@@ -93,7 +93,7 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
   const int i0 = (u - a.token_start[r] / tt - r) * tt;
   const int n = a.token_start[r + 1] - a.token_start[r];
   const int live_tokens = min(min(n, a.max_new), a.tokens - a.token_start[r]);
-  if ((a.split && n * a.group <= kKvSplitRows) || i0 < 0 || i0 >= live_tokens || a.token_start[r] < 0) return;
+  if (kv_few_rows(a, n) || i0 < 0 || i0 >= live_tokens || a.token_start[r] < 0) return;
   const int here = min(tt, live_tokens - i0);       // the workgroup's tokens
   const int live = here * a.group;                  // and rows
   const KvRows rows = kv_rows_of(a, r, i0, i0 + here - 1);
@@ -360,7 +360,7 @@ __global__ __launch_bounds__(kKvJoinThreads) void kv_tile_join_kernel(KvAttnArgs
     count -= step;
   }
   const int n = a.token_start[r + 1] - a.token_start[r], i = t - a.token_start[r];
-  if (a.token_start[r] < 0 || i >= min(n, a.max_new) || (a.split && n * a.group <= kKvSplitRows)) return;
+  if (a.token_start[r] < 0 || i >= min(n, a.max_new) || kv_few_rows(a, n)) return;
   // the rows of its workgroup
   const int tt = kv_token_of(a, kv_tile_rows(D, TYPE)), i0 = i / tt * tt;
   const int here = min(tt, min(min(n, a.max_new), a.tokens - a.token_start[r]) - i0);

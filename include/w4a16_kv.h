@@ -132,7 +132,7 @@ size_t w4a16_kv_attention_workspace_bytes(int tokens, int requests, int max_new,
  * Softmax statistics and sums in fp32, weights rounded to fp16, keys, values
  * and queries exact.  A weight is held times its page's value scale: beside
  * values beyond about 10^6 the weights of a page of zeros (scale 2^-100) can
- * underflow.  Requests of n * HQ / H <= 64 rows take one form, whose rows
+ * underflow.  Requests of min(n, max_new) * HQ / H <= 64 rows take one form, whose rows
  * depend on their own query, position and entries and on max_len alone: they
  * are bitwise equal in any batch and for any number of new tokens up to that
  * bound (a verify batch gives the rows of single-token calls).  Requests of more

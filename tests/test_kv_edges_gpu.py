@@ -68,3 +68,25 @@ def test_lengths_far_past_the_bound_read_nothing_of_a_window(kind, D, G):
     out = p.run(window=100, cache=cache)
     assert (out[:43] == 0).all()
     close(out[43:], want[43:], tol[43:])
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("H,G,D,lens,news,max_new", [
+    (1, 4, 64, [60], [17], 16),                          # 64 rows of the bound, 68 of the request
+    (2, 4, 128, [300, 50, 9, 700], [17, 30, 2, 300], 16),
+    (1, 5, 256, [90, 333], [13, 40], 12),
+    (1, 64, 64, [40, 41], [2, 1], 1),                    # a bound of one token
+    (2, 4, 64, [300, 90, 50], [60, 5, 17], 20),          # a bound of 80 rows: both forms
+    (1, 5, 256, [400], [399], 30),
+])
+def test_requests_of_more_tokens_than_max_new(kind, H, G, D, lens, news, max_new):
+    """A request's first max_new rows are written whatever it brings; the others stay as they were."""
+    say("attention max_new", kind, H, G, D, lens, news, max_new)
+    p = Problem(41, kind, H, G, D, 32, lens, news)
+    want, tol = p.want(1 / math.sqrt(D), 0)
+    q = p.q.cuda()
+    out = run_into(p, q, torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda"), max_new)
+    for r, n in enumerate(news):
+        a, b = p.start[r], p.start[r] + min(n, max_new)
+        close(out[a:b], want[a:b], tol[a:b])
+        assert (out[b:p.start[r + 1]] == 5).all(), r
