@@ -215,13 +215,12 @@ __device__ __forceinline__ void kv_weights(kv_f32x4 (&s)[NC][NP], const KvLaneRo
   }
 }
 
-// E4M3 codes of entries that hold nothing may be NaN, and 0 * NaN must not
-// enter the sums: the bytes of 16 value codes that stand for existing entries.
-__device__ __forceinline__ kv_u32x4 kv_existing_bytes(int left) {
-  auto bytes = [&](int b) {
-    const int k = left - 4 * b;
-    return k >= 4 ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
-  };
+// E4M3 codes of entries that no row attends (never filled, or a page's next use)
+// may be NaN, and 0 * NaN must not enter the sums: the bytes of 16 value codes
+// that stand for entries `skip` .. `left` - 1 of them.
+__device__ __forceinline__ kv_u32x4 kv_existing_bytes(int skip, int left) {
+  auto below = [](int k) { return k >= 4 ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << (8 * k)) - 1u; };
+  auto bytes = [&](int b) { return below(left - 4 * b) & ~below(skip - 4 * b); };
   return kv_u32x4{bytes(0), bytes(1), bytes(2), bytes(3)};
 }
 

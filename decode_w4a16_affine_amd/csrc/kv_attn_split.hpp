@@ -222,14 +222,16 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
     for (int i = 0; i < LD; ++i) stage[i * kWave + (key_put ^ key_turn(i * KR))] = kc[i];
   };
   auto put_values = [&](int j0, int page) W4K_INLINE {
-    // E4M3 codes of entries that hold nothing may be NaN, which weights of 0
-    // would not hide: where entries of the step are missing, their codes become 0
-    if (TYPE == W4A16_KV_FP8 && !(j0 + STEP <= rows.end && __all(page >= 0 || x >= STEP / 16))) {
+    // E4M3 codes of entries that no row attends may be NaN, which weights of 0
+    // would not hide: where the step has such entries, their codes become 0
+    if (TYPE == W4A16_KV_FP8 &&
+        !(j0 >= rows.begin && j0 + STEP <= rows.end && __all(page >= 0 || x >= STEP / 16))) {
       const int lane_first = kv_opaque(lane_block);
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
         const int block = (i * kWave >> pps << bs) + lane_first;
-        vc[i] = vc[i] & kv_existing_bytes(__shfl(page, block) >= 0 ? rows.end - (j0 + 16 * block) : 0);
+        const int at = j0 + 16 * block;
+        vc[i] = vc[i] & kv_existing_bytes(rows.begin - at, __shfl(page, block) >= 0 ? rows.end - at : 0);
       }
     }
     const int value_put = kv_opaque(value_put_0);

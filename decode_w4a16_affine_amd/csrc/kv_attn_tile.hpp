@@ -189,11 +189,11 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
     }
   };
   auto put_values = [&](int b, int j0, int page) W4K_INLINE {
-    // E4M3 codes of entries that hold nothing may be NaN, which weights of 0
-    // would not hide: where entries of the tile are missing, their codes become 0
-    if (TYPE == W4A16_KV_FP8 && !(j0 + kKvTile <= rows.end && __all(page >= 0))) {
+    // E4M3 codes of entries that no row attends may be NaN, which weights of 0
+    // would not hide: where the tile has such entries, their codes become 0
+    if (TYPE == W4A16_KV_FP8 && !(j0 >= rows.begin && j0 + kKvTile <= rows.end && __all(page >= 0))) {
       const int first = kv_opaque(j0 + 16 * g);
-      const kv_u32x4 exist = kv_existing_bytes(page >= 0 ? rows.end - first : 0);
+      const kv_u32x4 exist = kv_existing_bytes(rows.begin - first, page >= 0 ? rows.end - first : 0);
 #pragma unroll
       for (int i = 0; i < VL; ++i) vc[i] = vc[i] & exist;
     }

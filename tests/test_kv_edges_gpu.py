@@ -90,3 +90,29 @@ def test_requests_of_more_tokens_than_max_new(kind, H, G, D, lens, news, max_new
         a, b = p.start[r], p.start[r] + min(n, max_new)
         close(out[a:b], want[a:b], tol[a:b])
         assert (out[b:p.start[r + 1]] == 5).all(), r
+
+
+@pytest.mark.parametrize("H,G,D,page,lens,news,window", [
+    (2, 4, 64, 16, [600, 1111, 130, 20], [1, 1, 3, 1], 30),
+    (1, 8, 128, 32, [900, 700], [8, 5], 100),               # two row groups with begins of their own
+    (1, 5, 256, 64, [513, 900], [5, 3], 100),
+    (2, 4, 128, 256, [3000], [1], 512),
+    (2, 2, 128, 32, [400, 333], [100, 200], 64),            # the rest as tiles
+    (1, 4, 64, 64, [700], [150], 33),
+    (1, 5, 256, 64, [500, 300], [100, 33], 70),
+    (1, 8, 128, 64, [3000, 1100], [100, 9], 700),           # in parts of the cache
+    (1, 5, 256, 32, [3001], [40], 650),
+])
+def test_entries_before_a_window_may_hold_anything(H, G, D, page, lens, news, window):
+    """Their pages are still in the table, but hold NaN codes (reused, or never filled)."""
+    say("attention, NaN codes before a window", H, G, D, page, lens, news, window)
+    p = Problem(43, "fp8", H, G, D, page, lens, news)
+    kt, vt, ks, vs = p.device()
+    for r, (n, k) in enumerate(zip(lens, news)):
+        for j in range(max(0, n - k - window + 1)):
+            pg, off = int(p.table[r, j // page]), j % page
+            kt.view(torch.uint8)[pg, :, off] = 0x7F
+            vt.view(torch.uint8)[pg, :, :, off] = 0xFF if j % 2 else 0x7F
+    cache = (kt, vt, ks, vs)
+    p.check(window=window, cache=cache)
+    p.check(window=window, cache=cache, max_len=max(lens))
