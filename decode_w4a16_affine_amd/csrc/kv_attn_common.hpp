@@ -85,6 +85,7 @@ __device__ __forceinline__ bool kv_few_rows(const KvAttnArgs& a, int n) {
 // Where the rows of one workgroup lie: shared by the split kernel and the join.
 struct KvRows {
   int n, first, seq;      // new tokens, first token row, length of the request
+  int live;               // tokens that have a row: at most max_new, and rows of q
   int begin, end;         // cache entries any of the group's rows attends
 };
 
@@ -96,7 +97,8 @@ __device__ __forceinline__ KvRows kv_rows_of(const KvAttnArgs& a, int r, int i0,
   k.seq = a.seq_lens[r];
   const long long held = (long long)a.width << a.c.page_shift;
   const long long pos0 = (long long)k.seq - k.n;      // of token 0
-  const long long hi = pos0 + min(i1, min(k.n, a.max_new) - 1);
+  k.live = (int)min((long long)min(k.n, a.max_new), (long long)a.tokens - k.first);
+  const long long hi = pos0 + min(i1, k.live - 1);      // (entries of tokens without a row may hold anything)
   // 0 <= begin <= end <= max_len where anything is attended, and begin = max(end, 0) where
   // nothing is: whatever the lengths and the window, tiles are counted from a number
   // that a few of them more do not carry past 32 bits

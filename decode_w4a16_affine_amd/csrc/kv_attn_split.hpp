@@ -126,7 +126,7 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
   if (a.window == 0 && a.width > 0) page = pages(block << a.chunk_shift);
   const int i_first = kv_token_of(a, row0), i_last = kv_token_of(a, row0 + NC * 16 - 1);
   const KvRows rows = kv_rows_of(a, r, i_first, i_last);
-  const int live = min(rows.n, a.max_new) * a.group;       // rows of the request
+  const int live = rows.live * a.group;                    // rows of the request
   if (!kv_few_rows(a, rows.n) || row0 >= live) return;
   const int first = rows.begin >> a.chunk_shift;            // the group's first chunk
   const int at_begin = (first + block) << a.chunk_shift;
@@ -273,7 +273,7 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
   if constexpr (Q_LDS) __syncthreads();
   // positions that every row of the group attends need no mask
   const int all_hi = min(rows.seq - rows.n + i_first, rows.end - 1);
-  const int all_lo = a.window > 0 ? rows.seq - rows.n + min(i_last, min(rows.n, a.max_new) - 1) - a.window + 1 : 0;
+  const int all_lo = a.window > 0 ? rows.seq - rows.n + min(i_last, rows.live - 1) - a.window + 1 : 0;
 
   kv_f32x4 o[NC][DW];
   float m[NC], l[NC];
@@ -443,7 +443,7 @@ __global__ __launch_bounds__(kKvJoinThreads) void kv_join_kernel(KvAttnArgs a, c
   const int kh = blockIdx.x / max_rows, row = blockIdx.x % max_rows;
   const int row0 = row / (NC * 16) * (NC * 16);
   const KvRows rows = kv_rows_of(a, r, kv_token_of(a, row0), kv_token_of(a, row0 + NC * 16 - 1));
-  if (!kv_few_rows(a, rows.n) || row >= min(rows.n, a.max_new) * a.group) return;
+  if (!kv_few_rows(a, rows.n) || row >= rows.live * a.group) return;
   const int first = rows.begin >> a.chunk_shift;
   const int count = (max(rows.end - 1, rows.begin) >> a.chunk_shift) - first + 1;
   if (count <= 1) return;

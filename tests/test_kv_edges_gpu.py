@@ -116,3 +116,27 @@ def test_entries_before_a_window_may_hold_anything(H, G, D, page, lens, news, wi
     cache = (kt, vt, ks, vs)
     p.check(window=window, cache=cache)
     p.check(window=window, cache=cache, max_len=max(lens))
+
+
+@pytest.mark.parametrize("H,G,D,lens,news,T", [
+    (1, 4, 64, [40], [5], 3),
+    (2, 4, 128, [90, 40], [5, 3], 4),           # the second request has no row at all
+    (1, 5, 256, [70, 333], [3, 6], 5),
+    (2, 4, 128, [90], [70], 50),                # as tiles
+    (1, 5, 256, [30, 300], [2, 40], 31),
+])
+def test_entries_of_tokens_past_the_rows_of_q_may_hold_anything(H, G, D, lens, news, T):
+    """Tokens past T have no slot, so nothing was appended for them: their entries hold NaN codes."""
+    say("attention, fewer rows than tokens", H, G, D, lens, news, T)
+    p = Problem(47, "fp8", H, G, D, 32, lens, news)
+    want, tol = p.want(1 / math.sqrt(D), 0)
+    kt, vt, ks, vs = p.device()
+    for r, (n, k) in enumerate(zip(lens, news)):
+        for i in range(k):
+            if p.start[r] + i >= T:
+                j = n - k + i
+                kt.view(torch.uint8)[int(p.table[r, j // 32]), :, j % 32] = 0x7F
+                vt.view(torch.uint8)[int(p.table[r, j // 32]), :, :, j % 32] = 0x7F
+    q = p.q[:T].cuda()
+    out = run_into(p, q, torch.empty_like(q), max(news), cache=(kt, vt, ks, vs))
+    close(out, want[:T], tol[:T])
