@@ -89,7 +89,9 @@ __global__ __launch_bounds__(kKvThreads) void kv_plan_kernel(const int32_t* __re
       if (t >= tokens) break;
       const int b = (c + i) >> page_shift;
       const int page = b >= width ? -1 : b < held ? row[b] : fresh(b);
-      slot_map[t] = page >= 0 ? (page << page_shift) + ((c + i) & (P - 1)) : -1;
+      // (a page number of 2^31 / P or more is outside every cache: no slot, rather than one
+      // that wraps into another page)
+      slot_map[t] = page >= 0 && page <= 0x7FFFFFFF >> page_shift ? (page << page_shift) + ((c + i) & (P - 1)) : -1;
     }
   }
   // the wave of the last request knows the totals

@@ -81,7 +81,8 @@ typedef struct w4a16_kv_cache {
  *   pages_used[1]       sum of need
  * Where free_pages has fewer entries than needed (compare pages_used with
  * num_free), or a row fewer columns, the missing entries are -1 and so are
- * the slots in them: w4a16_kv_append skips those.  Slots past the step's
+ * the slots in them: w4a16_kv_append skips those.  A page number of 2^31 / P or
+ * more is outside every cache, and the slots in it are -1.  Slots past the step's
  * tokens (T may exceed them) are -1; tokens past T have no slot.
  */
 w4a16_status_t w4a16_kv_plan(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *free_pages,

@@ -140,3 +140,16 @@ def test_entries_of_tokens_past_the_rows_of_q_may_hold_anything(H, G, D, lens, n
     q = p.q[:T].cuda()
     out = run_into(p, q, torch.empty_like(q), max(news), cache=(kt, vt, ks, vs))
     close(out, want[:T], tol[:T])
+
+
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_plan_gives_no_slot_in_pages_outside_every_cache(page):
+    """Page numbers whose slots would pass 32 bits (held, and from the free list), beside the largest one that fits."""
+    top = 2 ** 31 // page           # the first that does not fit
+    say("plan, pages outside every cache", page)
+    table = i32([[top, 7, -1], [top - 1, -1, -1], [2 ** 31 - 1, -1, -1]])
+    seq, start, slots, used = w4.kv_plan(i32([page - 2, page - 1, 1]), i32([3, 2, 1]), i32([2 * top, top + 3, 5]),
+                                         table, 6, page)
+    torch.cuda.synchronize()
+    assert table.tolist() == [[top, 2 * top, -1], [top - 1, top + 3, -1], [2 ** 31 - 1, -1, -1]]
+    assert slots.tolist() == [-1, -1, -1, 2 ** 31 - 1, -1, -1] and used.tolist() == [2]
