@@ -1,6 +1,6 @@
 """Prompt, decode and verify steps of a small stack of W4 layers over the paged 8-bit cache.
 
-    python examples/decode_layers.py [--layers 4] [--kind int8|fp8] [--steps 16]
+    python examples/decode_layers.py [--layers 4] [--kind int8|fp8] [--steps 16] [--candidates 3]
 
 Every weight product, the cache and its attention are the library's; torch
 allocates, normalises (root mean square, no learned factor) and adds the
@@ -75,6 +75,19 @@ def norm(x):
     return (x * torch.rsqrt(x.square().mean(1, keepdim=True) + 1e-6)).to(torch.bfloat16)
 
 
+def give_back(table, lens, kept, page):
+    """The pages that requests cut from `lens` to `kept` tokens no longer reach; they leave the block table.
+
+    w4a16_kv_plan takes every page past a request's length from the free list, so a page that rejected candidates
+    opened belongs there again: left in the table, the next plan would write over it and nobody would hold it."""
+    col = torch.arange(table.shape[1], device=table.device)[None, :]
+    reach = lambda n: (n[:, None] + page - 1) // page  # noqa: E731
+    gone = (col >= reach(kept)) & (col < reach(lens)) & (table >= 0)
+    pages = table[gone]
+    table[gone] = -1
+    return pages
+
+
 class Stack:
     """Layers with a paged cache for `requests` requests of at most max_len tokens."""
 
@@ -104,13 +117,32 @@ class Stack:
             x = x + layer.mlp(norm(x)).float()
         h = norm(x)
         best = torch.cat([w4.lmhead_argmax(part, *self.embedding, want_logits=False)[0] for part in h.split(w4.MAX_M)])
-        # the pages are taken, the tokens held (a program that rejects candidates keeps fewer: set self.lens)
+        # the pages are taken, the tokens held (a program that rejects candidates keeps fewer: see keep)
         taken = int(used)
         if taken > self.free.numel():
             raise RuntimeError("out of cache pages")
         self.free = self.free[taken:].contiguous()
         self.lens = seq
         return best, h
+
+    def keep(self, lens):
+        """Keeps the first lens[r] tokens of each request: the candidates behind them were rejected."""
+        kept = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        if bool((kept > self.lens).any()):
+            raise ValueError(f"requests hold {self.lens.tolist()} tokens, {lens} asked to keep")
+        self.free = torch.cat([give_back(self.table, self.lens, kept, self.page), self.free])
+        self.lens = kept
+
+    def verify(self, tokens, guesses):
+        """One token and some candidates of each request (tokens [R], guesses [R, k]) in one step; those candidates
+        stay that agree with the stack's own choice up to there.  (the next tokens [R], how many stayed [R])"""
+        batch = torch.cat([tokens[:, None], guesses], dim=1)
+        held = self.lens.tolist()
+        best, _ = self.step(batch.flatten(), [batch.shape[1]] * len(held))
+        best = best.view(batch.shape)
+        stay = (best[:, :-1] == guesses).int().cumprod(1).sum(1)
+        self.keep([n + 1 + s for n, s in zip(held, stay.tolist())])
+        return best.gather(1, stay[:, None]).flatten(), stay
 
 
 def last_of(counts):
@@ -122,6 +154,7 @@ def main():
     ap.add_argument("--layers", type=int, default=4)
     ap.add_argument("--kind", choices=sorted(KINDS), default="int8")
     ap.add_argument("--steps", type=int, default=16)
+    ap.add_argument("--candidates", type=int, default=3)
     a = ap.parse_args()
     prompts = [700, 64, 333, 5]
     stack = Stack(layers=a.layers, kind=a.kind)
@@ -136,6 +169,13 @@ def main():
     ms = (time.perf_counter() - t) / a.steps * 1e3
     print(f"{a.layers} layers, {len(prompts)} requests, {a.kind} cache: {ms:.2f} ms a decode step; "
           f"lengths {stack.lens.tolist()}, last tokens {tokens.tolist()}")
+    # verify steps; the candidates are guesses (the token itself), so most are rejected
+    stayed = 0
+    for _ in range(a.steps):
+        tokens, stay = stack.verify(tokens, tokens[:, None].expand(-1, a.candidates))
+        stayed += int(stay.sum())
+    print(f"{a.steps} verify steps of {a.candidates} candidates: {stayed} stayed; lengths {stack.lens.tolist()}, "
+          f"{stack.free.numel()} pages free")
 
 
 if __name__ == "__main__":

@@ -84,6 +84,10 @@ typedef struct w4a16_kv_cache {
  * the slots in them: w4a16_kv_append skips those.  A page number of 2^31 / P or
  * more is outside every cache, and the slots in it are -1.  Slots past the step's
  * tokens (T may exceed them) are -1; tokens past T have no slot.
+ * A caller that drops tokens again (rejected candidates) passes the shorter
+ * ctx_lens to the next call and first returns what lies past them to its free
+ * pages: entries ceil(kept / P) <= b < ceil(length / P) of the request's row.
+ * They are written over, not kept: a page left there would be lost.
  */
 w4a16_status_t w4a16_kv_plan(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *free_pages,
                              int num_free, int32_t *block_table, int width, int32_t *seq_lens,

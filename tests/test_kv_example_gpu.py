@@ -57,3 +57,65 @@ def test_steps_agree_however_tokens_arrive(kind, window):
     alone = make()
     _, h1 = alone.step(first, [90, 0])
     assert rel(h1, h[:90]) < BOUND[kind]
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+def test_rejected_candidates_leave_no_trace(kind):
+    """Verify steps that reject some candidates, over page ends: the pages are all there afterwards, and the rows of the
+    accepted tokens are those of one prompt (within the bound above: rejected tokens are of the same kind, so the
+    scales that they may leave behind are those of some more tokens in the page)."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import decode_layers as ex
+
+    make = lambda: ex.Stack(layers=2, ffn=2560, vocab=1024, requests=2, max_len=192, page=16, kind=kind)  # noqa: E731
+    g = torch.Generator().manual_seed(9)
+    first, second, junk = (torch.randint(0, 1024, (n,), dtype=torch.int32, generator=g).cuda() for n in (90, 70, 64))
+    _, want = make().step(torch.cat([first, second]), [90, 70])
+    s = make()
+    _, h = s.step(torch.cat([first[:45], second[:30]]), [45, 30])
+    rows = [list(h.split([45, 30]))]
+    accepted = [(1, 3), (2, 1), (4, 4), (1, 2), (3, 2), (4, 3), (2, 4), (4, 4)]
+    for a, b in accepted:
+        lo = s.lens.tolist()
+        # the accepted tokens, then wrong candidates, of each request; seven tokens each, so that pages are opened
+        part = torch.cat([first[lo[0]:lo[0] + a], junk[:7 - a], second[lo[1]:lo[1] + b], junk[-(7 - b):]])
+        _, h = s.step(part, [7, 7])
+        rows.append([h[:a], h[7:7 + b]])
+        s.keep([lo[0] + a, lo[1] + b])
+        held = s.table[s.table >= 0].tolist()
+        assert sorted(held + s.free.tolist()) == list(range(24)) and len(held) == sum(-(-n // 16) for n in s.lens.tolist())
+    n = s.lens.tolist()
+    assert n == [45 + sum(a for a, _ in accepted), 30 + sum(b for _, b in accepted)]
+    for r, (at, count) in enumerate(((0, n[0]), (90, n[1]))):
+        assert rel(torch.cat([x[r] for x in rows]), want[at:at + count]) < BOUND[kind]
+    with pytest.raises(ValueError, match="asked to keep"):
+        s.keep([n[0] + 1, n[1]])
+
+
+def test_verify_keeps_the_stack_s_own_choices():
+    """A candidate that is the stack's own next token stays, and what follows a wrong one does not."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import decode_layers as ex
+
+    prompt = torch.randint(0, 1024, (41,), dtype=torch.int32, generator=torch.Generator().manual_seed(3)).cuda()
+
+    def verify(change):
+        s = ex.Stack(layers=1, ffn=2560, vocab=1024, requests=2, max_len=128, page=16)
+        best, _ = s.step(prompt, [30, 11])
+        after, stay = s.verify(*change(best[ex.last_of([30, 11])]))
+        assert s.lens.tolist() == [31 + int(stay[0]), 12 + int(stay[1])]
+        assert s.free.numel() == 16 - sum(-(-n // 16) for n in s.lens.tolist())
+        return after, stay.tolist()
+
+    wrong = torch.zeros((2, 5), dtype=torch.int32, device="cuda")
+    own, stay = verify(lambda t: (t, wrong))
+    assert stay == [0, 0] and 0 not in own.tolist()
+    guesses = wrong.clone()
+    guesses[0, 0] = own[0]
+    _, stay = verify(lambda t: (t, guesses))
+    assert stay == [1, 0]
+    guesses[1, 0] = own[1]
+    _, stay = verify(lambda t: (t, guesses))
+    assert stay == [1, 1]
