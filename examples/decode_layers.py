@@ -101,9 +101,14 @@ class Stack:
         self.free = torch.randperm(requests * width).to(torch.int32).cuda()
         self.table = torch.full((requests, width), -1, dtype=torch.int32, device="cuda")
         self.lens = torch.zeros((requests,), dtype=torch.int32, device="cuda")
+        self.held = [0] * requests                               # the same on the host
 
     def step(self, tokens, counts):
         """tokens [T]: counts[r] of each request, in request order.  (logits' argmax [T], final hidden rows [T, hidden])"""
+        held = [n + c for n, c in zip(self.held, counts)]
+        longest = max(held, default=0)
+        if longest > self.max_len:      # (past the block table's columns tokens have no slot: they would be lost)
+            raise ValueError(f"a request of {longest} tokens in a stack of max_len {self.max_len}")
         new = torch.tensor(counts, dtype=torch.int32, device="cuda")
         # where the tokens go: once for all layers
         seq, start, slots, used = w4.kv_plan(self.lens, new, self.free, self.table, tokens.numel(), self.page)
@@ -122,22 +127,22 @@ class Stack:
         if taken > self.free.numel():
             raise RuntimeError("out of cache pages")
         self.free = self.free[taken:].contiguous()
-        self.lens = seq
+        self.lens, self.held = seq, held
         return best, h
 
     def keep(self, lens):
         """Keeps the first lens[r] tokens of each request: the candidates behind them were rejected."""
+        if any(n > h for n, h in zip(lens, self.held)):
+            raise ValueError(f"requests hold {self.held} tokens, {lens} asked to keep")
         kept = torch.tensor(lens, dtype=torch.int32, device="cuda")
-        if bool((kept > self.lens).any()):
-            raise ValueError(f"requests hold {self.lens.tolist()} tokens, {lens} asked to keep")
         self.free = torch.cat([give_back(self.table, self.lens, kept, self.page), self.free])
-        self.lens = kept
+        self.lens, self.held = kept, list(lens)
 
     def verify(self, tokens, guesses):
         """One token and some candidates of each request (tokens [R], guesses [R, k]) in one step; those candidates
         stay that agree with the stack's own choice up to there.  (the next tokens [R], how many stayed [R])"""
         batch = torch.cat([tokens[:, None], guesses], dim=1)
-        held = self.lens.tolist()
+        held = self.held
         best, _ = self.step(batch.flatten(), [batch.shape[1]] * len(held))
         best = best.view(batch.shape)
         stay = (best[:, :-1] == guesses).int().cumprod(1).sum(1)

@@ -119,3 +119,21 @@ def test_verify_keeps_the_stack_s_own_choices():
     guesses[1, 0] = own[1]
     _, stay = verify(lambda t: (t, guesses))
     assert stay == [1, 1]
+
+
+def test_a_request_longer_than_the_stack_is_refused():
+    """Nothing is written, taken or counted by a step that would pass max_len; one that just fits is fine."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import decode_layers as ex
+
+    s = ex.Stack(layers=1, ffn=2560, vocab=1024, requests=2, max_len=40, page=16)
+    tokens = torch.arange(61, dtype=torch.int32, device="cuda")
+    s.step(tokens[:50], [30, 20])
+    before = [t.clone().view(torch.uint8) for t in (*s.caches[0], s.table, s.free, s.lens)]
+    with pytest.raises(ValueError, match="41 tokens in a stack of max_len 40"):
+        s.step(tokens[:12], [11, 1])
+    for t, b in zip((*s.caches[0], s.table, s.free, s.lens), before):
+        assert torch.equal(t.view(torch.uint8), b)
+    s.step(tokens[:11], [10, 1])
+    assert s.lens.tolist() == [40, 21]
