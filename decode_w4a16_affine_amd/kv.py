@@ -2,7 +2,8 @@
 
 Same conventions as the package's other functions: C-ABI names, tensors in,
 dtype and shape checks before any pointer reaches the library, the current
-stream of torch unless one is given, no fallback.
+stream of torch (of the tensors' GPU, which need not be the current one) unless
+one is given, no fallback.
 
 Tensor conventions (all on the same GPU; contiguous unless said otherwise):
   q, k, v, out            : torch.bfloat16; q, k, v may be parts of wider token
@@ -97,6 +98,16 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
+# A launch goes to the current GPU, and a null stream is that GPU's: a call whose tensors are on another one is made
+# again with theirs current.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _on(dev: int, fn, *args):
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
 def _raw_stream(stream, dev: int) -> int:
     if stream is None:
         return _current_stream(dev)
@@ -175,6 +186,9 @@ def w4a16_kv_plan(ctx_lens, new_lens, free_pages, block_table, seq_lens, token_s
     _vector(pages_used, "pages_used", 1)
     dev = _same_gpu(ctx_lens, new_lens, free_pages, block_table, seq_lens, token_start, slot_map, pages_used)
     _dense(ctx_lens, new_lens, free_pages, block_table, seq_lens, token_start, slot_map, pages_used)
+    if _current_device() != dev:
+        return _on(dev, w4a16_kv_plan, ctx_lens, new_lens, free_pages, block_table, seq_lens, token_start, slot_map,
+                   pages_used, page, stream)
     _check(kv_lib().w4a16_kv_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), num_free,
                                   block_table.data_ptr(), width, seq_lens.data_ptr(), token_start.data_ptr(),
                                   slot_map.data_ptr(), pages_used.data_ptr(), R, tokens, page,
@@ -199,6 +213,8 @@ def w4a16_kv_append(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, stream
         raise ValueError(f"k and v must have the same tokens, got {tokens} and {v_tokens}")
     dev = _same_gpu(k_cache, v_cache, k_scales, v_scales, slot_map, k, v)
     _dense(k_cache, v_cache, k_scales, v_scales, slot_map)
+    if _current_device() != dev:
+        return _on(dev, w4a16_kv_append, k, v, slot_map, k_cache, v_cache, k_scales, v_scales, stream)
     _check(kv_lib().w4a16_kv_append(k.data_ptr(), k_stride, v.data_ptr(), v_stride, slot_map.data_ptr(),
                                     ctypes.byref(c), tokens, _raw_stream(stream, dev)), "w4a16_kv_append")
 
@@ -231,6 +247,9 @@ def w4a16_kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq
         _dense(workspace)
     dev = _same_gpu(k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, out, q)
     _dense(k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, out)
+    if _current_device() != dev:
+        return _on(dev, w4a16_kv_attention, q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start,
+                   out, workspace, max_new, max_len, scale, window, stream)
     if max_len is None:
         max_len = inputs[3] * c.page
     _attention(ctypes.byref(c), inputs, q, block_table, seq_lens, token_start, out, workspace, max_new, max_len,
@@ -269,6 +288,8 @@ def w4a16_kv_dequant(k_cache, v_cache, k_scales, v_scales, pages, k_out, v_out, 
 def _dequant(c, inputs, n, k_out, v_out, stream):
     dev = _same_gpu(*inputs)
     _dense(*inputs)
+    if _current_device() != dev:
+        return _on(dev, _dequant, c, inputs, n, k_out, v_out, stream)
     _check(kv_lib().w4a16_kv_dequant(ctypes.byref(c), inputs[4].data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(),
                                      _raw_stream(stream, dev)), "w4a16_kv_dequant")
 
@@ -301,6 +322,8 @@ def kv_plan(ctx_lens, new_lens, free_pages, block_table, tokens: int, page: int,
     R, num_free, width = _plan_inputs(ctx_lens, new_lens, free_pages, block_table)
     dev = _same_gpu(ctx_lens, new_lens, free_pages, block_table)
     _dense(ctx_lens, new_lens, free_pages, block_table)
+    if _current_device() != dev:
+        return _on(dev, kv_plan, ctx_lens, new_lens, free_pages, block_table, tokens, page)
     out = ctx_lens.new_empty(2 * R + tokens + 2)      # (one allocation: its parts need no checks of their own)
     at = out.data_ptr()
     _check(kv_lib().w4a16_kv_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), num_free,
@@ -321,6 +344,9 @@ def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens,
     inputs = tokens, _, R, width = _attention_inputs(c, q, block_table, seq_lens, token_start)
     dev = _same_gpu(k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, q)
     _dense(k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start)
+    if _current_device() != dev:
+        return _on(dev, kv_attention, q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, max_new,
+                   max_len, scale, window)
     if max_len is None:
         max_len = width * c.page
     ref = ctypes.byref(c)
