@@ -135,6 +135,15 @@ def _cache(k_cache, v_cache, k_scales, v_scales) -> KVCache:
                    heads, page, dim)
 
 
+def _int32(names: str, *numbers) -> None:
+    """Refuses numbers that the C ABI's 32-bit integers cannot hold (ctypes would pass their low bits)."""
+    bits = 0
+    for n in numbers:
+        bits |= n
+    if not -1 <= bits >> 31 <= 0:       # (beside a negative one, which the library refuses, others may pass)
+        raise ValueError(f"{names} must fit 32 bits, got {numbers}")
+
+
 def _vector(t, name, n=None):
     """The length of an int32 vector (checked against n where given)."""
     if t.dtype != torch.int32:
@@ -180,6 +189,7 @@ def w4a16_kv_plan(ctx_lens, new_lens, free_pages, block_table, seq_lens, token_s
                   stream=None) -> None:
     """Block tables and slot maps of a step from request lengths (block_table [R, width] is updated in place)."""
     R, num_free, width = _plan_inputs(ctx_lens, new_lens, free_pages, block_table)
+    _int32("page", page)
     _vector(seq_lens, "seq_lens", R)
     _vector(token_start, "token_start", R + 1)
     tokens = _vector(slot_map, "slot_map")
@@ -222,6 +232,7 @@ def w4a16_kv_append(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, stream
 def w4a16_kv_attention_workspace_bytes(tokens: int, requests: int, max_new: int, max_len: int, window: int,
                                        q_heads: int, k_cache, v_cache, k_scales, v_scales) -> int:
     c = _cache(k_cache, v_cache, k_scales, v_scales)
+    _int32("tokens, requests, max_new, max_len, window, q_heads", tokens, requests, max_new, max_len, window, q_heads)
     return int(kv_lib().w4a16_kv_attention_workspace_bytes(tokens, requests, max_new, max_len, window, q_heads,
                                                            ctypes.byref(c)))
 
@@ -252,6 +263,7 @@ def w4a16_kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq
                    out, workspace, max_new, max_len, scale, window, stream)
     if max_len is None:
         max_len = inputs[3] * c.page
+    _int32("max_new, max_len, window", max_new, max_len, window)
     _attention(ctypes.byref(c), inputs, q, block_table, seq_lens, token_start, out, workspace, max_new, max_len,
                1.0 / math.sqrt(c.dim) if scale is None else scale, window, _raw_stream(stream, dev))
 
@@ -320,6 +332,7 @@ def kv_plan(ctx_lens, new_lens, free_pages, block_table, tokens: int, page: int,
         with _current(stream, ctx_lens):
             return kv_plan(ctx_lens, new_lens, free_pages, block_table, tokens, page)
     R, num_free, width = _plan_inputs(ctx_lens, new_lens, free_pages, block_table)
+    _int32("tokens, page", tokens, page)
     dev = _same_gpu(ctx_lens, new_lens, free_pages, block_table)
     _dense(ctx_lens, new_lens, free_pages, block_table)
     if _current_device() != dev:
@@ -349,6 +362,7 @@ def kv_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens,
                    max_len, scale, window)
     if max_len is None:
         max_len = width * c.page
+    _int32("max_new, max_len, window", max_new, max_len, window)
     ref = ctypes.byref(c)
     need = kv_lib().w4a16_kv_attention_workspace_bytes(tokens, R, max_new, max_len, window, q.shape[1], ref)
     out = torch.empty_like(q, memory_format=torch.contiguous_format)

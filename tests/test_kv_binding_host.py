@@ -81,3 +81,34 @@ def test_calls_run_on_the_tensors_gpu(library, current):
     for name, device, args in launches:
         assert device == 1 and args[-1] == 1001, name
     assert library.state["device"] == current
+
+
+@pytest.mark.parametrize("wide", [2 ** 31, 2 ** 32, 2 ** 32 + 1, 2 ** 40, -2 ** 31 - 1, -2 ** 32 + 5])
+def test_numbers_past_32_bits_are_refused(library, wide):
+    """Cut to their low bits, 2^32 tokens a request would be none (rows left unwritten) and a window of 2^32 + 1 be 1."""
+    cache, q, rows, slots, seq, start, table, one = step()
+    refuse = lambda what: pytest.raises(ValueError, match=f"{what}.* must fit 32 bits")  # noqa: E731
+    with refuse("page"):
+        w4.w4a16_kv_plan(seq, seq, one, table, seq, start, slots, one, wide)
+    for args in ((3, wide), (wide, 16)):
+        with refuse("tokens, page"):
+            w4.kv_plan(seq, seq, one, table, *args)
+    for kw in (dict(max_new=wide), dict(max_new=2, max_len=wide), dict(max_new=2, window=wide)):
+        with refuse("max_new, max_len, window"):
+            w4.w4a16_kv_attention(q, *cache, table, seq, start, q, None, **kw)
+        with refuse("max_new, max_len, window"):
+            w4.kv_attention(q, *cache, table, seq, start, **kw)
+    for at in range(6):
+        numbers = [3, 2, 2, 64, 0, 4]
+        numbers[at] = wide
+        with refuse("tokens, requests"):
+            w4.w4a16_kv_attention_workspace_bytes(*numbers, *cache)
+    assert library.calls == []
+
+
+def test_numbers_of_32_bits_reach_the_library(library):
+    cache, q, rows, slots, seq, start, table, one = step()
+    for n in (2 ** 31 - 1, -2 ** 31, -1):       # (what they mean is the library's to judge)
+        w4.w4a16_kv_attention(q, *cache, table, seq, start, q, None, n, max_len=n, window=n)
+        w4.w4a16_kv_plan(seq, seq, one, table, seq, start, slots, one, n)
+    assert len(library.calls) == 6
