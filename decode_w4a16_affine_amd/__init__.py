@@ -451,7 +451,7 @@ def pack(codes, stream=None):
 
 # ---- the paged 8-bit key/value cache (include/w4a16_kv.h) ------------------------
 
-from .kv import (KV_DIMS, KV_EXPORTS, KV_FP8, KV_INT8, KV_MAX_GROUP, KV_MAX_HEADS, KV_MAX_REQUESTS,  # noqa: E402
-                 KV_MAX_TOKENS, KV_MAX_WIDTH, KV_PAGES, KVCache, kv_attention, kv_cache, kv_dequant, kv_lib, kv_plan,
-                 w4a16_kv_append, w4a16_kv_attention, w4a16_kv_attention_workspace_bytes, w4a16_kv_dequant,
+from .kv import (KV_DIMS, KV_EXPORTS, KV_FP8, KV_INT8, KV_MAX_DEQUANT, KV_MAX_GROUP, KV_MAX_HEADS,  # noqa: E402
+                 KV_MAX_REQUESTS, KV_MAX_TOKENS, KV_MAX_WIDTH, KV_PAGES, KVCache, kv_attention, kv_cache, kv_dequant,
+                 kv_lib, kv_plan, w4a16_kv_append, w4a16_kv_attention, w4a16_kv_attention_workspace_bytes, w4a16_kv_dequant,
                  w4a16_kv_plan)

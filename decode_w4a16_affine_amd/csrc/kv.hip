@@ -655,7 +655,7 @@ w4a16_status_t w4a16_kv_dequant(const w4a16_kv_cache_t* cache, const int32_t* pa
                                 float* v_out, void* stream) {
   w4a16_status_t st = check_cache(cache);
   if (st != W4A16_OK) return st;
-  if (count < 0) return W4A16_ERR_SHAPE;
+  if (count < 0 || count > W4A16_KV_MAX_DEQUANT) return W4A16_ERR_SHAPE;      // (2^32 threads on a grid's axis)
   if (count == 0) return W4A16_OK;
   st = check_cache_pointers(cache);
   if (st != W4A16_OK) return st;

@@ -31,6 +31,7 @@ KV_MAX_TOKENS = 1 << 20     # W4A16_KV_MAX_TOKENS
 KV_MAX_HEADS = 1024         # W4A16_KV_MAX_HEADS
 KV_MAX_GROUP = 64           # W4A16_KV_MAX_GROUP
 KV_MAX_WIDTH = 1 << 22      # W4A16_KV_MAX_WIDTH
+KV_MAX_DEQUANT = (1 << 24) - 1   # W4A16_KV_MAX_DEQUANT
 
 KV_EXPORTS = ("w4a16_kv_plan", "w4a16_kv_append", "w4a16_kv_attention_workspace_bytes", "w4a16_kv_attention",
               "w4a16_kv_dequant")

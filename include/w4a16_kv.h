@@ -51,6 +51,7 @@ extern "C" {
 #define W4A16_KV_MAX_HEADS 1024
 #define W4A16_KV_MAX_GROUP 64
 #define W4A16_KV_MAX_WIDTH (1 << 22)
+#define W4A16_KV_MAX_DEQUANT ((1 << 24) - 1)    /* pages a w4a16_kv_dequant call */
 
 typedef enum w4a16_kv_type {
     W4A16_KV_INT8 = 0,
@@ -154,7 +155,7 @@ w4a16_status_t w4a16_kv_attention(const uint16_t *q, int64_t q_stride, const w4a
 /*
  * Values (code * scale, exact in fp32) of the pages pages[0 .. count):
  * k_out, v_out fp32 [count][H][P][D], both with tokens outermost.  A page
- * number outside the cache gives NaN.
+ * number outside the cache gives NaN.  count is at most W4A16_KV_MAX_DEQUANT.
  */
 w4a16_status_t w4a16_kv_dequant(const w4a16_kv_cache_t *cache, const int32_t *pages, int count, float *k_out,
                                 float *v_out, void *stream);

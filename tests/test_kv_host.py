@@ -144,6 +144,16 @@ def test_dequant_refuses_bad_arguments(L):
     assert dq(cache(k=None), None, 0, None, None, None) == OK
 
 
+def test_dequant_refuses_more_pages_than_a_launch_holds(L):
+    """2^24 pages of 256 threads are 2^32 on a grid's axis: an argument error, not a refused launch."""
+    text = header_text()
+    assert re.search(r"#define W4A16_KV_MAX_DEQUANT \(\(1 << 24\) - 1\)", text) and w4.KV_MAX_DEQUANT == 2 ** 24 - 1
+    for count in (2 ** 24, 2 ** 31 - 1):
+        assert L.w4a16_kv_dequant(cache(), A16, count, A16, A16, None) == ESHAPE
+    # (the largest count goes on to the pointers' checks)
+    assert L.w4a16_kv_dequant(cache(), None, 2 ** 24 - 1, A16, A16, None) == ENULL
+
+
 def test_binding_checks_shapes_before_the_library():
     bf, i32 = torch.bfloat16, torch.int32
     kc, vc, ks, vs = w4.kv_cache(4, 2, 64, 16, device="cpu")
