@@ -505,6 +505,7 @@ KvAttnArgs attention_args(const w4a16_kv_cache_t* cache, int tokens, int request
   // A call of one request of many new tokens is a prompt: without the launches
   // for requests of few it is 9 us shorter (it may still bring few, as tiles).
   a.split = requests > 1 || (int64_t)max_new * a.group <= kKvSplitRows;
+  a.by_token = tokens <= (int64_t)requests * a.split_tokens;
   const int rows = a.split_tokens * a.group;
   a.row_groups = rows <= 16 ? 1 : (rows + 31) / 32;
   a.chunk_shift = max_len <= 1024 ? 7 : max_len <= 4096 ? 8 : max_len <= 16384 ? 9 : 10;

@@ -285,7 +285,6 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
     for (int d = 0; d < DW; ++d) o[c][d] = kv_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
   const bool single = first == max(rows.end - 1, rows.begin) >> a.chunk_shift;     // one chunk holds all
-  const int max_rows = a.split_tokens * a.group;
   if (j0 < at_end) {
     load_keys(j0, page);
     load_values(j0, page);
@@ -404,7 +403,6 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
   const int d0 = 16 * DW * wave + 4 * g;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int row = row0 + 16 * c + x;
     if (out_at[c] < 0) continue;
     if (single) {
       const float inverse =
@@ -413,7 +411,7 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
 #pragma unroll
       for (int d = 0; d < DW; ++d) kv_store4(out + 16 * d, o[c][d], inverse);
     } else {
-      const size_t at = (((size_t)r * a.c.heads + kh) * max_rows + row) * a.chunks + block;
+      const size_t at = kv_part_row(a, out_at[c], r, rows.first) * a.chunks + block;
 #pragma unroll
       for (int d = 0; d < DW; ++d) *reinterpret_cast<kv_f32x4*>(part_o + at * D + d0 + 16 * d) = o[c][d];
       if (g == 0) {
@@ -447,7 +445,10 @@ __global__ __launch_bounds__(kKvJoinThreads) void kv_join_kernel(KvAttnArgs a, c
   const int first = rows.begin >> a.chunk_shift;
   const int count = (max(rows.end - 1, rows.begin) >> a.chunk_shift) - first + 1;
   if (count <= 1) return;
-  const size_t at = (((size_t)r * a.c.heads + kh) * max_rows + row) * a.chunks;
+  const int i = kv_token_of(a, row), t = rows.first + i;
+  if (t < 0 || t >= a.tokens) return;
+  const int out_row = t * a.q_heads + kh * a.group + row - i * a.group;
+  const size_t at = kv_part_row(a, out_row, r, rows.first) * a.chunks;
   // one thread a chunk (count <= kKvMaxChunks = the block's threads); threads
   // and slices go by the chunk's place in the cache, not by the group's first
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
@@ -493,9 +494,7 @@ __global__ __launch_bounds__(kKvJoinThreads) void kv_join_kernel(KvAttnArgs a, c
   if (slice > 0) return;
 #pragma unroll
   for (int s = 1; s < S; ++s) sum += s_o[s * (D / 4) + threadIdx.x];
-  const int i = kv_token_of(a, row), t = rows.first + i;
-  if (t < 0 || t >= a.tokens) return;
-  kv_store4(a.out + ((size_t)t * a.q_heads + kh * a.group + row - i * a.group) * D + d, sum, kv_inverse(ll));
+  kv_store4(a.out + (size_t)out_row * D + d, sum, kv_inverse(ll));
 }
 
 }  // namespace w4k

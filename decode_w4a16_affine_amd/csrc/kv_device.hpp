@@ -76,6 +76,7 @@ struct KvAttnArgs {
   int width, window, tokens, requests, max_new, max_len, q_heads, group;
   uint32_t group_inverse;      // ceil(2^16 / group): see kv_token_of
   bool split;                  // requests of few rows take the split form (else all take tiles)
+  bool by_token;               // its partial results lie by the step's tokens (else by request)
   // requests of few rows: log2 of the entries a chunk, chunks a row at most, row
   // groups a cache head, new tokens a request at most
   int chunk_shift, chunks, row_groups, split_tokens;
@@ -101,10 +102,17 @@ constexpr int kKvMaxChunks = 128;     // chunks of a row at most
 constexpr int kKvSplitRows = 64;      // requests of at most this many rows a cache head take the split form
 
 // A row and chunk's partial result: D floats of output, then these (the
-// maximum and four waves' sums).
+// maximum and four waves' sums).  Rows lie as in `out`, or as split_tokens tokens a
+// request where that is less (a step of many prompts' tokens): the rows that can
+// take the split form are at most either.
 constexpr int kKvPartStats = 5;
 inline size_t kv_partials(const KvAttnArgs& a) {
-  return a.split && a.chunks > 1 ? (size_t)a.requests * a.c.heads * a.split_tokens * a.group * a.chunks : 0;
+  const size_t by_request = (size_t)a.requests * a.split_tokens;
+  return a.split && a.chunks > 1 ? (a.by_token ? (size_t)a.tokens : by_request) * a.q_heads * a.chunks : 0;
+}
+// Row of the partial results of row out_row of `out`, which is of request r with first token row `first`.
+__device__ __forceinline__ size_t kv_part_row(const KvAttnArgs& a, int out_row, int r, int first) {
+  return a.by_token ? (size_t)out_row : out_row + ((int64_t)r * a.split_tokens - first) * a.q_heads;
 }
 
 // The tile form: waves of a workgroup, of which `share` take the same 32 rows

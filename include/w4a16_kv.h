@@ -115,7 +115,9 @@ w4a16_status_t w4a16_kv_append(const uint16_t *k, int64_t k_stride, const uint16
 
 /*
  * Bytes of workspace w4a16_kv_attention needs (0 is possible, and the answer
- * for invalid arguments).
+ * for invalid arguments): partial results of D + 5 floats for each of up to 128 chunks
+ * of max_len entries and each of min(T, R * min(max_new, 64 / (HQ / H))) * HQ rows,
+ * and, for few prompt tokens behind a long cache, of D + 2 for each part and row.
  */
 size_t w4a16_kv_attention_workspace_bytes(int tokens, int requests, int max_new, int max_len, int window,
                                           int q_heads, const w4a16_kv_cache_t *cache);

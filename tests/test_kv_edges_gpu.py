@@ -153,3 +153,27 @@ def test_plan_gives_no_slot_in_pages_outside_every_cache(page):
     torch.cuda.synchronize()
     assert table.tolist() == [[top, 2 * top, -1], [top - 1, top + 3, -1], [2 ** 31 - 1, -1, -1]]
     assert slots.tolist() == [-1, -1, -1, 2 ** 31 - 1, -1, -1] and used.tolist() == [2]
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("window", [0, 400])
+def test_rows_do_not_depend_on_where_partial_results_lie(kind, window):
+    """Partial results are placed by token or by request, whichever needs less: rows are the same in both."""
+    say("placement of partial results", kind, window)
+    lens = [1026, 700, 2050, 900, 333]
+    # tokens, and with 16 or 3 a request, up to 80 or 15 of them by token; tiles beside them
+    for news, max_new, sizes in (([5, 1, 16, 40, 2], 40, (64, 65, 80, 81, 300)), ([1, 3, 1, 2, 1], 3, (8, 15, 16, 200)),
+                                 ([1, 3, 1, 2, 1], 16, (8, 80, 81))):
+        p = Problem(71, kind, 2, 4, 128, 64, lens, news)
+        want, tol = p.want(1 / math.sqrt(128), window)
+        q = torch.cat([p.q, torch.zeros((300, 8, 128), dtype=torch.bfloat16)]).cuda()
+        few = [t for t in range(p.T) if not p.start[3] <= t < p.start[4] or news[3] <= 16]
+        first = None
+        for T in sizes:
+            out = run_into(p, q[:T], torch.full((T, 8, 128), 5.0, dtype=torch.bfloat16, device="cuda"), max_new,
+                           window=window)
+            close(out[:p.T], want, tol)
+            assert (out[p.T:] == 5).all()
+            rows = out[few].view(torch.int16)        # (the order of the tiles' sums may depend on the sizes)
+            first = rows if first is None else first
+            assert torch.equal(rows, first), T

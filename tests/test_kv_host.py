@@ -132,6 +132,24 @@ def test_attention_workspace_rules(L):
         assert att(A16, need - 1) == EWS and att(None, need) == EWS and att(A16 + 8, need) == EALIGN
 
 
+def test_attention_workspace_is_sized_by_the_rows_that_can_need_it(L):
+    """(D + 5) floats a row and chunk, for the rows of T tokens or of R requests of 64 / G tokens, whichever is less."""
+    def ws(T, R, mn, ml=4096, HQ=32, heads=8, **cache_args):
+        return L.w4a16_kv_attention_workspace_bytes(T, R, mn, ml, 0, HQ, cache(heads=heads, **cache_args))
+
+    row = 133 * 4               # D 128
+    assert ws(256, 256, 1) == 256 * 32 * 16 * row                # 4096 entries: chunks of 256
+    assert ws(256, 256, 16) == ws(256, 256, 1)                   # a bound of more tokens than there are
+    assert ws(600, 256, 4) == 600 * 32 * 16 * row
+    assert ws(1024, 256, 4) == 1024 * 32 * 16 * row == ws(1500, 256, 4)
+    # single tokens beside a prompt chunk, behind histories of up to 131072 (64 chunks): not 4.5 GB
+    assert ws(2255, 256, 2000, ml=131072) == 2255 * 32 * 64 * row
+    assert ws(8192, 256, 2000, ml=131072) == 256 * 16 * 32 * 64 * row
+    # statistics end on 16 bytes; one chunk needs nothing
+    assert ws(1, 1, 1, HQ=1, heads=1) == (16 * 128 + (16 * 5 + 3) // 4 * 4) * 4
+    assert ws(256, 256, 1, ml=128) == 0
+
+
 def test_dequant_refuses_bad_arguments(L):
     for args, want in BAD_CACHES:
         assert L.w4a16_kv_dequant(cache(**args), A16, 3, A16, A16, None) == want, args
