@@ -15,7 +15,7 @@ import torch
 import decode_w4a16_affine_amd as w4
 import kv_reference as ref
 from parity import say
-from test_kv_gpu import Problem, i32
+from test_kv_gpu import Problem, i32, run_append, same
 
 pytestmark = pytest.mark.gpu
 
@@ -177,3 +177,80 @@ def test_rows_do_not_depend_on_where_partial_results_lie(kind, window):
             rows = out[few].view(torch.int16)        # (the order of the tiles' sums may depend on the sizes)
             first = rows if first is None else first
             assert torch.equal(rows, first), T
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("D,G", [(64, 8), (128, 4), (256, 5)])
+@pytest.mark.parametrize("window", [0, 1, 258, 514, 700])
+def test_rows_of_candidates_that_cross_chunks_and_windows(kind, D, G, window):
+    """Verify rows equal single-token calls bit for bit where the candidates' entries end, or their windows begin, in
+    different chunks (up to 4096 entries, chunks have 256: ends at 512, 1024 and 2048; begins at 256 and 512)."""
+    say("candidates across chunks", kind, D, G, window)
+    lens, news = [1026, 514, 2050, 40], [5, 4, 3, 1]
+    p = Problem(59, kind, 2, G, D, 64, lens, news)
+    cache = p.device()
+    whole = p.run(cache=cache, window=window)
+    q, table = p.q.cuda(), i32(p.table)
+    for r, (n, k) in enumerate(zip(lens, news)):
+        for i in range(k):
+            t = int(p.start[r]) + i
+            one = w4.kv_attention(q[t:t + 1], *cache, table[r:r + 1], i32([n - k + i + 1]), i32([0, 1]), 1,
+                                  window=window)
+            assert torch.equal(one[0].view(torch.int16), whole[t].view(torch.int16)), (r, i)
+
+
+def test_more_requests_than_one_grid_axis():
+    """33000 single tokens (requests past 32768 lie on another axis of the launch) give the rows of smaller calls."""
+    R, pages, page, D = 33000, 50, 16, 64
+    say("attention of", R, "requests")
+    rng = np.random.default_rng(61)
+    p = Problem(61, "int8", 1, 1, D, page, [pages * page], [1])
+    cache = p.device()
+    lens = rng.integers(1, 300, R)
+    table = rng.integers(0, pages, (R, 19))
+    q = torch.from_numpy(rng.standard_normal((R, 1, D))).to(torch.bfloat16).cuda()
+    start = np.arange(R + 1)
+    whole = w4.kv_attention(q, *cache, i32(table), i32(lens), i32(start), 1)
+    for a, b in ((0, 20000), (20000, R)):
+        part = w4.kv_attention(q[a:b], *cache, i32(table[a:b]), i32(lens[a:b]), i32(start[:b - a + 1]), 1)
+        assert torch.equal(part.view(torch.int16), whole[a:b].view(torch.int16)), a
+    at = [0, 5, 32766, 32767, 32768, 32769, R - 2, R - 1]
+    want, tol = ref.attention(q[at].cpu().double().numpy(), p.kc, p.ks, p.vc, p.vs, table[at], lens[at],
+                              np.arange(len(at) + 1), 0.125, 0)
+    close(whole[at], want, tol)
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("D,page,singles", [(64, 16, 700), (128, 256, 90), (256, 64, 200)])
+def test_append_of_over_4096_tokens(kind, D, page, singles):
+    """Blocks that look at 64 tokens: a long run, runs of 1 to 5 tokens side by side, skipped slots, another long run."""
+    H, T = 2, 4500
+    say("append", kind, D, page, T)
+    rng = np.random.default_rng(67 + page)
+    pages = T // page + singles + 8
+    state = [*ref.random_codes(rng, pages, H, page, D, kind), *ref.random_codes(rng, pages, H, page, D, kind)]
+    ids = iter(rng.permutation(pages))
+    slots = []
+
+    def run(n, off):
+        while n > 0:
+            here = min(n, page - off)
+            p = next(ids)
+            slots.extend(p * page + off + i for i in range(here))
+            n, off = n - here, 0
+
+    run(1500, 5)
+    for s in range(singles):
+        run(1 + s % 5, int(rng.integers(0, page - 5)))
+        if s % 11 == 0:
+            slots.append(-1)
+    run(T - len(slots), page - 3)
+    slots = np.array(slots)
+    x_k, x_v = (torch.from_numpy(rng.standard_normal((T, H, D)) * np.exp2(rng.integers(-3, 4, (T, 1, 1)))
+                                 ).to(torch.bfloat16) for _ in range(2))
+    want = [a.copy() for a in state]
+    ref.append(x_k.double().numpy(), slots, want[0], want[1], kind)
+    ref.append(x_v.double().numpy(), slots, want[2], want[3], kind)
+    got = run_append(x_k, x_v, slots, state, kind)
+    for name, a, b in zip(("k codes", "k scales", "v codes", "v scales"), got[:4], want):
+        assert same(a, b), name
