@@ -150,6 +150,16 @@ def test_attention_workspace_is_sized_by_the_rows_that_can_need_it(L):
     assert ws(256, 256, 1, ml=128) == 0
 
 
+def test_attention_refuses_a_missing_or_small_workspace(L):
+    """4096 entries lie in several chunks: a workspace is needed, and its absence refused."""
+    need = L.w4a16_kv_attention_workspace_bytes(4, 4, 1, 4096, 0, 8, cache())
+    assert need > 0
+
+    def att(ws, size):
+        return L.w4a16_kv_attention(A16, 1024, cache(), A16, 64, A16, A16, A16, 1.0, 0, 4, 4, 1, 4096, 8, ws, size, None)
+    assert att(A16, need - 1) == EWS and att(A16, 0) == EWS and att(None, need) == EWS and att(A16 + 8, need) == EALIGN
+
+
 def test_dequant_refuses_bad_arguments(L):
     for args, want in BAD_CACHES:
         assert L.w4a16_kv_dequant(cache(**args), A16, 3, A16, A16, None) == want, args
