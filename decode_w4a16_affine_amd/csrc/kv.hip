@@ -23,7 +23,9 @@ __device__ __forceinline__ int kv_length(int n) { return min(max(n, 0), kKvMaxLe
 // request are a reduction over all earlier lengths (a few strided loads a
 // thread, from L2), so one launch does everything and no block waits for
 // another.  Bound by its one launch and three dependent loads: 40 requests of
-// 248 columns 3.5 us, 701 of 956 columns with 13k new tokens 5.1 (2.7 MB).
+// 248 columns 3.6 us, 701 of 956 columns with 13k new tokens 5.3 (2.7 MB).  (The
+// reduction grows with the square of the requests: of a whole call's time nothing
+// shows up to 4096 requests, 32768 take 64 us, 262144 2.8 ms.)
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(kKvThreads) void kv_plan_kernel(const int32_t* __restrict__ ctx_lens,
                                                              const int32_t* __restrict__ new_lens,
@@ -116,8 +118,12 @@ __global__ __launch_bounds__(kKvThreads) void kv_plan_kernel(const int32_t* __re
 // and head.  A single run is the whole block's; several (single tokens of
 // many requests) go to the block's waves in turn, without barriers.
 // Bound: HBM for prompts, 3 bytes a number: 11.8k tokens, 8 heads of 128, 72 MB,
-// 23 us, 3.1 TB/s (a block waits for its maximum before it writes); the launch and
-// two dependent loads for tokens: 64 requests 5.9 us, 24 verify batches 5.1.
+// 23 us, 3.2 TB/s (a block waits for its maximum before it writes).  Values of runs
+// over 64 tokens are read again for each 64 of them that are turned: in pages of 128
+// and 256 the same prompts take 30 and 31 us.  Single tokens: the launch and four
+// dependent loads (the slot, the run's slots, the row and the old scale, the
+// value words that the token shares with others): 64 requests 5.7 us, 24 verify
+// batches 5.1.
 // ---------------------------------------------------------------------------
 
 // Codes of four bf16 entries under factor f = 1 / scale (0 where the scale is NaN).
@@ -597,7 +603,11 @@ w4a16_status_t w4a16_kv_append(const uint16_t* k, int64_t k_stride, const uint16
   if (!k || !v || !slot_map) return W4A16_ERR_NULL;
   if (!kv_aligned(k, 16) || !kv_aligned(v, 16) || !kv_aligned(slot_map, 4)) return W4A16_ERR_ALIGN;
   // Tokens a block looks at: one while blocks are few, more where most tokens
-  // continue a run (11.8k tokens of three prompts in pages of 64, 16 / 32 / 64: 28 / 32 / 24 us)
+  // continue a run.  Measured (us, 1 / 4 / 16 / 64 tokens, 8 heads of 128): 11.8k tokens of
+  // three prompts in pages of 64, 210 / 41 / 31 / 23; 2000 of one, 43 / 15 / 8 / 11; 700
+  // verify batches of 5, 52 / 39 / 25 / 30.  The rule knows tokens, not runs, and
+  // single tokens of many requests want fewer: 64 of them 5 / 7 / 21 / 79, 512 23 / 14 /
+  // 21 / 69, 4000 156 / 68 / 72 / 101.
   const int span = tokens <= 256 ? 1 : tokens <= 4096 ? 16 : 64;
   with_cache_form(cache, [&](auto d, auto type) {
     hipLaunchKernelGGL((kv_append_kernel<decltype(d)::value, decltype(type)::value>),

@@ -60,10 +60,13 @@
 // 3 requests of 90001 to 120001 entries, 8 heads of 128, int8, 4 query heads
 // each: 645 MB, 114 us, 5.7 TB/s (the loads alone 5.9).  48 of 300 to 6000, E4M3,
 // pages of 32: 313 MB, 60 us, 5.2 TB/s.  With less to read, the start of a
-// workgroup (3 us until its first entries arrive) and the step's latency (about
-// 2 us for 128 entries of two heads' 256 elements and 30 rows): 16 verify batches
-// of 2 to 6 tokens in 1000 to 9000 entries, 70 MB, 30 us; one token in 717
-// entries 6.1 us and the join 3.1.
+// workgroup (3 us until its first entries arrive) and the latency of its steps: one
+// token in 717 entries, a step a workgroup, 6.3 us and the join 3.6.  16 verify
+// batches of 2 to 6 tokens in 1000 to 9000 entries, 10 heads of 256 over 2, 70 MB: 25.6
+// us and the join 4.5.  A workgroup that has entries lives 18 us on average there (by
+// its wave cycles), for four steps of 128 entries and 12 to 30 rows; its waves wait for
+// 37% of that, and vector, matrix and LDS units are busy for 18, 7 and 10% of the 25.6
+// us.  What makes up the 8 us between that life and the kernel's has not been measured.
 #pragma once
 
 #include <type_traits>
@@ -248,7 +251,7 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
   // this lane's rows: queries (in the keys' order) and positions
   kv_bf16x8 q[Q_LDS ? 1 : NC][2 * KC];
   KvLaneRows<NC> lr;
-  int out_at[NC];      // row of `out` (tokens * query heads <= 2^20 * 2^16 rows; see the host's check), or -1
+  int out_at[NC];      // row of `out` (tokens * query heads < 2^31: see the host's check), or -1
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int row = min(row0 + 16 * c + x, live - 1);

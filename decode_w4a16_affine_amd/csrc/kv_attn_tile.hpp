@@ -22,21 +22,27 @@
 // values of its half of the head's elements.  One buffer and two barriers: before
 // the first, the waves score and publish maxima; between them they write
 // weights, this tile's values and the next tile's keys.  (One wave for 32 rows:
-// 246 us instead of 166 for a prompt of 4099 tokens, 10 heads of 256.)  With int8
-// codes the conversions need registers that only eight waves (two pieces each
-// to convert instead of four) leave; four reloaded the queries from scratch
-// memory every tile (515 us instead of 207).
+// 246 us where two took 166, before operands were read ahead; a prompt of 4099
+// tokens, 10 heads of 256.)  With int8 codes the conversions need registers that
+// only eight waves (two pieces each to convert instead of four) leave; four
+// reloaded the queries from scratch memory every tile (515 us where eight took 207,
+// at that time).
 //
-// Bound and measured: the matrix products are 2 x 32 instructions of 16 cycles a
-// wave and tile, the softmax, the conversions and LDS (a wave reads 32 KB a tile)
-// as long each, and two waves a SIMD, which registers limit it to, overlap them
-// in part.  A tile of a lone workgroup takes 1.65 us for heads of 128 and 1.8 for
-// 256 (the products alone 0.43), of two that share a CU 2.1 and 2.25.  Four
+// Bound and measured.  The matrix products are 2 x 32 instructions of 16 cycles a
+// wave and tile, 1024 cycles; beside them a wave issues about 340 vector
+// instructions a tile for heads of 128, 1370 cycles, and reads 32 KB from LDS.  Four
 // prompt chunks of 200 to 2000 tokens behind up to 12000, 32 heads of 128 over 8,
-// int8: 604 us, 845 TFLOP/s.  A prompt of 4099 tokens, 10 heads of 256 over 2, E4M3:
-// 130 us, 660 TFLOP/s, as long as the 65 tiles of its last rows take.  (Eight
-// waves for heads of 128, 256 rows, half the conversions: the same 604 us, and
-// 30% slower where workgroups are few.)
+// int8: 600 us, 850 TFLOP/s; by counters the SIMDs' vector units are busy for 46% of
+// the launch and the matrix units for 35%, LDS for 26% without a bank conflict: two
+// waves a SIMD, which registers limit it to, hardly overlap the two.  (Most of the
+// vector work is the softmax's, not the conversions': eight waves for heads of 128,
+// 256 rows, halve these and took the same time, and 30% more where workgroups are
+// few.)  A tile of a lone workgroup takes 1.65 us for heads of 128 and 1.8 for 256
+// (the products alone 0.43), of two that share a CU 2.1 and 2.25.  A prompt of 4099
+// tokens, 10 heads of 256 over 2, E4M3: 131 us, 660 TFLOP/s, as long as the 65 tiles
+// of its last rows take, while a workgroup walks 33 on average (vector 28%, matrix
+// 27%).  The same in int8: 165 us; eight waves of 254 registers leave room for one
+// workgroup a CU, of which there are 328 for 256 CUs.
 #pragma once
 
 #include "kv_attn_common.hpp"

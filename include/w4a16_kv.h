@@ -108,6 +108,11 @@ w4a16_status_t w4a16_kv_plan(const int32_t *ctx_lens, const int32_t *new_lens, c
  * skipped.  A run with an infinity or NaN sets the page and head's scale to
  * NaN and its codes to 0 (so everything that reads that page sees NaN until
  * it is begun again); a NaN scale stays.
+ * A page's scale, and so its codes, depends on how its tokens arrived: on the
+ * largest entry of all runs written to it since it was begun, candidates that
+ * were rejected later included.  The codes of accepted tokens can therefore
+ * differ from those of single-token steps, as they can between a prompt and
+ * single tokens, by the rounding of a coarser step.
  */
 w4a16_status_t w4a16_kv_append(const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
                                const int32_t *slot_map, const w4a16_kv_cache_t *cache, int tokens,
@@ -140,12 +145,14 @@ size_t w4a16_kv_attention_workspace_bytes(int tokens, int requests, int max_new,
  * Softmax statistics and sums in fp32, weights rounded to fp16, keys, values
  * and queries exact.  A weight is held times its page's value scale: beside
  * values beyond about 10^6 the weights of a page of zeros (scale 2^-100) can
- * underflow.  Requests of min(n, max_new) * HQ / H <= 64 rows take one form, whose rows
- * depend on their own query, position and entries and on max_len alone: they
- * are bitwise equal in any batch and for any number of new tokens up to that
- * bound (a verify batch gives the rows of single-token calls).  Requests of more
- * take another, as does a call of one request with max_new * HQ / H > 64 (the
- * order of whose sums may depend on the call's sizes, never on chance).
+ * underflow.  A row whose logits are all -infinity is 0.
+ * Requests of min(n, max_new) * HQ / H <= 64 rows take one form, whose rows
+ * depend on their own query, position and entries and on max_len alone: over the
+ * same cache they are bitwise equal in any batch and for any number of new tokens
+ * up to that bound (a verify batch gives the rows of single-token calls; what it
+ * appended may differ, see w4a16_kv_append).  Requests of more take another, as
+ * does a call of one request with max_new * HQ / H > 64 (the order of whose sums
+ * may depend on the call's sizes, never on chance).
  * (T / (64 / (HQ / H)) + R) * H must not exceed 2^22 (the launch's size).
  */
 w4a16_status_t w4a16_kv_attention(const uint16_t *q, int64_t q_stride, const w4a16_kv_cache_t *cache,
