@@ -5,7 +5,8 @@ arguments: torch tensors become device pointers and the current HIP stream;
 every step of the computation runs in the library's kernels.  If the library
 is not built, importing works but every call raises.
 
-Tensor conventions (all on the same GPU, contiguous):
+Tensor conventions (all on the same GPU, which has to be the current one, since
+launches go there; contiguous):
   x, scales, biases, bf16 outputs : torch.bfloat16
   qw                              : torch.int32 (the uint32 words, bit for bit)
   ids, argmax, rows               : torch.int32
