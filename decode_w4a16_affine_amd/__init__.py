@@ -456,3 +456,8 @@ from .kv import (KV_DIMS, KV_EXPORTS, KV_FP8, KV_INT8, KV_MAX_DEQUANT, KV_MAX_GR
                  KV_MAX_REQUESTS, KV_MAX_TOKENS, KV_MAX_WIDTH, KV_PAGES, KVCache, kv_attention, kv_cache, kv_dequant,
                  kv_lib, kv_plan, w4a16_kv_append, w4a16_kv_attention, w4a16_kv_attention_workspace_bytes, w4a16_kv_dequant,
                  w4a16_kv_plan)
+
+# ---- what a serving step runs beside them (include/w4a16_step.h) -----------------
+
+from .step import (ROPE_INTERLEAVED, ROPE_MAX_AXES, ROPE_NORM, STEP_EXPORTS, qk_norm_rope, step_lib,  # noqa: E402
+                   w4a16_qk_norm_rope)

@@ -1,0 +1,159 @@
+"""Python binding of what a serving step runs beside the products and the cache (include/w4a16_step.h).
+
+Same conventions as kv.py: C-ABI names, tensors in, dtype and shape checks before any pointer reaches the library, the
+current stream of torch (of the tensors' GPU, which need not be the current one) unless one is given, no fallback.
+
+Tensor conventions (all on the same GPU; contiguous unless said otherwise):
+  q, k, outputs           : torch.bfloat16 [T, heads, D]; q, k may be parts of wider token rows (only their last two
+                            dimensions are dense), and so may q_out, k_out
+  norm weights            : torch.bfloat16 [D]
+  inv_freq                : torch.float32 [rot / 2]
+  positions               : torch.int32 [T], or [axes, T] with sections
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _check, _dtype, _shape
+from . import lib as _base_lib
+from .kv import _current, _current_device, _current_stream, _dense, _on, _raw_stream, _rows, _same_gpu
+
+ROPE_NORM = 1             # W4A16_ROPE_NORM
+ROPE_INTERLEAVED = 2      # W4A16_ROPE_INTERLEAVED
+ROPE_MAX_AXES = 4         # W4A16_ROPE_MAX_AXES
+
+STEP_EXPORTS = ("w4a16_qk_norm_rope",)
+
+_vp = ctypes.c_void_p
+_int = ctypes.c_int
+_i64 = ctypes.c_int64
+_float = ctypes.c_float
+
+_lib = None
+
+
+def step_lib() -> ctypes.CDLL:
+    """libw4a16.so with the prototypes of a serving step's operators."""
+    global _lib
+    if _lib is None:
+        L = _base_lib()
+        L.w4a16_qk_norm_rope.restype = _int
+        L.w4a16_qk_norm_rope.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _float, _vp, _vp, ctypes.POINTER(_int), _int, _vp,
+                                         _i64, _vp, _i64, _float, _int, _int, _int, _int, _int, _int, _vp]
+        _lib = L
+    return _lib
+
+
+# ---- norms of queries and keys, rotation ------------------------------------------
+
+def _head_rows(q, k):
+    """(tokens, D, [stride, heads] of q and of k); q or k may be None."""
+    x = k if q is None else q
+    if x is None:
+        raise ValueError("q and k are both None")
+    if x.dim() != 3:
+        raise ValueError(f"q and k must be 3-D [T, heads, D], got {list(x.shape)}")
+    dim = x.shape[2]
+    parts = [(0, 0, 0) if t is None else (*_rows(t, None, dim, name), t.shape[1]) for t, name in ((q, "q"), (k, "k"))]
+    if q is not None and k is not None and parts[0][0] != parts[1][0]:
+        raise ValueError(f"q and k must have the same tokens, got {parts[0][0]} and {parts[1][0]}")
+    return x.shape[0], dim, parts[0][1:], parts[1][1:]
+
+
+def _rotation(inv_freq, positions, sections, tokens):
+    """(rot, axes, sections as a C array or None)."""
+    if inv_freq is None:
+        if positions is not None or sections is not None:
+            raise ValueError("positions and sections need inv_freq")
+        return 0, 1, None
+    if positions is None:
+        raise ValueError("inv_freq needs positions")
+    _dtype(inv_freq, torch.float32, "inv_freq")
+    if inv_freq.dim() != 1:
+        raise ValueError(f"inv_freq must be 1-D [rot / 2], got {list(inv_freq.shape)}")
+    _dtype(positions, torch.int32, "positions")
+    half = inv_freq.shape[0]
+    if sections is None:
+        if positions.shape != (tokens,):
+            _shape(positions, (tokens,), "positions")
+        return 2 * half, 1, None
+    axes = len(sections)
+    if not 1 <= axes <= ROPE_MAX_AXES:
+        raise ValueError(f"1 to {ROPE_MAX_AXES} sections, got {axes}")
+    if min(sections) < 0 or sum(sections) != half:
+        raise ValueError(f"sections must be pair counts that sum to {half}, got {list(sections)}")
+    _shape(positions, (axes, tokens), "positions")
+    return 2 * half, axes, (_int * axes)(*sections)
+
+
+def _weight(w, dim, name):
+    if w is not None:
+        _dtype(w, torch.bfloat16, name)
+        _shape(w, (dim,), name)
+    return w
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _given(*ts):
+    return [t for t in ts if t is not None]
+
+
+def w4a16_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, eps: float = 1e-6,
+                       weight_offset: float = 0.0, norm: bool = True, interleaved: bool = False, sections=None,
+                       stream=None) -> None:
+    """q_out, k_out = q, k [T, heads, D], each head normed (norm) and its first 2 * len(inv_freq) elements rotated.
+
+    A weight None is a factor of 1; q (with q_out) or k (with k_out) None is left out; inv_freq None rotates nothing;
+    sections gives the pairs of each axis of positions [axes, T].  q_out may be q and k_out may be k."""
+    shapes = _head_rows(q, k)
+    tokens, dim, (_, q_heads), (_, k_heads) = shapes
+    outs = []
+    for x, out, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if (x is None) != (out is None):
+            raise ValueError(f"{name} goes with its input")
+        if out is not None and out.shape != x.shape:
+            _shape(out, x.shape, name)
+        outs.append((0, 0) if out is None else _rows(out, x.shape[1], dim, name))
+    _rope(shapes, q, k, q_weight, k_weight, inv_freq, positions, q_out, outs[0][1], k_out, outs[1][1], eps, weight_offset,
+          norm, interleaved, sections, stream)
+
+
+def _rope(shapes, q, k, q_weight, k_weight, inv_freq, positions, q_out, qo_stride, k_out, ko_stride, eps, weight_offset,
+          norm, interleaved, sections, stream):
+    tokens, dim, (q_stride, q_heads), (k_stride, k_heads) = shapes
+    _weight(q_weight, dim, "q_weight")
+    _weight(k_weight, dim, "k_weight")
+    rot, axes, sec = _rotation(inv_freq, positions, sections, tokens)
+    small = _given(q_weight, k_weight, inv_freq, positions)
+    dev = _same_gpu(*_given(q, k, q_out, k_out), *small)
+    _dense(*small)
+    if _current_device() != dev:
+        return _on(dev, _rope, shapes, q, k, q_weight, k_weight, inv_freq, positions, q_out, qo_stride, k_out, ko_stride,
+                   eps, weight_offset, norm, interleaved, sections, stream)
+    _check(step_lib().w4a16_qk_norm_rope(_ptr(q), q_stride, _ptr(k), k_stride, _ptr(q_weight), _ptr(k_weight),
+                                         weight_offset, _ptr(inv_freq), _ptr(positions), sec, axes, _ptr(q_out),
+                                         qo_stride, _ptr(k_out), ko_stride, eps,
+                                         (ROPE_NORM if norm else 0) | (ROPE_INTERLEAVED if interleaved else 0), tokens,
+                                         q_heads, k_heads, dim, rot, _raw_stream(stream, dev)), "w4a16_qk_norm_rope")
+
+
+# ---- allocating conveniences (torch allocates; the library computes) ------------
+
+def qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None, eps: float = 1e-6,
+                 weight_offset: float = 0.0, norm: bool = True, interleaved: bool = False, sections=None, stream=None):
+    """(q_out, k_out), dense and new (see w4a16_qk_norm_rope)."""
+    if stream is not None:
+        with _current(stream, k if q is None else q):
+            return qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, weight_offset, norm, interleaved,
+                                sections)
+    shapes = _head_rows(q, k)
+    q_out, k_out = (None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k))
+    dim = shapes[1]
+    _rope(shapes, q, k, q_weight, k_weight, inv_freq, positions, q_out, shapes[2][1] * dim, k_out, shapes[3][1] * dim, eps,
+          weight_offset, norm, interleaved, sections, None)
+    return q_out, k_out

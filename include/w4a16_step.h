@@ -1,0 +1,60 @@
+/*
+ * w4a16_step.h -- what a serving step of libw4a16.so (gfx950) runs beside the
+ * products (w4a16.h) and the paged 8-bit cache (w4a16_kv.h):
+ *
+ *   w4a16_qk_norm_rope         per layer, between the q/k/v products and w4a16_kv_append:
+ *                              norms of queries and keys for each head, positions rotated in
+ *
+ * Conventions: those of w4a16.h -- device pointers (host ones are named as such), `stream` a
+ * hipStream_t as void*, nothing allocated, no state, no synchronization, argument
+ * errors before anything is enqueued, deterministic, re-entrant.  Lengths,
+ * positions and sampling parameters are read on the device, so the calls can be
+ * captured in a graph and replayed as these change.  Sizes 0 succeed without work.
+ */
+#ifndef W4A16_STEP_H
+#define W4A16_STEP_H
+
+#include "w4a16_kv.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define W4A16_ROPE_MAX_AXES 4
+#define W4A16_ROPE_NORM 1            /* flags of w4a16_qk_norm_rope */
+#define W4A16_ROPE_INTERLEAVED 2
+
+/*
+ * Norm and rotation of a step's queries q [T][HQ][D] and keys k [T][H][D] (bf16,
+ * token rows q_stride and k_stride elements apart) into q_out and k_out (bf16,
+ * rows q_out_stride and k_out_stride apart):
+ *   y = x / sqrt(mean(x^2) + eps) * (weight + weight_offset)     over a head's D elements
+ * with W4A16_ROPE_NORM (without it y = x; a NULL weight is a factor of 1), then pair i
+ * of the first `rot` elements,
+ *   (y[i], y[i + rot / 2])  or with W4A16_ROPE_INTERLEAVED  (y[2i], y[2i + 1]),
+ * turned by the angle p * inv_freq[i]: (a cos - b sin, a sin + b cos).  The other
+ * elements stay y.  p is positions[t], or with several axes positions[axis][t] of the
+ * axis whose section pair i lies in (sections: a HOST array of `axes` pair counts that
+ * sum to rot / 2, in order; NULL with one axis).
+ *   q_weight, k_weight  bf16 [D];  inv_freq  fp32 [rot / 2];  positions  int32 [axes][T]
+ * Squares are summed, factors applied and pairs turned in fp32; an angle is reduced to one
+ * turn in fp64, exact to 2^-24 of a turn for every int32 position; one rounding to bf16
+ * at the end.  H 0 (a layer that reads another's keys) and HQ 0 are allowed, as is rot 0
+ * (no rotation; inv_freq and positions may be NULL).
+ * q_out may be q and k_out may be k (with the same stride); otherwise outputs do not
+ * overlap inputs.
+ * D 64, 128 or 256; rot a multiple of 8, at most D; T <= 2^20; HQ, H <= 2^16.
+ * Alignment: q, k, outputs, weights and inv_freq 16 bytes, positions 4, strides multiples of 8 elements.
+ */
+w4a16_status_t w4a16_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                                  const uint16_t *q_weight, const uint16_t *k_weight, float weight_offset,
+                                  const float *inv_freq, const int32_t *positions, const int *sections, int axes,
+                                  uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
+                                  float eps, int flags, int tokens, int q_heads, int k_heads, int dim, int rot,
+                                  void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* W4A16_STEP_H */
