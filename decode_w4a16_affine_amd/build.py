@@ -41,6 +41,7 @@ UNITS = [(f"inst_m{m}", "inst.hip", [f"-DW4K_M={m}"]) for m in range(1, 9)] + [
     ("kv", "kv.hip", []),
     # what a serving step runs beside them (include/w4a16_step.h)
     ("rope", "rope.hip", []),
+    ("sample", "sample.hip", []),
     # (matrix results in VGPRs here too: the softmax works on them between the products)
 ] + [(f"kv_attention_d{d}", "kv_attention.hip", [f"-DW4K_D={d}", "-mllvm", "-amdgpu-mfma-vgpr-form"])
      for d in (64, 128, 256)]

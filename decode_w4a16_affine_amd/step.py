@@ -9,6 +9,8 @@ Tensor conventions (all on the same GPU; contiguous unless said otherwise):
   norm weights            : torch.bfloat16 [D]
   inv_freq                : torch.float32 [rot / 2]
   positions               : torch.int32 [T], or [axes, T] with sections
+  logits                  : torch.float32 or torch.bfloat16 [M, N], rows may be parts of wider ones
+  uniforms, temperature, top_p, min_p, share : torch.float32 [M];  top_k, tokens : torch.int32 [M]
 """
 from __future__ import annotations
 
@@ -16,15 +18,18 @@ import ctypes
 
 import torch
 
-from . import _check, _dtype, _shape
+from . import OUT_BF16, OUT_F32, _check, _dtype, _shape
 from . import lib as _base_lib
-from .kv import _current, _current_device, _current_stream, _dense, _on, _raw_stream, _rows, _same_gpu
+from .kv import _current, _current_device, _dense, _int32, _on, _raw_stream, _rows, _same_gpu
 
 ROPE_NORM = 1             # W4A16_ROPE_NORM
 ROPE_INTERLEAVED = 2      # W4A16_ROPE_INTERLEAVED
 ROPE_MAX_AXES = 4         # W4A16_ROPE_MAX_AXES
 
-STEP_EXPORTS = ("w4a16_qk_norm_rope",)
+SAMPLE_MAX_ROWS = 65536   # W4A16_SAMPLE_MAX_ROWS
+SAMPLE_MAX_N = 1 << 20    # W4A16_SAMPLE_MAX_N
+
+STEP_EXPORTS = ("w4a16_qk_norm_rope", "w4a16_sample_workspace_bytes", "w4a16_sample")
 
 _vp = ctypes.c_void_p
 _int = ctypes.c_int
@@ -42,6 +47,10 @@ def step_lib() -> ctypes.CDLL:
         L.w4a16_qk_norm_rope.restype = _int
         L.w4a16_qk_norm_rope.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _float, _vp, _vp, ctypes.POINTER(_int), _int, _vp,
                                          _i64, _vp, _i64, _float, _int, _int, _int, _int, _int, _int, _vp]
+        L.w4a16_sample_workspace_bytes.restype = ctypes.c_size_t
+        L.w4a16_sample_workspace_bytes.argtypes = [_int, _int]
+        L.w4a16_sample.restype = _int
+        L.w4a16_sample.argtypes = [_vp, _int, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _int, _int, _vp]
         _lib = L
     return _lib
 
@@ -142,6 +151,77 @@ def _rope(shapes, q, k, q_weight, k_weight, inv_freq, positions, q_out, qo_strid
                                          q_heads, k_heads, dim, rot, _raw_stream(stream, dev)), "w4a16_qk_norm_rope")
 
 
+# ---- sampling -----------------------------------------------------------------------
+
+def w4a16_sample_workspace_bytes(M: int, N: int) -> int:
+    _int32("M, N", M, N)
+    return int(step_lib().w4a16_sample_workspace_bytes(M, N))
+
+
+def w4a16_sample(logits, uniforms, temperature, top_k, top_p, min_p, tokens, share, workspace, stream=None) -> None:
+    """tokens [M], share [M] or None: a token drawn from each row of logits [M, N] (see include/w4a16_step.h).
+
+    uniforms None draws the largest logits; temperature, top_k, top_p and min_p None are 1, 0 (off), 1 (off) and 0
+    (off); workspace: a uint8 device tensor of at least w4a16_sample_workspace_bytes bytes, or None where that is 0."""
+    rows = _logits(logits)
+    for t, name in ((tokens, "tokens"), (share, "share")):
+        if t is not None:
+            _row_values(t, rows[0], name)
+    if tokens is None:
+        raise ValueError("tokens is None")
+    if workspace is not None:
+        _dtype(workspace, torch.uint8, "workspace")
+    given = _given(tokens, share, workspace)
+    _same_gpu(logits, *given)
+    _dense(*given)
+    _sample(rows, logits, uniforms, temperature, top_k, top_p, min_p, tokens, share, workspace, stream)
+
+
+def _logits(logits):
+    """(M, N, row stride, dtype code)"""
+    if logits.dtype == torch.float32:
+        code = OUT_F32
+    elif logits.dtype == torch.bfloat16:
+        code = OUT_BF16
+    else:
+        raise TypeError(f"logits must be torch.float32 or torch.bfloat16, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be 2-D [M, N], got {list(logits.shape)}")
+    M, N = logits.shape
+    stride, unit = logits.stride()
+    if M <= 1:
+        stride = N                      # no second row: any valid stride
+    if N > 1 and unit != 1 or stride < N:
+        raise ValueError(f"rows of logits must be dense and apart, got strides {list(logits.stride())}")
+    return M, N, stride, code
+
+
+def _row_values(t, M, name):
+    want = torch.int32 if name in ("top_k", "tokens") else torch.float32
+    if t.dtype != want:
+        _dtype(t, want, name)
+    if t.shape != (M,):
+        _shape(t, (M,), name)
+
+
+def _sample(rows, logits, uniforms, temperature, top_k, top_p, min_p, tokens, share, workspace, stream):
+    M, N, stride, code = rows
+    given = []
+    for t, name in ((uniforms, "uniforms"), (temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"),
+                    (min_p, "min_p")):
+        if t is not None:
+            _row_values(t, M, name)
+            given.append(t)
+    dev = _same_gpu(logits, *given)
+    _dense(*given)
+    if _current_device() != dev:
+        return _on(dev, _sample, rows, logits, uniforms, temperature, top_k, top_p, min_p, tokens, share, workspace, stream)
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    _check(step_lib().w4a16_sample(logits.data_ptr(), code, stride, _ptr(uniforms), _ptr(temperature), _ptr(top_k),
+                                   _ptr(top_p), _ptr(min_p), tokens.data_ptr(), _ptr(share), ws, ws_bytes, M, N,
+                                   _raw_stream(stream, dev)), "w4a16_sample")
+
+
 # ---- allocating conveniences (torch allocates; the library computes) ------------
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None, eps: float = 1e-6,
@@ -157,3 +237,18 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=No
     _rope(shapes, q, k, q_weight, k_weight, inv_freq, positions, q_out, shapes[2][1] * dim, k_out, shapes[3][1] * dim, eps,
           weight_offset, norm, interleaved, sections, None)
     return q_out, k_out
+
+
+def sample(logits, uniforms=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """(tokens int32 [M], share fp32 [M]): a token drawn from each row of logits (see w4a16_sample)."""
+    if stream is not None:
+        with _current(stream, logits):
+            return sample(logits, uniforms, temperature, top_k, top_p, min_p)
+    rows = _logits(logits)
+    M, N = rows[:2]
+    need = step_lib().w4a16_sample_workspace_bytes(M, N)
+    tokens = logits.new_empty((M,), dtype=torch.int32)
+    share = logits.new_empty((M,), dtype=torch.float32)
+    ws = logits.new_empty((need,), dtype=torch.uint8) if need else None
+    _sample(rows, logits, uniforms, temperature, top_k, top_p, min_p, tokens, share, ws, None)
+    return tokens, share

@@ -4,6 +4,7 @@
  *
  *   w4a16_qk_norm_rope         per layer, between the q/k/v products and w4a16_kv_append:
  *                              norms of queries and keys for each head, positions rotated in
+ *   w4a16_sample               once a step: tokens drawn from the LM head's logits
  *
  * Conventions: those of w4a16.h -- device pointers (host ones are named as such), `stream` a
  * hipStream_t as void*, nothing allocated, no state, no synchronization, argument
@@ -23,6 +24,8 @@ extern "C" {
 #define W4A16_ROPE_MAX_AXES 4
 #define W4A16_ROPE_NORM 1            /* flags of w4a16_qk_norm_rope */
 #define W4A16_ROPE_INTERLEAVED 2
+#define W4A16_SAMPLE_MAX_ROWS 65536
+#define W4A16_SAMPLE_MAX_N (1 << 20)
 
 /*
  * Norm and rotation of a step's queries q [T][HQ][D] and keys k [T][H][D] (bf16,
@@ -52,6 +55,40 @@ w4a16_status_t w4a16_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uin
                                   uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
                                   float eps, int flags, int tokens, int q_heads, int k_heads, int dim, int rot,
                                   void *stream);
+
+/* Bytes of workspace w4a16_sample needs (0 for invalid arguments). */
+size_t w4a16_sample_workspace_bytes(int M, int N);
+
+/*
+ * Draws a token from each row of logits [M][N] (bf16 or fp32 per in_dtype, a w4a16_out_t;
+ * rows `stride` elements apart).  With v the row's largest logit and
+ *   w[i] = exp((logits[i] - v) / temperature)
+ * in 64 bits, and tokens in the order of falling logits (equal ones: lowest index first), a
+ * token is kept if
+ *   fewer than top_k tokens come before it (top_k <= 0: no limit), and
+ *   the weights before it sum to less than top_p times the sum of what top_k keeps
+ *   (top_p not below 1: no limit), and
+ *   w >= min_p (min_p not above 0: no limit);
+ * the first token is always kept.  The drawn one is the first in index order whose
+ * running sum of kept weights exceeds u times their sum (the last kept one if none does).
+ *   tokens  int32 [M]
+ *   share   fp32 [M], or NULL: the drawn token's weight divided by the sum of kept weights
+ *   uniforms fp32 [M], in [0, 1); NULL only if temperature is 0 everywhere, which the call
+ *           cannot see: NULL uniforms draw the largest logit
+ *   temperature, top_p, min_p  fp32 [M], top_k int32 [M]; NULL: 1, 1, 0 and 0 for all rows
+ * A temperature that is not above 0 draws the largest logit (lowest index first) with share
+ * 1; one above FLT_MAX counts as FLT_MAX.  Logits of -infinity have weight 0 and are never
+ * drawn; a row of nothing else gives token -1 and share 0.  With a logit of +infinity only
+ * those of +infinity have weight.  A row with a NaN gives its first NaN and share NaN.
+ * Sums of weights are of integers, or in a fixed order: the same call gives the same tokens.
+ * workspace: w4a16_sample_workspace_bytes(M, N) bytes, not initialised.
+ * M <= W4A16_SAMPLE_MAX_ROWS, N <= W4A16_SAMPLE_MAX_N.  N 0: tokens -1, shares 0.
+ * Alignment: logits by their type (rows need no more), fp32 and int32 arrays 4, workspace 16.
+ */
+w4a16_status_t w4a16_sample(const void *logits, int in_dtype, int64_t stride, const float *uniforms,
+                            const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                            int32_t *tokens, float *share, void *workspace, size_t workspace_bytes, int M, int N,
+                            void *stream);
 
 #ifdef __cplusplus
 }

@@ -34,3 +34,40 @@ def rope(x, weight, offset, eps, norm, inv_freq, positions, sections, interleave
         y[..., at], y[..., bt] = a * c - b * s, a * s + b * c
         size[..., at] = size[..., bt] = np.abs(a) + np.abs(b)
     return y, 32 * F32_STEP * size
+
+
+def kept(x, temperature, top_k, top_p, min_p):
+    """The tokens of one row (float64) that the limits keep, first to last, and their weights; temperature > 0."""
+    order = np.lexsort((np.arange(len(x)), -x))                   # falling logits, ties by the lower index
+    with np.errstate(invalid="ignore"):
+        away = x[order] - x[order[0]]
+    away[x[order] == x[order[0]]] = 0.0                           # (infinity less itself)
+    w = np.exp(away / min(temperature, float(np.finfo(np.float32).max)))
+    n = len(x)
+    if top_k > 0:
+        n = min(n, top_k)
+    if top_p < 1:
+        before = np.concatenate([[0.0], np.cumsum(w[:n])])
+        n = min(n, int((before[:n] < top_p * before[n]).sum()))
+    if min_p > 0:
+        n = min(n, int((w >= min_p).sum()))
+    n = max(n, 1)
+    return order[:n], w[:n]
+
+
+def sample(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """(token, share) of one row of float64 logits; parameters are the float64 values of fp32 ones."""
+    nan = np.flatnonzero(np.isnan(x))
+    if len(nan):
+        return int(nan[0]), float("nan")
+    if len(x) == 0 or x.max() == -np.inf:
+        return -1, 0.0
+    if not temperature > 0 or u is None:
+        return int(np.argmax(x)), 1.0
+    tokens, w = kept(x, temperature, top_k, top_p if top_p < 1 else 1.0, min_p if min_p > 0 else 0.0)
+    by_index = np.argsort(tokens)
+    tokens, w = tokens[by_index], w[by_index]
+    running = np.cumsum(w)
+    at = int((running <= u * running[-1]).sum()) if u > 0 else int(np.flatnonzero(running > 0)[0])
+    at = min(at, int(np.flatnonzero(w > 0)[-1]))
+    return int(tokens[at]), w[at] / running[-1]

@@ -1,0 +1,254 @@
+"""GPU tests of w4a16_sample (include/w4a16_step.h) against the 64-bit definition (step_reference.sample).
+
+Tokens have to be equal: borders between them lie within 2^-27 of the definition's at worst (below), and the seeded
+numbers keep away from those by more.  A share is one rounding to fp32 away (2^-24), and what its denominator is off by:
+each of N weights is held to half of 2^-e, e = 62 - log2(N) rounded up, beside a sum of at least 1."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import decode_w4a16_affine_amd as w4
+import step_reference as ref
+from parity import say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    w4.step_lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def f32(values):
+    return torch.tensor(np.asarray(values, dtype=np.float32), device="cuda")
+
+
+def i32(values):
+    return torch.tensor(np.asarray(values, dtype=np.int32), device="cuda")
+
+
+class Problem:
+    """Logits (float64 values of the given type) and parameters of each row (None: off)."""
+
+    def __init__(self, x, dtype, u, temperature=None, top_k=None, top_p=None, min_p=None, pad=0):
+        x = torch.as_tensor(np.asarray(x))
+        M, N = x.shape
+        wide = torch.full((M, N + pad), 1e30, dtype=dtype, device="cuda")
+        self.logits = wide[:, pad:]
+        self.logits.copy_(x)
+        self.x = self.logits.cpu().double().numpy()
+        self.u = None if u is None else np.asarray(u, dtype=np.float32)
+        self.floats = [None if v is None else np.asarray(v, dtype=np.float32) for v in (temperature, top_p, min_p)]
+        self.top_k = top_k
+
+    def args(self):
+        t, p, m = (None if v is None else f32(v) for v in self.floats)
+        return (self.logits, None if self.u is None else f32(self.u), t, None if self.top_k is None else i32(self.top_k), p, m)
+
+    def want(self):
+        out = []
+        for r in range(len(self.x)):
+            t, p, m = (None if v is None else float(v[r]) for v in self.floats)
+            out.append(ref.sample(self.x[r], None if self.u is None else float(self.u[r]), 1.0 if t is None else t,
+                                  0 if self.top_k is None else int(self.top_k[r]), 1.0 if p is None else p,
+                                  0.0 if m is None else m))
+        return out
+
+    def check(self):
+        tokens, share = w4.sample(*self.args())
+        tokens, share = tokens.cpu().numpy(), share.cpu().numpy()
+        for r, (token, part) in enumerate(self.want()):
+            assert tokens[r] == token, (r, tokens[r], token, share[r], part)
+            if np.isnan(part):
+                assert np.isnan(share[r])
+            else:
+                N = self.x.shape[1]
+                off = ref.F32_STEP + N * 2.0 ** (max(N - 1, 0).bit_length() - 63) + 2.0 ** -50
+                assert abs(share[r] - part) <= off * part, (r, share[r], part)
+        return tokens
+
+
+def rows(seed, M, N, spread=2.0):
+    rng = np.random.default_rng(seed)
+    x = rng.normal(size=(M, N)) * spread
+    for r in range(M):      # some that stand out
+        at = rng.integers(0, N, size=min(N, 30))
+        x[r, at] = 5 + 6 * rng.random(len(at))
+    return x, rng.random(M), rng
+
+
+SIZES = [(1, 1), (3, 2), (5, 7), (2, 63), (4, 64), (3, 65), (7, 1000), (2, 1023), (2, 1024), (3, 1025), (4, 4096), (3, 8191),
+         (2, 8193), (3, 50001), (2, 100003), (2, 262144), (1, 1 << 20)]
+DTYPES = [torch.float32, torch.bfloat16]
+
+
+@pytest.mark.parametrize("M,N", SIZES)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("params", ["free", "top_k", "large_k", "top_p", "min_p", "k_p", "large_k_p", "all"])
+def test_sizes_and_limits(M, N, dtype, params):
+    say("sample", M, N, dtype, params)
+    x, u, rng = rows(N, M, N)
+    kw = dict(temperature=rng.uniform(0.4, 1.5, M))
+    if params in ("top_k", "k_p", "all"):
+        kw["top_k"] = rng.integers(1, 70, M)
+    if params in ("large_k", "large_k_p"):
+        kw["top_k"] = rng.integers(max(1, N // 3), N + 5, M)
+    if params in ("top_p", "k_p", "large_k_p", "all"):
+        kw["top_p"] = rng.uniform(0.3, 0.99, M)
+    if params in ("min_p", "all"):
+        kw["min_p"] = rng.uniform(0.0005, 0.3, M)
+    Problem(x, dtype, u, **kw, pad=N % 5).check()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_rows_that_ask_for_different_things(dtype):
+    say("sample mixed", dtype)
+    M, N = 96, 33333
+    x, u, rng = rows(5, M, N)
+    Problem(x, dtype, u, temperature=rng.choice([0.0, 0.3, 1.0, 2.5], M), top_k=rng.choice([0, -3, 1, 2, 40, 2000, N, 10 ** 9], M),
+            top_p=rng.choice([1.0, 2.0, np.nan, 0.0, -1.0, 0.1, 0.9, 0.999], M),
+            min_p=rng.choice([0.0, -1.0, np.nan, 1e-6, 0.05, 0.5, 1.0, 1.5, np.inf], M)).check()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N", [5, 700, 20000])
+def test_equal_logits(dtype, N):
+    """Ties everywhere: limits cut between equal tokens by their index."""
+    say("sample ties", dtype, N)
+    rng = np.random.default_rng(7)
+    M = 24
+    x = rng.integers(0, 3, size=(M, N)).astype(np.float64)
+    x[:8] = 1.25
+    x[20:] = np.where(rng.random((4, N)) < 0.5, 0.0, -0.0)
+    Problem(x, dtype, rng.random(M), top_k=rng.choice([0, 1, N // 2, max(1, N - 1)], M),
+            top_p=rng.choice([1.0, 0.5, 0.25, 0.75], M), temperature=rng.choice([1.0, 0.7], M)).check()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_uniforms_at_their_ends(dtype):
+    """0 gives the first kept token of weight, 1 and beyond the last, also of a row masked at both ends."""
+    say("sample ends", dtype)
+    x, _, rng = rows(9, 12, 5000)
+    x[:, :17] = -np.inf
+    x[:, 4000:] = -np.inf
+    u = [0.0, 1.0, 2.0, np.inf, -1.0, np.nan, 1 - 2.0 ** -24, 2.0 ** -149] + [0.5] * 4
+    p = Problem(x, dtype, u)
+    p.u[5] = 0.0      # (the definition's first token is what NaN gives too)
+    want = p.want()
+    p.u[5] = np.nan
+    tokens, _ = w4.sample(*p.args())
+    assert tokens.cpu().tolist() == [t for t, _ in want]
+    assert tokens[0] == 17 and tokens[1] == 3999 and tokens[3] == 3999
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N", [1, 40, 9000])
+def test_infinities_nan_and_masked_rows(dtype, N):
+    say("sample special values", dtype, N)
+    x, u, rng = rows(11, 12, N)
+    low = float(torch.finfo(dtype).min)
+    x[0] = -np.inf
+    x[1] = low                                        # a mask of the type's lowest value: equal tokens
+    x[2, :] = low
+    x[2, N // 2] = 3.0
+    x[3, N // 3] = np.inf
+    x[4, ::2] = np.inf                                # several: each with the same weight
+    x[5, N // 2:] = np.nan
+    x[6] = -np.inf
+    x[6, N - 1] = -5.0
+    x[7] = np.nan
+    x[8, ::2] = -np.inf
+    x[9] = low / 2
+    x[9, 0] = low
+    x[10] *= 1e30
+    x[11] *= 1e-30
+    p = Problem(x, dtype, u)
+    tokens = p.check()
+    assert tokens[0] == -1
+    p = Problem(x, dtype, u, temperature=[1e-38, 1e-45, 3e38, np.inf, 1.0, 0.0, 0.5, 0.0, np.inf, 1e30, 1e30, 1e-30],
+                top_k=[3] * 12, top_p=[0.9] * 12, min_p=[0.01] * 12)
+    p.check()
+    p = Problem(x, dtype, u, temperature=[np.inf] * 12)
+    p.check()
+    assert (Problem(x, dtype, None).check()[[1, 3]] == [0, N // 3]).all()
+
+
+def test_shares_follow_the_distribution():
+    """Uniforms spread evenly over [0, 1) give each token as often as its weight says (within one)."""
+    say("sample frequencies")
+    n, N = 4096, 50
+    rng = np.random.default_rng(3)
+    x = np.repeat(rng.normal(size=(1, N)) * 2, n, 0)
+    p = Problem(x, torch.float32, (np.arange(n) + 0.5) / n)
+    tokens, share = w4.sample(*p.args())
+    counts = np.bincount(tokens.cpu().numpy(), minlength=N)
+    w = np.exp(p.x[0] - p.x[0].max())
+    assert (np.abs(counts - n * w / w.sum()) <= 1).all()
+
+
+def test_nothing_to_do():
+    say("sample of no rows")
+    tokens, share = w4.sample(torch.empty((0, 50), device="cuda"), torch.empty((0,), device="cuda"))
+    assert tokens.shape == (0,) and share.shape == (0,)
+    tokens, share = w4.sample(torch.empty((300, 0), device="cuda"), torch.zeros((300,), device="cuda"))
+    assert (tokens == -1).all() and (share == 0).all()
+
+
+def test_without_shares_and_with_a_small_workspace():
+    say("sample workspace")
+    x, u, rng = rows(13, 4, 30000)
+    p = Problem(x, torch.float32, u, top_p=[0.9] * 4)
+    need = w4.w4a16_sample_workspace_bytes(4, 30000)
+    ws = torch.full((max(need, 16) + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+    tokens = torch.full((6,), -7, dtype=torch.int32, device="cuda")
+    w4.w4a16_sample(*p.args(), tokens[1:5].contiguous(), None, ws)
+    got = torch.empty((4,), dtype=torch.int32, device="cuda")
+    w4.w4a16_sample(*p.args(), got, None, ws[:max(need, 16)])
+    assert got.cpu().tolist() == [t for t, _ in p.want()]
+    assert (ws[max(need, 16):] == 0xFF).all()
+    if need:
+        with pytest.raises(w4.W4A16Error):
+            w4.w4a16_sample(*p.args(), got, None, ws[:need - 1])
+        with pytest.raises(w4.W4A16Error):
+            w4.w4a16_sample(*p.args(), got, None, None)
+
+
+def test_captured_and_on_two_streams():
+    """A graph follows logits, numbers and parameters that change; calls on two streams at once give the same tokens."""
+    say("sample captured")
+    x, u, rng = rows(15, 20, 40000)
+    p = Problem(x, torch.float32, u, temperature=rng.uniform(0.5, 1, 20), top_k=rng.choice([0, 20, 3000], 20),
+                top_p=rng.choice([1.0, 0.9], 20), min_p=rng.choice([0.0, 0.01], 20))
+    args = p.args()
+    need = w4.w4a16_sample_workspace_bytes(20, 40000)
+    ws = [torch.empty((need,), dtype=torch.uint8, device="cuda") if need else None for _ in range(2)]
+    tokens, share = torch.empty((20,), dtype=torch.int32, device="cuda"), torch.empty((20,), device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        w4.w4a16_sample(*args, tokens, share, ws[0])
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w4.w4a16_sample(*args, tokens, share, ws[0])
+    for i in range(4):
+        args[0].copy_(args[0].roll(777, dims=1) * 1.01)
+        args[1].copy_(args[1].roll(1))
+        args[3].copy_(args[3].roll(1))
+        torch.cuda.synchronize()
+        tokens.fill_(-9)
+        graph.replay()
+        got = torch.empty_like(tokens)
+        with torch.cuda.stream(side):                        # while the replay may run
+            w4.w4a16_sample(*args, got, None, ws[1])
+        torch.cuda.synchronize()
+        want, part = w4.sample(*args)
+        assert torch.equal(tokens, want) and torch.equal(got, want) and torch.equal(share, part)
+    p.x, p.u, p.top_k = args[0].cpu().double().numpy(), args[1].cpu().numpy(), args[3].cpu().numpy()
+    assert tokens.cpu().tolist() == [t for t, _ in p.want()]

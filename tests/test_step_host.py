@@ -112,3 +112,67 @@ def test_rope_definition_by_hand():
     w = np.full(64, 0.5)
     y, _ = ref.rope(x, w, 1.0, 0.0, True, np.zeros(0), np.array([[0]]), None, False)
     assert np.allclose(y[0, 0, 0], 3 * 1.5 / np.sqrt(38 / 64))
+
+
+def test_sample_constants_match_the_header():
+    assert constant("SAMPLE_MAX_ROWS") == w4.SAMPLE_MAX_ROWS and constant("SAMPLE_MAX_N") == w4.SAMPLE_MAX_N
+
+
+def test_sample_refuses_bad_arguments(L):
+    need = L.w4a16_sample_workspace_bytes(3, 1000)
+
+    def sample(x=A16, dtype=1, stride=1000, u=A16, t=A16, k=A16, p=A16, m=A16, tokens=A16, share=A16, ws=A16, ws_bytes=need,
+               M=3, N=1000):
+        return L.w4a16_sample(x, dtype, stride, u, t, k, p, m, tokens, share, ws, ws_bytes, M, N, None)
+
+    for bad in (dict(dtype=2), dict(dtype=-1)):
+        assert sample(**bad) == EUNSUP, bad
+    for bad in (dict(M=-1), dict(M=65537), dict(N=-1), dict(N=2 ** 20 + 1, stride=2 ** 21), dict(stride=999),
+                dict(stride=-1), dict(stride=2 ** 40 + 1)):
+        assert sample(**bad) == ESHAPE, bad
+    for bad in ("x", "tokens"):
+        assert sample(**{bad: None}) == ENULL, bad
+    for bad in ("x", "u", "t", "k", "p", "m", "tokens", "share"):
+        assert sample(**{bad: A16 + 2}) == EALIGN, bad
+    assert sample(x=A16 + 1, dtype=0) == EALIGN
+    assert sample(M=0) == OK and sample(M=0, x=None, tokens=None, ws=None, ws_bytes=0) == OK
+    assert L.w4a16_sample_workspace_bytes(-1, 5) == 0 and L.w4a16_sample_workspace_bytes(5, 2 ** 20 + 1) == 0
+
+
+def test_sample_binding_refuses_bad_tensors():
+    x, f, i = host(3, 50, dtype=torch.float32), host(3, dtype=torch.float32), host(3, dtype=torch.int32)
+    for bad, kind in ((dict(logits=x.double()), TypeError), (dict(logits=x[0]), ValueError), (dict(logits=x.T), ValueError),
+                      (dict(logits=x[:1].expand(3, 50)), ValueError), (dict(uniforms=f.double()), TypeError),
+                      (dict(uniforms=f[:2]), ValueError), (dict(temperature=f[:, None]), ValueError),
+                      (dict(top_k=f), TypeError), (dict(top_k=i[:1]), ValueError), (dict(top_p=i), TypeError),
+                      (dict(min_p=i), TypeError), (dict(), ValueError)):      # (host tensors)
+        with pytest.raises(kind):
+            w4.sample(**{**dict(logits=x, uniforms=f), **bad})
+    for tokens, share, ws in ((f, f, None), (i[:1], f, None), (i, i, None), (i, f[:2], None), (i, f, f), (None, f, None)):
+        with pytest.raises((TypeError, ValueError)):
+            w4.w4a16_sample(x, f, None, None, None, None, tokens, share, ws)
+    with pytest.raises(ValueError):
+        w4.w4a16_sample_workspace_bytes(2 ** 33, 5)
+
+
+def test_sample_definition_by_hand():
+    x = np.log(np.array([0.1, 0.4, 0.05, 0.4, 0.05]))
+    pick = lambda u, **kw: ref.sample(x, u, **kw)[0]  # noqa: E731
+    assert [pick(u) for u in (0.0, 0.09, 0.11, 0.49, 0.51, 0.54, 0.56, 0.94, 0.96, 1.5)] == [0, 0, 1, 1, 2, 2, 3, 3, 4, 4]
+    assert [pick(u, top_k=1) for u in (0.0, 0.99)] == [1, 1]                 # the lower index of equal ones
+    assert [pick(u, top_k=2) for u in (0.49, 0.51)] == [1, 3]
+    assert [pick(u, top_p=0.3) for u in (0.0, 0.99)] == [1, 1]
+    assert [pick(u, top_p=0.5) for u in (0.49, 0.51)] == [1, 3]
+    assert pick(0.99, top_p=0.85) == 3 and pick(0.0, top_p=0.85) == 0
+    assert pick(0.0, min_p=0.3) == 1 and pick(0.0, min_p=0.2) == 0
+    assert pick(0.99, top_k=4, top_p=0.99) == 3 and pick(0.53, top_k=4) == 2    # 0.05 of 0.95: the lower index
+    assert ref.sample(x, 0.2, top_k=2)[1] == pytest.approx(0.5)
+    assert pick(0.9, temperature=0.0) == 1 and pick(None) == 1
+    assert pick(0.9, min_p=2.0) == 1 and pick(0.9, top_p=0.0) == 1
+    x[2] = -np.inf
+    assert ref.sample(x, 0.525)[0] == 1 and ref.sample(x, 1.0)[0] == 4
+    assert ref.sample(np.full(3, -np.inf), 0.5) == (-1, 0.0)
+    x[4] = np.inf
+    assert ref.sample(x, 0.0) == (4, 1.0)
+    x[3] = np.nan
+    assert ref.sample(x, 0.0)[0] == 3
