@@ -460,4 +460,6 @@ from .kv import (KV_DIMS, KV_EXPORTS, KV_FP8, KV_INT8, KV_MAX_DEQUANT, KV_MAX_GR
 # ---- what a serving step runs beside them (include/w4a16_step.h) -----------------
 
 from .step import (ROPE_INTERLEAVED, ROPE_MAX_AXES, ROPE_NORM, SAMPLE_MAX_N, SAMPLE_MAX_ROWS, STEP_EXPORTS,  # noqa: E402
-                   qk_norm_rope, sample, step_lib, w4a16_qk_norm_rope, w4a16_sample, w4a16_sample_workspace_bytes)
+                   kv_attention_shared, qk_norm_rope, sample, step_lib, w4a16_kv_attention_shared,
+                   w4a16_kv_attention_shared_workspace_bytes, w4a16_qk_norm_rope, w4a16_sample,
+                   w4a16_sample_workspace_bytes)

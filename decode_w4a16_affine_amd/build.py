@@ -2,8 +2,9 @@
 
 The decode kernels are instantiated once per activation-row count in separate
 objects (csrc/inst.hip compiled with -DW4K_M=1..8), the prefill kernels and
-the C ABI in two more, the key/value cache and its attention (once per head
-size) in four, all compiled in parallel and linked into one library.
+the C ABI in two more, the key/value cache, its attention and that behind
+shared entries (once per head size each) and a step's other operators in ten,
+all compiled in parallel and linked into one library.
 """
 import concurrent.futures as cf
 import os
@@ -42,9 +43,10 @@ UNITS = [(f"inst_m{m}", "inst.hip", [f"-DW4K_M={m}"]) for m in range(1, 9)] + [
     # what a serving step runs beside them (include/w4a16_step.h)
     ("rope", "rope.hip", []),
     ("sample", "sample.hip", []),
+    ("kv_shared", "kv_shared.hip", []),
     # (matrix results in VGPRs here too: the softmax works on them between the products)
-] + [(f"kv_attention_d{d}", "kv_attention.hip", [f"-DW4K_D={d}", "-mllvm", "-amdgpu-mfma-vgpr-form"])
-     for d in (64, 128, 256)]
+] + [(f"{name}_d{d}", f"{name}.hip", [f"-DW4K_D={d}", "-mllvm", "-amdgpu-mfma-vgpr-form"])
+     for name in ("kv_attention", "kv_shared_attention") for d in (64, 128, 256)]
 
 _NOISE = "not a recognized feature for this target"
 

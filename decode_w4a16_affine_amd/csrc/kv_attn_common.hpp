@@ -107,6 +107,16 @@ __device__ __forceinline__ KvRows kv_rows_of(const KvAttnArgs& a, int r, int i0,
   return k;
 }
 
+__device__ __forceinline__ int kv_shared_entries(const KvSharedArgs& a) {
+  return min(max(a.shared_len[0], 0), a.max_shared);
+}
+// Of these rows' entries those behind the shared ones.
+__device__ __forceinline__ void kv_keep_own(const KvSharedArgs& a, KvRows& k) {
+  const int shared = kv_shared_entries(a);
+  k.end = min(k.end, shared + a.max_own);
+  k.begin = min(shared, k.end);
+}
+
 // The parts of the cache (a.part entries each) that rows of the tile form attend.
 struct KvParts {
   int first, count;

@@ -84,9 +84,11 @@ constexpr int kKvGridRequests = 32768;             // requests on the grid's y a
 // (a reload of a spilled register would wait for the loads in flight).
 constexpr int kv_split_occupancy(int D, int NC) { return D == 256 ? 2 : D == 128 || NC == 2 ? 3 : 4; }
 
-template <int D, int TYPE, int NC>
-__global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) void kv_split_kernel(
-    KvAttnArgs a, float* part_o, float* part_ml) {
+// Behind shared entries (Args = KvSharedArgs) a request's own ones alone are taken, and
+// every result is partial: another kernel joins it with those of the shared entries.
+template <int D, int TYPE, int NC, class Args>
+__device__ __forceinline__ void kv_split_body(const Args& a, float* part_o, float* part_ml) {
+  constexpr bool SHARED = kv_behind_shared<Args>;
   constexpr int W = kKvSplitWaves;
   constexpr int T = kKvSplitTile, E = T / 4, STEP = W * T;
   constexpr int NP = T / 16;                       // pieces of scores
@@ -126,11 +128,15 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
     return (j0 + 16 * x) >> shift < a.width && page >= 0 && page < a.c.pages ? page : -1;
   };
   int page = 0, page_after = 0;
-  if (a.window == 0 && a.width > 0) page = pages(block << a.chunk_shift);
+  if (!SHARED && a.window == 0 && a.width > 0) page = pages(block << a.chunk_shift);
   const int i_first = kv_token_of(a, row0), i_last = kv_token_of(a, row0 + NC * 16 - 1);
-  const KvRows rows = kv_rows_of(a, r, i_first, i_last);
+  KvRows rows = kv_rows_of(a, r, i_first, i_last);
   const int live = rows.live * a.group;                    // rows of the request
   if (!kv_few_rows(a, rows.n) || row0 >= live) return;
+  if constexpr (SHARED) {
+    kv_keep_own(a, rows);
+    if (rows.begin >= rows.end) return;
+  }
   const int first = rows.begin >> a.chunk_shift;            // the group's first chunk
   const int at_begin = (first + block) << a.chunk_shift;
   const int at_end = (int)min((long long)at_begin + (1LL << a.chunk_shift), (long long)rows.end);
@@ -245,7 +251,7 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
     }
   };
   int j0 = max(at_begin, rows.begin & ~(STEP - 1));
-  if (a.window > 0 && rows.begin < rows.end) page = pages(j0);
+  if ((SHARED || a.window > 0) && rows.begin < rows.end) page = pages(j0);
   page = checked(j0, page);
 
   // this lane's rows: queries (in the keys' order) and positions
@@ -259,7 +265,7 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
     const bool ok = row0 + 16 * c + x < live && t >= 0 && t < a.tokens;
     out_at[c] = ok ? t * a.q_heads + h : -1;
     lr.hi[c] = ok ? min(rows.seq - rows.n + i, rows.end - 1) : -1;
-    lr.lo[c] = a.window > 0 ? rows.seq - rows.n + i - a.window + 1 : 0;
+    lr.lo[c] = SHARED ? rows.begin : a.window > 0 ? rows.seq - rows.n + i - a.window + 1 : 0;
     const uint16_t* qp = a.q + (ok ? (size_t)t * a.q_stride + (size_t)h * D : 0) + 16 * g;
     if constexpr (Q_LDS) {      // the waves share the rows: each puts a quarter of the pieces (read after a barrier)
 #pragma unroll
@@ -276,7 +282,9 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
   if constexpr (Q_LDS) __syncthreads();
   // positions that every row of the group attends need no mask
   const int all_hi = min(rows.seq - rows.n + i_first, rows.end - 1);
-  const int all_lo = a.window > 0 ? rows.seq - rows.n + min(i_last, rows.live - 1) - a.window + 1 : 0;
+  const int all_lo = SHARED         ? rows.begin
+                     : a.window > 0 ? rows.seq - rows.n + min(i_last, rows.live - 1) - a.window + 1
+                                    : 0;
 
   kv_f32x4 o[NC][DW];
   float m[NC], l[NC];
@@ -287,7 +295,7 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
 #pragma unroll
     for (int d = 0; d < DW; ++d) o[c][d] = kv_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  const bool single = first == max(rows.end - 1, rows.begin) >> a.chunk_shift;     // one chunk holds all
+  const bool single = !SHARED && first == max(rows.end - 1, rows.begin) >> a.chunk_shift;     // one chunk holds all
   if (j0 < at_end) {
     load_keys(j0, page);
     load_values(j0, page);
@@ -414,7 +422,8 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
 #pragma unroll
       for (int d = 0; d < DW; ++d) kv_store4(out + 16 * d, o[c][d], inverse);
     } else {
-      const size_t at = kv_part_row(a, out_at[c], r, rows.first) * a.chunks + block;
+      const size_t at = SHARED ? (size_t)out_at[c] * (a.parts + a.chunks) + a.parts + block
+                               : kv_part_row(a, out_at[c], r, rows.first) * a.chunks + block;
 #pragma unroll
       for (int d = 0; d < DW; ++d) *reinterpret_cast<kv_f32x4*>(part_o + at * D + d0 + 16 * d) = o[c][d];
       if (g == 0) {
@@ -423,6 +432,12 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
       }
     }
   }
+}
+
+template <int D, int TYPE, int NC>
+__global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) void kv_split_kernel(
+    KvAttnArgs a, float* part_o, float* part_ml) {
+  kv_split_body<D, TYPE, NC>(a, part_o, part_ml);
 }
 
 // Joins the chunks of one row (grid: cache head and row, request) in chunk order:

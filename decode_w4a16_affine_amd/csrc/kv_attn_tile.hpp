@@ -68,10 +68,23 @@ __device__ __forceinline__ int kv_tile_owner(const int32_t* token_start, int req
   return lo;
 }
 
-template <int D, int TYPE>
-__global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_kernel(KvAttnArgs a,
-                                                                                             float* part_o,
-                                                                                             float* part_ml) {
+// The last request that begins at or before token t.
+__device__ __forceinline__ int kv_request_of(const KvAttnArgs& a, int t) {
+  int r = 0;
+  for (int count = a.requests; count > 1;) {
+    const int step = count >> 1;
+    if (a.token_start[r + step] <= t) r += step;
+    count -= step;
+  }
+  return r;
+}
+
+// Over shared entries (Args = KvSharedArgs) the rows of all requests, token by token, are
+// tiled as if they were one request's; each attends the entries up to its own position,
+// and every result is partial.
+template <int D, int TYPE, class Args>
+__device__ __forceinline__ void kv_tile_body(const Args& a, float* part_o, float* part_ml) {
+  constexpr bool SHARED = kv_behind_shared<Args>;
   constexpr int NC = kKvTileCols, W = kv_tile_waves(D, TYPE), HS = kv_tile_share(D);
   constexpr int KC = D / 64;              // 16-byte pieces of a key a lane multiplies
   constexpr int NP = 4 / HS;              // 16-entry pieces of a tile that a wave scores
@@ -94,18 +107,46 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
   // tiles together, the last head's long ones began late: 770 us instead of 638).
   const int kh = blockIdx.x % a.c.heads;
   const int u = (gridDim.x - 1 - blockIdx.x) / a.c.heads;
-  const int r = __builtin_amdgcn_readfirstlane(kv_tile_owner(a.token_start, a.requests, tt, u));
-  if (r < 0) return;
-  const int i0 = (u - a.token_start[r] / tt - r) * tt;
-  const int n = a.token_start[r + 1] - a.token_start[r];
-  const int live_tokens = min(min(n, a.max_new), a.tokens - a.token_start[r]);
-  if (kv_few_rows(a, n) || i0 < 0 || i0 >= live_tokens || a.token_start[r] < 0) return;
+  int r = 0, i0, n, live_tokens;
+  if constexpr (SHARED) {
+    i0 = u * tt;
+    n = a.token_start[a.requests] - a.token_start[0];
+    live_tokens = min(n, a.tokens - a.token_start[0]);
+    if (i0 >= live_tokens || a.token_start[0] < 0) return;
+  } else {
+    r = __builtin_amdgcn_readfirstlane(kv_tile_owner(a.token_start, a.requests, tt, u));
+    if (r < 0) return;
+    i0 = (u - a.token_start[r] / tt - r) * tt;
+    n = a.token_start[r + 1] - a.token_start[r];
+    live_tokens = min(min(n, a.max_new), a.tokens - a.token_start[r]);
+    if (kv_few_rows(a, n) || i0 < 0 || i0 >= live_tokens || a.token_start[r] < 0) return;
+  }
   const int here = min(tt, live_tokens - i0);       // the workgroup's tokens
   const int live = here * a.group;                  // and rows
-  const KvRows rows = kv_rows_of(a, r, i0, i0 + here - 1);
+  KvRows rows;
   const int shift = a.c.page_shift, P = 1 << shift;
+  int last[2] = {-1, -1};      // SHARED: the last entry that tokens i0 + lane and i0 + 64 + lane attend
+  if constexpr (SHARED) {
+    const int first = a.token_start[0];
+    const int shared = (int)min((long long)kv_shared_entries(a), (long long)a.width << shift);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (i * kWave >= here) break;
+      const int t = first + i0 + min(i * kWave + lane, here - 1);
+      const int owner = kv_request_of(a, t);
+      const long long pos = (long long)a.seq_lens[owner] - (a.token_start[owner + 1] - t);
+      last[i] = (int)max(min(pos, shared - 1LL), -1LL);
+    }
+    // (shared entries that none of these rows attends may hold anything)
+    int end = max(last[0], last[1]) + 1;
+#pragma unroll
+    for (int off = kWave / 2; off > 0; off >>= 1) end = max(end, __shfl_xor(end, off));
+    rows = KvRows{n, first, 0, live_tokens, 0, __builtin_amdgcn_readfirstlane(end)};
+  } else {
+    rows = kv_rows_of(a, r, i0, i0 + here - 1);
+  }
   // the part of the cache (all of it if a.parts is 1) that this workgroup walks
-  const KvParts parts = kv_parts_of(a, rows);
+  const KvParts parts = SHARED ? KvParts{0, (rows.end + a.part - 1) / a.part} : kv_parts_of(a, rows);
   const int part = blockIdx.y;
   if (part >= parts.count) return;
   const int part_begin = (parts.first + part) * a.part;
@@ -123,20 +164,43 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
     const int i = kv_token_of(a, row), h = kh * a.group + row - i * a.group;
     const int t = rows.first + i0 + i;
     const bool ok = wrow + 16 * c + x < live;
-    lr.hi[c] = ok ? min(pos0 + i, rows.end - 1) : -1;
-    lr.lo[c] = a.window > 0 ? pos0 + i - a.window + 1 : 0;
+    if constexpr (SHARED) {
+      const int low = __shfl(last[0], i & (kWave - 1)), high = __shfl(last[1], i & (kWave - 1));
+      lr.hi[c] = ok ? (i < kWave ? low : high) : -1;
+      lr.lo[c] = 0;
+    } else {
+      lr.hi[c] = ok ? min(pos0 + i, rows.end - 1) : -1;
+      lr.lo[c] = a.window > 0 ? pos0 + i - a.window + 1 : 0;
+    }
     out_at[c] = ok ? t * a.q_heads + h : -1;
     const uint16_t* qp = a.q + t * a.q_stride + (size_t)h * D + 16 * g;
 #pragma unroll
     for (int k = 0; k < 2 * KC; ++k) q[c][k] = kv_query8(qp + 64 * (k >> 1) + 8 * (k & 1), a.q_sign);
   }
   // entries that some row of the pair attends, and those that every row does
-  const int first_pos = pos0 + kv_token_of(a, min(wrow, live - 1));
-  const int last_pos = pos0 + kv_token_of(a, min(wrow + NC * 16, live) - 1);
-  const int any_hi = wrow < live ? min(last_pos, rows.end - 1) : -1;
-  const int any_lo = a.window > 0 ? first_pos - a.window + 1 : 0;
-  const int all_hi = min(first_pos, rows.end - 1);
-  const int all_lo = a.window > 0 ? last_pos - a.window + 1 : 0;
+  int any_hi, any_lo = 0, all_hi, all_lo = 0;
+  if constexpr (SHARED) {
+    any_hi = -1, all_hi = rows.end - 1;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      any_hi = max(any_hi, lr.hi[c]);
+      all_hi = min(all_hi, out_at[c] < 0 ? all_hi : lr.hi[c]);
+    }
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) {      // (lanes x, x + 16 .. have the same rows)
+      any_hi = max(any_hi, __shfl_xor(any_hi, off));
+      all_hi = min(all_hi, __shfl_xor(all_hi, off));
+    }
+    any_hi = __builtin_amdgcn_readfirstlane(any_hi);
+    all_hi = __builtin_amdgcn_readfirstlane(all_hi);
+  } else {
+    const int first_pos = pos0 + kv_token_of(a, min(wrow, live - 1));
+    const int last_pos = pos0 + kv_token_of(a, min(wrow + NC * 16, live) - 1);
+    any_hi = wrow < live ? min(last_pos, rows.end - 1) : -1;
+    any_lo = a.window > 0 ? first_pos - a.window + 1 : 0;
+    all_hi = min(first_pos, rows.end - 1);
+    all_lo = a.window > 0 ? last_pos - a.window + 1 : 0;
+  }
 
   kv_f32x4 o[NC][DH];
   float m[NC], l[NC];
@@ -331,21 +395,31 @@ __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_ker
     if (out_at[c] < 0) continue;
     const float sum = HS == 1 ? l[c] : s_m[wave & ~1][16 * c + x] + s_m[wave | 1][16 * c + x];
     const int d0 = 16 * DH * half + 4 * g;
-    if (parts.count == 1) {
+    if (!SHARED && parts.count == 1) {
       const float inverse = kv_inverse(sum);
       uint16_t* out = a.out + (size_t)out_at[c] * D + d0;
 #pragma unroll
       for (int d = 0; d < DH; ++d) kv_store4(out + 16 * d, o[c][d], inverse);
     } else {
-      const size_t at = (size_t)out_at[c] * a.parts + part;
+      const size_t at = (size_t)out_at[c] * (SHARED ? a.parts + a.chunks : a.parts) + part;
 #pragma unroll
       for (int d = 0; d < DH; ++d) *reinterpret_cast<kv_f32x4*>(part_o + at * D + d0 + 16 * d) = o[c][d];
       if (g == 0 && half == 0) {
-        part_ml[kKvTileStats * at] = m[c];
-        part_ml[kKvTileStats * at + 1] = sum;
+        constexpr int stats = SHARED ? kKvPartStats : kKvTileStats;
+        part_ml[stats * at] = m[c];
+        part_ml[stats * at + 1] = sum;
+        if constexpr (SHARED)      // (one sum where the split form has its waves')
+#pragma unroll
+          for (int w = 2; w < stats; ++w) part_ml[stats * at + w] = 0.0f;
       }
     }
   }
+}
+
+template <int D, int TYPE>
+__global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_kernel(KvAttnArgs a, float* part_o,
+                                                                                  float* part_ml) {
+  kv_tile_body<D, TYPE>(a, part_o, part_ml);
 }
 
 // Joins the parts of a row in their order: D / 4 threads a row (bound by two reads
@@ -359,12 +433,7 @@ __global__ __launch_bounds__(kKvJoinThreads) void kv_tile_join_kernel(KvAttnArgs
   const int d = 4 * (threadIdx.x % (D / 4));
   const int t = row / a.q_heads;
   if (t >= a.tokens || t < a.token_start[0]) return;
-  int r = 0;                                                    // the last request that begins at or before t
-  for (int count = a.requests; count > 1;) {
-    const int step = count >> 1;
-    if (a.token_start[r + step] <= t) r += step;
-    count -= step;
-  }
+  const int r = kv_request_of(a, t);
   const int n = a.token_start[r + 1] - a.token_start[r], i = t - a.token_start[r];
   if (a.token_start[r] < 0 || i >= min(n, a.max_new) || kv_few_rows(a, n)) return;
   // the rows of its workgroup
@@ -402,6 +471,82 @@ __global__ __launch_bounds__(kKvJoinThreads) void kv_tile_join_kernel(KvAttnArgs
     }
   }
   kv_store4(a.out + (size_t)row * D + d, sum, kv_inverse(sum_l));
+}
+
+// Joins a row's partial results behind shared entries: the parts of these, then the
+// chunks of its own, in this order (grid: cache head and row, request).  One thread a
+// partial result for the factors, D / 4 threads for four elements each of one slice of
+// the results.
+template <int D>
+__global__ __launch_bounds__(kKvJoinThreads) void kv_shared_join_kernel(KvSharedArgs a, const float* part_o,
+                                                                        const float* part_ml) {
+  constexpr int S = kKvJoinThreads / (D / 4);
+  static_assert(kKvMaxParts + kKvMaxChunks <= kKvJoinThreads, "one thread a partial result");
+  __shared__ float s_f[kKvJoinThreads];
+  __shared__ float s_w[2][kKvJoinThreads / kWave];
+  __shared__ kv_f32x4 s_o[kKvJoinThreads];
+  const int max_rows = a.split_tokens * a.group;
+  const int r = blockIdx.z * kKvGridRequests + blockIdx.y;
+  if (r >= a.requests) return;
+  const int kh = blockIdx.x / max_rows, row = blockIdx.x % max_rows;
+  const int i = kv_token_of(a, row);
+  KvRows rows = kv_rows_of(a, r, i, i);      // of this row alone
+  const int t = rows.first + i;
+  if (row >= rows.live * a.group || t < 0 || t >= a.tokens) return;
+  const int shared = min(kv_shared_entries(a), rows.end);
+  const int parts = (shared + a.part - 1) / a.part;
+  kv_keep_own(a, rows);
+  const int chunks = rows.begin < rows.end
+                         ? ((rows.end - 1) >> a.chunk_shift) - (rows.begin >> a.chunk_shift) + 1
+                         : 0;
+  const int count = parts + chunks;
+  const int out_row = t * a.q_heads + kh * a.group + row - i * a.group;
+  const size_t at = (size_t)out_row * (a.parts + a.chunks);
+  auto place = [&](int c) W4K_INLINE { return at + (c < parts ? c : a.parts + c - parts); };
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int slice = threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
+  float m = kKvNone, l = 0.0f;
+  if ((int)threadIdx.x < count) {
+    const float* ml = part_ml + kKvPartStats * place(threadIdx.x);
+    m = ml[0];
+    l = ((ml[1] + ml[2]) + ml[3]) + ml[4];
+  }
+  auto load = [&](int c) W4K_INLINE { return *reinterpret_cast<const kv_f32x4*>(part_o + place(c) * D + d); };
+  // a slice's first results do not wait for the factors
+  kv_f32x4 v0 = {0.0f, 0.0f, 0.0f, 0.0f}, v1 = v0;
+  if (slice < count) v0 = load(slice);
+  if (slice + S < count) v1 = load(slice + S);
+  float top = m;
+#pragma unroll
+  for (int off = kWave / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+  if (lane == 0) s_w[0][wave] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kKvJoinThreads / kWave; ++w) top = fmaxf(top, s_w[0][w]);
+  const float f = __builtin_amdgcn_exp2f(m - top);
+  s_f[threadIdx.x] = f;
+  float sum_l = l * f;
+#pragma unroll
+  for (int off = kWave / 2; off > 0; off >>= 1) sum_l += __shfl_xor(sum_l, off);
+  if (lane == 0) s_w[1][wave] = sum_l;
+  __syncthreads();
+  float ll = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kKvJoinThreads / kWave; ++w) ll += s_w[1][w];
+  kv_f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto add = [&](kv_f32x4 v, int c) W4K_INLINE {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(v[e], s_f[c], sum[e]);
+  };
+  if (slice < count) add(v0, slice);
+  if (slice + S < count) add(v1, slice + S);
+  for (int c = slice + 2 * S; c < count; c += S) add(load(c), c);
+  s_o[threadIdx.x] = sum;
+  __syncthreads();
+  if (slice > 0) return;
+#pragma unroll
+  for (int s = 1; s < S; ++s) sum += s_o[s * (D / 4) + threadIdx.x];
+  kv_store4(a.out + (size_t)out_row * D + d, sum, kv_inverse(ll));
 }
 
 }  // namespace w4k

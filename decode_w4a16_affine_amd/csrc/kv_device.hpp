@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "qmm_device.hpp"
 #include "w4a16_kv.h"
 
@@ -84,9 +86,21 @@ struct KvAttnArgs {
   int parts, part;
 };
 
-// Launchers (kv_attention.hip, once per head size).
+// Attention behind shared entries (w4a16_kv_attention_shared): entries before s =
+// min(max(shared_len[0], 0), max_shared) are read through row 0 of the block table for
+// all rows by the tile form, a request's own through its row by the split form, and a row's
+// partial results (`parts` of the shared entries, then `chunks` of its own) are joined.
+struct KvSharedArgs : KvAttnArgs {
+  const int32_t* shared_len;
+  int max_shared, max_own;
+};
+template <class Args>
+constexpr bool kv_behind_shared = std::is_same_v<Args, KvSharedArgs>;
+
+// Launchers (kv_attention.hip and kv_shared_attention.hip, once per head size).
 #define W4K_DECLARE_KV(D)                                                                     \
-  hipError_t kv_attention_d##D(int type, const KvAttnArgs& a, void* workspace, hipStream_t st);
+  hipError_t kv_attention_d##D(int type, const KvAttnArgs& a, void* workspace, hipStream_t st); \
+  hipError_t kv_shared_d##D(int type, const KvSharedArgs& a, void* workspace, hipStream_t st);
 W4K_DECLARE_KV(64)
 W4K_DECLARE_KV(128)
 W4K_DECLARE_KV(256)
@@ -121,6 +135,7 @@ __device__ __forceinline__ size_t kv_part_row(const KvAttnArgs& a, int out_row, 
 constexpr int kKvTile = 64;           // cache entries at once
 constexpr int kKvTileCols = 2;        // 16-row pieces a wave (or the waves that share rows)
 constexpr int kKvTileStats = 2;
+constexpr int kKvMaxParts = 128;      // parts of shared entries at most
 constexpr int kv_tile_share(int D) { return D == 256 ? 2 : 1; }
 constexpr int kv_tile_waves(int D, int type) { return D == 256 && type == W4A16_KV_INT8 ? 8 : 4; }
 constexpr int kv_tile_rows(int D, int type) { return kv_tile_waves(D, type) / kv_tile_share(D) * kKvTileCols * 16; }
@@ -135,6 +150,10 @@ inline size_t kv_split_floats(const KvAttnArgs& a, int D) {
 }
 inline size_t kv_workspace_floats(const KvAttnArgs& a, int D) {
   return kv_split_floats(a, D) + kv_tile_partials(a) * (D + kKvTileStats);
+}
+// Behind shared entries: results of each row of `out`, then their statistics.
+inline size_t kv_shared_partials(const KvSharedArgs& a) {
+  return (size_t)a.tokens * a.q_heads * (a.parts + a.chunks);
 }
 
 }  // namespace w4k

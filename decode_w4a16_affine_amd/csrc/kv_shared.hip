@@ -1,0 +1,132 @@
+// C ABI of the attention behind shared entries (w4a16_kv_attention_shared of
+// include/w4a16_step.h): argument checks and launch parameters.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "kv_host.hpp"
+#include "w4a16_step.h"
+
+namespace w4k {
+
+namespace {
+
+constexpr int kMaxEntries = 1 << 28;
+
+w4a16_status_t check_shared(const w4a16_kv_cache_t* cache, int tokens, int requests, int max_new, int max_shared,
+                            int max_own, int q_heads) {
+  const w4a16_status_t st = check_cache(cache);
+  if (st != W4A16_OK) return st;
+  if (tokens < 0 || requests < 0 || max_new < 0 || max_shared < 0 || max_own < 0 || q_heads < 1) return W4A16_ERR_SHAPE;
+  if (tokens > W4A16_KV_MAX_TOKENS || requests > W4A16_KV_MAX_REQUESTS || max_shared > kMaxEntries ||
+      max_own > kMaxEntries)
+    return W4A16_ERR_SHAPE;
+  if (q_heads % cache->heads || (int64_t)tokens * q_heads > 0x7FFFFFFFLL) return W4A16_ERR_SHAPE;
+  const int group = q_heads / cache->heads;
+  if (group > W4A16_KV_MAX_GROUP || (int64_t)max_new * group > kKvSplitRows) return W4A16_ERR_UNSUPPORTED;
+  // the tiles' grid (at least 64 rows each) within the launch limit of 2^32 threads
+  const int64_t tiles = tokens / (64 / group) + requests;
+  if (tiles * cache->heads > (1 << 22)) return W4A16_ERR_SHAPE;
+  return W4A16_OK;
+}
+
+// The launch parameters of a call from its (checked) sizes, all of them above 0.
+KvSharedArgs shared_args(const w4a16_kv_cache_t* cache, int tokens, int requests, int max_new, int max_shared,
+                         int max_own, int q_heads) {
+  KvSharedArgs a{};
+  a.c = device_cache(cache);
+  a.tokens = tokens;
+  a.requests = requests;
+  a.max_new = max_new;
+  a.max_len = 2 * kMaxEntries;
+  a.max_shared = max_shared;
+  a.max_own = max_own;
+  a.q_heads = q_heads;
+  a.group = q_heads / cache->heads;
+  a.group_inverse = (65536u + a.group - 1) / a.group;
+  a.split_tokens = max_new;
+  a.split = true;
+  a.by_token = true;
+  const int rows = a.split_tokens * a.group;
+  a.row_groups = rows <= 16 ? 1 : (rows + 31) / 32;
+  // chunks of a request's own entries, which may begin inside one
+  a.chunk_shift = max_own <= 1024 ? 7 : max_own <= 4096 ? 8 : max_own <= 16384 ? 9 : 10;
+  auto in_chunks = [&](int64_t n) { return (n + (1LL << a.chunk_shift) - 1) >> a.chunk_shift; };
+  while (in_chunks(max_own) > kKvMaxChunks - 1) ++a.chunk_shift;
+  a.chunks = max_own > 0 ? (int)in_chunks(max_own) + 1 : 0;
+  // Parts of the shared entries: as many workgroups as the card holds (512, two a CU), six
+  // tiles each at least.
+  a.part = kKvTile;
+  if (max_shared > 0) {
+    const int tile_tokens = kv_tile_rows(cache->dim, cache->type) / a.group;
+    const int64_t workgroups = (int64_t)((tokens + tile_tokens - 1) / tile_tokens) * cache->heads;
+    const int64_t wanted = std::min<int64_t>({512 / workgroups, max_shared / (6 * kKvTile), kKvMaxParts});
+    const int64_t parts = wanted > 1 ? wanted : 1;
+    a.part = (int)((max_shared + parts * kKvTile - 1) / (parts * kKvTile)) * kKvTile;
+    a.parts = (max_shared + a.part - 1) / a.part;
+  }
+  return a;
+}
+
+size_t shared_workspace(const KvSharedArgs& a, int dim) {
+  return kv_shared_partials(a) * (dim + kKvPartStats) * sizeof(float);
+}
+
+}  // namespace
+
+}  // namespace w4k
+
+using namespace w4k;
+
+extern "C" {
+
+size_t w4a16_kv_attention_shared_workspace_bytes(int tokens, int requests, int max_new, int max_shared, int max_own,
+                                                 int q_heads, const w4a16_kv_cache_t* cache) {
+  if (check_shared(cache, tokens, requests, max_new, max_shared, max_own, q_heads) != W4A16_OK) return 0;
+  if (tokens == 0 || requests == 0 || max_new == 0) return 0;
+  return shared_workspace(shared_args(cache, tokens, requests, max_new, max_shared, max_own, q_heads), cache->dim);
+}
+
+w4a16_status_t w4a16_kv_attention_shared(const uint16_t* q, int64_t q_stride, const w4a16_kv_cache_t* cache,
+                                         const int32_t* block_table, int width, const int32_t* seq_lens,
+                                         const int32_t* token_start, const int32_t* shared_len, uint16_t* out,
+                                         float scale, int tokens, int requests, int max_new, int max_shared,
+                                         int max_own, int q_heads, void* workspace, size_t workspace_bytes,
+                                         void* stream) {
+  w4a16_status_t st = check_shared(cache, tokens, requests, max_new, max_shared, max_own, q_heads);
+  if (st != W4A16_OK) return st;
+  if (width < 0 || width > W4A16_KV_MAX_WIDTH || q_stride < (int64_t)q_heads * cache->dim || q_stride % 8 ||
+      q_stride > (1LL << 40))
+    return W4A16_ERR_SHAPE;
+  if (tokens == 0 || requests == 0 || max_new == 0) return W4A16_OK;
+  if (cache->pages == 0) return W4A16_ERR_SHAPE;      // masked entries are read from page 0
+  st = check_cache_pointers(cache);
+  if (st != W4A16_OK) return st;
+  if (!q || !out || !seq_lens || !token_start || !shared_len || (width > 0 && !block_table)) return W4A16_ERR_NULL;
+  if (!kv_aligned(q, 16) || !kv_aligned(out, 16) || !kv_aligned(block_table, 4) || !kv_aligned(seq_lens, 4) ||
+      !kv_aligned(token_start, 4) || !kv_aligned(shared_len, 4))
+    return W4A16_ERR_ALIGN;
+  KvSharedArgs a = shared_args(cache, tokens, requests, max_new, max_shared, max_own, q_heads);
+  const size_t need = shared_workspace(a, cache->dim);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  if (!kv_aligned(workspace, 16)) return W4A16_ERR_ALIGN;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.table = block_table;
+  a.width = width;
+  a.seq_lens = seq_lens;
+  a.token_start = token_start;
+  a.shared_len = shared_len;
+  a.out = out;
+  a.scale_log2 = __builtin_fabsf(scale) * 1.44269504088896340736f;
+  a.q_sign = scale < 0.0f ? 0x80008000u : 0u;
+  hipStream_t s = (hipStream_t)stream;
+  switch (cache->dim) {
+    case 64: return kv_launched(kv_shared_d64(cache->type, a, workspace, s));
+    case 128: return kv_launched(kv_shared_d128(cache->type, a, workspace, s));
+    default: return kv_launched(kv_shared_d256(cache->type, a, workspace, s));
+  }
+}
+
+}  // extern "C"

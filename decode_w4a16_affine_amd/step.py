@@ -15,12 +15,14 @@ Tensor conventions (all on the same GPU; contiguous unless said otherwise):
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
 from . import OUT_BF16, OUT_F32, _check, _dtype, _shape
 from . import lib as _base_lib
-from .kv import _current, _current_device, _dense, _int32, _on, _raw_stream, _rows, _same_gpu
+from .kv import (KVCache, _attention_inputs, _cache, _current, _current_device, _dense, _int32, _on, _raw_stream, _rows,
+                 _same_gpu, _vector)
 
 ROPE_NORM = 1             # W4A16_ROPE_NORM
 ROPE_INTERLEAVED = 2      # W4A16_ROPE_INTERLEAVED
@@ -29,7 +31,8 @@ ROPE_MAX_AXES = 4         # W4A16_ROPE_MAX_AXES
 SAMPLE_MAX_ROWS = 65536   # W4A16_SAMPLE_MAX_ROWS
 SAMPLE_MAX_N = 1 << 20    # W4A16_SAMPLE_MAX_N
 
-STEP_EXPORTS = ("w4a16_qk_norm_rope", "w4a16_sample_workspace_bytes", "w4a16_sample")
+STEP_EXPORTS = ("w4a16_qk_norm_rope", "w4a16_kv_attention_shared_workspace_bytes", "w4a16_kv_attention_shared",
+                "w4a16_sample_workspace_bytes", "w4a16_sample")
 
 _vp = ctypes.c_void_p
 _int = ctypes.c_int
@@ -47,6 +50,12 @@ def step_lib() -> ctypes.CDLL:
         L.w4a16_qk_norm_rope.restype = _int
         L.w4a16_qk_norm_rope.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _float, _vp, _vp, ctypes.POINTER(_int), _int, _vp,
                                          _i64, _vp, _i64, _float, _int, _int, _int, _int, _int, _int, _vp]
+        cache = ctypes.POINTER(KVCache)
+        L.w4a16_kv_attention_shared_workspace_bytes.restype = ctypes.c_size_t
+        L.w4a16_kv_attention_shared_workspace_bytes.argtypes = [_int] * 6 + [cache]
+        L.w4a16_kv_attention_shared.restype = _int
+        L.w4a16_kv_attention_shared.argtypes = [_vp, _i64, cache, _vp, _int, _vp, _vp, _vp, _vp, _float, _int, _int, _int,
+                                                _int, _int, _int, _vp, ctypes.c_size_t, _vp]
         L.w4a16_sample_workspace_bytes.restype = ctypes.c_size_t
         L.w4a16_sample_workspace_bytes.argtypes = [_int, _int]
         L.w4a16_sample.restype = _int
@@ -151,6 +160,64 @@ def _rope(shapes, q, k, q_weight, k_weight, inv_freq, positions, q_out, qo_strid
                                          q_heads, k_heads, dim, rot, _raw_stream(stream, dev)), "w4a16_qk_norm_rope")
 
 
+# ---- attention behind shared entries ------------------------------------------------
+
+def w4a16_kv_attention_shared_workspace_bytes(tokens: int, requests: int, max_new: int, max_shared: int, max_own: int,
+                                              q_heads: int, k_cache, v_cache, k_scales, v_scales) -> int:
+    c = _cache(k_cache, v_cache, k_scales, v_scales)
+    _int32("tokens, requests, max_new, max_shared, max_own, q_heads", tokens, requests, max_new, max_shared, max_own,
+           q_heads)
+    return int(step_lib().w4a16_kv_attention_shared_workspace_bytes(tokens, requests, max_new, max_shared, max_own,
+                                                                    q_heads, ctypes.byref(c)))
+
+
+def w4a16_kv_attention_shared(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, shared_len, out,
+                              workspace, max_new: int, max_shared: int, max_own: int, scale: float = None,
+                              stream=None) -> None:
+    """out [T, HQ, D] = causal attention of q [T, HQ, D] for requests that begin with the same shared_len [1] entries.
+
+    Those lie in the pages of block_table's row 0, a request's others in those of its own row; max_new, max_shared
+    and max_own bound the requests' new tokens, shared_len and the entries behind it; the rest as
+    w4a16_kv_attention has it.  workspace: a uint8 device tensor of at least
+    w4a16_kv_attention_shared_workspace_bytes bytes, or None where that is 0."""
+    c = _cache(k_cache, v_cache, k_scales, v_scales)
+    inputs = _attention_inputs(c, q, block_table, seq_lens, token_start)
+    if out.dtype != torch.bfloat16:
+        _dtype(out, torch.bfloat16, "out")
+    if out.shape != q.shape:
+        _shape(out, q.shape, "out")
+    if workspace is not None:
+        _dtype(workspace, torch.uint8, "workspace")
+        _same_gpu(out, workspace)
+        _dense(workspace)
+    _same_gpu(q, out)
+    _dense(out)
+    _shared(c, inputs, q, (k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, shared_len), out,
+            workspace, max_new, max_shared, max_own, scale, stream)
+
+
+def _shared(c, inputs, q, ts, out, workspace, max_new, max_shared, max_own, scale, stream):
+    _vector(ts[7], "shared_len", 1)
+    _int32("max_new, max_shared, max_own", max_new, max_shared, max_own)
+    dev = _same_gpu(*ts, q)
+    _dense(*ts)
+    if _current_device() != dev:
+        return _on(dev, _shared, c, inputs, q, ts, out, workspace, max_new, max_shared, max_own, scale, stream)
+    tokens, q_stride, R, width = inputs
+    ref = ctypes.byref(c)
+    if out is None:      # the allocating form
+        need = step_lib().w4a16_kv_attention_shared_workspace_bytes(tokens, R, max_new, max_shared, max_own, q.shape[1], ref)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        workspace = q.new_empty(need, dtype=torch.uint8) if need else None
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    _check(step_lib().w4a16_kv_attention_shared(q.data_ptr(), q_stride, ref, ts[4].data_ptr(), width, ts[5].data_ptr(),
+                                                ts[6].data_ptr(), ts[7].data_ptr(), out.data_ptr(),
+                                                1.0 / math.sqrt(c.dim) if scale is None else scale, tokens, R, max_new,
+                                                max_shared, max_own, q.shape[1], ws, ws_bytes, _raw_stream(stream, dev)),
+           "w4a16_kv_attention_shared")
+    return out
+
+
 # ---- sampling -----------------------------------------------------------------------
 
 def w4a16_sample_workspace_bytes(M: int, N: int) -> int:
@@ -237,6 +304,19 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=No
     _rope(shapes, q, k, q_weight, k_weight, inv_freq, positions, q_out, shapes[2][1] * dim, k_out, shapes[3][1] * dim, eps,
           weight_offset, norm, interleaved, sections, None)
     return q_out, k_out
+
+
+def kv_attention_shared(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, shared_len,
+                        max_new: int, max_shared: int, max_own: int, scale: float = None, stream=None):
+    """Attention of a step behind shared entries: a new out [T, HQ, D] (see w4a16_kv_attention_shared)."""
+    if stream is not None:
+        with _current(stream, q):
+            return kv_attention_shared(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start,
+                                       shared_len, max_new, max_shared, max_own, scale)
+    c = _cache(k_cache, v_cache, k_scales, v_scales)
+    inputs = _attention_inputs(c, q, block_table, seq_lens, token_start)
+    return _shared(c, inputs, q, (k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, shared_len),
+                   None, None, max_new, max_shared, max_own, scale, None)
 
 
 def sample(logits, uniforms=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):

@@ -4,6 +4,8 @@
  *
  *   w4a16_qk_norm_rope         per layer, between the q/k/v products and w4a16_kv_append:
  *                              norms of queries and keys for each head, positions rotated in
+ *   w4a16_kv_attention_shared  per layer: attention for a batch whose requests begin with the
+ *                              same cache entries, read once for all of them
  *   w4a16_sample               once a step: tokens drawn from the LM head's logits
  *
  * Conventions: those of w4a16.h -- device pointers (host ones are named as such), `stream` a
@@ -55,6 +57,36 @@ w4a16_status_t w4a16_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uin
                                   uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
                                   float eps, int flags, int tokens, int q_heads, int k_heads, int dim, int rot,
                                   void *stream);
+
+/*
+ * Bytes of workspace w4a16_kv_attention_shared needs (0 for invalid arguments): D + 5
+ * floats for each part of the shared entries, or chunk of a request's own, and row of `out`.
+ */
+size_t w4a16_kv_attention_shared_workspace_bytes(int tokens, int requests, int max_new, int max_shared, int max_own,
+                                                 int q_heads, const w4a16_kv_cache_t *cache);
+
+/*
+ * w4a16_kv_attention (without a window) for decode and verify steps of requests that begin
+ * with the same entries: with s = min(max(shared_len[0], 0), max_shared), entry j of every
+ * request lies in page
+ *   block_table[0][j / P] for j < s,   block_table[r][j / P] from there on,
+ * so the shared entries are read once for all requests (those columns of the other rows are
+ * not looked at).  s need not end a page.  Rows, positions and masks are those of
+ * w4a16_kv_attention: the row at position pos attends entries 0 .. pos (also where pos < s).
+ * max_new bounds the requests' new tokens, max_own their entries from s on (entries from
+ * s + max_own on are unread); rows past max_new stay unwritten.
+ * max_new * HQ / H must not exceed 64: prompts' many rows read each entry once for many of
+ * them in w4a16_kv_attention already (W4A16_ERR_UNSUPPORTED).
+ * The arithmetic is w4a16_kv_attention's; the order of sums depends on the call's sizes
+ * (tokens, requests, max_*) and s, never on chance.  max_shared, max_own <= 2^28; the other
+ * limits and the alignment are w4a16_kv_attention's.
+ */
+w4a16_status_t w4a16_kv_attention_shared(const uint16_t *q, int64_t q_stride, const w4a16_kv_cache_t *cache,
+                                         const int32_t *block_table, int width, const int32_t *seq_lens,
+                                         const int32_t *token_start, const int32_t *shared_len, uint16_t *out,
+                                         float scale, int tokens, int requests, int max_new, int max_shared,
+                                         int max_own, int q_heads, void *workspace, size_t workspace_bytes,
+                                         void *stream);
 
 /* Bytes of workspace w4a16_sample needs (0 for invalid arguments). */
 size_t w4a16_sample_workspace_bytes(int M, int N);

@@ -4,6 +4,8 @@ from __future__ import annotations
 
 import numpy as np
 
+import kv_reference
+
 BF16_STEP = 2.0 ** -8       # a rounding to bf16 is off by at most half a step: this much of the value
 F32_STEP = 2.0 ** -24
 
@@ -71,3 +73,25 @@ def sample(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     at = int((running <= u * running[-1]).sum()) if u > 0 else int(np.flatnonzero(running > 0)[0])
     at = min(at, int(np.flatnonzero(w > 0)[-1]))
     return int(tokens[at]), w[at] / running[-1]
+
+
+def entry_table(table, lens, page, shared, max_own):
+    """Entry by entry, [R, longest]: page * P + offset of what each request's entry j < shared + max_own lies in, or -1.
+
+    table [R, width]: row 0's pages up to entry `shared`, each row's own from there on."""
+    longest = max([0, *lens])
+    out = np.full((len(lens), max(1, longest)), -1)
+    for r in range(len(lens)):
+        for j in range(min(longest, shared + max_own, table.shape[1] * page)):
+            p = table[0 if j < shared else r, j // page]
+            out[r, j] = p * page + j % page if p >= 0 else -1
+    return out
+
+
+def shared_attention(q, kc, ks, vc, vs, table, lens, start, scale, shared, max_own):
+    """(out, bound) of attention behind shared entries, as kv_reference.attention has them over a cache of one entry a
+    page.  (Its bound leaves 2^-21 of exponentials for the join's: the hardware's are off by 2^-23.)"""
+    pages, H, P, D = kc.shape
+    flat = lambda c: c.transpose(0, 2, 1, 3).reshape(pages * P, H, 1, D)  # noqa: E731
+    return kv_reference.attention(q, flat(kc), np.repeat(ks, P, 0), flat(vc), np.repeat(vs, P, 0),
+                                  entry_table(table, lens, P, shared, max_own), lens, start, scale, 0)

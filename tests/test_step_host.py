@@ -176,3 +176,72 @@ def test_sample_definition_by_hand():
     assert ref.sample(x, 0.0) == (4, 1.0)
     x[3] = np.nan
     assert ref.sample(x, 0.0)[0] == 3
+
+
+def cache(k=A16, v=A16, ks=A16, vs=A16, kind=0, pages=8, heads=2, page=64, dim=128):
+    return ctypes.byref(w4.KVCache(k, v, ks, vs, kind, pages, heads, page, dim))
+
+
+def test_shared_attention_refuses_bad_arguments(L):
+    sizes = (3, 3, 2, 500, 100, 8)
+    need = L.w4a16_kv_attention_shared_workspace_bytes(*sizes, cache())
+    assert need > 0
+
+    def attn(q=A16, stride=1024, c=None, table=A16, width=10, seq=A16, start=A16, s=A16, out=A16, T=3, R=3, new=2, shared=500,
+             own=100, HQ=8, ws=A16, ws_bytes=need):
+        return L.w4a16_kv_attention_shared(q, stride, cache() if c is None else c, table, width, seq, start, s, out, 0.1, T, R, new, shared,
+                                           own, HQ, ws, ws_bytes, None)
+
+    for bad in (dict(kind=2), dict(dim=96), dict(page=48)):
+        assert attn(c=cache(**bad)) == EUNSUP, bad
+    for bad in (dict(heads=0), dict(heads=1025), dict(pages=-1), dict(pages=2 ** 25), dict(pages=0)):
+        assert attn(c=cache(**bad)) == ESHAPE, bad
+    for bad in (dict(T=-1), dict(T=2 ** 20 + 1), dict(R=-1), dict(R=2 ** 20 + 1), dict(new=-1), dict(shared=-1), dict(own=-1),
+                dict(shared=2 ** 28 + 1), dict(own=2 ** 28 + 1), dict(HQ=0), dict(HQ=7), dict(width=-1),
+                dict(width=2 ** 22 + 1), dict(stride=1016), dict(stride=1028), dict(stride=2 ** 40 + 8)):
+        assert attn(**bad) == ESHAPE, bad
+    assert attn(HQ=130, stride=2 ** 20) == EUNSUP                   # 65 heads a cache head
+    assert attn(new=17) == EUNSUP                                   # 17 tokens of 4 heads: over 64 rows
+    assert attn(T=2 ** 20, R=2 ** 20, c=cache(heads=8), HQ=512, new=1, stride=2 ** 20) == ESHAPE
+    for bad in ("q", "table", "seq", "start", "s", "out"):
+        assert attn(**{bad: None}) == ENULL, bad
+    for bad in ("q", "out"):
+        assert attn(**{bad: A16 + 8}) == EALIGN, bad
+    for bad in ("table", "seq", "start", "s"):
+        assert attn(**{bad: A16 + 2}) == EALIGN, bad
+    for bad in ("k", "v"):
+        assert attn(c=cache(**{bad: None})) == ENULL and attn(c=cache(**{bad: A16 + 8})) == EALIGN
+    assert attn(ws_bytes=need - 1) == EWS and attn(ws=None) == EWS and attn(ws=A16 + 8) == EALIGN
+    assert attn(c=ctypes.POINTER(w4.KVCache)()) == ENULL
+    for empty in (dict(T=0), dict(R=0), dict(new=0)):
+        assert attn(**empty, q=None, ws=None, ws_bytes=0) == OK, empty
+    ws = L.w4a16_kv_attention_shared_workspace_bytes
+    assert ws(0, 3, 2, 500, 100, 8, cache()) == 0 and ws(3, 3, 17, 500, 100, 8, cache()) == 0
+    assert ws(3, 3, 2, 0, 0, 8, cache()) == 0
+    # one part of 500 entries, two chunks of 128 for 100 that may begin inside one
+    assert need == 3 * 8 * 3 * (128 + 5) * 4
+
+
+def test_shared_attention_binding_refuses_bad_tensors():
+    c = w4.kv_cache(4, 2, 64, 16, device="cpu")
+    i = lambda *n: host(*n, dtype=torch.int32)  # noqa: E731
+    good = dict(q=host(3, 4, 64), block_table=i(2, 5), seq_lens=i(2), token_start=i(3), shared_len=i(1), max_new=2,
+                max_shared=20, max_own=30)
+    for bad, kind in ((dict(q=host(3, 4, 128)), ValueError), (dict(q=good["q"].float()), TypeError),
+                      (dict(block_table=i(3, 5)), ValueError), (dict(seq_lens=i(2).long()), TypeError),
+                      (dict(token_start=i(2)), ValueError), (dict(shared_len=i(2)), ValueError),
+                      (dict(shared_len=i(1).float()), TypeError), (dict(max_own=2 ** 31), ValueError),
+                      (dict(max_shared=2 ** 40), ValueError), (dict(), ValueError)):      # (host tensors)
+        with pytest.raises(kind):
+            kw = {**good, **bad}
+            w4.kv_attention_shared(kw.pop("q"), *c, **kw)
+    for out, ws in ((host(3, 4, 128), None), (host(3, 4, 64).float(), None), (host(3, 4, 64), host(5))):
+        with pytest.raises((TypeError, ValueError)):
+            kw = dict(good)
+            w4.w4a16_kv_attention_shared(kw.pop("q"), *c, **kw, out=out, workspace=ws)
+
+
+def test_shared_entries_by_hand():
+    table = np.array([[3, 1, 7], [9, 4, 5]])
+    assert ref.entry_table(table, [5, 6], 2, 3, 2).tolist() == [[6, 7, 2, 3, 14, -1], [6, 7, 2, 9, 10, -1]]
+    assert ref.entry_table(table, [5, 2], 2, 0, 9).tolist() == [[6, 7, 2, 3, 14], [18, 19, 8, 9, 10]]
