@@ -113,6 +113,7 @@ size_t w4a16_sample_workspace_bytes(int M, int N);
  * drawn; a row of nothing else gives token -1 and share 0.  With a logit of +infinity only
  * those of +infinity have weight.  A row with a NaN gives its first NaN and share NaN.
  * Sums of weights are of integers, or in a fixed order: the same call gives the same tokens.
+ * (A weight counts to 2^-62 N of the largest: tokens of less may be passed over, also as "the last kept one".)
  * workspace: w4a16_sample_workspace_bytes(M, N) bytes, not initialised.
  * M <= W4A16_SAMPLE_MAX_ROWS, N <= W4A16_SAMPLE_MAX_N.  N 0: tokens -1, shares 0.
  * Alignment: logits by their type (rows need no more), fp32 and int32 arrays 4, workspace 16.

@@ -135,7 +135,12 @@ def test_sample_refuses_bad_arguments(L):
     for bad in ("x", "u", "t", "k", "p", "m", "tokens", "share"):
         assert sample(**{bad: A16 + 2}) == EALIGN, bad
     assert sample(x=A16 + 1, dtype=0) == EALIGN
+    assert need > 0 and sample(ws=None) == EWS and sample(ws_bytes=need - 1) == EWS and sample(ws=A16 + 8) == EALIGN
     assert sample(M=0) == OK and sample(M=0, x=None, tokens=None, ws=None, ws_bytes=0) == OK
+    # rows go through in turns of 16384 chunks of 8192 tokens
+    ws = L.w4a16_sample_workspace_bytes
+    assert ws(65536, 2 ** 20) == ws(128, 2 ** 20) < 200 << 20 and ws(65536, 1) == ws(16384, 1) > ws(16383, 1)
+    assert ws(0, 5) == 0 and ws(5, 0) == 0
     assert L.w4a16_sample_workspace_bytes(-1, 5) == 0 and L.w4a16_sample_workspace_bytes(5, 2 ** 20 + 1) == 0
 
 
