@@ -3,7 +3,7 @@
 // With C = (falling logit, rising index) as one 64-bit number every limit is "the tokens up
 // to some C": top_k's is the C of the k-th token, top_p's that of the first token at which
 // the running sum of weights reaches its share.  So nothing is sorted: a histogram over
-// buckets of logits (1 / 8 of a temperature wide) tells which buckets the limits lie in, and
+// buckets of logits (1 / 12 of a temperature wide) tells which buckets the limits lie in, and
 // only those buckets' tokens are looked at one by one.
 //
 // Launches.  scan: a workgroup reads a chunk of 8192 logits into registers; its largest
@@ -30,6 +30,9 @@ namespace w4k {
 
 namespace {
 
+// lambdas over register arrays must be inlined for these to stay in registers
+#define W4K_INLINE __attribute__((always_inline))
+
 constexpr int kSampleThreads = 1024;
 constexpr int kSampleWaves = kSampleThreads / kWave;
 constexpr int kSampleSub = 1024;      // tokens whose weights are summed together before the draw
@@ -41,11 +44,18 @@ constexpr int kLane = 16;                             // logits a lane holds
 constexpr int kChunk = kScanThreads * kLane;          // and a workgroup
 constexpr int kChunks = W4A16_SAMPLE_MAX_N / kChunk;
 constexpr int kBuckets = 256;
-constexpr float kBucketsPerUnit = 8.0f;               // of (logit / temperature)
+constexpr float kBucketsPerUnit = 12.0f;              // of (logit / temperature)
 constexpr int kListed = 1024;                         // tokens of a chunk that are listed at most
 constexpr int kSmallK = 512;                          // limits of so few tokens need no weights from the scan
 constexpr int kChunkScale = 49;                       // a chunk's weights are multiples of 2^-49 (8192 of them below 2^63)
-static_assert(kChunk == 1 << (62 - kChunkScale) && kChunks <= kSampleThreads && kBuckets <= kScanThreads, "");
+// A bucket of a chunk: its tokens times 2^50, and their weights, multiples of 2^-36 (8192 below 2^50).  Its limits
+// are found with a margin for that, and what a weight is off by, 2^-37 of the largest, divides among the tokens'
+// borders: one in 10^6 rows or fewer would draw a neighbour.
+constexpr int kBinScale = 36, kBinCount = 50;
+constexpr int kSorted = 1024;                         // listed tokens that are sorted at most
+constexpr int kHeld = 8;                              // listed tokens that a thread of the draw holds
+static_assert(kChunk == 1 << (62 - kChunkScale) && kChunk <= 1 << (kBinCount - kBinScale - 1), "sums fit");
+static_assert(kChunks <= kSampleThreads && kBuckets <= kScanThreads && kSorted == kSampleThreads, "a thread each");
 static_assert(kSampleSub == kSampleThreads && kSampleSubs <= kSampleThreads, "one thread a token, or a piece");
 
 struct SampleArgs {
@@ -59,13 +69,12 @@ struct SampleArgs {
   int log2_scale;      // weights are multiples of 2^-log2_scale
   // of these rows (see sample_places)
   int chunks;
+  int list_threads;    // of the draw, for each chunk's list: a power of two
   float* top;          // [M][chunks] largest logit of a chunk, NaN if it has one
   uint32_t* top_at;    // [M][chunks] its first token, or the first NaN
   double* mass;        // [M][chunks] rows without limits: weights, of a chunk's largest logit
   uint64_t* kept;      // [M][chunks] others: weights of the buckets in front of lo, of a row's
-  uint64_t* bins;      // [M][chunks][kBuckets] weights of a chunk's buckets, of its largest logit
-  uint32_t* counts;    // [M][chunks][kBuckets] tokens of a chunk's buckets
-  uint64_t* total;     // [M][chunks] weights of a chunk
+  uint64_t* bins;      // [M][chunks][kBuckets] tokens and weights of a chunk's buckets, of its largest logit
   uint32_t* listed;    // [M][chunks] tokens in lo .. hi
   uint2* list;         // [M][chunks][kListed] these: logit, token
   struct SampleCut* cut;      // [M]
@@ -76,7 +85,7 @@ struct SampleCut {
   int lo, hi;          // buckets
   int before;          // tokens in front of lo
   int min_p_alone;     // top_k and top_p end behind hi
-  uint64_t total;      // all weights, of the row's largest logit
+  uint64_t total;      // all weights, as kept (SampleArgs)
 };
 
 // A row's parameters.
@@ -114,16 +123,22 @@ __device__ __forceinline__ uint32_t sample_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
   return u >> 31 ? ~u : u | 0x80000000u;
 }
-// Position in the order of falling logits: smaller comes first.
+// Position in the order of falling logits: smaller comes first.  (And the logit back.)
 __device__ __forceinline__ uint64_t sample_order(float v, int i) { return (uint64_t)~sample_key(v) << 32 | (uint32_t)i; }
 
+__device__ __forceinline__ float sample_logit(uint64_t c) {
+  const uint32_t key = ~(uint32_t)(c >> 32);
+  return __uint_as_float(key >> 31 ? key & 0x7FFFFFFFu : ~key);
+}
+
+// (logit - top) / temperature: 0 for the largest also where that is infinite
 __device__ __forceinline__ double sample_log_weight(float v, float top, double inv_t) {
   return v == top ? 0.0 : ((double)v - (double)top) * inv_t;
 }
-// The weight times 2^log2_scale.  2^t = 2^n 2^f with |f| <= 1/2, the latter by its Taylor series to
-// f^11: off by 2^-47 of it (the rest of the series 2^-47, t's rounding 2^-47 where t is above -64).
-__device__ __forceinline__ double sample_weight(float v, float top, double inv_t, int log2_scale) {
-  const double t = fmax(sample_log_weight(v, top, inv_t) * 1.4426950408889634074, -1000.0);
+// 2^t times 2^scale for t <= 0, below 2^-1000 as there.  2^t = 2^n 2^f with |f| <= 1/2, the latter by its Taylor
+// series to f^11: off by 2^-47 of it (the rest of the series 2^-47, t's rounding 2^-47 where t is above -64).
+__device__ __forceinline__ double sample_exp2(double t, int scale) {
+  t = fmax(t, -1000.0);
   const double n = __builtin_rint(t), f = t - n;
   double y = 4.4455382718708101e-10;
   y = __builtin_fma(y, f, 7.0549116208011209e-09);
@@ -134,23 +149,28 @@ __device__ __forceinline__ double sample_weight(float v, float top, double inv_t
   y = __builtin_fma(y, f, 1.3333558146428441e-03);
   y = __builtin_fma(y, f, 9.6181291076284769e-03);
   y = __builtin_fma(y, f, 5.5504108664821576e-02);
-  y = __builtin_fma(y, f, 2.4022650695910071e-01);
+  y = __builtin_fma(y, f, 2.4022650695910069e-01);
   y = __builtin_fma(y, f, 6.9314718055994529e-01);
   y = __builtin_fma(y, f, 1.0);
-  return __builtin_ldexp(y, (int)n + log2_scale);
+  return __builtin_ldexp(y, (int)n + scale);
 }
-// The same rounded to an integer, for scales up to 2^49: it appears in the low bits of 2^52 and it.
-__device__ __forceinline__ uint64_t sample_units(float v, float top, double inv_t) {
-  return (uint64_t)__double_as_longlong(sample_weight(v, top, inv_t, kChunkScale) + 0x1p52) & 0xFFFFFFFFFFFFFull;
+constexpr double kLog2E = 1.4426950408889634074;
+// A weight times 2^log2_scale
+__device__ __forceinline__ double sample_weight(float v, float top, double inv_t, int log2_scale) {
+  return sample_exp2(sample_log_weight(v, top, inv_t) * kLog2E, log2_scale);
+}
+// A weight held in integers: it appears in the low bits of 2^52 and it (at most 2^50).
+__device__ __forceinline__ uint64_t sample_units(double w) {
+  return (uint64_t)__double_as_longlong(w + 0x1p52) & 0xFFFFFFFFFFFFFull;
 }
 
-// A logit's bucket counted from any fixed one; grows with the logit.  (Far logits share
-// the outermost ones.)
+// A logit's bucket counted from any fixed one; grows with the logit.  (A sum with 1.5 * 2^23 is rounded
+// to an integer; far logits share the outermost ones.)
 __device__ __forceinline__ float sample_bucket_scale(double inv_t) {
   return fminf(kBucketsPerUnit * (float)inv_t, 0x1p100f);
 }
 __device__ __forceinline__ int sample_bucket(float v, float scale) {
-  return (int)__builtin_floorf(fminf(fmaxf(v * scale, -0x1p23f), 0x1p23f));
+  return __float_as_int(__builtin_amdgcn_fmed3f(__builtin_fmaf(v, scale, 0x1.8p23f), 0x1p23f, 0x1.fffffep23f));
 }
 // Counted down from the one of a row's or chunk's largest logit, and the last one for all behind it.
 __device__ __forceinline__ int sample_below(int top_bucket, float v, float scale) {
@@ -199,70 +219,149 @@ __device__ __forceinline__ void sample_load_chunk(const T* row, int chunk, int N
   for (int x = 0; x < kLane; x += V) sample_load_row<V>(row, sample_token<T>(chunk, x), N, v + x);
 }
 
+// A wave's running sums: rows of 16 lanes by shifts within them, then their last lanes' to the rows behind.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t sample_from_lane(uint64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xF, false);
+  return (uint64_t)hi << 32 | lo;
+}
+__device__ __forceinline__ uint64_t sample_wave_scan(uint64_t v) {
+  v += sample_from_lane<0x111, 0xF>(v);
+  v += sample_from_lane<0x112, 0xF>(v);
+  v += sample_from_lane<0x114, 0xF>(v);
+  v += sample_from_lane<0x118, 0xF>(v);
+  v += sample_from_lane<0x142, 0xA>(v);      // lane 15 to the second row, lane 47 to the fourth
+  v += sample_from_lane<0x143, 0xC>(v);      // lane 31 to the upper half
+  return v;
+}
 // Sums over the block's threads.  Values of threads before this one, and of all (returned).
-__device__ __forceinline__ uint64_t sample_scan(uint64_t v, uint64_t& before, uint64_t (&s_waves)[kSampleWaves]) {
+template <int WAVES>
+__device__ __forceinline__ uint64_t sample_scan(uint64_t v, uint64_t& before, uint64_t (&s_waves)[WAVES]) {
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  uint64_t sum = v;
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const uint64_t o = __shfl_up((unsigned long long)sum, off);
-    if (lane >= off) sum += o;
-  }
+  const uint64_t sum = sample_wave_scan(v);
   __syncthreads();      // (s_waves may still be read from a scan before)
   if (lane == kWave - 1) s_waves[wave] = sum;
   __syncthreads();
-  uint64_t total = 0, earlier = 0;
-#pragma unroll
-  for (int w = 0; w < kSampleWaves; ++w) {
-    if (w == wave) earlier = total;
-    total += s_waves[w];
-  }
-  before = earlier + sum - v;
-  return total;
+  // each row of lanes scans the waves' sums
+  static_assert(WAVES <= 16, "a lane of a row each");
+  uint64_t upto = (lane & 15) < WAVES ? s_waves[lane & 15] : 0;
+  upto += sample_from_lane<0x111, 0xF>(upto);
+  upto += sample_from_lane<0x112, 0xF>(upto);
+  upto += sample_from_lane<0x114, 0xF>(upto);
+  upto += sample_from_lane<0x118, 0xF>(upto);
+  auto of_wave = [&](int w) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(upto >> 32), w) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)upto, w);
+  };
+  const int w = __builtin_amdgcn_readfirstlane(wave);
+  before = (w ? of_wave(w - 1) : 0) + sum - v;
+  return of_wave(WAVES - 1);
 }
 
 struct SampleShared {
   uint64_t bins[kSampleBins];
   uint64_t waves[kSampleWaves];
   uint64_t found[2];
+  uint32_t few;
   uint64_t chunk[kChunks];      // kept weights
-  uint32_t listed[kChunks];
+  uint32_t listed[kChunks], place[kChunks];
 };
 
+// Sorts the threads' numbers, the smallest to thread 0, by compare and exchange (bitonic);
+// n: a power of two of threads that have one, at least a wave's.
+__device__ __forceinline__ uint64_t sample_sort(uint64_t c, int n, uint64_t* s_swap) {
+  const int i = threadIdx.x;
+  for (int k = 2; k <= n; k <<= 1) {
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      uint64_t other;
+      if (j >= kWave) {
+        __syncthreads();
+        s_swap[i] = c;
+        __syncthreads();
+        other = s_swap[i ^ j];
+      } else {
+        if (i >= n) continue;      // (whole waves)
+        other = __shfl_xor((unsigned long long)c, j);
+      }
+      const bool smaller = ((i & k) == 0) == ((i & j) == 0);
+      c = (other < c) == smaller ? other : c;
+    }
+  }
+  return c;
+}
+
 // The first C (in order) at which the running sum of `measure` reaches target, 1 <=
-// target <= the sum over all.  visit(f) calls f(C, measure) for the thread's tokens.
-template <class Visit>
-__device__ uint64_t sample_select(Visit&& visit, uint64_t target, SampleShared& sh) {
-  // digits of C: 11, 11 and 10 bits of the logit, 12 (always 0), 10 and 10 of the index
-  constexpr int shifts[5] = {53, 42, 32, 10, 0};
-  uint64_t prefix = 0, base = 0;      // C's digits so far; the sum in front of them
-  int known = 64;                     // bits below which C is not known yet
-#pragma unroll 1
-  for (int d = 0; d < 5; ++d) {
-    const int shift = shifts[d];
-    for (int b = threadIdx.x; b < kSampleBins; b += kSampleThreads) sh.bins[b] = 0;
+// target <= the sum over all.  visit(f) calls f(C, measure) for the thread's tokens, at(C) is
+// its measure again.  Bins over the range of the tokens' C tell which of them has it; a bin
+// of few tokens is sorted, another one is divided again.
+template <class Visit, class Measure>
+__device__ __forceinline__ uint64_t sample_select(Visit&& visit, Measure&& measure_of, uint64_t target, SampleShared& sh) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  uint64_t lo = ~0ull, hi = 0;
+  visit([&](uint64_t c, uint64_t) W4K_INLINE {
+    lo = c < lo ? c : lo;
+    hi = c > hi ? c : hi;
+  });
+#pragma unroll
+  for (int off = kWave / 2; off > 0; off >>= 1) {
+    const uint64_t l = __shfl_xor((unsigned long long)lo, off), h = __shfl_xor((unsigned long long)hi, off);
+    lo = l < lo ? l : lo;
+    hi = h > hi ? h : hi;
+  }
+  __syncthreads();
+  if (lane == 0) sh.bins[wave] = lo, sh.bins[kSampleWaves + wave] = hi;
+  __syncthreads();
+  for (int w = 0; w < kSampleWaves; ++w) {
+    lo = sh.bins[w] < lo ? sh.bins[w] : lo;
+    hi = sh.bins[kSampleWaves + w] > hi ? sh.bins[kSampleWaves + w] : hi;
+  }
+  uint64_t base = 0;      // the sum in front of lo
+  for (;;) {
+    const uint64_t range = hi - lo;
+    const int bits = range ? 64 - __builtin_clzll(range) : 0, shift = bits > 11 ? bits - 11 : 0;
+    static_assert(kSampleBins == 1 << 11, "the shift");
     __syncthreads();
-    visit([&](uint64_t c, uint64_t measure) {
-      if (known == 64 || c >> known == prefix >> known)
-        atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[(c >> shift) & (kSampleBins - 1)]), measure);
+    sh.bins[tid] = 0, sh.bins[tid + kSampleThreads] = 0;
+    if (tid == 0) sh.found[0] = 0, sh.found[1] = 0, sh.few = 0;
+    __syncthreads();
+    visit([&](uint64_t c, uint64_t measure) W4K_INLINE {
+      if (c >= lo && c <= hi) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[(c - lo) >> shift]), measure);
     });
     __syncthreads();
-    const uint64_t v0 = sh.bins[2 * threadIdx.x], v1 = sh.bins[2 * threadIdx.x + 1];
+    const uint64_t v0 = sh.bins[2 * tid], v1 = sh.bins[2 * tid + 1];
     uint64_t before;
     sample_scan(v0 + v1, before, sh.waves);
     before += base;
     if (before < target && before + v0 + v1 >= target) {      // one thread's
       const bool second = before + v0 < target;
-      sh.found[0] = 2 * threadIdx.x + second;
+      sh.found[0] = 2 * tid + second;
       sh.found[1] = before + (second ? v0 : 0);
     }
     __syncthreads();
-    prefix |= sh.found[0] << shift;
+    lo += sh.found[0] << shift;
+    hi = lo + ((1ull << shift) - 1) < hi ? lo + ((1ull << shift) - 1) : hi;
     base = sh.found[1];
-    known = d == 2 ? 20 : shift;
+    if (shift == 0) return lo;
+    // the bin's tokens, in order, if they are few
+    visit([&](uint64_t c, uint64_t) W4K_INLINE {
+      if (c < lo || c > hi) return;
+      const uint32_t at = atomicAdd(&sh.few, 1u);
+      if (at < kSorted) sh.bins[at] = c;
+    });
     __syncthreads();
+    const int n = (int)sh.few;
+    if (n > kSorted) continue;
+    int threads = kWave;
+    while (threads < n) threads <<= 1;
+    const uint64_t c = sample_sort(tid < n ? sh.bins[tid] : ~0ull, threads, sh.bins + kSampleThreads);
+    const uint64_t m = tid < n ? measure_of(c) : 0;
+    sample_scan(m, before, sh.waves);
+    before += base;
+    if (before < target && before + m >= target) sh.found[0] = c;
+    __syncthreads();
+    return sh.found[0];
   }
-  return prefix;
 }
 
 // A row's chunks: its largest logit and that one's token, or its first NaN's.
@@ -270,18 +369,33 @@ struct SampleTop {
   float top;
   uint32_t at;
 };
-__device__ __forceinline__ SampleTop sample_row_top(const SampleArgs& a, int r) {
-  // every wave goes through all chunks (up to 128: two a lane)
+// Every wave goes through all chunks, two a lane; their loads come first (sample_tops), so that
+// others can be on their way beside them.
+static_assert(kChunks <= 2 * kWave, "two chunks a lane");
+struct SampleTops {
+  float top[2];
+  uint32_t at[2];
+};
+__device__ __forceinline__ SampleTops sample_tops(const SampleArgs& a, int r) {
   const int lane = threadIdx.x & (kWave - 1);
+  SampleTops t;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const size_t c = (size_t)r * a.chunks + min(lane + i * kWave, a.chunks - 1);
+    t.top[i] = a.top[c];
+    t.at[i] = a.top_at[c];
+  }
+  return t;
+}
+__device__ __forceinline__ SampleTop sample_row_top(const SampleTops& t) {
   float top = -__builtin_inff();
   uint32_t at = ~0u, nan = ~0u;
-  for (int c = lane; c < a.chunks; c += kWave) {
-    const float v = a.top[(size_t)r * a.chunks + c];
-    const uint32_t i = a.top_at[(size_t)r * a.chunks + c];
-    if (v != v)
-      nan = min(nan, i);
-    else if (v > top || at == ~0u)
-      top = v, at = i;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (t.top[i] != t.top[i])
+      nan = min(nan, t.at[i]);
+    else if (t.top[i] > top || (t.top[i] == top && t.at[i] < at))
+      top = t.top[i], at = t.at[i];
   }
 #pragma unroll
   for (int off = kWave / 2; off > 0; off >>= 1) {
@@ -297,9 +411,8 @@ __device__ __forceinline__ SampleTop sample_row_top(const SampleArgs& a, int r) 
 // scan
 // ---------------------------------------------------------------------------
 template <class T>
-__global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a) {
+__global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs a) {
   __shared__ uint64_t s_bins[kBuckets];
-  __shared__ uint32_t s_counts[kBuckets];
   __shared__ float s_top[kScanWaves];
   __shared__ uint32_t s_at[kScanWaves];
   __shared__ double s_sum[kScanWaves];
@@ -308,7 +421,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a)
   float v[kLane];
   sample_load_chunk(row, chunk, a.N, v);
   const SampleRow p = sample_row(a, r);
-  if (tid < kBuckets) s_bins[tid] = 0, s_counts[tid] = 0;
+  if (tid < kBuckets) s_bins[tid] = 0;
   const size_t at = (size_t)r * a.chunks + chunk;
   // the largest logit (fmaxf leaves NaN out), and the first token that has it or is NaN
   float top = v[0];
@@ -334,30 +447,46 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a)
   if (lane == 0) s_at[wave] = first;
   double sum = 0.0;
   if (!p.greedy && !nan && top > -__builtin_inff()) {
-    if (!sample_limited(p)) {
+    const double inv_t = p.inv_t * kLog2E;
+    const float scale = sample_bucket_scale(p.inv_t);
+    const int top_bucket = sample_bucket(top, scale);
+    // f(logit, weight times 2^scale), four at a time: more would take too many registers
+    auto weights = [&](int log2_scale, auto&& f) W4K_INLINE {
+      if (top == __builtin_inff()) {      // (only its equals have one)
 #pragma unroll
-      for (int x = 0; x < kLane; ++x) sum += sample_weight(v[x], top, p.inv_t, 0);
+        for (int x = 0; x < kLane; ++x) f(v[x], v[x] == top ? __builtin_ldexp(1.0, log2_scale) : 0.0);
+      } else {
 #pragma unroll
-      for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
-    } else {
-      const float scale = sample_bucket_scale(p.inv_t);
-      const int top_bucket = sample_bucket(top, scale);
-      const bool few = sample_few(p);
-      uint64_t units = 0;
-#pragma unroll
-      for (int x = 0; x < kLane; ++x) {
-        const int b = sample_below(top_bucket, v[x], scale);
-        const uint64_t w = few ? 0 : sample_units(v[x], top, p.inv_t);
-        units += w;
-        // (what the last bucket has is the rest)
-        if (b < kBuckets - 1) {
-          atomicAdd(&s_counts[b], 1u);
-          if (!few) atomicAdd(reinterpret_cast<unsigned long long*>(&s_bins[b]), w);
+        for (int x = 0; x < kLane; ++x) {
+          f(v[x], sample_exp2(((double)v[x] - (double)top) * inv_t, log2_scale));
+          if (x % 4 == 3) __builtin_amdgcn_sched_barrier(0);
         }
       }
+    };
+    if (!sample_limited(p)) {
+      weights(0, [&](float, double w) W4K_INLINE { sum += w; });
 #pragma unroll
-      for (int off = kWave / 2; off > 0; off >>= 1) units += __shfl_xor((unsigned long long)units, off);
-      sum = __longlong_as_double((long long)units);
+      for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+    } else if (sample_few(p)) {
+#pragma unroll
+      for (int x = 0; x < kLane; ++x) {      // (the upper half of a bucket)
+        const int b = sample_below(top_bucket, v[x], scale);
+        if (b < kBuckets - 1) atomicAdd(reinterpret_cast<uint32_t*>(&s_bins[b]) + 1, 1u << (kBinCount - 32));
+      }
+    } else {
+      // The last bucket's weights are added up first and its tokens not counted (they are the rest):
+      // it may have most of a chunk, whose additions would wait for each other.
+      uint64_t rest = 0;
+      weights(kBinScale, [&](float x, double w) W4K_INLINE {
+        const uint64_t units = sample_units(w);
+        const int b = sample_below(top_bucket, x, scale);
+        if (b < kBuckets - 1)
+          atomicAdd(reinterpret_cast<unsigned long long*>(&s_bins[b]), units + (1ull << kBinCount));
+        else
+          rest += units;
+      });
+      rest = sample_wave_scan(rest);
+      if (lane == kWave - 1 && rest) atomicAdd(reinterpret_cast<unsigned long long*>(&s_bins[kBuckets - 1]), rest);
     }
   }
   if (lane == 0) s_sum[wave] = sum;
@@ -367,89 +496,102 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a)
     for (int w = 0; w < kScanWaves; ++w) first = min(first, s_at[w]);
     a.top[at] = nan ? __builtin_nanf("") : top;
     a.top_at[at] = first;
-    double all = 0.0;
-    uint64_t units = 0;
 #pragma unroll
-    for (int w = 0; w < kScanWaves; ++w) {
-      all += s_sum[w];
-      units += (uint64_t)__double_as_longlong(s_sum[w]);
-    }
-    a.mass[at] = all;
-    a.total[at] = units;
+    for (int w = 1; w < kScanWaves; ++w) sum += s_sum[w];
+    a.mass[at] = sum;
   }
-  if (sample_limited(p) && tid < kBuckets) {
-    a.counts[at * kBuckets + tid] = s_counts[tid];
-    if (!sample_few(p)) a.bins[at * kBuckets + tid] = s_bins[tid];
-  }
+  if (sample_limited(p) && tid < kBuckets) a.bins[at * kBuckets + tid] = s_bins[tid];
 }
 
 // ---------------------------------------------------------------------------
-// cut: a thread a bucket
+// cut: a row's buckets from its chunks'
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(kBuckets) void sample_cut_kernel(SampleArgs a) {
+constexpr int kCutThreads = 1024;
+constexpr int kCutScale = 42;      // (2^20 weights below 2^63)
+constexpr int kCutAhead = 8;       // buckets a thread has on their way
+__device__ __forceinline__ double sample_bin_mass(uint64_t bin) {
+  return (double)(bin & ((1ull << kBinCount) - 1)) * (1.0 / (1ull << kBinScale));
+}
+
+__global__ __launch_bounds__(kCutThreads) void sample_cut_kernel(SampleArgs a) {
   __shared__ double s_factor[kChunks];
   __shared__ int s_shift[kChunks];
-  __shared__ double s_waves[kBuckets / kWave];
-  __shared__ uint32_t s_counts[kBuckets / kWave];
-  __shared__ double s_mass[kBuckets];
+  __shared__ uint64_t s_mass[kBuckets];
   __shared__ uint32_t s_count[kBuckets];
+  __shared__ uint64_t s_waves[2][kBuckets / kWave];
   __shared__ int s_first[4];
-  const int r = blockIdx.x, b = threadIdx.x, lane = b & (kWave - 1), wave = b / kWave;
+  const int r = blockIdx.x, b = threadIdx.x, lane = b & (kWave - 1);
+  const SampleTops tops = sample_tops(a, r);
+  const uint64_t* const bins = a.bins + (size_t)r * a.chunks * kBuckets;
+  const int all = a.chunks * kBuckets;
+  uint64_t bin[kCutAhead];
+#pragma unroll
+  for (int i = 0; i < kCutAhead; ++i) bin[i] = bins[min(b + i * kCutThreads, all - 1)];
   const SampleRow p = sample_row(a, r);
-  const SampleTop row = sample_row_top(a, r);
+  const SampleTop row = sample_row_top(tops);
   if (p.greedy || !sample_limited(p) || !(row.top > -__builtin_inff())) return;
-  const bool few = sample_few(p);
   const float scale = sample_bucket_scale(p.inv_t);
   const int top_bucket = sample_bucket(row.top, scale);
-  double total = 0.0;
-  for (int c = b; c < a.chunks; c += kBuckets) {
-    const float top = a.top[(size_t)r * a.chunks + c];
-    // (a chunk of -infinity alone has no weights; its tokens lie in the last bucket)
-    s_factor[c] = top > -__builtin_inff() ? sample_weight(top, row.top, p.inv_t, 0) : 0.0;
-    s_shift[c] = top > -__builtin_inff() ? min(top_bucket - sample_bucket(top, scale), kBuckets) : kBuckets;
+  if (b < kWave) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = lane + i * kWave;
+      if (c >= a.chunks) break;
+      // (a chunk of -infinity alone has no weights; its tokens lie in the last bucket)
+      const float top = tops.top[i];
+      s_factor[c] = top > -__builtin_inff() ? sample_weight(top, row.top, p.inv_t, kCutScale) : 0.0;
+      s_shift[c] = top > -__builtin_inff() ? min(top_bucket - sample_bucket(top, scale), kBuckets) : kBuckets;
+    }
   }
+  if (b < kBuckets) s_mass[b] = 0, s_count[b] = 0;
   if (b < 4) s_first[b] = kBuckets - 1;
   __syncthreads();
-  double mass = 0.0;
-  uint32_t count = 0;
-  for (int c = 0; c < a.chunks; ++c) {
-    const size_t at = (size_t)r * a.chunks + c;
-    if (!few) total += __builtin_ldexp((double)a.total[at], -kChunkScale) * s_factor[c];
-    const int from = b - s_shift[c];
-    if (from < 0 || b == kBuckets - 1) continue;
-    count += a.counts[at * kBuckets + from];
-    if (!few) mass += __builtin_ldexp((double)a.bins[at * kBuckets + from], -kChunkScale) * s_factor[c];
-  }
-  // sums over the buckets up to this one, in a fixed order
-  double upto = mass;
-  uint32_t counted = count;
+  // sums of integers: their order does not matter
+  for (int i0 = b; i0 < all; i0 += kCutAhead * kCutThreads) {
 #pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const double m = __shfl_up(upto, off);
-    const uint32_t n = (uint32_t)__shfl_up((int)counted, off);
-    if (lane >= off) upto += m, counted += n;
+    for (int i = 0; i < kCutAhead; ++i) {
+      const int at = i0 + i * kCutThreads;
+      if (at < all && bin[i]) {
+        const int c = at / kBuckets, to = min(at % kBuckets + s_shift[c], kBuckets - 1);
+        atomicAdd(&s_count[to], (uint32_t)(bin[i] >> kBinCount));
+        atomicAdd(reinterpret_cast<unsigned long long*>(&s_mass[to]),
+                  (uint64_t)__builtin_rint(sample_bin_mass(bin[i]) * s_factor[c]));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kCutAhead; ++i) bin[i] = bins[min(i0 + (kCutAhead + i) * kCutThreads, all - 1)];
   }
-  if (lane == kWave - 1) s_waves[wave] = upto, s_counts[wave] = counted;
   __syncthreads();
-  for (int w = 0; w < wave; ++w) upto += s_waves[w], counted += s_counts[w];
-  if (b == kBuckets - 1) upto = total, counted = a.N;
-  s_mass[b] = upto, s_count[b] = counted;
+  if (b >= kBuckets) return;
+  const int wave = b / kWave;
+  // sums over the buckets up to this one
+  uint64_t units = sample_wave_scan(s_mass[b]), counted = sample_wave_scan(s_count[b]);
+  if (lane == kWave - 1) s_waves[0][wave] = units, s_waves[1][wave] = counted;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) units += s_waves[0][w], counted += s_waves[1][w];
+  if (b == kBuckets - 1) counted = a.N;
+  uint64_t total_units = 0;
+  for (int w = 0; w < kBuckets / kWave; ++w) total_units += s_waves[0][w];
+  s_mass[b] = units, s_count[b] = (uint32_t)counted;
+  auto mass_of = [&](uint64_t u) { return __builtin_ldexp((double)u, -kCutScale); };
+  const double upto = mass_of(units), total = mass_of(total_units);
   __syncthreads();
   // the first bucket at which each limit may lie; the last one if none does
-  if (p.k && counted >= (uint32_t)p.k) atomicMin(&s_first[0], b);
+  if (p.k && counted >= (uint64_t)p.k) atomicMin(&s_first[0], b);
   __syncthreads();
   const int k_at = p.k ? s_first[0] : kBuckets;
   int lo = k_at, hi = k_at;
   bool min_p_alone = false;
-  if (few) {
+  if (sample_few(p)) {
     lo = 0;
   } else {
     if (p.top_p < 1.0f) {
-      // Sums are exact to 2^-40: a border that near leaves both buckets open.  The weights that top_k
-      // keeps end somewhere in its bucket.
-      const double least = p.k ? (k_at ? s_mass[k_at - 1] : 0.0) : total, most = p.k ? s_mass[k_at] : total;
-      if (upto * (1.0 + 0x1p-40) >= p.top_p * least) atomicMin(&s_first[1], b);
-      if (upto >= p.top_p * most * (1.0 + 0x1p-40)) atomicMin(&s_first[2], b);
+      // Sums are exact to 2^-24 (2^-37 times 8192 for each of 128 chunks at worst, 2^-28 where errors
+      // cancel), beside a total of at least 1: a border that near leaves both buckets open.  The weights
+      // that top_k keeps end somewhere in its bucket.
+      const double least = p.k ? (k_at ? mass_of(s_mass[k_at - 1]) : 0.0) : total, most = p.k ? mass_of(s_mass[k_at]) : total;
+      if (upto + 0x1p-16 >= p.top_p * least) atomicMin(&s_first[1], b);
+      if (upto >= p.top_p * most + 0x1p-16) atomicMin(&s_first[2], b);
       __syncthreads();
       lo = min(lo, s_first[1]);
       hi = p.k ? k_at : s_first[2];      // (with top_k, its sum is needed exactly)
@@ -482,9 +624,11 @@ __global__ __launch_bounds__(kScanThreads) void sample_collect_kernel(SampleArgs
   const T* const row = static_cast<const T*>(a.logits) + r * a.stride;
   float v[kLane];
   sample_load_chunk(row, chunk, a.N, v);
-  const SampleTop top = sample_row_top(a, r);
-  if (!(top.top > -__builtin_inff())) return;
+  const SampleTops tops = sample_tops(a, r);
+  const uint64_t bin = tid < kBuckets ? a.bins[((size_t)r * a.chunks + chunk) * kBuckets + tid] : 0;
   const SampleCut cut = a.cut[r];
+  const SampleTop top = sample_row_top(tops);
+  if (!(top.top > -__builtin_inff())) return;
   if (tid == 0) s_count = 0;
   __syncthreads();
   const size_t at = (size_t)r * a.chunks + chunk;
@@ -506,7 +650,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_collect_kernel(SampleArgs
   double sum = 0.0;
   if (!sample_few(p) && tid < kBuckets && chunk_top > -__builtin_inff() &&
       tid + top_bucket - sample_bucket(chunk_top, scale) < cut.lo)
-    sum = __builtin_ldexp((double)a.bins[at * kBuckets + tid], -kChunkScale);
+    sum = sample_bin_mass(bin);
 #pragma unroll
   for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
   if (lane == 0) s_sum[wave] = sum;
@@ -526,10 +670,25 @@ __global__ __launch_bounds__(kScanThreads) void sample_collect_kernel(SampleArgs
 template <class T>
 __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs a) {
   __shared__ SampleShared sh;
-  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int r = blockIdx.x, tid = threadIdx.x;
   const T* const row = static_cast<const T*>(a.logits) + r * a.stride;
+  const size_t at0 = (size_t)r * a.chunks;
+  // What the launches before left, all at once: what is read one after the other costs a
+  // microsecond or two each.  `threads` threads a chunk for its listed tokens.
+  const SampleTops tops = sample_tops(a, r);
+  const int mine = min(tid, a.chunks - 1);
+  const int threads = a.list_threads;
+  const int list_chunk = tid / threads, list_at = tid & (threads - 1);
+  const float mine_top = a.top[at0 + mine];
+  const double mine_mass = a.mass[at0 + mine];
+  uint32_t mine_listed = a.listed[at0 + mine];
+  uint64_t mine_kept = a.kept[at0 + mine];
+  const SampleCut cut = a.cut[r];
+  const float u = a.uniforms ? a.uniforms[r] : 0.0f;
+  const uint2* const list = a.list + (at0 + min(list_chunk, a.chunks - 1)) * kListed + list_at;
+  const uint2 first_entry = *list;
   const SampleRow p = sample_row(a, r);
-  const SampleTop first = sample_row_top(a, r);
+  const SampleTop first = sample_row_top(tops);
   const float top = first.top;
   if (p.greedy || !(top > -__builtin_inff())) {
     if (tid == 0) {
@@ -539,88 +698,125 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
     return;
   }
   auto weight = [&](float v) { return (uint64_t)__builtin_rint(sample_weight(v, top, p.inv_t, a.log2_scale)); };
-  const size_t at0 = (size_t)r * a.chunks;
+  auto weight_of = [&](uint64_t c) { return weight(sample_logit(c)); };
   uint64_t last = ~0ull;      // the last C that top_k and top_p keep
   int sure = kBuckets;        // buckets in front of it are kept whole
   const double least = p.min_p > 0.0f ? log((double)p.min_p) : -__builtin_inf();
   const float scale = sample_bucket_scale(p.inv_t);
   const int top_bucket = sample_bucket(top, scale);
+  uint64_t before;
   if (!sample_limited(p)) {
-    if (tid < a.chunks) {
-      const float chunk_top = a.top[at0 + tid];
-      sh.chunk[tid] = chunk_top > -__builtin_inff()
-                          ? (uint64_t)__builtin_rint(a.mass[at0 + tid] * sample_weight(chunk_top, top, p.inv_t, a.log2_scale))
+    if (tid < a.chunks)
+      sh.chunk[tid] = mine_top > -__builtin_inff()
+                          ? (uint64_t)__builtin_rint(mine_mass * sample_weight(mine_top, top, p.inv_t, a.log2_scale))
                           : 0;
-    }
     __syncthreads();
   } else {
-    const SampleCut cut = a.cut[r];
-    uint64_t kept = 0;
-    int listed = 0;
-    if (tid < a.chunks) {
-      listed = (int)a.listed[at0 + tid];
-      kept = sample_few(p) ? 0 : a.kept[at0 + tid];
-      sh.listed[tid] = min(listed, kListed);
-      sh.chunk[tid] = kept;
-    }
-    const bool overflow = __syncthreads_or(listed > kListed);
-    // tokens whose order decides: those listed, or all of the row behind `sure` whole buckets
+    if (tid >= a.chunks || sample_few(p)) mine_kept = 0;
+    if (tid >= a.chunks) mine_listed = 0;
+    // (lists that a thread cannot hold its part of are left, and the row's logits are read instead)
+    const bool overflow = __syncthreads_or(mine_listed > (uint32_t)min(kListed, threads * kHeld));
     sure = overflow ? 0 : cut.lo;
-    if (overflow && tid < a.chunks) sh.chunk[tid] = 0, kept = 0;
-    uint64_t before;
-    const uint64_t base = sample_scan(kept, before, sh.waves);      // (and a barrier)
-    auto visit = [&](auto&& f) {
-      if (overflow) {
-        for (int i = tid; i < a.N; i += kSampleThreads) f(sample_load(row + i), i);
-      } else {
-        for (int c = wave; c < a.chunks; c += kSampleWaves)
-          for (int j = lane; j < (int)sh.listed[c]; j += kWave) {
-            const uint2 e = a.list[(at0 + c) * kListed + j];
-            f(__uint_as_float(e.x), (int)e.y);
-          }
-      }
-    };
-    bool none = false;      // no listed token is kept
+    if (overflow) mine_kept = 0;
+    if (tid < a.chunks) sh.chunk[tid] = mine_kept, sh.listed[tid] = mine_listed;
+    const uint64_t base = sample_scan(mine_kept, before, sh.waves);      // (and a barrier)
     const bool others = overflow || !cut.min_p_alone;
-    if (p.k && others) {
-      const int64_t k = p.k - (overflow ? 0 : cut.before);
-      uint64_t count = 0;
-      visit([&](float, int) { ++count; });
-      // (fewer are listed where top_p ends in front of the k-th)
-      if ((int64_t)sample_scan(count, before, sh.waves) >= k)
-        last = sample_select([&](auto&& f) { visit([&](float v, int i) { f(sample_order(v, i), 1); }); }, (uint64_t)k, sh);
+    const uint64_t all_listed = sample_scan(mine_listed, before, sh.waves);
+    if (tid < a.chunks) sh.place[tid] = (uint32_t)before;
+    const int count = list_chunk < a.chunks ? (int)sh.listed[list_chunk] : 0;
+    uint64_t c[kHeld];
+    auto order = [&](uint2 e) { return sample_order(__uint_as_float(e.x), (int)e.y); };
+    if (!overflow) {
+#pragma unroll
+      for (int e = 0; e < kHeld; ++e) {
+        c[e] = ~0ull;
+        if (list_at + e * threads < count) c[e] = order(e ? list[e * threads] : first_entry);
+      }
     }
-    if (p.top_p < 1.0f && others) {
-      const uint64_t limit = last;
-      uint64_t sum = 0;
-      visit([&](float v, int i) { sum += sample_order(v, i) <= limit ? weight(v) : 0; });
-      sum = sample_scan(sum, before, sh.waves);
-      const uint64_t all = p.k || overflow ? base + sum : cut.total;
-      const uint64_t target = (uint64_t)__builtin_ceil((double)p.top_p * (double)all);
-      if (target <= base && base > 0)
-        none = true;
-      else if (target - base < sum)
-        last = sample_select(
-            [&](auto&& f) {
-              visit([&](float v, int i) {
-                const uint64_t c = sample_order(v, i);
-                if (c <= limit) f(c, weight(v));
-              });
-            },
-            target > base ? target - base : 1, sh);
-    }
-    if (none) last = 0;
-    visit([&](float v, int i) {
-      if (sample_order(v, i) <= last && sample_log_weight(v, top, p.inv_t) >= least)
-        atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk[i / kChunk]), weight(v));
-    });
+    sh.bins[tid] = ~0ull;
     __syncthreads();
+    if (!overflow && all_listed <= kSorted) {
+      // in order: the limits are numbers of tokens
+      const int n = (int)all_listed;
+#pragma unroll
+      for (int e = 0; e < kHeld; ++e)
+        if (c[e] != ~0ull) sh.bins[sh.place[list_chunk] + list_at + e * threads] = c[e];
+      __syncthreads();
+      int sorted = kWave;
+      while (sorted < n) sorted <<= 1;
+      const uint64_t mine_c = sample_sort(sh.bins[tid], sorted, sh.bins + kSampleThreads);
+      const float v = sample_logit(mine_c);
+      bool kept = tid < n;
+      const uint64_t w = kept ? weight(v) : 0;
+      if (p.k && others) kept = kept && tid < p.k - cut.before;
+      if (p.top_p < 1.0f && others) {
+        const uint64_t sum = sample_scan(kept ? w : 0, before, sh.waves);
+        const uint64_t all = p.k ? base + sum : cut.total;
+        kept = kept && (base + before < (uint64_t)__builtin_ceil((double)p.top_p * (double)all) || base + before == 0);
+      }
+      const int keep = __syncthreads_count(kept);
+      if (tid == keep - 1) sh.found[0] = mine_c;
+      kept = kept && sample_log_weight(v, top, p.inv_t) >= least;
+      if (kept) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk[(uint32_t)mine_c / kChunk]), w);
+      __syncthreads();
+      last = keep ? sh.found[0] : 0;
+    } else {
+      uint64_t w[kHeld];
+      if (!overflow) {
+#pragma unroll
+        for (int e = 0; e < kHeld; ++e) w[e] = c[e] != ~0ull ? weight_of(c[e]) : 0;
+      }
+      // calls f(C, weight) for the thread's tokens
+      auto visit = [&](auto&& f) W4K_INLINE {
+        if (overflow) {
+          for (int i = tid; i < a.N; i += kSampleThreads) {
+            const float v = sample_load(row + i);
+            f(sample_order(v, i), weight(v));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < kHeld; ++e)
+            if (c[e] != ~0ull) f(c[e], w[e]);
+        }
+      };
+      bool none = false;      // no listed token is kept
+      if (p.k && others) {
+        const int64_t k = p.k - (overflow ? 0 : cut.before);
+        // (fewer are listed where top_p ends in front of the k-th)
+        if ((overflow ? (int64_t)a.N : (int64_t)all_listed) >= k)
+          last = sample_select([&](auto&& f) W4K_INLINE { visit([&](uint64_t c, uint64_t) W4K_INLINE { f(c, 1); }); },
+                               [](uint64_t) { return (uint64_t)1; }, (uint64_t)k, sh);
+      }
+      if (p.top_p < 1.0f && others) {
+        const uint64_t limit = last;
+        uint64_t sum = 0;
+        visit([&](uint64_t c, uint64_t w) W4K_INLINE { sum += c <= limit ? w : 0; });
+        sum = sample_scan(sum, before, sh.waves);
+        const uint64_t all = p.k || overflow ? base + sum : cut.total;
+        const uint64_t target = (uint64_t)__builtin_ceil((double)p.top_p * (double)all);
+        if (target <= base && base > 0)
+          none = true;
+        else if (target - base < sum)
+          last = sample_select(
+              [&](auto&& f) W4K_INLINE {
+                visit([&](uint64_t c, uint64_t w) W4K_INLINE {
+                  if (c <= limit) f(c, w);
+                });
+              },
+              weight_of, target > base ? target - base : 1, sh);
+      }
+      if (none) last = 0;
+      visit([&](uint64_t c, uint64_t w) W4K_INLINE {
+        if (c <= last && sample_log_weight(sample_logit(c), top, p.inv_t) >= least)
+          atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk[(uint32_t)c / kChunk]), w);
+      });
+      __syncthreads();
+    }
   }
   // the chunk: the first whose running sum exceeds u * total, that is its whole part
-  uint64_t before;
   uint64_t sum = tid < a.chunks ? sh.chunk[tid] : 0;
   const uint64_t total = sample_scan(sum, before, sh.waves);
-  const double at = (double)a.uniforms[r] * (double)total;
+  const double at = (double)u * (double)total;
   uint64_t target = at > 0.0 ? at < 9e18 ? (uint64_t)at : ~0ull : 0;
   target = target < total ? target : total - 1;
   if (tid == 0) sh.found[0] = 0, sh.found[1] = 0;
@@ -644,7 +840,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
                                               (sample_order(v[e], i0 + e) <= last &&
                                                sample_log_weight(v[e], top, p.inv_t) >= least)
                                         : true;
-    w[e] = kept ? sample_units(v[e], chunk_top, p.inv_t) : 0;
+    w[e] = kept ? sample_units(sample_weight(v[e], chunk_top, p.inv_t, kChunkScale)) : 0;
     sum += w[e];
   }
   const uint64_t in_chunk = sample_scan(sum, before, sh.waves);
@@ -677,7 +873,7 @@ __global__ __launch_bounds__(256) void sample_none_kernel(SampleArgs a) {
 
 int sample_chunks(int N) { return (N + kChunk - 1) / kChunk; }
 
-// Rows that go through the launches together: a chunk takes 11.5 KB of workspace.
+// Rows that go through the launches together: a chunk takes 10.3 KB of workspace.
 int sample_rows_at_once(int M, int N) {
   const int most = 16384 / sample_chunks(N);
   return M < most ? M : most;
@@ -686,6 +882,8 @@ int sample_rows_at_once(int M, int N) {
 // Places of `rows` rows' arrays in the workspace; the bytes they take.
 size_t sample_places(SampleArgs& a, uintptr_t ws, int rows) {
   a.chunks = sample_chunks(a.N);
+  a.list_threads = kSampleThreads;
+  while (a.list_threads * a.chunks > kSampleThreads) a.list_threads >>= 1;
   const size_t n = (size_t)rows * a.chunks;
   size_t at = 0;
   auto take = [&](auto*& p, size_t count) {
@@ -694,10 +892,8 @@ size_t sample_places(SampleArgs& a, uintptr_t ws, int rows) {
   };
   take(a.list, n * kListed);
   take(a.bins, n * kBuckets);
-  take(a.counts, n * kBuckets);
   take(a.mass, n);
   take(a.kept, n);
-  take(a.total, n);
   take(a.cut, rows);
   take(a.top, n);
   take(a.top_at, n);
@@ -716,7 +912,7 @@ void sample_launch(SampleArgs a, void* ws, hipStream_t st) {
     const dim3 grid(a.chunks, a.M);
     hipLaunchKernelGGL(sample_scan_kernel<T>, grid, dim3(kScanThreads), 0, st, a);
     if (limits) {
-      hipLaunchKernelGGL(sample_cut_kernel, dim3(a.M), dim3(kBuckets), 0, st, a);
+      hipLaunchKernelGGL(sample_cut_kernel, dim3(a.M), dim3(kCutThreads), 0, st, a);
       hipLaunchKernelGGL(sample_collect_kernel<T>, grid, dim3(kScanThreads), 0, st, a);
     }
     hipLaunchKernelGGL(sample_draw_kernel<T>, dim3(a.M), dim3(kSampleThreads), 0, st, a);
