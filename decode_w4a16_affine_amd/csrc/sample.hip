@@ -7,13 +7,13 @@
 // only those buckets' tokens are looked at one by one.
 //
 // Launches.  scan: a workgroup reads a chunk of 8192 logits into registers; its largest
-// logit, and either the sum of its weights (rows without limits) or its histogram.  cut: a
-// workgroup a row adds the histograms and finds the buckets lo .. hi that the limits
-// lie in.  collect: reads the logits again and lists the tokens of these buckets.  draw: a
-// workgroup a row finds the last kept token among the listed ones, adds the kept weights
-// of each chunk, picks a chunk and looks up the token in it.  A call without limits skips cut
-// and collect.  A row whose lists overflow (thousands of tokens of a chunk in one bucket: ties)
-// is left to one workgroup, which finds the limits digit by digit from the logits themselves.
+// logit, and either the sum of its weights (rows without limits) or its histogram.
+// collect: adds the row's histograms, finds the buckets lo .. hi that the limits lie in, reads
+// the logits again and lists the tokens of these buckets.  draw: a workgroup a row finds the
+// last kept token among the listed ones, adds the kept weights of each chunk, picks a
+// chunk and looks up the token in it.  A call without limits skips collect.  A row whose
+// lists overflow (thousands of tokens of a chunk in one bucket: ties) is left to the
+// draw's workgroup, which finds the limits from the logits themselves.
 //
 // Weights exp((logit - largest) / temperature) are computed in fp64 and added as integers of
 // 2^-e (e = 62 - log2 N for a row: its sum stays below 2^63), or in a fixed order: sums do not
@@ -47,6 +47,7 @@ constexpr int kBuckets = 256;
 constexpr float kBucketsPerUnit = 12.0f;              // of (logit / temperature)
 constexpr int kListed = 1024;                         // tokens of a chunk that are listed at most
 constexpr int kSmallK = 512;                          // limits of so few tokens need no weights from the scan
+constexpr int kCutScale = 42;                         // sums of a row's buckets (2^20 weights below 2^63)
 constexpr int kChunkScale = 49;                       // a chunk's weights are multiples of 2^-49 (8192 of them below 2^63)
 // A bucket of a chunk: its tokens times 2^50, and their weights, multiples of 2^-36 (8192 below 2^50).  Its limits
 // are found with a margin for that, and what a weight is off by, 2^-37 of the largest, divides among the tokens'
@@ -71,7 +72,6 @@ struct SampleArgs {
   int chunks;
   int list_threads;    // of the draw, for each chunk's list: a power of two
   float* top;          // [M][chunks] largest logit of a chunk, NaN if it has one
-  uint32_t* top_at;    // [M][chunks] its first token, or the first NaN
   double* mass;        // [M][chunks] rows without limits: weights, of a chunk's largest logit
   uint64_t* kept;      // [M][chunks] others: weights of the buckets in front of lo, of a row's
   uint64_t* bins;      // [M][chunks][kBuckets] tokens and weights of a chunk's buckets, of its largest logit
@@ -100,7 +100,11 @@ __device__ __forceinline__ SampleRow sample_row(const SampleArgs& a, int r) {
   SampleRow p;
   const float t = a.temperature ? a.temperature[r] : 1.0f;
   p.greedy = !(t > 0.0f) || !a.uniforms;
-  p.inv_t = 1.0 / (double)fminf(t, 3.402823466e38f);
+  // (an estimate and two steps of Newton's: to 2^-51 of it, without a division's special cases)
+  const double td = (double)fminf(fmaxf(t, 0x1p-149f), 3.402823466e38f);
+  double inv = __builtin_amdgcn_rcp(td);
+  inv = __builtin_fma(__builtin_fma(-td, inv, 1.0), inv, inv);
+  p.inv_t = __builtin_fma(__builtin_fma(-td, inv, 1.0), inv, inv);
   p.k = a.top_k ? a.top_k[r] : 0;
   p.k = p.k > 0 && p.k < a.N ? p.k : 0;
   p.top_p = a.top_p ? a.top_p[r] : 1.0f;
@@ -235,6 +239,24 @@ __device__ __forceinline__ uint64_t sample_wave_scan(uint64_t v) {
   v += sample_from_lane<0x143, 0xC>(v);      // lane 31 to the upper half
   return v;
 }
+// A wave's sum, in a fixed order.
+__device__ __forceinline__ double sample_wave_sum(double v) {
+  auto from = [&](auto ctrl, auto rows) {
+    return __longlong_as_double((long long)sample_from_lane<decltype(ctrl)::value, decltype(rows)::value>(
+        (uint64_t)__double_as_longlong(v)));
+  };
+  using std::integral_constant;
+  integral_constant<int, 0xF> all;
+  v += from(integral_constant<int, 0x111>{}, all);
+  v += from(integral_constant<int, 0x112>{}, all);
+  v += from(integral_constant<int, 0x114>{}, all);
+  v += from(integral_constant<int, 0x118>{}, all);
+  v += from(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});
+  v += from(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  return __longlong_as_double((long long)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), kWave - 1) << 32 |
+                                          (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, kWave - 1)));
+}
 // Sums over the block's threads.  Values of threads before this one, and of all (returned).
 template <int WAVES>
 __device__ __forceinline__ uint64_t sample_scan(uint64_t v, uint64_t& before, uint64_t (&s_waves)[WAVES]) {
@@ -268,25 +290,61 @@ struct SampleShared {
   uint32_t listed[kChunks], place[kChunks];
 };
 
+// The number that lane i ^ J holds, without a way through LDS.
+template <int J>
+__device__ __forceinline__ uint32_t sample_across(uint32_t v) {
+  const int x = (int)v;
+  if constexpr (J == 1) return (uint32_t)__builtin_amdgcn_update_dpp(x, x, 0xB1, 0xF, 0xF, false);
+  if constexpr (J == 2) return (uint32_t)__builtin_amdgcn_update_dpp(x, x, 0x4E, 0xF, 0xF, false);
+  if constexpr (J == 4) {      // 7 - i of each eight, then 3 - i of each four
+    const int y = __builtin_amdgcn_update_dpp(x, x, 0x141, 0xF, 0xF, false);
+    return (uint32_t)__builtin_amdgcn_update_dpp(y, y, 0x1B, 0xF, 0xF, false);
+  }
+  if constexpr (J == 8) return (uint32_t)__builtin_amdgcn_update_dpp(x, x, 0x128, 0xF, 0xF, false);      // turned by 8 of 16
+  // a swap with its own copy leaves the lane's number in one and the other's in the other
+  if constexpr (J == 16) {
+    auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return (threadIdx.x & 16) ? s[0] : s[1];
+  }
+  if constexpr (J == 32) {
+    auto s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return (threadIdx.x & 32) ? s[0] : s[1];
+  }
+}
+template <int J>
+__device__ __forceinline__ uint64_t sample_exchange(uint64_t c, bool up) {
+  const uint64_t other = (uint64_t)sample_across<J>((uint32_t)(c >> 32)) << 32 | sample_across<J>((uint32_t)c);
+  return (other < c) == (up == ((threadIdx.x & J) == 0)) ? other : c;
+}
+template <int J>
+__device__ __forceinline__ uint64_t sample_merge(uint64_t c, bool up) {
+  c = sample_exchange<J>(c, up);
+  if constexpr (J > 1) c = sample_merge<J / 2>(c, up);
+  return c;
+}
 // Sorts the threads' numbers, the smallest to thread 0, by compare and exchange (bitonic);
 // n: a power of two of threads that have one, at least a wave's.
 __device__ __forceinline__ uint64_t sample_sort(uint64_t c, int n, uint64_t* s_swap) {
   const int i = threadIdx.x;
-  for (int k = 2; k <= n; k <<= 1) {
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      uint64_t other;
-      if (j >= kWave) {
-        __syncthreads();
-        s_swap[i] = c;
-        __syncthreads();
-        other = s_swap[i ^ j];
-      } else {
-        if (i >= n) continue;      // (whole waves)
-        other = __shfl_xor((unsigned long long)c, j);
-      }
-      const bool smaller = ((i & k) == 0) == ((i & j) == 0);
-      c = (other < c) == smaller ? other : c;
+  const bool in = __builtin_amdgcn_readfirstlane(i) < n;      // (whole waves)
+  if (in) {
+    c = sample_merge<1>(c, (i & 2) == 0);
+    c = sample_merge<2>(c, (i & 4) == 0);
+    c = sample_merge<4>(c, (i & 8) == 0);
+    c = sample_merge<8>(c, (i & 16) == 0);
+    c = sample_merge<16>(c, (i & 32) == 0);
+    c = sample_merge<32>(c, (i & 64) == 0);
+  }
+  for (int k = 2 * kWave; k <= n; k <<= 1) {
+    const bool up = (i & k) == 0;
+    for (int j = k >> 1; j >= kWave; j >>= 1) {
+      __syncthreads();
+      s_swap[i] = c;
+      __syncthreads();
+      const uint64_t other = s_swap[i ^ j];
+      c = (other < c) == (up == ((i & j) == 0)) ? other : c;
     }
+    if (in) c = sample_merge<32>(c, up);
   }
   return c;
 }
@@ -364,47 +422,36 @@ __device__ __forceinline__ uint64_t sample_select(Visit&& visit, Measure&& measu
   }
 }
 
-// A row's chunks: its largest logit and that one's token, or its first NaN's.
-struct SampleTop {
-  float top;
-  uint32_t at;
-};
-// Every wave goes through all chunks, two a lane; their loads come first (sample_tops), so that
-// others can be on their way beside them.
+// A row's largest logit (NaN if it has one) from its chunks': every wave goes through all,
+// two a lane; their loads come first, so that others can be on their way beside them.
 static_assert(kChunks <= 2 * kWave, "two chunks a lane");
 struct SampleTops {
   float top[2];
-  uint32_t at[2];
 };
 __device__ __forceinline__ SampleTops sample_tops(const SampleArgs& a, int r) {
   const int lane = threadIdx.x & (kWave - 1);
   SampleTops t;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const size_t c = (size_t)r * a.chunks + min(lane + i * kWave, a.chunks - 1);
-    t.top[i] = a.top[c];
-    t.at[i] = a.top_at[c];
-  }
+  for (int i = 0; i < 2; ++i) t.top[i] = a.top[(size_t)r * a.chunks + min(lane + i * kWave, a.chunks - 1)];
   return t;
 }
-__device__ __forceinline__ SampleTop sample_row_top(const SampleTops& t) {
-  float top = -__builtin_inff();
-  uint32_t at = ~0u, nan = ~0u;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (t.top[i] != t.top[i])
-      nan = min(nan, t.at[i]);
-    else if (t.top[i] > top || (t.top[i] == top && t.at[i] < at))
-      top = t.top[i], at = t.at[i];
-  }
-#pragma unroll
-  for (int off = kWave / 2; off > 0; off >>= 1) {
-    const float v = __shfl_xor(top, off);
-    const uint32_t i = (uint32_t)__shfl_xor((int)at, off);
-    nan = min(nan, (uint32_t)__shfl_xor((int)nan, off));
-    if (v > top || (v == top && i < at)) top = v, at = i;
-  }
-  return nan != ~0u ? SampleTop{__builtin_nanf(""), nan} : SampleTop{top, at};
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float sample_max_row(float v) {
+  return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, ROWS, 0xF, false)));
+}
+// The largest of a wave's numbers (fmaxf leaves NaN out).
+__device__ __forceinline__ float sample_wave_max(float v) {
+  v = sample_max_row<0x111, 0xF>(v);
+  v = sample_max_row<0x112, 0xF>(v);
+  v = sample_max_row<0x114, 0xF>(v);
+  v = sample_max_row<0x118, 0xF>(v);
+  v = sample_max_row<0x142, 0xA>(v);
+  v = sample_max_row<0x143, 0xC>(v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), kWave - 1));
+}
+__device__ __forceinline__ float sample_row_top(const SampleTops& t) {
+  if (__any(t.top[0] != t.top[0] || t.top[1] != t.top[1])) return __builtin_nanf("");
+  return sample_wave_max(fmaxf(t.top[0], t.top[1]));
 }
 
 // ---------------------------------------------------------------------------
@@ -414,7 +461,6 @@ template <class T>
 __global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs a) {
   __shared__ uint64_t s_bins[kBuckets];
   __shared__ float s_top[kScanWaves];
-  __shared__ uint32_t s_at[kScanWaves];
   __shared__ double s_sum[kScanWaves];
   const int chunk = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const T* const row = static_cast<const T*>(a.logits) + r * a.stride;
@@ -423,28 +469,19 @@ __global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs
   const SampleRow p = sample_row(a, r);
   if (tid < kBuckets) s_bins[tid] = 0;
   const size_t at = (size_t)r * a.chunks + chunk;
-  // the largest logit (fmaxf leaves NaN out), and the first token that has it or is NaN
-  float top = v[0];
+  // the largest logit (fmaxf leaves NaN out)
+  float top = -__builtin_inff();
   bool nan = false;
 #pragma unroll
   for (int x = 0; x < kLane; ++x) {
     top = fmaxf(top, v[x]);
     nan |= v[x] != v[x];
   }
-  top = top == top ? top : -__builtin_inff();
-#pragma unroll
-  for (int off = kWave / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+  top = sample_wave_max(top);
   if (lane == 0) s_top[wave] = top;
   nan = __syncthreads_or(nan);
 #pragma unroll
   for (int w = 0; w < kScanWaves; ++w) top = fmaxf(top, s_top[w]);
-  uint32_t first = ~0u;
-#pragma unroll
-  for (int x = kLane - 1; x >= 0; --x)      // (a lane's tokens grow with x)
-    if (nan ? v[x] != v[x] : v[x] == top) first = sample_token<T>(chunk, x);
-#pragma unroll
-  for (int off = kWave / 2; off > 0; off >>= 1) first = min(first, (uint32_t)__shfl_xor((int)first, off));
-  if (lane == 0) s_at[wave] = first;
   double sum = 0.0;
   if (!p.greedy && !nan && top > -__builtin_inff()) {
     const double inv_t = p.inv_t * kLog2E;
@@ -465,8 +502,7 @@ __global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs
     };
     if (!sample_limited(p)) {
       weights(0, [&](float, double w) W4K_INLINE { sum += w; });
-#pragma unroll
-      for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+      sum = sample_wave_sum(sum);
     } else if (sample_few(p)) {
 #pragma unroll
       for (int x = 0; x < kLane; ++x) {      // (the upper half of a bucket)
@@ -492,10 +528,7 @@ __global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs
   if (lane == 0) s_sum[wave] = sum;
   __syncthreads();
   if (tid == 0) {
-#pragma unroll
-    for (int w = 0; w < kScanWaves; ++w) first = min(first, s_at[w]);
     a.top[at] = nan ? __builtin_nanf("") : top;
-    a.top_at[at] = first;
 #pragma unroll
     for (int w = 1; w < kScanWaves; ++w) sum += s_sum[w];
     a.mass[at] = sum;
@@ -504,163 +537,174 @@ __global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs
 }
 
 // ---------------------------------------------------------------------------
-// cut: a row's buckets from its chunks'
+// collect
 // ---------------------------------------------------------------------------
-constexpr int kCutThreads = 1024;
-constexpr int kCutScale = 42;      // (2^20 weights below 2^63)
-constexpr int kCutAhead = 8;       // buckets a thread has on their way
+constexpr int kAtOnce = 16;        // chunks whose buckets are added at once
+constexpr int kSlices = kScanThreads / kBuckets;
+constexpr int kAhead = kAtOnce / kSlices;      // of which a thread has this many
 __device__ __forceinline__ double sample_bin_mass(uint64_t bin) {
-  return (double)(bin & ((1ull << kBinCount) - 1)) * (1.0 / (1ull << kBinScale));
+  return __longlong_as_double((long long)((bin & ((1ull << kBinCount) - 1)) | 0x433ull << 52)) - 0x1p52;
 }
 
-__global__ __launch_bounds__(kCutThreads) void sample_cut_kernel(SampleArgs a) {
+// Every workgroup of a row finds the buckets lo .. hi by itself (a launch for it alone took
+// 7.6 us for one row, this one with it 2 us more than without).
+template <class T>
+__global__ __launch_bounds__(kScanThreads) void sample_collect_kernel(SampleArgs a) {
+  __shared__ uint64_t s_bins[kAtOnce][kBuckets];
   __shared__ double s_factor[kChunks];
   __shared__ int s_shift[kChunks];
-  __shared__ uint64_t s_mass[kBuckets];
+  __shared__ double s_mass[kBuckets];
   __shared__ uint32_t s_count[kBuckets];
   __shared__ uint64_t s_waves[2][kBuckets / kWave];
   __shared__ int s_first[4];
-  const int r = blockIdx.x, b = threadIdx.x, lane = b & (kWave - 1);
+  __shared__ SampleCut s_cut;
+  __shared__ uint32_t s_listed;
+  __shared__ double s_sum[kScanWaves];
+  const int chunk = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int b = tid % kBuckets, slice = tid / kBuckets;
+  const T* const row = static_cast<const T*>(a.logits) + r * a.stride;
+  const size_t at = (size_t)r * a.chunks + chunk;
+  // all loads of the launch at once
   const SampleTops tops = sample_tops(a, r);
-  const uint64_t* const bins = a.bins + (size_t)r * a.chunks * kBuckets;
-  const int all = a.chunks * kBuckets;
-  uint64_t bin[kCutAhead];
+  const uint64_t* const bins = a.bins + (size_t)r * a.chunks * kBuckets + b;
+  uint64_t bin[kAhead];
+  auto load_bins = [&](int c0) W4K_INLINE {
 #pragma unroll
-  for (int i = 0; i < kCutAhead; ++i) bin[i] = bins[min(b + i * kCutThreads, all - 1)];
+    for (int i = 0; i < kAhead; ++i) bin[i] = bins[min(c0 + i * kSlices + slice, a.chunks - 1) * kBuckets];
+  };
+  load_bins(0);
+  const uint64_t own_bin = bins[chunk * kBuckets];
+  const float own_top = a.top[at];
+  float v[kLane];
+  sample_load_chunk(row, chunk, a.N, v);
   const SampleRow p = sample_row(a, r);
-  const SampleTop row = sample_row_top(tops);
-  if (p.greedy || !sample_limited(p) || !(row.top > -__builtin_inff())) return;
+  if (p.greedy || !sample_limited(p)) return;
+  const float top = sample_row_top(tops);
+  if (!(top > -__builtin_inff())) return;
   const float scale = sample_bucket_scale(p.inv_t);
-  const int top_bucket = sample_bucket(row.top, scale);
-  if (b < kWave) {
+  const int top_bucket = sample_bucket(top, scale);
+  if (tid < kWave) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int c = lane + i * kWave;
       if (c >= a.chunks) break;
       // (a chunk of -infinity alone has no weights; its tokens lie in the last bucket)
-      const float top = tops.top[i];
-      s_factor[c] = top > -__builtin_inff() ? sample_weight(top, row.top, p.inv_t, kCutScale) : 0.0;
-      s_shift[c] = top > -__builtin_inff() ? min(top_bucket - sample_bucket(top, scale), kBuckets) : kBuckets;
+      const float t = tops.top[i];
+      s_factor[c] = t > -__builtin_inff() ? sample_weight(t, top, p.inv_t, -kBinScale) : 0.0;
+      s_shift[c] = t > -__builtin_inff() ? min(top_bucket - sample_bucket(t, scale), kBuckets) : kBuckets;
     }
   }
-  if (b < kBuckets) s_mass[b] = 0, s_count[b] = 0;
-  if (b < 4) s_first[b] = kBuckets - 1;
-  __syncthreads();
-  // sums of integers: their order does not matter
-  for (int i0 = b; i0 < all; i0 += kCutAhead * kCutThreads) {
+  if (tid < 4) s_first[tid] = kBuckets - 1;
+  if (tid == 0) s_listed = 0;
+  // a row's bucket: those of its chunks, shifted by their largest logits; what lies behind is the last one's
+  double mass = 0.0, behind = 0.0;
+  uint32_t count = 0;
+  for (int c0 = 0; c0 < a.chunks; c0 += kAtOnce) {
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kCutAhead; ++i) {
-      const int at = i0 + i * kCutThreads;
-      if (at < all && bin[i]) {
-        const int c = at / kBuckets, to = min(at % kBuckets + s_shift[c], kBuckets - 1);
-        atomicAdd(&s_count[to], (uint32_t)(bin[i] >> kBinCount));
-        atomicAdd(reinterpret_cast<unsigned long long*>(&s_mass[to]),
-                  (uint64_t)__builtin_rint(sample_bin_mass(bin[i]) * s_factor[c]));
+    for (int i = 0; i < kAhead; ++i) s_bins[i * kSlices + slice][b] = bin[i];
+    load_bins(c0 + kAtOnce);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int in = i * kSlices + slice, c = c0 + in;
+      if (c >= a.chunks) break;
+      const int shift = s_shift[c], from = b - shift;
+      const double factor = s_factor[c];
+      if (from >= 0 && b < kBuckets - 1) {
+        const uint64_t x = s_bins[in][from];
+        mass = __builtin_fma(sample_bin_mass(x), factor, mass);
+        count += (uint32_t)(x >> kBinCount);
       }
+      if (b + shift >= kBuckets - 1) behind = __builtin_fma(sample_bin_mass(s_bins[in][b]), factor, behind);
     }
-#pragma unroll
-    for (int i = 0; i < kCutAhead; ++i) bin[i] = bins[min(i0 + (kCutAhead + i) * kCutThreads, all - 1)];
+  }
+  // (s_bins is free: both slices' sums)
+  __syncthreads();
+  double* const s_part = reinterpret_cast<double*>(s_bins);
+  if (slice == 1) s_part[b] = mass, s_part[kBuckets + b] = behind, s_count[b] = count;
+  static_assert(kSlices == 2, "the sums of two");
+  __syncthreads();
+  uint64_t units = 0, counted = 0, units_behind = 0;
+  if (slice == 0) {
+    auto in_units = [&](double m) { return (uint64_t)__builtin_rint(__builtin_ldexp(m, kCutScale)); };
+    units = sample_wave_scan(in_units(mass + s_part[b]));
+    units_behind = sample_wave_scan(in_units(behind + s_part[kBuckets + b]));
+    counted = sample_wave_scan(count + s_count[b]);
+    if (lane == kWave - 1) s_waves[0][wave] = units, s_waves[1][wave] = counted, s_part[2 * kBuckets + wave] = units_behind;
   }
   __syncthreads();
-  if (b >= kBuckets) return;
-  const int wave = b / kWave;
   // sums over the buckets up to this one
-  uint64_t units = sample_wave_scan(s_mass[b]), counted = sample_wave_scan(s_count[b]);
-  if (lane == kWave - 1) s_waves[0][wave] = units, s_waves[1][wave] = counted;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) units += s_waves[0][w], counted += s_waves[1][w];
-  if (b == kBuckets - 1) counted = a.N;
   uint64_t total_units = 0;
-  for (int w = 0; w < kBuckets / kWave; ++w) total_units += s_waves[0][w];
-  s_mass[b] = units, s_count[b] = (uint32_t)counted;
+  for (int w = 0; w < kBuckets / kWave; ++w) total_units += s_waves[0][w] + (uint64_t)s_part[2 * kBuckets + w];
+  for (int w = 0; w < min(wave, kBuckets / kWave); ++w) units += s_waves[0][w], counted += s_waves[1][w];
+  if (b == kBuckets - 1) units = total_units, counted = a.N;
   auto mass_of = [&](uint64_t u) { return __builtin_ldexp((double)u, -kCutScale); };
   const double upto = mass_of(units), total = mass_of(total_units);
-  __syncthreads();
+  if (slice == 0) s_mass[b] = upto, s_count[b] = (uint32_t)counted;
   // the first bucket at which each limit may lie; the last one if none does
-  if (p.k && counted >= (uint64_t)p.k) atomicMin(&s_first[0], b);
+  if (slice == 0 && p.k && counted >= (uint64_t)p.k) atomicMin(&s_first[0], b);
   __syncthreads();
   const int k_at = p.k ? s_first[0] : kBuckets;
-  int lo = k_at, hi = k_at;
-  bool min_p_alone = false;
-  if (sample_few(p)) {
-    lo = 0;
-  } else {
-    if (p.top_p < 1.0f) {
-      // Sums are exact to 2^-24 (2^-37 times 8192 for each of 128 chunks at worst, 2^-28 where errors
-      // cancel), beside a total of at least 1: a border that near leaves both buckets open.  The weights
-      // that top_k keeps end somewhere in its bucket.
-      const double least = p.k ? (k_at ? mass_of(s_mass[k_at - 1]) : 0.0) : total, most = p.k ? mass_of(s_mass[k_at]) : total;
-      if (upto + 0x1p-16 >= p.top_p * least) atomicMin(&s_first[1], b);
-      if (upto >= p.top_p * most + 0x1p-16) atomicMin(&s_first[2], b);
-      __syncthreads();
-      lo = min(lo, s_first[1]);
-      hi = p.k ? k_at : s_first[2];      // (with top_k, its sum is needed exactly)
-    }
-    if (p.min_p > 0.0f) {
-      // the bucket of the least weight, by fp32 arithmetic on its edge: one to either side
-      const float edge = (float)((double)row.top + log((double)p.min_p) / p.inv_t);
-      const int at = sample_below(top_bucket, fminf(fmaxf(edge, -3e38f), row.top), scale);
-      min_p_alone = at + 1 < lo || (!p.k && p.top_p >= 1.0f);
-      if (min_p_alone) hi = at + 1;
-      lo = min(lo, at - 1);
-    }
+  if (slice == 0 && !sample_few(p) && p.top_p < 1.0f) {
+    // Sums are exact to 2^-24 (2^-37 times 8192 for each of 128 chunks at worst, 2^-28 where errors
+    // cancel), beside a total of at least 1: a border that near leaves both buckets open.  The weights
+    // that top_k keeps end somewhere in its bucket.
+    const double least = p.k ? (k_at ? s_mass[k_at - 1] : 0.0) : total, most = p.k ? s_mass[k_at] : total;
+    if (upto + 0x1p-16 >= p.top_p * least) atomicMin(&s_first[1], b);
+    if (upto >= p.top_p * most + 0x1p-16) atomicMin(&s_first[2], b);
   }
-  lo = max(lo, 0), hi = min(hi, kBuckets - 1);
-  if (b == 0)
-    a.cut[r] = SampleCut{lo, hi, lo ? (int)s_count[lo - 1] : 0, min_p_alone,
-                         (uint64_t)__builtin_rint(__builtin_ldexp(total, a.log2_scale))};
-}
-
-// ---------------------------------------------------------------------------
-// collect
-// ---------------------------------------------------------------------------
-template <class T>
-__global__ __launch_bounds__(kScanThreads) void sample_collect_kernel(SampleArgs a) {
-  __shared__ uint32_t s_count;
-  __shared__ double s_sum[kScanWaves];
-  const int chunk = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  const SampleRow p = sample_row(a, r);
-  if (p.greedy || !sample_limited(p)) return;
-  const T* const row = static_cast<const T*>(a.logits) + r * a.stride;
-  float v[kLane];
-  sample_load_chunk(row, chunk, a.N, v);
-  const SampleTops tops = sample_tops(a, r);
-  const uint64_t bin = tid < kBuckets ? a.bins[((size_t)r * a.chunks + chunk) * kBuckets + tid] : 0;
-  const SampleCut cut = a.cut[r];
-  const SampleTop top = sample_row_top(tops);
-  if (!(top.top > -__builtin_inff())) return;
-  if (tid == 0) s_count = 0;
   __syncthreads();
-  const size_t at = (size_t)r * a.chunks + chunk;
-  const float scale = sample_bucket_scale(p.inv_t);
-  const int top_bucket = sample_bucket(top.top, scale);
+  if (tid == 0) {
+    int lo = k_at, hi = k_at;
+    bool min_p_alone = false;
+    if (sample_few(p)) {
+      lo = 0;
+    } else {
+      if (p.top_p < 1.0f) {
+        lo = min(lo, s_first[1]);
+        hi = p.k ? k_at : s_first[2];      // (with top_k, its sum is needed exactly)
+      }
+      if (p.min_p > 0.0f) {
+        // the bucket of the least weight, by fp32 arithmetic on its edge: one to either side
+        const float edge = (float)((double)top + log((double)p.min_p) / p.inv_t);
+        const int edge_at = sample_below(top_bucket, fminf(fmaxf(edge, -3e38f), top), scale);
+        min_p_alone = edge_at + 1 < lo || (!p.k && p.top_p >= 1.0f);
+        if (min_p_alone) hi = edge_at + 1;
+        lo = min(lo, edge_at - 1);
+      }
+    }
+    lo = max(lo, 0), hi = min(hi, kBuckets - 1);
+    s_cut = SampleCut{lo, hi, lo ? (int)s_count[lo - 1] : 0, min_p_alone,
+                      (uint64_t)__builtin_rint(__builtin_ldexp(total, a.log2_scale))};
+    if (chunk == 0) a.cut[r] = s_cut;
+  }
+  __syncthreads();
+  const int lo = s_cut.lo, hi = s_cut.hi;
 #pragma unroll
   for (int x = 0; x < kLane; ++x) {
-    const int i = sample_token<T>(chunk, x), b = sample_below(top_bucket, v[x], scale);
-    const bool mine = b >= cut.lo && b <= cut.hi && i < a.N;
+    const int i = sample_token<T>(chunk, x), below = sample_below(top_bucket, v[x], scale);
+    const bool mine = below >= lo && below <= hi && i < a.N;
     const uint64_t all = __ballot(mine);
     if (!all) continue;
     uint32_t slot = 0;
-    if (lane == __builtin_ctzll(all)) slot = atomicAdd(&s_count, (uint32_t)__builtin_popcountll(all));
+    if (lane == __builtin_ctzll(all)) slot = atomicAdd(&s_listed, (uint32_t)__builtin_popcountll(all));
     slot = (uint32_t)__shfl((int)slot, __builtin_ctzll(all)) + __builtin_popcountll(all & ((1ull << lane) - 1));
     if (mine && slot < kListed) a.list[at * kListed + slot] = make_uint2(__float_as_uint(v[x]), (uint32_t)i);
   }
   // weights of the chunk's buckets in front of lo
-  const float chunk_top = a.top[at];
   double sum = 0.0;
-  if (!sample_few(p) && tid < kBuckets && chunk_top > -__builtin_inff() &&
-      tid + top_bucket - sample_bucket(chunk_top, scale) < cut.lo)
-    sum = sample_bin_mass(bin);
-#pragma unroll
-  for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+  if (!sample_few(p) && slice == 0 && own_top > -__builtin_inff() && b + top_bucket - sample_bucket(own_top, scale) < lo)
+    sum = sample_bin_mass(own_bin);
+  sum = sample_wave_sum(sum);
   if (lane == 0) s_sum[wave] = sum;
   __syncthreads();
   if (tid == 0) {
     for (int w = 1; w < kScanWaves; ++w) sum += s_sum[w];
-    a.kept[at] = chunk_top > -__builtin_inff()
-                     ? (uint64_t)__builtin_rint(sum * sample_weight(chunk_top, top.top, p.inv_t, a.log2_scale))
+    a.kept[at] = own_top > -__builtin_inff()
+                     ? (uint64_t)__builtin_rint(sum * sample_weight(own_top, top, p.inv_t, a.log2_scale - kBinScale))
                      : 0;
-    a.listed[at] = s_count;
+    a.listed[at] = s_listed;
   }
 }
 
@@ -688,11 +732,25 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
   const uint2* const list = a.list + (at0 + min(list_chunk, a.chunks - 1)) * kListed + list_at;
   const uint2 first_entry = *list;
   const SampleRow p = sample_row(a, r);
-  const SampleTop first = sample_row_top(tops);
-  const float top = first.top;
+  const float top = sample_row_top(tops);
   if (p.greedy || !(top > -__builtin_inff())) {
+    // the first NaN, or the first of the largest: of the first chunk that has one
+    auto is = [&](float v) { return top != top ? v != v : v == top; };
+    if (tid == 0) sh.few = ~0u;
+    __syncthreads();
+    if (tid < a.chunks && is(mine_top)) atomicMin(&sh.few, (uint32_t)tid);
+    __syncthreads();
+    const int chunk = (int)min(sh.few, (uint32_t)a.chunks - 1);
+    __syncthreads();
+    if (tid == 0) sh.few = ~0u;
+    __syncthreads();
+    uint32_t at = ~0u;
+    for (int i = kChunk * chunk + tid; i < min(kChunk * (chunk + 1), a.N); i += kSampleThreads)
+      if (is(sample_load(row + i))) at = min(at, (uint32_t)i);
+    if (at != ~0u) atomicMin(&sh.few, at);
+    __syncthreads();
     if (tid == 0) {
-      a.tokens[r] = top == -__builtin_inff() ? -1 : (int)first.at;
+      a.tokens[r] = top == -__builtin_inff() ? -1 : (int)sh.few;
       if (a.share) a.share[r] = top != top ? top : top == -__builtin_inff() ? 0.0f : 1.0f;
     }
     return;
@@ -896,7 +954,6 @@ size_t sample_places(SampleArgs& a, uintptr_t ws, int rows) {
   take(a.kept, n);
   take(a.cut, rows);
   take(a.top, n);
-  take(a.top_at, n);
   take(a.listed, n);
   return at;
 }
@@ -911,10 +968,7 @@ void sample_launch(SampleArgs a, void* ws, hipStream_t st) {
     sample_places(a, (uintptr_t)ws, at_once);
     const dim3 grid(a.chunks, a.M);
     hipLaunchKernelGGL(sample_scan_kernel<T>, grid, dim3(kScanThreads), 0, st, a);
-    if (limits) {
-      hipLaunchKernelGGL(sample_cut_kernel, dim3(a.M), dim3(kCutThreads), 0, st, a);
-      hipLaunchKernelGGL(sample_collect_kernel<T>, grid, dim3(kScanThreads), 0, st, a);
-    }
+    if (limits) hipLaunchKernelGGL(sample_collect_kernel<T>, grid, dim3(kScanThreads), 0, st, a);
     hipLaunchKernelGGL(sample_draw_kernel<T>, dim3(a.M), dim3(kSampleThreads), 0, st, a);
     // the next rows
     a.logits = static_cast<const T*>(a.logits) + a.M * a.stride;
