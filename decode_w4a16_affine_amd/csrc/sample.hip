@@ -91,7 +91,7 @@ struct SampleCut {
 // A row's parameters.
 struct SampleRow {
   bool greedy;         // the largest logit is the only one kept
-  double inv_t;        // 1 / temperature
+  double t, inv_t;     // temperature, and 1 / it
   int k;               // 0: no limit
   float top_p, min_p;  // >= 1, 0: no limit
 };
@@ -101,10 +101,10 @@ __device__ __forceinline__ SampleRow sample_row(const SampleArgs& a, int r) {
   const float t = a.temperature ? a.temperature[r] : 1.0f;
   p.greedy = !(t > 0.0f) || !a.uniforms;
   // (an estimate and two steps of Newton's: to 2^-51 of it, without a division's special cases)
-  const double td = (double)fminf(fmaxf(t, 0x1p-149f), 3.402823466e38f);
-  double inv = __builtin_amdgcn_rcp(td);
-  inv = __builtin_fma(__builtin_fma(-td, inv, 1.0), inv, inv);
-  p.inv_t = __builtin_fma(__builtin_fma(-td, inv, 1.0), inv, inv);
+  p.t = (double)fminf(fmaxf(t, 0x1p-149f), 3.402823466e38f);
+  double inv = __builtin_amdgcn_rcp(p.t);
+  inv = __builtin_fma(__builtin_fma(-p.t, inv, 1.0), inv, inv);
+  p.inv_t = __builtin_fma(__builtin_fma(-p.t, inv, 1.0), inv, inv);
   p.k = a.top_k ? a.top_k[r] : 0;
   p.k = p.k > 0 && p.k < a.N ? p.k : 0;
   p.top_p = a.top_p ? a.top_p[r] : 1.0f;
@@ -317,6 +317,13 @@ __device__ __forceinline__ uint64_t sample_exchange(uint64_t c, bool up) {
   return (other < c) == (up == ((threadIdx.x & J) == 0)) ? other : c;
 }
 template <int J>
+__device__ __forceinline__ uint64_t sample_wave_least(uint64_t c) {
+  const uint64_t other = (uint64_t)sample_across<J>((uint32_t)(c >> 32)) << 32 | sample_across<J>((uint32_t)c);
+  c = other < c ? other : c;
+  if constexpr (J > 1) c = sample_wave_least<J / 2>(c);
+  return c;
+}
+template <int J>
 __device__ __forceinline__ uint64_t sample_merge(uint64_t c, bool up) {
   c = sample_exchange<J>(c, up);
   if constexpr (J > 1) c = sample_merge<J / 2>(c, up);
@@ -361,12 +368,7 @@ __device__ __forceinline__ uint64_t sample_select(Visit&& visit, Measure&& measu
     lo = c < lo ? c : lo;
     hi = c > hi ? c : hi;
   });
-#pragma unroll
-  for (int off = kWave / 2; off > 0; off >>= 1) {
-    const uint64_t l = __shfl_xor((unsigned long long)lo, off), h = __shfl_xor((unsigned long long)hi, off);
-    lo = l < lo ? l : lo;
-    hi = h > hi ? h : hi;
-  }
+  lo = sample_wave_least<32>(lo), hi = ~sample_wave_least<32>(~hi);
   __syncthreads();
   if (lane == 0) sh.bins[wave] = lo, sh.bins[kSampleWaves + wave] = hi;
   __syncthreads();
@@ -546,43 +548,38 @@ __device__ __forceinline__ double sample_bin_mass(uint64_t bin) {
   return __longlong_as_double((long long)((bin & ((1ull << kBinCount) - 1)) | 0x433ull << 52)) - 0x1p52;
 }
 
-// Every workgroup of a row finds the buckets lo .. hi by itself (a launch for it alone took
-// 7.6 us for one row, this one with it 2 us more than without).
-template <class T>
-__global__ __launch_bounds__(kScanThreads) void sample_collect_kernel(SampleArgs a) {
-  __shared__ uint64_t s_bins[kAtOnce][kBuckets];
-  __shared__ double s_factor[kChunks];
-  __shared__ int s_shift[kChunks];
-  __shared__ double s_mass[kBuckets];
-  __shared__ uint32_t s_count[kBuckets];
-  __shared__ uint64_t s_waves[2][kBuckets / kWave];
-  __shared__ int s_first[4];
-  __shared__ SampleCut s_cut;
-  __shared__ uint32_t s_listed;
-  __shared__ double s_sum[kScanWaves];
-  const int chunk = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  const int b = tid % kBuckets, slice = tid / kBuckets;
-  const T* const row = static_cast<const T*>(a.logits) + r * a.stride;
-  const size_t at = (size_t)r * a.chunks + chunk;
-  // all loads of the launch at once
-  const SampleTops tops = sample_tops(a, r);
-  const uint64_t* const bins = a.bins + (size_t)r * a.chunks * kBuckets + b;
+// The buckets that a row's limits lie in, by one workgroup of kScanThreads threads.
+struct SampleCutShared {
+  uint64_t bins[kAtOnce][kBuckets];
+  double factor[kChunks];
+  int shift[kChunks];
+  double mass[kBuckets];
+  uint32_t count[kBuckets];
+  uint64_t waves[3][kBuckets / kWave];
+  int first[3];
+  SampleCut cut;
+};
+struct SampleCutLoads {
   uint64_t bin[kAhead];
-  auto load_bins = [&](int c0) W4K_INLINE {
+};
+__device__ __forceinline__ void sample_cut_load(const SampleArgs& a, int r, int c0, SampleCutLoads& l) {
+  const int b = threadIdx.x % kBuckets, slice = threadIdx.x / kBuckets;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) bin[i] = bins[min(c0 + i * kSlices + slice, a.chunks - 1) * kBuckets];
-  };
-  load_bins(0);
-  const uint64_t own_bin = bins[chunk * kBuckets];
-  const float own_top = a.top[at];
-  float v[kLane];
-  sample_load_chunk(row, chunk, a.N, v);
-  const SampleRow p = sample_row(a, r);
-  if (p.greedy || !sample_limited(p)) return;
-  const float top = sample_row_top(tops);
-  if (!(top > -__builtin_inff())) return;
+  for (int i = 0; i < kAhead; ++i)
+    l.bin[i] = a.bins[((size_t)r * a.chunks + min(c0 + i * kSlices + slice, a.chunks - 1)) * kBuckets + b];
+}
+__device__ __forceinline__ SampleCut sample_find_cut(const SampleArgs& a, int r, const SampleRow& p, const SampleTops& tops,
+                                                    float top, SampleCutLoads& l, SampleCutShared& sh) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int b = tid % kBuckets, slice = tid / kBuckets;
   const float scale = sample_bucket_scale(p.inv_t);
   const int top_bucket = sample_bucket(top, scale);
+  // the bucket of the least weight, by fp32 arithmetic on its edge
+  int edge_at = kBuckets;
+  if (p.min_p > 0.0f) {
+    const float edge = (float)((double)top + log((double)p.min_p) * p.t);
+    edge_at = sample_below(top_bucket, fminf(fmaxf(edge, -3e38f), top), scale);
+  }
   if (tid < kWave) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -590,111 +587,171 @@ __global__ __launch_bounds__(kScanThreads) void sample_collect_kernel(SampleArgs
       if (c >= a.chunks) break;
       // (a chunk of -infinity alone has no weights; its tokens lie in the last bucket)
       const float t = tops.top[i];
-      s_factor[c] = t > -__builtin_inff() ? sample_weight(t, top, p.inv_t, -kBinScale) : 0.0;
-      s_shift[c] = t > -__builtin_inff() ? min(top_bucket - sample_bucket(t, scale), kBuckets) : kBuckets;
+      sh.factor[c] = t > -__builtin_inff() ? sample_weight(t, top, p.inv_t, -kBinScale) : 0.0;
+      sh.shift[c] = t > -__builtin_inff() ? min(top_bucket - sample_bucket(t, scale), kBuckets) : kBuckets;
     }
   }
-  if (tid < 4) s_first[tid] = kBuckets - 1;
-  if (tid == 0) s_listed = 0;
+  if (tid < 3) sh.first[tid] = kBuckets - 1;
   // a row's bucket: those of its chunks, shifted by their largest logits; what lies behind is the last one's
   double mass = 0.0, behind = 0.0;
   uint32_t count = 0;
   for (int c0 = 0; c0 < a.chunks; c0 += kAtOnce) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) s_bins[i * kSlices + slice][b] = bin[i];
-    load_bins(c0 + kAtOnce);
+    for (int i = 0; i < kAhead; ++i) sh.bins[i * kSlices + slice][b] = l.bin[i];
+    if (c0 + kAtOnce < a.chunks) sample_cut_load(a, r, c0 + kAtOnce, l);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int in = i * kSlices + slice, c = c0 + in;
       if (c >= a.chunks) break;
-      const int shift = s_shift[c], from = b - shift;
-      const double factor = s_factor[c];
+      const int shift = sh.shift[c], from = b - shift;
+      const double factor = sh.factor[c];
       if (from >= 0 && b < kBuckets - 1) {
-        const uint64_t x = s_bins[in][from];
+        const uint64_t x = sh.bins[in][from];
         mass = __builtin_fma(sample_bin_mass(x), factor, mass);
         count += (uint32_t)(x >> kBinCount);
       }
-      if (b + shift >= kBuckets - 1) behind = __builtin_fma(sample_bin_mass(s_bins[in][b]), factor, behind);
+      if (b + shift >= kBuckets - 1) behind = __builtin_fma(sample_bin_mass(sh.bins[in][b]), factor, behind);
     }
   }
-  // (s_bins is free: both slices' sums)
+  // (bins is free: the second slice's sums)
   __syncthreads();
-  double* const s_part = reinterpret_cast<double*>(s_bins);
-  if (slice == 1) s_part[b] = mass, s_part[kBuckets + b] = behind, s_count[b] = count;
+  double* const s_part = reinterpret_cast<double*>(sh.bins);
+  if (slice == 1) s_part[b] = mass, s_part[kBuckets + b] = behind, sh.count[b] = count;
   static_assert(kSlices == 2, "the sums of two");
   __syncthreads();
-  uint64_t units = 0, counted = 0, units_behind = 0;
+  uint64_t units = 0, counted = 0;
   if (slice == 0) {
     auto in_units = [&](double m) { return (uint64_t)__builtin_rint(__builtin_ldexp(m, kCutScale)); };
     units = sample_wave_scan(in_units(mass + s_part[b]));
-    units_behind = sample_wave_scan(in_units(behind + s_part[kBuckets + b]));
-    counted = sample_wave_scan(count + s_count[b]);
-    if (lane == kWave - 1) s_waves[0][wave] = units, s_waves[1][wave] = counted, s_part[2 * kBuckets + wave] = units_behind;
+    const uint64_t units_behind = sample_wave_scan(in_units(behind + s_part[kBuckets + b]));
+    counted = sample_wave_scan(count + sh.count[b]);
+    if (lane == kWave - 1) sh.waves[0][wave] = units, sh.waves[1][wave] = counted, sh.waves[2][wave] = units_behind;
   }
   __syncthreads();
   // sums over the buckets up to this one
   uint64_t total_units = 0;
-  for (int w = 0; w < kBuckets / kWave; ++w) total_units += s_waves[0][w] + (uint64_t)s_part[2 * kBuckets + w];
-  for (int w = 0; w < min(wave, kBuckets / kWave); ++w) units += s_waves[0][w], counted += s_waves[1][w];
+#pragma unroll
+  for (int w = 0; w < kBuckets / kWave; ++w) {
+    total_units += sh.waves[0][w] + sh.waves[2][w];
+    if (w < wave) units += sh.waves[0][w], counted += sh.waves[1][w];
+  }
   if (b == kBuckets - 1) units = total_units, counted = a.N;
   auto mass_of = [&](uint64_t u) { return __builtin_ldexp((double)u, -kCutScale); };
   const double upto = mass_of(units), total = mass_of(total_units);
-  if (slice == 0) s_mass[b] = upto, s_count[b] = (uint32_t)counted;
+  if (slice == 0) sh.mass[b] = upto, sh.count[b] = (uint32_t)counted;
   // the first bucket at which each limit may lie; the last one if none does
-  if (slice == 0 && p.k && counted >= (uint64_t)p.k) atomicMin(&s_first[0], b);
+  auto first_of = [&](bool reached, int which) {
+    const uint64_t there = __ballot(reached);
+    if (there && lane == 0) atomicMin(&sh.first[which], wave * kWave + __builtin_ctzll(there));
+  };
+  if (slice == 0 && p.k) first_of(counted >= (uint64_t)p.k, 0);
   __syncthreads();
-  const int k_at = p.k ? s_first[0] : kBuckets;
-  if (slice == 0 && !sample_few(p) && p.top_p < 1.0f) {
+  const int k_at = p.k ? sh.first[0] : kBuckets;
+  const bool few = sample_few(p);
+  if (slice == 0 && !few && p.top_p < 1.0f) {
     // Sums are exact to 2^-24 (2^-37 times 8192 for each of 128 chunks at worst, 2^-28 where errors
     // cancel), beside a total of at least 1: a border that near leaves both buckets open.  The weights
     // that top_k keeps end somewhere in its bucket.
-    const double least = p.k ? (k_at ? s_mass[k_at - 1] : 0.0) : total, most = p.k ? s_mass[k_at] : total;
-    if (upto + 0x1p-16 >= p.top_p * least) atomicMin(&s_first[1], b);
-    if (upto >= p.top_p * most + 0x1p-16) atomicMin(&s_first[2], b);
+    const double least = p.k ? (k_at ? sh.mass[k_at - 1] : 0.0) : total, most = p.k ? sh.mass[k_at] : total;
+    first_of(upto + 0x1p-16 >= p.top_p * least, 1);
+    first_of(upto >= p.top_p * most + 0x1p-16, 2);
   }
   __syncthreads();
-  if (tid == 0) {
-    int lo = k_at, hi = k_at;
-    bool min_p_alone = false;
-    if (sample_few(p)) {
-      lo = 0;
-    } else {
-      if (p.top_p < 1.0f) {
-        lo = min(lo, s_first[1]);
-        hi = p.k ? k_at : s_first[2];      // (with top_k, its sum is needed exactly)
-      }
-      if (p.min_p > 0.0f) {
-        // the bucket of the least weight, by fp32 arithmetic on its edge: one to either side
-        const float edge = (float)((double)top + log((double)p.min_p) / p.inv_t);
-        const int edge_at = sample_below(top_bucket, fminf(fmaxf(edge, -3e38f), top), scale);
-        min_p_alone = edge_at + 1 < lo || (!p.k && p.top_p >= 1.0f);
-        if (min_p_alone) hi = edge_at + 1;
-        lo = min(lo, edge_at - 1);
-      }
+  int lo = k_at, hi = k_at;
+  bool min_p_alone = false;
+  if (few) {
+    lo = 0;
+  } else {
+    if (p.top_p < 1.0f) {
+      lo = min(lo, sh.first[1]);
+      hi = p.k ? k_at : sh.first[2];      // (with top_k, its sum is needed exactly)
     }
-    lo = max(lo, 0), hi = min(hi, kBuckets - 1);
-    s_cut = SampleCut{lo, hi, lo ? (int)s_count[lo - 1] : 0, min_p_alone,
-                      (uint64_t)__builtin_rint(__builtin_ldexp(total, a.log2_scale))};
-    if (chunk == 0) a.cut[r] = s_cut;
+    if (p.min_p > 0.0f) {      // one bucket to either side of the edge's
+      min_p_alone = edge_at + 1 < lo || (!p.k && p.top_p >= 1.0f);
+      if (min_p_alone) hi = edge_at + 1;
+      lo = min(lo, edge_at - 1);
+    }
+  }
+  lo = max(lo, 0), hi = min(hi, kBuckets - 1);
+  return SampleCut{lo, hi, lo ? (int)sh.count[lo - 1] : 0, min_p_alone,
+                   (uint64_t)__builtin_rint(__builtin_ldexp(total, a.log2_scale))};
+}
+
+__global__ __launch_bounds__(kScanThreads) void sample_cut_kernel(SampleArgs a) {
+  __shared__ SampleCutShared sh;
+  const int r = blockIdx.x;
+  const SampleTops tops = sample_tops(a, r);
+  SampleCutLoads l;
+  sample_cut_load(a, r, 0, l);
+  const SampleRow p = sample_row(a, r);
+  if (p.greedy || !sample_limited(p)) return;
+  const float top = sample_row_top(tops);
+  if (!(top > -__builtin_inff())) return;
+  const SampleCut cut = sample_find_cut(a, r, p, tops, top, l, sh);
+  if (threadIdx.x == 0) a.cut[r] = cut;
+}
+
+// CUT: every workgroup of a row finds its buckets by itself, instead of a launch before this one.
+template <class T, bool CUT>
+__global__ __launch_bounds__(kScanThreads) void sample_collect_kernel(SampleArgs a) {
+  struct Empty {};
+  __shared__ std::conditional_t<CUT, SampleCutShared, Empty> sh;
+  __shared__ uint32_t s_listed;
+  __shared__ double s_sum[kScanWaves];
+  const int chunk = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const T* const row = static_cast<const T*>(a.logits) + r * a.stride;
+  const size_t at = (size_t)r * a.chunks + chunk;
+  // all loads of the launch at once
+  const SampleTops tops = sample_tops(a, r);
+  SampleCutLoads l;
+  SampleCut cut;
+  if constexpr (CUT)
+    sample_cut_load(a, r, 0, l);
+  else
+    cut = a.cut[r];
+  const uint64_t own_bin = a.bins[at * kBuckets + tid % kBuckets];
+  const float own_top = a.top[at];
+  float v[kLane];
+  sample_load_chunk(row, chunk, a.N, v);
+  const SampleRow p = sample_row(a, r);
+  if (p.greedy || !sample_limited(p)) return;
+  const float top = sample_row_top(tops);
+  if (!(top > -__builtin_inff())) return;
+  if (tid == 0) s_listed = 0;
+  if constexpr (CUT) {
+    cut = sample_find_cut(a, r, p, tops, top, l, sh);
+    if (chunk == 0 && tid == 0) a.cut[r] = cut;
   }
   __syncthreads();
-  const int lo = s_cut.lo, hi = s_cut.hi;
+  const float scale = sample_bucket_scale(p.inv_t);
+  const int top_bucket = sample_bucket(top, scale);
+  // the lane's tokens in lo .. hi, and their places in the chunk's list
+  uint32_t mine = 0;
 #pragma unroll
   for (int x = 0; x < kLane; ++x) {
-    const int i = sample_token<T>(chunk, x), below = sample_below(top_bucket, v[x], scale);
-    const bool mine = below >= lo && below <= hi && i < a.N;
-    const uint64_t all = __ballot(mine);
-    if (!all) continue;
+    const int below = sample_below(top_bucket, v[x], scale);
+    mine |= (below >= cut.lo && below <= cut.hi && sample_token<T>(chunk, x) < a.N ? 1u : 0u) << x;
+  }
+  if (__any(mine)) {
+    const uint32_t count = __builtin_popcount(mine), upto = (uint32_t)sample_wave_scan(count);
     uint32_t slot = 0;
-    if (lane == __builtin_ctzll(all)) slot = atomicAdd(&s_listed, (uint32_t)__builtin_popcountll(all));
-    slot = (uint32_t)__shfl((int)slot, __builtin_ctzll(all)) + __builtin_popcountll(all & ((1ull << lane) - 1));
-    if (mine && slot < kListed) a.list[at * kListed + slot] = make_uint2(__float_as_uint(v[x]), (uint32_t)i);
+    if (lane == kWave - 1) slot = atomicAdd(&s_listed, upto);
+    slot = (uint32_t)__builtin_amdgcn_readlane((int)slot, kWave - 1) + upto - count;
+#pragma unroll
+    for (int x = 0; x < kLane; ++x) {
+      if (mine >> x & 1) {
+        if (slot < kListed)
+          a.list[at * kListed + slot] = make_uint2(__float_as_uint(v[x]), (uint32_t)sample_token<T>(chunk, x));
+        ++slot;
+      }
+    }
   }
   // weights of the chunk's buckets in front of lo
   double sum = 0.0;
-  if (!sample_few(p) && slice == 0 && own_top > -__builtin_inff() && b + top_bucket - sample_bucket(own_top, scale) < lo)
+  if (!sample_few(p) && tid < kBuckets && own_top > -__builtin_inff() &&
+      tid + top_bucket - sample_bucket(own_top, scale) < cut.lo)
     sum = sample_bin_mass(own_bin);
   sum = sample_wave_sum(sum);
   if (lane == 0) s_sum[wave] = sum;
@@ -968,7 +1025,13 @@ void sample_launch(SampleArgs a, void* ws, hipStream_t st) {
     sample_places(a, (uintptr_t)ws, at_once);
     const dim3 grid(a.chunks, a.M);
     hipLaunchKernelGGL(sample_scan_kernel<T>, grid, dim3(kScanThreads), 0, st, a);
-    if (limits) hipLaunchKernelGGL(sample_collect_kernel<T>, grid, dim3(kScanThreads), 0, st, a);
+    // (a workgroup for each CU at most: they find the buckets side by side)
+    if (limits && a.chunks * a.M <= 256) {
+      hipLaunchKernelGGL((sample_collect_kernel<T, true>), grid, dim3(kScanThreads), 0, st, a);
+    } else if (limits) {
+      hipLaunchKernelGGL(sample_cut_kernel, dim3(a.M), dim3(kScanThreads), 0, st, a);
+      hipLaunchKernelGGL((sample_collect_kernel<T, false>), grid, dim3(kScanThreads), 0, st, a);
+    }
     hipLaunchKernelGGL(sample_draw_kernel<T>, dim3(a.M), dim3(kSampleThreads), 0, st, a);
     // the next rows
     a.logits = static_cast<const T*>(a.logits) + a.M * a.stride;
