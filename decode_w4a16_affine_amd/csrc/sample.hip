@@ -139,24 +139,26 @@ __device__ __forceinline__ float sample_logit(uint64_t c) {
 __device__ __forceinline__ double sample_log_weight(float v, float top, double inv_t) {
   return v == top ? 0.0 : ((double)v - (double)top) * inv_t;
 }
-// 2^t times 2^scale for t <= 0, below 2^-1000 as there.  2^t = 2^n 2^f with |f| <= 1/2, the latter by its Taylor
-// series to f^11: off by 2^-47 of it (the rest of the series 2^-47, t's rounding 2^-47 where t is above -64).
+// 2^t times 2^scale for t <= 0, below 2^-1000 as there.  2^t = 2^n 2^f with |f| <= 1/2, the latter as 1 + f q(f), q the
+// polynomial through (2^f - 1) / f at the nine Chebyshev points: off by 2^-44.6 of it.  n appears in the low bits
+// of a sum with 1.5 * 2^52 and is added to the exponent's: conversions to and from fp64, rint and ldexp take four
+// times as long as a sum (256 tempered rows of 262144: @@ us with them instead of @@).
 __device__ __forceinline__ double sample_exp2(double t, int scale) {
   t = fmax(t, -1000.0);
-  const double n = __builtin_rint(t), f = t - n;
-  double y = 4.4455382718708101e-10;
-  y = __builtin_fma(y, f, 7.0549116208011209e-09);
-  y = __builtin_fma(y, f, 1.0178086009239696e-07);
-  y = __builtin_fma(y, f, 1.3215486790144305e-06);
-  y = __builtin_fma(y, f, 1.5252733804059838e-05);
-  y = __builtin_fma(y, f, 1.5403530393381606e-04);
-  y = __builtin_fma(y, f, 1.3333558146428441e-03);
-  y = __builtin_fma(y, f, 9.6181291076284769e-03);
-  y = __builtin_fma(y, f, 5.5504108664821576e-02);
-  y = __builtin_fma(y, f, 2.4022650695910069e-01);
-  y = __builtin_fma(y, f, 6.9314718055994529e-01);
+  const double shifted = t + 0x1.8p52, f = t - (shifted - 0x1.8p52);
+  double y = 1.0203121063391729e-07;
+  y = __builtin_fma(y, f, 1.3255224878668817e-06);
+  y = __builtin_fma(y, f, 1.525268684626772e-05);
+  y = __builtin_fma(y, f, 1.5403455852453838e-04);
+  y = __builtin_fma(y, f, 1.3333558179043112e-03);
+  y = __builtin_fma(y, f, 9.618129159402558e-03);
+  y = __builtin_fma(y, f, 5.5504108664760424e-02);
+  y = __builtin_fma(y, f, 2.402265069581299e-01);
+  y = __builtin_fma(y, f, 6.931471805599453e-01);
   y = __builtin_fma(y, f, 1.0);
-  return __builtin_ldexp(y, (int)n + scale);
+  const uint64_t u = (uint64_t)__double_as_longlong(y);
+  const uint32_t n = (uint32_t)__double_as_longlong(shifted) + (uint32_t)scale;
+  return __longlong_as_double((long long)((uint64_t)((uint32_t)(u >> 32) + (n << 20)) << 32 | (uint32_t)u));
 }
 constexpr double kLog2E = 1.4426950408889634074;
 // A weight times 2^log2_scale
@@ -480,32 +482,37 @@ __global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs
     nan |= v[x] != v[x];
   }
   top = sample_wave_max(top);
+  // f(logit, weight times 2^scale), four at a time: more would take too many registers
+  const double inv_t = p.inv_t * kLog2E;
+  auto weights = [&](int log2_scale, auto&& f) W4K_INLINE {
+    if (top == __builtin_inff()) {      // (only its equals have one)
+#pragma unroll
+      for (int x = 0; x < kLane; ++x) f(v[x], v[x] == top ? __builtin_ldexp(1.0, log2_scale) : 0.0);
+    } else {
+#pragma unroll
+      for (int x = 0; x < kLane; ++x) {
+        f(v[x], sample_exp2(((double)v[x] - (double)top) * inv_t, log2_scale));
+        if (x % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+  // Without limits a wave takes its own largest logit: it computes while others wait for their logits
+  // (all of them behind one barrier, the two times added up: 256 rows of 262144 71 us instead of @@).
+  const bool limited = sample_limited(p);
+  if (!p.greedy && !limited) {
+    double sum = 0.0;
+    if (top > -__builtin_inff()) weights(0, [&](float, double w) W4K_INLINE { sum += w; });
+    sum = sample_wave_sum(sum);
+    if (lane == 0) s_sum[wave] = sum;
+  }
   if (lane == 0) s_top[wave] = top;
   nan = __syncthreads_or(nan);
 #pragma unroll
   for (int w = 0; w < kScanWaves; ++w) top = fmaxf(top, s_top[w]);
-  double sum = 0.0;
-  if (!p.greedy && !nan && top > -__builtin_inff()) {
-    const double inv_t = p.inv_t * kLog2E;
+  if (!p.greedy && limited && !nan && top > -__builtin_inff()) {
     const float scale = sample_bucket_scale(p.inv_t);
     const int top_bucket = sample_bucket(top, scale);
-    // f(logit, weight times 2^scale), four at a time: more would take too many registers
-    auto weights = [&](int log2_scale, auto&& f) W4K_INLINE {
-      if (top == __builtin_inff()) {      // (only its equals have one)
-#pragma unroll
-        for (int x = 0; x < kLane; ++x) f(v[x], v[x] == top ? __builtin_ldexp(1.0, log2_scale) : 0.0);
-      } else {
-#pragma unroll
-        for (int x = 0; x < kLane; ++x) {
-          f(v[x], sample_exp2(((double)v[x] - (double)top) * inv_t, log2_scale));
-          if (x % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-    };
-    if (!sample_limited(p)) {
-      weights(0, [&](float, double w) W4K_INLINE { sum += w; });
-      sum = sample_wave_sum(sum);
-    } else if (sample_few(p)) {
+    if (sample_few(p)) {
 #pragma unroll
       for (int x = 0; x < kLane; ++x) {      // (the upper half of a bucket)
         const int b = sample_below(top_bucket, v[x], scale);
@@ -527,15 +534,16 @@ __global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs
       if (lane == kWave - 1 && rest) atomicAdd(reinterpret_cast<unsigned long long*>(&s_bins[kBuckets - 1]), rest);
     }
   }
-  if (lane == 0) s_sum[wave] = sum;
-  __syncthreads();
-  if (tid == 0) {
-    a.top[at] = nan ? __builtin_nanf("") : top;
-#pragma unroll
-    for (int w = 1; w < kScanWaves; ++w) sum += s_sum[w];
-    a.mass[at] = sum;
+  if (limited) {
+    __syncthreads();
+    if (tid < kBuckets) a.bins[at * kBuckets + tid] = s_bins[tid];
+  } else if (wave == 0 && !p.greedy) {
+    const float t = s_top[lane % kScanWaves];
+    double sum = lane < kScanWaves && t > -__builtin_inff() ? s_sum[lane] * sample_weight(t, top, p.inv_t, 0) : 0.0;
+    sum = sample_wave_sum(sum);
+    if (lane == 0) a.mass[at] = sum;
   }
-  if (sample_limited(p) && tid < kBuckets) a.bins[at * kBuckets + tid] = s_bins[tid];
+  if (tid == 0) a.top[at] = nan ? __builtin_nanf("") : top;
 }
 
 // ---------------------------------------------------------------------------
