@@ -117,6 +117,23 @@ __device__ __forceinline__ void kv_keep_own(const KvSharedArgs& a, KvRows& k) {
   k.begin = min(shared, k.end);
 }
 
+// The last request that begins at or before token t.
+__device__ __forceinline__ int kv_request_of(const KvAttnArgs& a, int t) {
+  int r = 0;
+  for (int count = a.requests; count > 1;) {
+    const int step = count >> 1;
+    if (a.token_start[r + step] <= t) r += step;
+    count -= step;
+  }
+  return r;
+}
+// The last of the first `shared` entries that token t attends, or -1.
+__device__ __forceinline__ int kv_last_shared(const KvAttnArgs& a, int t, int shared) {
+  const int owner = kv_request_of(a, t);
+  const long long pos = (long long)a.seq_lens[owner] - (a.token_start[owner + 1] - t);
+  return (int)max(min(pos, shared - 1LL), -1LL);
+}
+
 // The parts of the cache (a.part entries each) that rows of the tile form attend.
 struct KvParts {
   int first, count;

@@ -84,11 +84,12 @@ constexpr int kKvGridRequests = 32768;             // requests on the grid's y a
 // (a reload of a spilled register would wait for the loads in flight).
 constexpr int kv_split_occupancy(int D, int NC) { return D == 256 ? 2 : D == 128 || NC == 2 ? 3 : 4; }
 
-// Behind shared entries (Args = KvSharedArgs) a request's own ones alone are taken, and
-// every result is partial: another kernel joins it with those of the shared entries.
+// Behind shared entries (Args = KvSharedArgs) a request's own ones alone are taken; over them
+// (KvPrefixArgs) the rows of all requests are taken as if they were one's, each with its own
+// last entry.  Both give partial results, which another kernel joins.
 template <int D, int TYPE, int NC, class Args>
 __device__ __forceinline__ void kv_split_body(const Args& a, float* part_o, float* part_ml) {
-  constexpr bool SHARED = kv_behind_shared<Args>;
+  constexpr bool SHARED = kv_behind_shared<Args>, PREFIX = kv_over_shared<Args>;
   constexpr int W = kKvSplitWaves;
   constexpr int T = kKvSplitTile, E = T / 4, STEP = W * T;
   constexpr int NP = T / 16;                       // pieces of scores
@@ -109,8 +110,10 @@ __device__ __forceinline__ void kv_split_body(const Args& a, float* part_o, floa
   // Workgroups go to the eight XCDs in turn.  Heads run fastest, then row
   // groups, then a request's chunks, so that every request is spread over all
   // XCDs (with requests fastest, those of ragged batches were unevenly loaded)
-  const int r = blockIdx.z * kKvGridRequests + blockIdx.y;
+  const int r = blockIdx.z * kKvGridRequests + blockIdx.y;      // (PREFIX: 0)
   if (r >= a.requests) return;
+  int chunk_shift = a.chunk_shift;
+  if constexpr (PREFIX) chunk_shift = a.part_shift;
   int block = blockIdx.x;
   const int kh = block % a.c.heads;
   block /= a.c.heads;
@@ -128,18 +131,36 @@ __device__ __forceinline__ void kv_split_body(const Args& a, float* part_o, floa
     return (j0 + 16 * x) >> shift < a.width && page >= 0 && page < a.c.pages ? page : -1;
   };
   int page = 0, page_after = 0;
-  if (!SHARED && a.window == 0 && a.width > 0) page = pages(block << a.chunk_shift);
+  if (!SHARED && a.window == 0 && a.width > 0) page = pages(block << chunk_shift);
   const int i_first = kv_token_of(a, row0), i_last = kv_token_of(a, row0 + NC * 16 - 1);
-  KvRows rows = kv_rows_of(a, r, i_first, i_last);
+  KvRows rows;
+  int last = -1;      // PREFIX: the last entry that token `lane` attends (there are at most 64)
+  if constexpr (PREFIX) {
+    rows.first = a.token_start[0];
+    rows.n = a.token_start[a.requests] - rows.first;
+    rows.live = min(rows.n, a.tokens - rows.first);
+    if (rows.first < 0 || row0 >= rows.live * a.group) return;
+    const int shared = (int)min((long long)kv_shared_entries(a), (long long)a.width << shift);
+    if (lane < rows.live) last = kv_last_shared(a, rows.first + lane, shared);
+    int end = lane >= i_first && lane <= i_last ? last + 1 : 0;
+#pragma unroll
+    for (int off = kWave / 2; off > 0; off >>= 1) end = max(end, __shfl_xor(end, off));
+    rows.end = __builtin_amdgcn_readfirstlane(end);
+    rows.begin = rows.seq = 0;
+    if (rows.end == 0) return;
+  } else {
+    rows = kv_rows_of(a, r, i_first, i_last);
+    if (!kv_few_rows(a, rows.n)) return;
+  }
   const int live = rows.live * a.group;                    // rows of the request
-  if (!kv_few_rows(a, rows.n) || row0 >= live) return;
+  if (row0 >= live) return;
   if constexpr (SHARED) {
     kv_keep_own(a, rows);
     if (rows.begin >= rows.end) return;
   }
-  const int first = rows.begin >> a.chunk_shift;            // the group's first chunk
-  const int at_begin = (first + block) << a.chunk_shift;
-  const int at_end = (int)min((long long)at_begin + (1LL << a.chunk_shift), (long long)rows.end);
+  const int first = rows.begin >> chunk_shift;              // the group's first chunk
+  const int at_begin = (first + block) << chunk_shift;
+  const int at_end = (int)min((long long)at_begin + (1LL << chunk_shift), (long long)rows.end);
   if (block > 0 && at_begin >= at_end) return;
 
   // No load stands under a condition: entries without a page read page 0 instead
@@ -264,7 +285,12 @@ __device__ __forceinline__ void kv_split_body(const Args& a, float* part_o, floa
     const int i = kv_token_of(a, row), t = rows.first + i, h = kh * a.group + row - i * a.group;
     const bool ok = row0 + 16 * c + x < live && t >= 0 && t < a.tokens;
     out_at[c] = ok ? t * a.q_heads + h : -1;
-    lr.hi[c] = ok ? min(rows.seq - rows.n + i, rows.end - 1) : -1;
+    if constexpr (PREFIX) {
+      const int mine = __shfl(last, i);
+      lr.hi[c] = ok ? mine : -1;
+    } else {
+      lr.hi[c] = ok ? min(rows.seq - rows.n + i, rows.end - 1) : -1;
+    }
     lr.lo[c] = SHARED ? rows.begin : a.window > 0 ? rows.seq - rows.n + i - a.window + 1 : 0;
     const uint16_t* qp = a.q + (ok ? (size_t)t * a.q_stride + (size_t)h * D : 0) + 16 * g;
     if constexpr (Q_LDS) {      // the waves share the rows: each puts a quarter of the pieces (read after a barrier)
@@ -281,7 +307,13 @@ __device__ __forceinline__ void kv_split_body(const Args& a, float* part_o, floa
   }
   if constexpr (Q_LDS) __syncthreads();
   // positions that every row of the group attends need no mask
-  const int all_hi = min(rows.seq - rows.n + i_first, rows.end - 1);
+  int all_hi = min(rows.seq - rows.n + i_first, rows.end - 1);
+  if constexpr (PREFIX) {
+    all_hi = lane >= i_first && lane <= min(i_last, rows.live - 1) ? last : rows.end - 1;
+#pragma unroll
+    for (int off = kWave / 2; off > 0; off >>= 1) all_hi = min(all_hi, __shfl_xor(all_hi, off));
+    all_hi = __builtin_amdgcn_readfirstlane(all_hi);
+  }
   const int all_lo = SHARED         ? rows.begin
                      : a.window > 0 ? rows.seq - rows.n + min(i_last, rows.live - 1) - a.window + 1
                                     : 0;
@@ -295,7 +327,8 @@ __device__ __forceinline__ void kv_split_body(const Args& a, float* part_o, floa
 #pragma unroll
     for (int d = 0; d < DW; ++d) o[c][d] = kv_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  const bool single = !SHARED && first == max(rows.end - 1, rows.begin) >> a.chunk_shift;     // one chunk holds all
+  const bool single =      // one chunk holds all
+      !SHARED && !PREFIX && first == max(rows.end - 1, rows.begin) >> chunk_shift;
   if (j0 < at_end) {
     load_keys(j0, page);
     load_values(j0, page);
@@ -422,8 +455,8 @@ __device__ __forceinline__ void kv_split_body(const Args& a, float* part_o, floa
 #pragma unroll
       for (int d = 0; d < DW; ++d) kv_store4(out + 16 * d, o[c][d], inverse);
     } else {
-      const size_t at = SHARED ? (size_t)out_at[c] * (a.parts + a.chunks) + a.parts + block
-                               : kv_part_row(a, out_at[c], r, rows.first) * a.chunks + block;
+      const size_t at = SHARED || PREFIX ? (size_t)out_at[c] * (a.parts + a.chunks) + (SHARED ? a.parts : 0) + block
+                                         : kv_part_row(a, out_at[c], r, rows.first) * a.chunks + block;
 #pragma unroll
       for (int d = 0; d < DW; ++d) *reinterpret_cast<kv_f32x4*>(part_o + at * D + d0 + 16 * d) = o[c][d];
       if (g == 0) {

@@ -68,17 +68,6 @@ __device__ __forceinline__ int kv_tile_owner(const int32_t* token_start, int req
   return lo;
 }
 
-// The last request that begins at or before token t.
-__device__ __forceinline__ int kv_request_of(const KvAttnArgs& a, int t) {
-  int r = 0;
-  for (int count = a.requests; count > 1;) {
-    const int step = count >> 1;
-    if (a.token_start[r + step] <= t) r += step;
-    count -= step;
-  }
-  return r;
-}
-
 // Over shared entries (Args = KvSharedArgs) the rows of all requests, token by token, are
 // tiled as if they were one request's; each attends the entries up to its own position,
 // and every result is partial.
@@ -132,10 +121,7 @@ __device__ __forceinline__ void kv_tile_body(const Args& a, float* part_o, float
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (i * kWave >= here) break;
-      const int t = first + i0 + min(i * kWave + lane, here - 1);
-      const int owner = kv_request_of(a, t);
-      const long long pos = (long long)a.seq_lens[owner] - (a.token_start[owner + 1] - t);
-      last[i] = (int)max(min(pos, shared - 1LL), -1LL);
+      last[i] = kv_last_shared(a, first + i0 + min(i * kWave + lane, here - 1), shared);
     }
     // (shared entries that none of these rows attends may hold anything)
     int end = max(last[0], last[1]) + 1;

@@ -88,14 +88,20 @@ struct KvAttnArgs {
 
 // Attention behind shared entries (w4a16_kv_attention_shared): entries before s =
 // min(max(shared_len[0], 0), max_shared) are read through row 0 of the block table for
-// all rows by the tile form, a request's own through its row by the split form, and a row's
-// partial results (`parts` of the shared entries, then `chunks` of its own) are joined.
+// all rows, by the tile form or by the split form, a request's own through its row by the
+// split form, and a row's partial results (`parts` of the shared entries, then `chunks` of its
+// own) are joined.
 struct KvSharedArgs : KvAttnArgs {
   const int32_t* shared_len;
   int max_shared, max_own;
+  int part_shift;              // the split form over shared entries: log2 of `part`, else 0
 };
 template <class Args>
 constexpr bool kv_behind_shared = std::is_same_v<Args, KvSharedArgs>;
+// The split form over the shared entries themselves.
+struct KvPrefixArgs : KvSharedArgs {};
+template <class Args>
+constexpr bool kv_over_shared = std::is_same_v<Args, KvPrefixArgs>;
 
 // Launchers (kv_attention.hip and kv_shared_attention.hip, once per head size).
 #define W4K_DECLARE_KV(D)                                                                     \

@@ -13,6 +13,7 @@ namespace w4k {
 namespace {
 
 constexpr int kMaxEntries = 1 << 28;
+constexpr int kPartTiles = 4;        // tiles of a part at least
 
 w4a16_status_t check_shared(const w4a16_kv_cache_t* cache, int tokens, int requests, int max_new, int max_shared,
                             int max_own, int q_heads) {
@@ -55,13 +56,18 @@ KvSharedArgs shared_args(const w4a16_kv_cache_t* cache, int tokens, int requests
   auto in_chunks = [&](int64_t n) { return (n + (1LL << a.chunk_shift) - 1) >> a.chunk_shift; };
   while (in_chunks(max_own) > kKvMaxChunks - 1) ++a.chunk_shift;
   a.chunks = max_own > 0 ? (int)in_chunks(max_own) + 1 : 0;
-  // Parts of the shared entries: as many workgroups as the card holds (512, two a CU), six
-  // tiles each at least.
+  // Parts of the shared entries.  Few rows in all take the split form, in its chunks.
   a.part = kKvTile;
-  if (max_shared > 0) {
+  if (max_shared > 0 && (int64_t)tokens * a.group <= kKvSplitRows) {
+    a.part_shift = max_shared <= 1024 ? 7 : max_shared <= 4096 ? 8 : max_shared <= 16384 ? 9 : 10;
+    while ((max_shared - 1) >> a.part_shift >= kKvMaxParts) ++a.part_shift;
+    a.part = 1 << a.part_shift;
+    a.parts = (max_shared + a.part - 1) >> a.part_shift;
+  } else if (max_shared > 0) {
+    // as many workgroups as the card holds (512, two a CU), some tiles each at least
     const int tile_tokens = kv_tile_rows(cache->dim, cache->type) / a.group;
     const int64_t workgroups = (int64_t)((tokens + tile_tokens - 1) / tile_tokens) * cache->heads;
-    const int64_t wanted = std::min<int64_t>({512 / workgroups, max_shared / (6 * kKvTile), kKvMaxParts});
+    const int64_t wanted = std::min<int64_t>({512 / workgroups, max_shared / (kPartTiles * kKvTile), kKvMaxParts});
     const int64_t parts = wanted > 1 ? wanted : 1;
     a.part = (int)((max_shared + parts * kKvTile - 1) / (parts * kKvTile)) * kKvTile;
     a.parts = (max_shared + a.part - 1) / a.part;

@@ -21,6 +21,12 @@ __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) v
   kv_split_body<D, TYPE, NC>(a, part_o, part_ml);
 }
 
+template <int D, int TYPE, int NC>
+__global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) void kv_prefix_split_kernel(
+    KvPrefixArgs a, float* part_o, float* part_ml) {
+  kv_split_body<D, TYPE, NC>(a, part_o, part_ml);
+}
+
 template <int TYPE>
 hipError_t kv_shared_typed(const KvSharedArgs& a, void* workspace, hipStream_t st) {
   constexpr int D = W4K_D;
@@ -29,7 +35,16 @@ hipError_t kv_shared_typed(const KvSharedArgs& a, void* workspace, hipStream_t s
   const int rows = a.split_tokens * a.group;
   const unsigned ry = a.requests < kKvGridRequests ? a.requests : kKvGridRequests;
   const unsigned rz = (a.requests + kKvGridRequests - 1) / kKvGridRequests;
-  if (a.parts > 0) {
+  if (a.part_shift > 0 && a.parts > 0) {
+    KvPrefixArgs p{a};
+    const int all_rows = a.tokens * a.group;
+    p.row_groups = all_rows <= 16 ? 1 : (all_rows + 31) / 32;
+    const dim3 grid(a.c.heads * p.row_groups * a.parts), block(kKvSplitWaves * kWave);
+    if (all_rows <= 16)
+      hipLaunchKernelGGL((kv_prefix_split_kernel<D, TYPE, 1>), grid, block, 0, st, p, part_o, part_ml);
+    else
+      hipLaunchKernelGGL((kv_prefix_split_kernel<D, TYPE, 2>), grid, block, 0, st, p, part_o, part_ml);
+  } else if (a.parts > 0) {
     const int tt = kv_tile_rows(D, TYPE) / a.group;
     hipLaunchKernelGGL((kv_shared_tile_kernel<D, TYPE>), dim3((unsigned)((a.tokens + tt - 1) / tt * a.c.heads), a.parts),
                        dim3(kv_tile_waves(D, TYPE) * kWave), 0, st, a, part_o, part_ml);

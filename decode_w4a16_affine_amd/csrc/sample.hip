@@ -221,8 +221,19 @@ __device__ __forceinline__ int sample_token(int chunk, int x) {
 template <class T>
 __device__ __forceinline__ void sample_load_chunk(const T* row, int chunk, int N, float (&v)[kLane]) {
   constexpr int V = kPiece<T>;
+  if ((chunk + 1) * kChunk <= N) {      // (no load under a condition)
+    const T* const p = row + sample_token<T>(chunk, 0);
 #pragma unroll
-  for (int x = 0; x < kLane; x += V) sample_load_row<V>(row, sample_token<T>(chunk, x), N, v + x);
+    for (int x = 0; x < kLane; x += V) {
+      float some[V];
+      sample_load_some(p + x * kWave, some);
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[x + e] = some[e];
+    }
+  } else {
+#pragma unroll
+    for (int x = 0; x < kLane; x += V) sample_load_row<V>(row, sample_token<T>(chunk, x), N, v + x);
+  }
 }
 
 // A wave's running sums: rows of 16 lanes by shifts within them, then their last lanes' to the rows behind.
@@ -482,16 +493,21 @@ __global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs
     nan |= v[x] != v[x];
   }
   top = sample_wave_max(top);
-  // f(logit, weight times 2^scale), four at a time: more would take too many registers
+  // f(logit, weight times 2^scale), four at a time: more would take too many registers.  Where the
+  // largest logit is moderate one fma gives the exponent, off by 2^-41 for all alike.
   const double inv_t = p.inv_t * kLog2E;
   auto weights = [&](int log2_scale, auto&& f) W4K_INLINE {
-    if (top == __builtin_inff()) {      // (only its equals have one)
+    const double away = -(double)top * inv_t;
+    if (away < 4096.0 && away > -4096.0) {
 #pragma unroll
-      for (int x = 0; x < kLane; ++x) f(v[x], v[x] == top ? __builtin_ldexp(1.0, log2_scale) : 0.0);
+      for (int x = 0; x < kLane; ++x) {
+        f(v[x], sample_exp2(__builtin_fma((double)v[x], inv_t, away), log2_scale));
+        if (x % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+      }
     } else {
 #pragma unroll
       for (int x = 0; x < kLane; ++x) {
-        f(v[x], sample_exp2(((double)v[x] - (double)top) * inv_t, log2_scale));
+        f(v[x], sample_weight(v[x], top, p.inv_t, log2_scale));
         if (x % 4 == 3) __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -779,7 +795,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_collect_kernel(SampleArgs
 template <class T>
 __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs a) {
   __shared__ SampleShared sh;
-  const int r = blockIdx.x, tid = threadIdx.x;
+  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & (kWave - 1);
   const T* const row = static_cast<const T*>(a.logits) + r * a.stride;
   const size_t at0 = (size_t)r * a.chunks;
   // What the launches before left, all at once: what is read one after the other costs a
@@ -929,10 +945,33 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
               weight_of, target > base ? target - base : 1, sh);
       }
       if (none) last = 0;
-      visit([&](uint64_t c, uint64_t w) W4K_INLINE {
-        if (c <= last && sample_log_weight(sample_logit(c), top, p.inv_t) >= least)
-          atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk[(uint32_t)c / kChunk]), w);
-      });
+      // the kept weights of each chunk: a wave's together, or those of the threads that hold a chunk's list
+      // (additions of one token each to few sums would wait for each other)
+      auto kept_weight = [&](uint64_t c, uint64_t w) W4K_INLINE {
+        return c <= last && sample_log_weight(sample_logit(c), top, p.inv_t) >= least ? w : 0;
+      };
+      auto add = [&](int chunk, uint64_t sum) W4K_INLINE {
+        if (sum) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk[chunk]), sum);
+      };
+      if (overflow) {
+        for (int i0 = 0; i0 < a.N; i0 += kChunk) {
+          uint64_t sum = 0;
+          for (int i = i0 + tid; i < min(i0 + kChunk, a.N); i += kSampleThreads) {
+            const float v = sample_load(row + i);
+            sum += kept_weight(sample_order(v, i), weight(v));
+          }
+          sum = sample_wave_scan(sum);
+          if (lane == kWave - 1) add(i0 / kChunk, sum);
+        }
+      } else {
+        uint64_t sum = 0;
+#pragma unroll
+        for (int e = 0; e < kHeld; ++e) sum += c[e] != ~0ull ? kept_weight(c[e], w[e]) : 0;
+        sum = sample_wave_scan(sum);
+        const int part = min(threads, kWave);
+        const uint64_t earlier = __shfl((unsigned long long)sum, max(lane - part, 0));
+        if ((lane & (part - 1)) == part - 1 && list_chunk < a.chunks) add(list_chunk, sum - (lane >= part ? earlier : 0));
+      }
       __syncthreads();
     }
   }
