@@ -127,11 +127,39 @@ __device__ __forceinline__ int kv_request_of(const KvAttnArgs& a, int t) {
   }
   return r;
 }
-// The last of the first `shared` entries that token t attends, or -1.
-__device__ __forceinline__ int kv_last_shared(const KvAttnArgs& a, int t, int shared) {
-  const int owner = kv_request_of(a, t);
-  const long long pos = (long long)a.seq_lens[owner] - (a.token_start[owner + 1] - t);
-  return (int)max(min(pos, shared - 1LL), -1LL);
+// Positions of a batch's tokens.  Each lane of a wave holds one request (of more than 64, every
+// step-th one's first token): one round of loads and a search across lanes, where a search through
+// memory waits for a load at each of its steps.
+struct KvOwners {
+  int step, start, base;      // base: with one request a lane, what a token's position exceeds its row by
+};
+__device__ __forceinline__ KvOwners kv_owners(const KvAttnArgs& a) {
+  KvOwners o;
+  o.step = (a.requests + kWave - 1) / kWave;
+  const int r = min((int)(threadIdx.x & (kWave - 1)) * o.step, a.requests - 1);
+  o.start = a.token_start[r];
+  o.base = o.step == 1 ? (int)((uint32_t)a.seq_lens[r] - (uint32_t)a.token_start[r + 1]) : 0;
+  return o;
+}
+// The last of the first `shared` entries that token t attends, or -1 (by a whole wave).
+__device__ __forceinline__ int kv_last_shared(const KvAttnArgs& a, const KvOwners& o, int t, int shared) {
+  int l = 0;      // the last lane whose request begins at or before t
+  for (int count = (a.requests + o.step - 1) / o.step; count > 1;) {
+    const int half = count >> 1;
+    if (__shfl(o.start, l + half) <= t) l += half;
+    count -= half;
+  }
+  long long base = __shfl(o.base, l);
+  if (o.step > 1) {
+    int r = l * o.step;
+    for (int count = min(o.step, a.requests - r); count > 1;) {
+      const int half = count >> 1;
+      if (a.token_start[r + half] <= t) r += half;
+      count -= half;
+    }
+    base = (long long)a.seq_lens[r] - a.token_start[r + 1];
+  }
+  return (int)max(min(base + t, shared - 1LL), -1LL);
 }
 
 // The parts of the cache (a.part entries each) that rows of the tile form attend.

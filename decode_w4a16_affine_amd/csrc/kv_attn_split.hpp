@@ -131,17 +131,25 @@ __device__ __forceinline__ void kv_split_body(const Args& a, float* part_o, floa
     return (j0 + 16 * x) >> shift < a.width && page >= 0 && page < a.c.pages ? page : -1;
   };
   int page = 0, page_after = 0;
-  if (!SHARED && a.window == 0 && a.width > 0) page = pages(block << chunk_shift);
+  int page_of = -1;      // SHARED: where the page that is looked up first begins, if shared_len is its bound
+  if constexpr (SHARED) {
+    page_of = block == 0 ? a.max_shared & ~(STEP - 1) : ((a.max_shared >> chunk_shift) + block) << chunk_shift;
+    if (a.width > 0) page = pages(page_of);
+  } else if (a.window == 0 && a.width > 0) {
+    page = pages(block << chunk_shift);
+  }
   const int i_first = kv_token_of(a, row0), i_last = kv_token_of(a, row0 + NC * 16 - 1);
   KvRows rows;
   int last = -1;      // PREFIX: the last entry that token `lane` attends (there are at most 64)
   if constexpr (PREFIX) {
+    const KvOwners owners = kv_owners(a);
     rows.first = a.token_start[0];
     rows.n = a.token_start[a.requests] - rows.first;
     rows.live = min(rows.n, a.tokens - rows.first);
     if (rows.first < 0 || row0 >= rows.live * a.group) return;
     const int shared = (int)min((long long)kv_shared_entries(a), (long long)a.width << shift);
-    if (lane < rows.live) last = kv_last_shared(a, rows.first + lane, shared);
+    last = kv_last_shared(a, owners, rows.first + min(lane, rows.live - 1), shared);
+    if (lane >= rows.live) last = -1;
     int end = lane >= i_first && lane <= i_last ? last + 1 : 0;
 #pragma unroll
     for (int off = kWave / 2; off > 0; off >>= 1) end = max(end, __shfl_xor(end, off));
@@ -272,7 +280,7 @@ __device__ __forceinline__ void kv_split_body(const Args& a, float* part_o, floa
     }
   };
   int j0 = max(at_begin, rows.begin & ~(STEP - 1));
-  if ((SHARED || a.window > 0) && rows.begin < rows.end) page = pages(j0);
+  if (SHARED ? j0 != page_of : a.window > 0 && rows.begin < rows.end) page = pages(j0);
   page = checked(j0, page);
 
   // this lane's rows: queries (in the keys' order) and positions

@@ -97,7 +97,9 @@ __device__ __forceinline__ void kv_tile_body(const Args& a, float* part_o, float
   const int kh = blockIdx.x % a.c.heads;
   const int u = (gridDim.x - 1 - blockIdx.x) / a.c.heads;
   int r = 0, i0, n, live_tokens;
+  KvOwners owners;
   if constexpr (SHARED) {
+    owners = kv_owners(a);
     i0 = u * tt;
     n = a.token_start[a.requests] - a.token_start[0];
     live_tokens = min(n, a.tokens - a.token_start[0]);
@@ -121,7 +123,7 @@ __device__ __forceinline__ void kv_tile_body(const Args& a, float* part_o, float
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (i * kWave >= here) break;
-      last[i] = kv_last_shared(a, first + i0 + min(i * kWave + lane, here - 1), shared);
+      last[i] = kv_last_shared(a, owners, first + i0 + min(i * kWave + lane, here - 1), shared);
     }
     // (shared entries that none of these rows attends may hold anything)
     int end = max(last[0], last[1]) + 1;

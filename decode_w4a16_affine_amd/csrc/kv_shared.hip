@@ -13,6 +13,7 @@ namespace w4k {
 namespace {
 
 constexpr int kMaxEntries = 1 << 28;
+constexpr int kSplitFill = 512;      // workgroups of the split form
 constexpr int kPartTiles = 4;        // tiles of a part at least
 
 w4a16_status_t check_shared(const w4a16_kv_cache_t* cache, int tokens, int requests, int max_new, int max_shared,
@@ -59,8 +60,10 @@ KvSharedArgs shared_args(const w4a16_kv_cache_t* cache, int tokens, int requests
   // Parts of the shared entries.  Few rows in all take the split form, in its chunks.
   a.part = kKvTile;
   if (max_shared > 0 && (int64_t)tokens * a.group <= kKvSplitRows) {
-    a.part_shift = max_shared <= 1024 ? 7 : max_shared <= 4096 ? 8 : max_shared <= 16384 ? 9 : 10;
-    while ((max_shared - 1) >> a.part_shift >= kKvMaxParts) ++a.part_shift;
+    const int64_t groups = (int64_t)cache->heads * ((tokens * a.group + 31) / 32);
+    a.part_shift = 7;
+    while ((max_shared - 1) >> a.part_shift >= kKvMaxParts || groups * (max_shared >> a.part_shift) > kSplitFill)
+      ++a.part_shift;
     a.part = 1 << a.part_shift;
     a.parts = (max_shared + a.part - 1) >> a.part_shift;
   } else if (max_shared > 0) {

@@ -223,8 +223,10 @@ def test_shared_attention_refuses_bad_arguments(L):
     ws = L.w4a16_kv_attention_shared_workspace_bytes
     assert ws(0, 3, 2, 500, 100, 8, cache()) == 0 and ws(3, 3, 17, 500, 100, 8, cache()) == 0
     assert ws(3, 3, 2, 0, 0, 8, cache()) == 0
-    # one part of 500 entries, two chunks of 128 for 100 that may begin inside one
-    assert need == 3 * 8 * 3 * (128 + 5) * 4
+    # few rows: 500 entries in four parts of 128; two chunks of 128 for 100 that may begin inside one
+    assert need == 3 * 8 * (4 + 2) * (128 + 5) * 4
+    # more: tiles of 64, 8000 entries in 25 parts of five (of four they would be more than 31)
+    assert ws(64, 64, 1, 8000, 100, 32, cache(heads=8)) == 64 * 32 * (25 + 2) * (128 + 5) * 4
 
 
 def test_shared_attention_binding_refuses_bad_tensors():
