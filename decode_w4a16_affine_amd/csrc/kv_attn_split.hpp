@@ -84,37 +84,50 @@ constexpr int kKvGridRequests = 32768;             // requests on the grid's y a
 // (a reload of a spilled register would wait for the loads in flight).
 constexpr int kv_split_occupancy(int D, int NC) { return D == 256 ? 2 : D == 128 || NC == 2 ? 3 : 4; }
 
+// Queries stay in LDS where a third wave a SIMD, or the products' operands, need
+// their registers (16 requests of 16 tokens, 4 query heads of 128: 71 us instead of
+// 79); with D = 256 there is room to read those of the next piece ahead.
+constexpr bool kv_split_queries_in_lds(int D, int NC) { return NC == 2 && D >= 128; }
+
+// What the waves of a workgroup share.
+template <int D, int NC>
+struct KvSplitShared {
+  static constexpr int W = kKvSplitWaves;
+  kv_u32x4 stage[W][kKvSplitTile * D / (16 * kWave) * kWave];      // a wave's keys, then its values
+  kv_u32x4 p[W][NC][kWave];                                        // the step's weights as operands
+  kv_u32x4 q[kv_split_queries_in_lds(D, NC) ? NC * 2 * (D / 64) : 0][kWave];
+  float m[W][NC * 16], l[W][NC * 16];
+};
+
 // Behind shared entries (Args = KvSharedArgs) a request's own ones alone are taken; over them
 // (KvPrefixArgs) the rows of all requests are taken as if they were one's, each with its own
 // last entry.  Both give partial results, which another kernel joins.
+// r: the request (PREFIX: 0); block: its cache head, rows and chunk.
 template <int D, int TYPE, int NC, class Args>
-__device__ __forceinline__ void kv_split_body(const Args& a, float* part_o, float* part_ml) {
+__device__ __forceinline__ void kv_split_body(const Args& a, KvSplitShared<D, NC>& shared, int block, int r, float* part_o,
+                                              float* part_ml) {
   constexpr bool SHARED = kv_behind_shared<Args>, PREFIX = kv_over_shared<Args>;
   constexpr int W = kKvSplitWaves;
   constexpr int T = kKvSplitTile, E = T / 4, STEP = W * T;
   constexpr int NP = T / 16;                       // pieces of scores
-  // Queries stay in LDS where a third wave a SIMD, or the products' operands, need
-  // their registers (16 requests of 16 tokens, 4 query heads of 128: 71 us instead of
-  // 79); with D = 256 there is room to read those of the next piece ahead.
-  constexpr bool Q_LDS = NC == 2 && D >= 128;
+  constexpr bool Q_LDS = kv_split_queries_in_lds(D, NC);
   constexpr int QB = D == 256 ? 2 : 1;             // pieces of queries in registers
   constexpr int KC = D / 64;                       // 16-byte pieces of a key a lane multiplies
   constexpr int DW = D / 16 / W;                   // 16-row pieces of the output a wave owns
   constexpr int LD = T * D / (16 * kWave);         // 16-byte loads a lane and step, keys and values each
-  __shared__ kv_u32x4 s_stage[W][LD * kWave];      // a wave's keys, then its values
-  __shared__ kv_u32x4 s_p[W][NC][kWave];           // the step's weights as operands
-  __shared__ kv_u32x4 s_q[Q_LDS ? NC * 2 * KC : 1][kWave];
-  __shared__ float s_m[W][NC * 16], s_l[W][NC * 16];
+  auto& s_stage = shared.stage;
+  auto& s_p = shared.p;
+  auto& s_q = shared.q;
+  auto& s_m = shared.m;
+  auto& s_l = shared.l;
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int x = lane & 15, g = lane >> 4;
   // Workgroups go to the eight XCDs in turn.  Heads run fastest, then row
   // groups, then a request's chunks, so that every request is spread over all
   // XCDs (with requests fastest, those of ragged batches were unevenly loaded)
-  const int r = blockIdx.z * kKvGridRequests + blockIdx.y;      // (PREFIX: 0)
   if (r >= a.requests) return;
   int chunk_shift = a.chunk_shift;
   if constexpr (PREFIX) chunk_shift = a.part_shift;
-  int block = blockIdx.x;
   const int kh = block % a.c.heads;
   block /= a.c.heads;
   const int row0 = block % a.row_groups * (NC * 16);
@@ -140,15 +153,15 @@ __device__ __forceinline__ void kv_split_body(const Args& a, float* part_o, floa
   }
   const int i_first = kv_token_of(a, row0), i_last = kv_token_of(a, row0 + NC * 16 - 1);
   KvRows rows;
-  int last = -1;      // PREFIX: the last entry that token `lane` attends (there are at most 64)
+  int last = -1;      // PREFIX: the last entry that token `lane` attends (there are at most 64, of 512 rows)
   if constexpr (PREFIX) {
     const KvOwners owners = kv_owners(a);
     rows.first = a.token_start[0];
     rows.n = a.token_start[a.requests] - rows.first;
     rows.live = min(rows.n, a.tokens - rows.first);
     if (rows.first < 0 || row0 >= rows.live * a.group) return;
-    const int shared = (int)min((long long)kv_shared_entries(a), (long long)a.width << shift);
-    last = kv_last_shared(a, owners, rows.first + min(lane, rows.live - 1), shared);
+    const int entries = (int)min((long long)kv_shared_entries(a), (long long)a.width << shift);
+    last = kv_last_shared(a, owners, rows.first + min(lane, rows.live - 1), entries);
     if (lane >= rows.live) last = -1;
     int end = lane >= i_first && lane <= i_last ? last + 1 : 0;
 #pragma unroll
@@ -478,7 +491,8 @@ __device__ __forceinline__ void kv_split_body(const Args& a, float* part_o, floa
 template <int D, int TYPE, int NC>
 __global__ __launch_bounds__(kKvSplitWaves * kWave, kv_split_occupancy(D, NC)) void kv_split_kernel(
     KvAttnArgs a, float* part_o, float* part_ml) {
-  kv_split_body<D, TYPE, NC>(a, part_o, part_ml);
+  __shared__ KvSplitShared<D, NC> shared;
+  kv_split_body<D, TYPE, NC>(a, shared, blockIdx.x, blockIdx.z * kKvGridRequests + blockIdx.y, part_o, part_ml);
 }
 
 // Joins the chunks of one row (grid: cache head and row, request) in chunk order:

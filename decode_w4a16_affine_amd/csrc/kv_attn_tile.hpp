@@ -68,11 +68,23 @@ __device__ __forceinline__ int kv_tile_owner(const int32_t* token_start, int req
   return lo;
 }
 
+// What the waves of a workgroup share.
+template <int D, int TYPE>
+struct KvTileShared {
+  static constexpr int W = kv_tile_waves(D, TYPE), HS = kv_tile_share(D), NB = HS == 1 ? 2 : 1;
+  kv_u32x4 k[NB][4 * (D / 64) * 2 * kWave];      // [buffer][piece t][sum step][lane]
+  kv_u32x4 v[NB][D / 16 * 2 * kWave];            // [buffer][piece d][sum step][lane]
+  kv_u32x4 p[HS == 2 ? W : 0][kKvTileCols][kWave];      // a wave's weights as an operand
+  float m[HS == 2 ? W : 0][kKvTileCols * 16];
+};
+
 // Over shared entries (Args = KvSharedArgs) the rows of all requests, token by token, are
 // tiled as if they were one request's; each attends the entries up to its own position,
 // and every result is partial.
+// block of `blocks`: the workgroup's rows; part: of the cache (see KvParts).
 template <int D, int TYPE, class Args>
-__device__ __forceinline__ void kv_tile_body(const Args& a, float* part_o, float* part_ml) {
+__device__ __forceinline__ void kv_tile_body(const Args& a, KvTileShared<D, TYPE>& shared, int block, int blocks, int part,
+                                             float* part_o, float* part_ml) {
   constexpr bool SHARED = kv_behind_shared<Args>;
   constexpr int NC = kKvTileCols, W = kv_tile_waves(D, TYPE), HS = kv_tile_share(D);
   constexpr int KC = D / 64;              // 16-byte pieces of a key a lane multiplies
@@ -81,12 +93,12 @@ __device__ __forceinline__ void kv_tile_body(const Args& a, float* part_o, float
   constexpr int KU = 4 * KC, VU = DT;     // 64-lane pieces of a tile's keys and values
   constexpr int KL = KU / W, VL = VU / W;   // of which a wave loads
   static_assert(KU % W == 0 && VU % W == 0 && KC % KL == 0, "each wave loads the same");
-  constexpr int NB = HS == 1 ? 2 : 1;       // buffers
+  constexpr int NB = KvTileShared<D, TYPE>::NB;       // buffers
   constexpr int AHEAD = D == 256 ? 3 : 4;   // operands read ahead of their products, as registers allow
-  __shared__ kv_u32x4 s_k[NB][KU * 2 * kWave];      // [piece t][sum step][lane]
-  __shared__ kv_u32x4 s_v[NB][VU * 2 * kWave];      // [piece d][sum step][lane]
-  __shared__ kv_u32x4 s_p[HS == 2 ? W : 1][NC][kWave];      // a wave's weights as an operand
-  __shared__ float s_m[W][NC * 16];
+  auto& s_k = shared.k;
+  auto& s_v = shared.v;
+  auto& s_p = shared.p;
+  auto& s_m = shared.m;
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int x = lane & 15, g = lane >> 4;
   const int half = HS == 2 ? wave & 1 : 0;
@@ -94,8 +106,8 @@ __device__ __forceinline__ void kv_tile_body(const Args& a, float* part_o, float
   // Heads run fastest: a head's workgroups share an XCD's L2 (eight heads), and
   // the last tokens, which attend most, go first for every head (with a head's
   // tiles together, the last head's long ones began late: 770 us instead of 638).
-  const int kh = blockIdx.x % a.c.heads;
-  const int u = (gridDim.x - 1 - blockIdx.x) / a.c.heads;
+  const int kh = block % a.c.heads;
+  const int u = (blocks - 1 - block) / a.c.heads;
   int r = 0, i0, n, live_tokens;
   KvOwners owners;
   if constexpr (SHARED) {
@@ -119,11 +131,11 @@ __device__ __forceinline__ void kv_tile_body(const Args& a, float* part_o, float
   int last[2] = {-1, -1};      // SHARED: the last entry that tokens i0 + lane and i0 + 64 + lane attend
   if constexpr (SHARED) {
     const int first = a.token_start[0];
-    const int shared = (int)min((long long)kv_shared_entries(a), (long long)a.width << shift);
+    const int entries = (int)min((long long)kv_shared_entries(a), (long long)a.width << shift);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (i * kWave >= here) break;
-      last[i] = kv_last_shared(a, owners, first + i0 + min(i * kWave + lane, here - 1), shared);
+      last[i] = kv_last_shared(a, owners, first + i0 + min(i * kWave + lane, here - 1), entries);
     }
     // (shared entries that none of these rows attends may hold anything)
     int end = max(last[0], last[1]) + 1;
@@ -135,7 +147,6 @@ __device__ __forceinline__ void kv_tile_body(const Args& a, float* part_o, float
   }
   // the part of the cache (all of it if a.parts is 1) that this workgroup walks
   const KvParts parts = SHARED ? KvParts{0, (rows.end + a.part - 1) / a.part} : kv_parts_of(a, rows);
-  const int part = blockIdx.y;
   if (part >= parts.count) return;
   const int part_begin = (parts.first + part) * a.part;
   const int part_end = (int)min((long long)part_begin + a.part, (long long)rows.end);
@@ -407,7 +418,8 @@ __device__ __forceinline__ void kv_tile_body(const Args& a, float* part_o, float
 template <int D, int TYPE>
 __global__ __launch_bounds__(kv_tile_waves(D, TYPE) * kWave, 2) void kv_tile_kernel(KvAttnArgs a, float* part_o,
                                                                                   float* part_ml) {
-  kv_tile_body<D, TYPE>(a, part_o, part_ml);
+  __shared__ KvTileShared<D, TYPE> shared;
+  kv_tile_body<D, TYPE>(a, shared, blockIdx.x, gridDim.x, blockIdx.y, part_o, part_ml);
 }
 
 // Joins the parts of a row in their order: D / 4 threads a row (bound by two reads

@@ -13,6 +13,7 @@ namespace w4k {
 namespace {
 
 constexpr int kMaxEntries = 1 << 28;
+constexpr int kSplitSteps = 768;     // of 128 entries and 32 rows
 constexpr int kSplitFill = 512;      // workgroups of the split form
 constexpr int kPartTiles = 4;        // tiles of a part at least
 
@@ -57,25 +58,47 @@ KvSharedArgs shared_args(const w4a16_kv_cache_t* cache, int tokens, int requests
   auto in_chunks = [&](int64_t n) { return (n + (1LL << a.chunk_shift) - 1) >> a.chunk_shift; };
   while (in_chunks(max_own) > kKvMaxChunks - 1) ++a.chunk_shift;
   a.chunks = max_own > 0 ? (int)in_chunks(max_own) + 1 : 0;
-  // Parts of the shared entries.  Few rows in all take the split form, in its chunks.
+  // The form over the shared entries.  The split form's workgroup has 32 rows and a step of 128
+  // entries, short ones side by side; the tile form converts an entry once for 128 rows.  The
+  // split form takes 64 rows, or more while its steps are few.  Measured (us in a graph, split / tile):
+  // 70 rows of 256 over 2 heads behind 1000 entries 12.2 / 26.2, 4000 15.8 / 25.2, 12000 25.3 / 29.1,
+  // 50000 53.5 / 42.9; 120 of 64 over 4 behind 1000 10.9 / 15.8, 8000 17.3 / 16.7; 96 of 128 over 8
+  // behind 8000 29.9 / 31.6, 100001 172 / 91; 256 behind 30000 101 / 84.
   a.part = kKvTile;
-  if (max_shared > 0 && (int64_t)tokens * a.group <= kKvSplitRows) {
-    const int64_t groups = (int64_t)cache->heads * ((tokens * a.group + 31) / 32);
+  const int rows_shared = tokens <= kWave ? tokens * a.group : kKvMaxSharedRows + 1;
+  const int64_t groups = (int64_t)cache->heads * ((rows_shared + 31) / 32);
+  if (max_shared > 0 && (rows_shared <= kKvSplitRows || (rows_shared <= kKvMaxSharedRows &&
+                                                         groups * ((max_shared + 127) / 128) <= kSplitSteps))) {
+    // Chunks of one step while their workgroups are fewer than the card holds (us, 256 / 512 / 1024 at most):
+    // 16 rows behind 100001, 8 heads of 128, 61.0 / 55.7 / 61.6; 64 behind 8000 29.9 / 31.0 / 39.6.
     a.part_shift = 7;
     while ((max_shared - 1) >> a.part_shift >= kKvMaxParts || groups * (max_shared >> a.part_shift) > kSplitFill)
       ++a.part_shift;
     a.part = 1 << a.part_shift;
     a.parts = (max_shared + a.part - 1) >> a.part_shift;
   } else if (max_shared > 0) {
-    // as many workgroups as the card holds (512, two a CU), some tiles each at least
+    // Parts for a workgroup a CU, so that the requests' own run beside them (64 single tokens behind 8000 and
+    // up to 2000 of their own, 62 us; for two a CU 66), and for two where tiles are many (24 behind
+    // 100001: 87; for one 99), which eight waves of heads of 256 leave no room for.  Each
+    // row and part costs D + 5 floats written and read again: four tiles at least (us, 2 / 3 / 4 / 6: 61
+    // tokens of 16 requests behind 6000, 16 heads of 64 over 4, 28.0 / 27.0 / 24.5 / 25.7).
     const int tile_tokens = kv_tile_rows(cache->dim, cache->type) / a.group;
     const int64_t workgroups = (int64_t)((tokens + tile_tokens - 1) / tile_tokens) * cache->heads;
-    const int64_t wanted = std::min<int64_t>({512 / workgroups, max_shared / (kPartTiles * kKvTile), kKvMaxParts});
+    const int64_t tiles = workgroups * (max_shared / kKvTile);
+    const int64_t fill = tiles > 256 * 32 && kv_tile_waves(cache->dim, cache->type) == 4 ? 512 : 256;
+    const int64_t wanted = std::min<int64_t>({fill / workgroups, max_shared / (kPartTiles * kKvTile), kKvMaxParts});
     const int64_t parts = wanted > 1 ? wanted : 1;
     a.part = (int)((max_shared + parts * kKvTile - 1) / (parts * kKvTile)) * kKvTile;
     a.parts = (max_shared + a.part - 1) / a.part;
   }
   return a;
+}
+
+// The launch: workgroups over shared entries (of at least 64 rows) and of the requests' own.
+bool shared_launch_fits(const KvSharedArgs& a) {
+  const int64_t over = (int64_t)(a.tokens / (64 / a.group) + 1) * a.c.heads * a.parts;
+  const int64_t own = (int64_t)a.c.heads * a.row_groups * a.chunks * a.requests;
+  return over + own <= (1 << 22);      // (of up to 512 threads, 2^32 of which are a launch's limit)
 }
 
 size_t shared_workspace(const KvSharedArgs& a, int dim) {
@@ -94,7 +117,8 @@ size_t w4a16_kv_attention_shared_workspace_bytes(int tokens, int requests, int m
                                                  int q_heads, const w4a16_kv_cache_t* cache) {
   if (check_shared(cache, tokens, requests, max_new, max_shared, max_own, q_heads) != W4A16_OK) return 0;
   if (tokens == 0 || requests == 0 || max_new == 0) return 0;
-  return shared_workspace(shared_args(cache, tokens, requests, max_new, max_shared, max_own, q_heads), cache->dim);
+  const KvSharedArgs a = shared_args(cache, tokens, requests, max_new, max_shared, max_own, q_heads);
+  return shared_launch_fits(a) ? shared_workspace(a, cache->dim) : 0;
 }
 
 w4a16_status_t w4a16_kv_attention_shared(const uint16_t* q, int64_t q_stride, const w4a16_kv_cache_t* cache,
@@ -117,6 +141,7 @@ w4a16_status_t w4a16_kv_attention_shared(const uint16_t* q, int64_t q_stride, co
       !kv_aligned(token_start, 4) || !kv_aligned(shared_len, 4))
     return W4A16_ERR_ALIGN;
   KvSharedArgs a = shared_args(cache, tokens, requests, max_new, max_shared, max_own, q_heads);
+  if (!shared_launch_fits(a)) return W4A16_ERR_SHAPE;
   const size_t need = shared_workspace(a, cache->dim);
   if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
   if (!kv_aligned(workspace, 16)) return W4A16_ERR_ALIGN;

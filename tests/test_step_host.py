@@ -225,8 +225,8 @@ def test_shared_attention_refuses_bad_arguments(L):
     assert ws(3, 3, 2, 0, 0, 8, cache()) == 0
     # few rows: 500 entries in four parts of 128; two chunks of 128 for 100 that may begin inside one
     assert need == 3 * 8 * (4 + 2) * (128 + 5) * 4
-    # more: tiles of 64, 8000 entries in 25 parts of five (of four they would be more than 31)
-    assert ws(64, 64, 1, 8000, 100, 32, cache(heads=8)) == 64 * 32 * (25 + 2) * (128 + 5) * 4
+    # more: tiles of 64 for a workgroup a CU, 8000 entries in 16 parts of eight
+    assert ws(64, 64, 1, 8000, 100, 32, cache(heads=8)) == 64 * 32 * (16 + 2) * (128 + 5) * 4
 
 
 def test_shared_attention_binding_refuses_bad_tensors():
