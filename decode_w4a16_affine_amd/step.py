@@ -66,18 +66,30 @@ def step_lib() -> ctypes.CDLL:
 
 # ---- norms of queries and keys, rotation ------------------------------------------
 
+def _head(t, name):
+    """Tokens, heads, D and token stride of a [T, heads, D] tensor whose token rows are dense."""
+    if t.dtype is not torch.bfloat16:
+        _dtype(t, torch.bfloat16, name)
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be 3-D [T, heads, D], got {list(shape)}")
+    tokens, heads, dim = shape
+    return tokens, heads, dim, heads * dim if t.is_contiguous() else _rows(t, heads, dim, name)[1]
+
+
+_NO_HEAD = (0, 0, 0, 0)
+
+
 def _head_rows(q, k):
-    """(tokens, D, [stride, heads] of q and of k); q or k may be None."""
-    x = k if q is None else q
-    if x is None:
-        raise ValueError("q and k are both None")
-    if x.dim() != 3:
-        raise ValueError(f"q and k must be 3-D [T, heads, D], got {list(x.shape)}")
-    dim = x.shape[2]
-    parts = [(0, 0, 0) if t is None else (*_rows(t, None, dim, name), t.shape[1]) for t, name in ((q, "q"), (k, "k"))]
-    if q is not None and k is not None and parts[0][0] != parts[1][0]:
-        raise ValueError(f"q and k must have the same tokens, got {parts[0][0]} and {parts[1][0]}")
-    return x.shape[0], dim, parts[0][1:], parts[1][1:]
+    """(q's and k's tokens, heads, D and stride); q or k may be None."""
+    a = _NO_HEAD if q is None else _head(q, "q")
+    b = _NO_HEAD if k is None else _head(k, "k")
+    if k is None:
+        if q is None:
+            raise ValueError("q and k are both None")
+    elif q is not None and (a[0] != b[0] or a[2] != b[2]):
+        raise ValueError(f"q and k must have the same tokens and D, got {list(q.shape)} and {list(k.shape)}")
+    return a, b
 
 
 def _rotation(inv_freq, positions, sections, tokens):
@@ -89,10 +101,11 @@ def _rotation(inv_freq, positions, sections, tokens):
     if positions is None:
         raise ValueError("inv_freq needs positions")
     _dtype(inv_freq, torch.float32, "inv_freq")
-    if inv_freq.dim() != 1:
-        raise ValueError(f"inv_freq must be 1-D [rot / 2], got {list(inv_freq.shape)}")
+    shape = inv_freq.shape
+    if len(shape) != 1:
+        raise ValueError(f"inv_freq must be 1-D [rot / 2], got {list(shape)}")
     _dtype(positions, torch.int32, "positions")
-    half = inv_freq.shape[0]
+    half = shape[0]
     if sections is None:
         if positions.shape != (tokens,):
             _shape(positions, (tokens,), "positions")
@@ -107,10 +120,9 @@ def _rotation(inv_freq, positions, sections, tokens):
 
 
 def _weight(w, dim, name):
-    if w is not None:
-        _dtype(w, torch.bfloat16, name)
+    _dtype(w, torch.bfloat16, name)
+    if w.shape != (dim,):
         _shape(w, (dim,), name)
-    return w
 
 
 def _ptr(t):
@@ -128,36 +140,44 @@ def w4a16_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_o
 
     A weight None is a factor of 1; q (with q_out) or k (with k_out) None is left out; inv_freq None rotates nothing;
     sections gives the pairs of each axis of positions [axes, T].  q_out may be q and k_out may be k."""
-    shapes = _head_rows(q, k)
-    tokens, dim, (_, q_heads), (_, k_heads) = shapes
-    outs = []
+    rows = _head_rows(q, k)
+    strides = []
     for x, out, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
         if (x is None) != (out is None):
             raise ValueError(f"{name} goes with its input")
         if out is not None and out.shape != x.shape:
             _shape(out, x.shape, name)
-        outs.append((0, 0) if out is None else _rows(out, x.shape[1], dim, name))
-    _rope(shapes, q, k, q_weight, k_weight, inv_freq, positions, q_out, outs[0][1], k_out, outs[1][1], eps, weight_offset,
+        strides.append(0 if out is None else _head(out, name)[3])
+    _same_gpu(*_given(q, k, q_out, k_out))
+    _rope(rows, q, k, q_weight, k_weight, inv_freq, positions, q_out, strides[0], k_out, strides[1], eps, weight_offset,
           norm, interleaved, sections, stream)
 
 
-def _rope(shapes, q, k, q_weight, k_weight, inv_freq, positions, q_out, qo_stride, k_out, ko_stride, eps, weight_offset,
+def _rope(rows, q, k, q_weight, k_weight, inv_freq, positions, q_out, qo_stride, k_out, ko_stride, eps, weight_offset,
           norm, interleaved, sections, stream):
-    tokens, dim, (q_stride, q_heads), (k_stride, k_heads) = shapes
-    _weight(q_weight, dim, "q_weight")
-    _weight(k_weight, dim, "k_weight")
+    (tokens, q_heads, dim, q_stride), (k_tokens, k_heads, k_dim, k_stride) = rows
+    if q is None:
+        tokens, dim = k_tokens, k_dim
+    if q_weight is not None:
+        _weight(q_weight, dim, "q_weight")
+    if k_weight is not None:
+        _weight(k_weight, dim, "k_weight")
     rot, axes, sec = _rotation(inv_freq, positions, sections, tokens)
     small = _given(q_weight, k_weight, inv_freq, positions)
-    dev = _same_gpu(*_given(q, k, q_out, k_out), *small)
+    dev = _same_gpu(k if q is None else q, *(small if q is None or k is None else (k, *small)))
     _dense(*small)
     if _current_device() != dev:
-        return _on(dev, _rope, shapes, q, k, q_weight, k_weight, inv_freq, positions, q_out, qo_stride, k_out, ko_stride,
+        return _on(dev, _rope, rows, q, k, q_weight, k_weight, inv_freq, positions, q_out, qo_stride, k_out, ko_stride,
                    eps, weight_offset, norm, interleaved, sections, stream)
+    if q_out is None and k_out is None:      # the allocating form
+        q_out, k_out = (None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k))
+        qo_stride, ko_stride = q_heads * dim, k_heads * dim
     _check(step_lib().w4a16_qk_norm_rope(_ptr(q), q_stride, _ptr(k), k_stride, _ptr(q_weight), _ptr(k_weight),
                                          weight_offset, _ptr(inv_freq), _ptr(positions), sec, axes, _ptr(q_out),
                                          qo_stride, _ptr(k_out), ko_stride, eps,
                                          (ROPE_NORM if norm else 0) | (ROPE_INTERLEAVED if interleaved else 0), tokens,
                                          q_heads, k_heads, dim, rot, _raw_stream(stream, dev)), "w4a16_qk_norm_rope")
+    return q_out, k_out
 
 
 # ---- attention behind shared entries ------------------------------------------------
@@ -298,12 +318,8 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=No
         with _current(stream, k if q is None else q):
             return qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, weight_offset, norm, interleaved,
                                 sections)
-    shapes = _head_rows(q, k)
-    q_out, k_out = (None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k))
-    dim = shapes[1]
-    _rope(shapes, q, k, q_weight, k_weight, inv_freq, positions, q_out, shapes[2][1] * dim, k_out, shapes[3][1] * dim, eps,
-          weight_offset, norm, interleaved, sections, None)
-    return q_out, k_out
+    return _rope(_head_rows(q, k), q, k, q_weight, k_weight, inv_freq, positions, None, 0, None, 0, eps, weight_offset, norm,
+                 interleaved, sections, None)
 
 
 def kv_attention_shared(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, token_start, shared_len,
