@@ -12,6 +12,11 @@
 // token and wave.  The angle in turns is position * frequency / 2 pi in fp64 (a far
 // position has thousands of turns, whose fraction fp32 would lose), its
 // fraction's sine and cosine in fp32.
+//
+// Bound and measured: rows read and written once.  11801 tokens of 40 heads of 128,
+// 242 MB: 48 us, 5.0 TB/s (a copy of 2 GiB: 4.9); 4099 of 20 with positions of
+// three axes, 42 MB: 10.6 us, 4.0 TB/s.  A step of 48 tokens takes 3.2 us: one launch and
+// two loads that wait for each other (positions and rows).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -24,7 +29,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWaves = kRopeThreads / kWave;
-constexpr int kRopeFill = 8192;      // waves that fill the card: 8 a SIMD
+constexpr int kRopeFill = 2048;      // waves that share a step's heads
 
 struct RopeArgs {
   const uint16_t *q, *k, *qw, *kw;
@@ -227,8 +232,10 @@ w4a16_status_t w4a16_qk_norm_rope(const uint16_t* q, int64_t q_stride, const uin
   a.axes = axes;
   a.eps = eps;
   a.offset = weight_offset;
-  // Wave-fuls of heads a wave: one while waves are few, so that a small step is spread
-  // over the card; all of a token's where tokens alone fill it.
+  // Wave-fuls of heads a wave: one while waves are few, so that a small step is spread over
+  // the card; more where they share their token's sines.  Measured (us in a graph, for at least 2048 /
+  // 8192 / 16384 waves): 4099 tokens of 20 heads of 128 with three axes 10.6 / 13.6 / 16.7, 1500 of
+  // 40 8.8 / 11.9 / 11.8, 11801 of 40 48.0 / 47.5 / 46.7.
   const int fulls = (a.heads + kWave * 8 / dim - 1) / (kWave * 8 / dim);
   const int64_t waves = (int64_t)tokens * fulls;
   a.span = waves <= kRopeFill ? 1 : (int)(waves / kRopeFill) < fulls ? (int)(waves / kRopeFill) : fulls;
