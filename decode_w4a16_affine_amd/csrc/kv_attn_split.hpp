@@ -153,7 +153,7 @@ __device__ __forceinline__ void kv_split_body(const Args& a, KvSplitShared<D, NC
   }
   const int i_first = kv_token_of(a, row0), i_last = kv_token_of(a, row0 + NC * 16 - 1);
   KvRows rows;
-  int last = -1;      // PREFIX: the last entry that token `lane` attends (there are at most 64, of 512 rows)
+  int last = -1;      // PREFIX: the last entry that token `lane` attends (there are at most 64)
   if constexpr (PREFIX) {
     const KvOwners owners = kv_owners(a);
     rows.first = a.token_start[0];

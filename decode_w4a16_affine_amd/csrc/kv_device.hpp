@@ -142,7 +142,7 @@ constexpr int kKvTile = 64;           // cache entries at once
 constexpr int kKvTileCols = 2;        // 16-row pieces a wave (or the waves that share rows)
 constexpr int kKvTileStats = 2;
 constexpr int kKvMaxParts = 128;      // parts of shared entries at most
-constexpr int kKvMaxSharedRows = 512; // rows (of up to 64 tokens) a cache head in the split form over them
+constexpr int kKvMaxSharedRows = 128; // rows (of up to 64 tokens) a cache head in the split form over them
 constexpr int kv_tile_share(int D) { return D == 256 ? 2 : 1; }
 constexpr int kv_tile_waves(int D, int type) { return D == 256 && type == W4A16_KV_INT8 ? 8 : 4; }
 constexpr int kv_tile_rows(int D, int type) { return kv_tile_waves(D, type) / kv_tile_share(D) * kKvTileCols * 16; }

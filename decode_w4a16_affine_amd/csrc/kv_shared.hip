@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kMaxEntries = 1 << 28;
 constexpr int kSplitSteps = 768;     // of 128 entries and 32 rows
+constexpr int kOwnFill = 2048;       // workgroups of the requests' own entries
 constexpr int kSplitFill = 512;      // workgroups of the split form
 constexpr int kPartTiles = 4;        // tiles of a part at least
 
@@ -53,17 +54,21 @@ KvSharedArgs shared_args(const w4a16_kv_cache_t* cache, int tokens, int requests
   a.by_token = true;
   const int rows = a.split_tokens * a.group;
   a.row_groups = rows <= 16 ? 1 : (rows + 31) / 32;
-  // chunks of a request's own entries, which may begin inside one
-  a.chunk_shift = max_own <= 1024 ? 7 : max_own <= 4096 ? 8 : max_own <= 16384 ? 9 : 10;
+  // Chunks of a request's own entries, which may begin inside one: of one step while the workgroups
+  // are few.  Measured (us in a graph, at most 512 / 1024 / 2048 / 4096): 64 requests with up to 2000 of
+  // their own 60.8 / 60.5 / 60.0 / 62.0, 24 37.6 / 32.1 / 31.3 / 35.5, 16 with up to 8000 59.6 / 50.4 /
+  // 49.6 / 50.2.
+  const int64_t own_groups = (int64_t)requests * cache->heads * a.row_groups;
+  a.chunk_shift = 7;
   auto in_chunks = [&](int64_t n) { return (n + (1LL << a.chunk_shift) - 1) >> a.chunk_shift; };
-  while (in_chunks(max_own) > kKvMaxChunks - 1) ++a.chunk_shift;
+  while (in_chunks(max_own) > kKvMaxChunks - 1 || own_groups * (max_own >> a.chunk_shift) > kOwnFill) ++a.chunk_shift;
   a.chunks = max_own > 0 ? (int)in_chunks(max_own) + 1 : 0;
   // The form over the shared entries.  The split form's workgroup has 32 rows and a step of 128
   // entries, short ones side by side; the tile form converts an entry once for 128 rows.  The
   // split form takes 64 rows, or more while its steps are few.  Measured (us in a graph, split / tile):
   // 70 rows of 256 over 2 heads behind 1000 entries 12.2 / 26.2, 4000 15.8 / 25.2, 12000 25.3 / 29.1,
   // 50000 53.5 / 42.9; 120 of 64 over 4 behind 1000 10.9 / 15.8, 8000 17.3 / 16.7; 96 of 128 over 8
-  // behind 8000 29.9 / 31.6, 100001 172 / 91; 256 behind 30000 101 / 84.
+  // behind 8000 29.9 / 31.6, 100001 172 / 91; 250 of 256 over 2 behind 4000 28.5 / 25.7.
   a.part = kKvTile;
   const int rows_shared = tokens <= kWave ? tokens * a.group : kKvMaxSharedRows + 1;
   const int64_t groups = (int64_t)cache->heads * ((rows_shared + 31) / 32);

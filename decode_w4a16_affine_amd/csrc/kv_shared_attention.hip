@@ -1,5 +1,17 @@
 // Attention behind entries that a batch's requests share (w4a16_kv_attention_shared of
 // include/w4a16_step.h).  Compiled once per head size (W4K_D = 64, 128, 256).
+//
+// softmax over (shared, own) entries is joined from both sides' (maximum, sum, output): the
+// shared entries are attended by all requests' rows at once, in the form that their number
+// makes the better one (kv_shared.hip), a request's own by its rows alone, in the split
+// form; kv_shared_join_kernel adds the parts of each row.
+//
+// Bound and measured (in a graph).  64 single tokens, 32 heads of 128 over 8, E4M3, behind 8000
+// shared and up to 2000 own entries, 148 MB: 60 us, of which the join takes 8 (23 MB of partial
+// results written and read again).  The tiles' registers leave the own entries' workgroups two a
+// CU where three stream better: in launches of their own the tiles took 26 and the others 32.
+// (w4a16_kv_attention reads 1.2 GB for that.)  24 behind 100001, int8, 229 MB: 87 us; 96 of a
+// tile's 128 rows, a quarter of the units idle.  8 behind 1501, 10 heads of 256 over 2: 12.6 us.
 #include "kv_attn_split.hpp"
 #include "kv_attn_tile.hpp"
 #include "kv_device.hpp"
