@@ -1,15 +1,20 @@
 """Prompt, decode and verify steps of a small stack of W4 layers over the paged 8-bit cache.
 
     python examples/decode_layers.py [--layers 4] [--kind int8|fp8] [--steps 16] [--candidates 3]
+        [--rope-base 10000] [--share 640] [--temperature 0.8 [--top-k 50] [--top-p 0.95] [--min-p 0.02]]
 
-Every weight product, the cache and its attention are the library's; torch
-allocates, normalises (root mean square, no learned factor) and adds the
-residuals.  Weights are random (synthetic.quantized_weights), so what is
+Every weight product, the cache and its attention, the rotation and the sampling
+are the library's; torch allocates, normalises the hidden rows (root mean square, no
+learned factor) and adds the residuals.  Weights are random (synthetic.quantized_weights), so what is
 generated means nothing: the example shows how the entry points fit together.
 A step brings some tokens of each request (a prompt, one token, or candidates
 to verify), and its bookkeeping (w4a16_kv_plan) is made once for all layers:
 
-  plan -> per layer: q/k/v products -> append -> attention -> o product -> MLP -> LM head
+  plan -> per layer: q/k/v products -> (head norms, positions rotated in) -> append -> attention
+       -> o product -> MLP -> LM head -> largest logits, or tokens drawn from them
+
+Requests that begin with the same tokens can share their pages (Stack.share): steps of few
+tokens a request then read these once for all of them.
 """
 from __future__ import annotations
 
@@ -51,6 +56,8 @@ class Layer:
         self.q, self.o = Weights(q_heads * dim, hidden, seed), Weights(hidden, q_heads * dim, seed + 1)
         self.k, self.v = Weights(kv_heads * dim, hidden, seed + 2), Weights(kv_heads * dim, hidden, seed + 3)
         self.gate_up, self.down = Weights(2 * ffn, hidden, seed + 4), Weights(hidden, ffn, seed + 5)
+        norms = 1 + 0.2 * torch.randn((2, dim), generator=torch.Generator().manual_seed(seed + 6))
+        self.q_norm, self.k_norm = norms.to(torch.bfloat16).cuda()
 
     def qkv(self, x):
         out = [torch.empty((x.shape[0], w.N), dtype=torch.bfloat16, device=x.device) for w in (self.q, self.k, self.v)]
@@ -92,7 +99,7 @@ class Stack:
     """Layers with a paged cache for `requests` requests of at most max_len tokens."""
 
     def __init__(self, layers=2, hidden=2560, ffn=10240, q_heads=10, kv_heads=2, dim=256, vocab=4096, requests=4,
-                 max_len=2048, page=64, kind="int8", window=0, seed=0):
+                 max_len=2048, page=64, kind="int8", window=0, seed=0, rope_base=None):
         self.embedding = Weights(vocab, hidden, seed + 100)      # tied: gathered rows in, LM head out
         self.layers = [Layer(hidden, ffn, q_heads, kv_heads, dim, seed + 1000 * (i + 1)) for i in range(layers)]
         self.heads, self.dim, self.page, self.max_len, self.window = (q_heads, kv_heads), dim, page, max_len, window
@@ -102,6 +109,10 @@ class Stack:
         self.table = torch.full((requests, width), -1, dtype=torch.int32, device="cuda")
         self.lens = torch.zeros((requests,), dtype=torch.int32, device="cuda")
         self.held = [0] * requests                               # the same on the host
+        # with a base: queries and keys normed for each head and turned by their positions
+        self.inv_freq = None if rope_base is None else rope_base ** (-torch.arange(0, dim, 2) / dim).float().cuda()
+        self.shared = 0                                          # entries that all requests begin with
+        self.shared_len = torch.zeros((1,), dtype=torch.int32, device="cuda")
 
     def step(self, tokens, counts):
         """tokens [T]: counts[r] of each request, in request order.  (logits' argmax [T], final hidden rows [T, hidden])"""
@@ -112,13 +123,17 @@ class Stack:
         new = torch.tensor(counts, dtype=torch.int32, device="cuda")
         # where the tokens go: once for all layers
         seq, start, slots, used = w4.kv_plan(self.lens, new, self.free, self.table, tokens.numel(), self.page)
+        positions = None
+        if self.inv_freq is not None:
+            positions = torch.cat([torch.arange(n, n + c) for n, c in zip(self.held, counts)]).int().cuda()
         x = w4.gather_rows(*self.embedding, tokens).float()
         for layer, cache in zip(self.layers, self.caches):
-            q, k, v = layer.qkv(norm(x))
-            w4.w4a16_kv_append(k.view(-1, self.heads[1], self.dim), v.view(-1, self.heads[1], self.dim), slots, *cache)
-            a = w4.kv_attention(q.view(-1, self.heads[0], self.dim), *cache, self.table, seq, start, max(counts),
-                                max_len=self.max_len, window=self.window)
-            x = x + layer.o(a.view(q.shape)).float()
+            q, k, v = (t.view(t.shape[0], -1, self.dim) for t in layer.qkv(norm(x)))
+            if positions is not None:
+                w4.w4a16_qk_norm_rope(q, k, layer.q_norm, layer.k_norm, self.inv_freq, positions, q, k)
+            w4.w4a16_kv_append(k, v, slots, *cache)
+            a = self.attention(q, cache, seq, start, max(counts))
+            x = x + layer.o(a.flatten(1)).float()
             x = x + layer.mlp(norm(x)).float()
         h = norm(x)
         best = torch.cat([w4.lmhead_argmax(part, *self.embedding, want_logits=False)[0] for part in h.split(w4.MAX_M)])
@@ -130,10 +145,36 @@ class Stack:
         self.lens, self.held = seq, held
         return best, h
 
+    def attention(self, q, cache, seq, start, most):
+        rows = most * (self.heads[0] // self.heads[1])
+        if self.shared and not self.window and rows <= 64:
+            return w4.kv_attention_shared(q, *cache, self.table, seq, start, self.shared_len, most, max_shared=self.shared,
+                                          max_own=self.max_len - self.shared)
+        return w4.kv_attention(q, *cache, self.table, seq, start, most, max_len=self.max_len, window=self.window)
+
+    def share(self, tokens):
+        """All requests begin with these tokens, a whole number of pages, which are brought and held once."""
+        n = tokens.numel()
+        if any(self.held) or n % self.page or n > self.max_len:
+            raise ValueError(f"{n} tokens to share: whole pages of {self.page}, up to {self.max_len}, before any other step")
+        self.step(tokens, [n] + [0] * (len(self.held) - 1))
+        self.table[1:] = self.table[0]
+        self.lens, self.held = torch.full_like(self.lens, n), [n] * len(self.held)
+        self.shared = n
+        self.shared_len.fill_(n)
+
+    def draw(self, h, uniforms, temperature, top_k=0, top_p=1.0, min_p=0.0):
+        """Tokens drawn from the logits of final hidden rows h [R, hidden] by numbers uniforms [R] in [0, 1)."""
+        each = lambda v, dtype: torch.full(uniforms.shape, v, dtype=dtype, device="cuda")  # noqa: E731
+        return w4.sample(self.embedding(h), uniforms, each(temperature, torch.float32), each(top_k, torch.int32),
+                         each(top_p, torch.float32), each(min_p, torch.float32))[0]
+
     def keep(self, lens):
         """Keeps the first lens[r] tokens of each request: the candidates behind them were rejected."""
         if any(n > h for n, h in zip(lens, self.held)):
             raise ValueError(f"requests hold {self.held} tokens, {lens} asked to keep")
+        if min(lens) < self.shared:
+            raise ValueError(f"{lens} asked to keep of requests that share {self.shared}")
         kept = torch.tensor(lens, dtype=torch.int32, device="cuda")
         self.free = torch.cat([give_back(self.table, self.lens, kept, self.page), self.free])
         self.lens, self.held = kept, list(lens)
@@ -160,16 +201,33 @@ def main():
     ap.add_argument("--kind", choices=sorted(KINDS), default="int8")
     ap.add_argument("--steps", type=int, default=16)
     ap.add_argument("--candidates", type=int, default=3)
+    ap.add_argument("--rope-base", type=float, help="norm queries and keys and rotate positions in, with this base")
+    ap.add_argument("--share", type=int, default=0, help="tokens that all requests begin with (whole pages of 64)")
+    ap.add_argument("--temperature", type=float, default=0.0, help="draw tokens (0: take the largest logits)")
+    ap.add_argument("--top-k", type=int, default=0)
+    ap.add_argument("--top-p", type=float, default=1.0)
+    ap.add_argument("--min-p", type=float, default=0.0)
     a = ap.parse_args()
     prompts = [700, 64, 333, 5]
-    stack = Stack(layers=a.layers, kind=a.kind)
-    tokens = torch.randint(0, 4096, (sum(prompts),), dtype=torch.int32, generator=torch.Generator().manual_seed(1)).cuda()
-    best, _ = stack.step(tokens, prompts)
-    tokens = best[last_of(prompts)]
+    stack = Stack(layers=a.layers, kind=a.kind, rope_base=a.rope_base)
+    generator = torch.Generator().manual_seed(1)
+    if a.share:
+        stack.share(torch.randint(0, 4096, (a.share,), dtype=torch.int32, generator=torch.Generator().manual_seed(2)).cuda())
+    tokens = torch.randint(0, 4096, (sum(prompts),), dtype=torch.int32, generator=generator).cuda()
+
+    def choose(best, h):
+        if not a.temperature:
+            return best
+        uniforms = torch.rand((h.shape[0],), generator=generator).cuda()
+        return stack.draw(h, uniforms, a.temperature, a.top_k, a.top_p, a.min_p)
+
+    last = last_of(prompts)
+    best, h = stack.step(tokens, prompts)
+    tokens = choose(best[last], h[last])
     torch.cuda.synchronize()
     t = time.perf_counter()
     for _ in range(a.steps):
-        tokens, _ = stack.step(tokens, [1] * len(prompts))
+        tokens = choose(*stack.step(tokens, [1] * len(prompts)))
     torch.cuda.synchronize()
     ms = (time.perf_counter() - t) / a.steps * 1e3
     print(f"{a.layers} layers, {len(prompts)} requests, {a.kind} cache: {ms:.2f} ms a decode step; "
