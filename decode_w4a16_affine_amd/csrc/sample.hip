@@ -8,10 +8,11 @@
 //
 // Launches.  scan: a workgroup reads a chunk of 8192 logits into registers; its largest
 // logit, and either the sum of its weights (rows without limits) or its histogram.
-// collect: adds the row's histograms, finds the buckets lo .. hi that the limits lie in, reads
-// the logits again and lists the tokens of these buckets.  draw: a workgroup a row finds the
+// cut: a workgroup a row adds the chunks' histograms and finds the buckets lo .. hi that the
+// limits lie in.  collect: reads the logits again and lists the tokens of these buckets; where the
+// chunks are few each of its workgroups makes the cut for itself (see kCutAlone).  draw: a workgroup a row finds the
 // last kept token among the listed ones, adds the kept weights of each chunk, picks a
-// chunk and looks up the token in it.  A call without limits skips collect.  A row whose
+// chunk and looks up the token in it.  A call without limits has scan and draw alone.  A row whose
 // lists overflow (thousands of tokens of a chunk in one bucket: ties) is left to the
 // draw's workgroup, which finds the limits from the logits themselves.
 //
@@ -20,6 +21,14 @@
 // depend on the order in which atomics arrive, and the answer is always the same.
 // (fp32 would be off by 2^-24 of the larger weights at every border between the tokens,
 // of which a row has up to 2^20.)
+//
+// What bounds it.  Many rows: the scan, at the rate of its fp64 weights or of memory, whichever is
+// slower (256 rows of 262144 fp32 without limits: 64 us for 268 MB, 4.2 TB/s, and 9 for the
+// draw; 48 rows of bf16 with top_p and min_p: 15.7 for 25 MB and every weight, cut 7.0,
+// collect 9.4, draw 19).  One row: the latency of the stages behind each other, each with two or
+// three trips to memory (262144 fp32, top_k and top_p: scan 4.0, collect with its cut 9.8, draw 8.8).
+// A draw's workgroup has a CU to itself and is bound by its own instructions: what one wave can do
+// it does alone, 11 us before instead of 8.8, and 25 instead of 19 for the 48.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -35,8 +44,6 @@ namespace {
 
 constexpr int kSampleThreads = 1024;
 constexpr int kSampleWaves = kSampleThreads / kWave;
-constexpr int kSampleSub = 1024;      // tokens whose weights are summed together before the draw
-constexpr int kSampleSubs = W4A16_SAMPLE_MAX_N / kSampleSub;
 constexpr int kSampleBins = 2048;
 constexpr int kScanThreads = 512;
 constexpr int kScanWaves = kScanThreads / kWave;
@@ -45,6 +52,9 @@ constexpr int kChunk = kScanThreads * kLane;          // and a workgroup
 constexpr int kChunks = W4A16_SAMPLE_MAX_N / kChunk;
 constexpr int kBuckets = 256;
 constexpr float kBucketsPerUnit = 12.0f;              // of (logit / temperature)
+// Up to a workgroup for each CU collect makes the cut itself, side by side, and a launch is saved (8 rows of 262144
+// with top_k and top_p 33.3 us in a graph, with a cut of its own 34.6; 16 rows 38.0 and 37.9, 24 43.6 and 41.5).
+constexpr int kCutAlone = 256;
 constexpr int kListed = 1024;                         // tokens of a chunk that are listed at most
 constexpr int kSmallK = 512;                          // limits of so few tokens need no weights from the scan
 constexpr int kCutScale = 42;                         // sums of a row's buckets (2^20 weights below 2^63)
@@ -57,7 +67,6 @@ constexpr int kSorted = 1024;                         // listed tokens that are 
 constexpr int kHeld = 8;                              // listed tokens that a thread of the draw holds
 static_assert(kChunk == 1 << (62 - kChunkScale) && kChunk <= 1 << (kBinCount - kBinScale - 1), "sums fit");
 static_assert(kChunks <= kSampleThreads && kBuckets <= kScanThreads && kSorted == kSampleThreads, "a thread each");
-static_assert(kSampleSub == kSampleThreads && kSampleSubs <= kSampleThreads, "one thread a token, or a piece");
 
 struct SampleArgs {
   const void* logits;
@@ -142,7 +151,7 @@ __device__ __forceinline__ double sample_log_weight(float v, float top, double i
 // 2^t times 2^scale for t <= 0, below 2^-1000 as there.  2^t = 2^n 2^f with |f| <= 1/2, the latter as 1 + f q(f), q the
 // polynomial through (2^f - 1) / f at the nine Chebyshev points: off by 2^-44.6 of it.  n appears in the low bits
 // of a sum with 1.5 * 2^52 and is added to the exponent's: conversions to and from fp64, rint and ldexp take four
-// times as long as a sum (256 tempered rows of 262144: @@ us with them instead of @@).
+// times as long as a sum (256 tempered rows of 262144: 70 us with them, 64 without).
 __device__ __forceinline__ double sample_exp2(double t, int scale) {
   t = fmax(t, -1000.0);
   const double shifted = t + 0x1.8p52, f = t - (shifted - 0x1.8p52);
@@ -238,70 +247,77 @@ __device__ __forceinline__ void sample_load_chunk(const T* row, int chunk, int N
 
 // A wave's running sums: rows of 16 lanes by shifts within them, then their last lanes' to the rows behind.
 template <int CTRL, int ROWS>
-__device__ __forceinline__ uint64_t sample_from_lane(uint64_t v) {
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xF, false);
-  return (uint64_t)hi << 32 | lo;
+__device__ __forceinline__ uint32_t sample_from_lane(uint32_t v) {
+  // (of lanes that have no source, or are not of ROWS, 0)
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, ROWS == 0xF);
 }
-__device__ __forceinline__ uint64_t sample_wave_scan(uint64_t v) {
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t sample_from_lane(uint64_t v) {
+  return (uint64_t)sample_from_lane<CTRL, ROWS>((uint32_t)(v >> 32)) << 32 | sample_from_lane<CTRL, ROWS>((uint32_t)v);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double sample_from_lane(double v) {
+  return __longlong_as_double((long long)sample_from_lane<CTRL, ROWS>((uint64_t)__double_as_longlong(v)));
+}
+template <class V>
+__device__ __forceinline__ V sample_row_scan(V v) {
   v += sample_from_lane<0x111, 0xF>(v);
   v += sample_from_lane<0x112, 0xF>(v);
   v += sample_from_lane<0x114, 0xF>(v);
   v += sample_from_lane<0x118, 0xF>(v);
+  return v;
+}
+template <class V>
+__device__ __forceinline__ V sample_wave_scan(V v) {
+  v = sample_row_scan(v);
   v += sample_from_lane<0x142, 0xA>(v);      // lane 15 to the second row, lane 47 to the fourth
   v += sample_from_lane<0x143, 0xC>(v);      // lane 31 to the upper half
   return v;
 }
+__device__ __forceinline__ uint32_t sample_of_lane(uint32_t v, int lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+__device__ __forceinline__ uint64_t sample_of_lane(uint64_t v, int lane) {
+  return (uint64_t)sample_of_lane((uint32_t)(v >> 32), lane) << 32 | sample_of_lane((uint32_t)v, lane);
+}
 // A wave's sum, in a fixed order.
 __device__ __forceinline__ double sample_wave_sum(double v) {
-  auto from = [&](auto ctrl, auto rows) {
-    return __longlong_as_double((long long)sample_from_lane<decltype(ctrl)::value, decltype(rows)::value>(
-        (uint64_t)__double_as_longlong(v)));
-  };
-  using std::integral_constant;
-  integral_constant<int, 0xF> all;
-  v += from(integral_constant<int, 0x111>{}, all);
-  v += from(integral_constant<int, 0x112>{}, all);
-  v += from(integral_constant<int, 0x114>{}, all);
-  v += from(integral_constant<int, 0x118>{}, all);
-  v += from(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});
-  v += from(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});
-  const uint64_t u = (uint64_t)__double_as_longlong(v);
-  return __longlong_as_double((long long)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), kWave - 1) << 32 |
-                                          (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, kWave - 1)));
-}
-// Sums over the block's threads.  Values of threads before this one, and of all (returned).
-template <int WAVES>
-__device__ __forceinline__ uint64_t sample_scan(uint64_t v, uint64_t& before, uint64_t (&s_waves)[WAVES]) {
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const uint64_t sum = sample_wave_scan(v);
-  __syncthreads();      // (s_waves may still be read from a scan before)
-  if (lane == kWave - 1) s_waves[wave] = sum;
-  __syncthreads();
-  // each row of lanes scans the waves' sums
-  static_assert(WAVES <= 16, "a lane of a row each");
-  uint64_t upto = (lane & 15) < WAVES ? s_waves[lane & 15] : 0;
-  upto += sample_from_lane<0x111, 0xF>(upto);
-  upto += sample_from_lane<0x112, 0xF>(upto);
-  upto += sample_from_lane<0x114, 0xF>(upto);
-  upto += sample_from_lane<0x118, 0xF>(upto);
-  auto of_wave = [&](int w) {
-    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(upto >> 32), w) << 32 |
-           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)upto, w);
-  };
-  const int w = __builtin_amdgcn_readfirstlane(wave);
-  before = (w ? of_wave(w - 1) : 0) + sum - v;
-  return of_wave(WAVES - 1);
+  return __longlong_as_double((long long)sample_of_lane((uint64_t)__double_as_longlong(sample_wave_scan(v)), kWave - 1));
 }
 
+// What a row's workgroup of the draw shares.
 struct SampleShared {
   uint64_t bins[kSampleBins];
   uint64_t waves[kSampleWaves];
   uint64_t found[2];
   uint32_t few;
-  uint64_t chunk[kChunks];      // kept weights
-  uint32_t listed[kChunks], place[kChunks];
+  uint64_t chunk[2 * kWave];      // kept weights
+  uint32_t listed[2 * kWave], place[2 * kWave];
+  // what its first wave makes of the row, so that others do not: sixteen waves on four SIMDs take
+  // sixteen cycles for an instruction, one takes four
+  float top, top_p;
+  double inv_t, least;
+  int special, limited, overflow, alone, k, sure, picked;
+  uint64_t base, total, all;
+  uint32_t all_listed;
 };
+
+// Sums over the block's first `waves` waves (the others only wait): of threads before this one, and of all.
+__device__ __forceinline__ uint64_t sample_scan(uint64_t v, uint64_t& before, int waves, SampleShared& sh) {
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  __syncthreads();      // (sh.waves may still be read from a scan before)
+  uint64_t sum = 0;
+  if (wave < waves) {
+    sum = sample_wave_scan(v);
+    if (lane == kWave - 1) sh.waves[wave] = sum;
+  }
+  __syncthreads();
+  // each row of lanes scans the waves' sums
+  static_assert(kSampleWaves == 16, "a lane of a row each");
+  const uint64_t upto = sample_row_scan((lane & 15) < waves ? sh.waves[lane & 15] : (uint64_t)0);
+  before = (wave ? sample_of_lane(upto, wave - 1) : 0) + sum - v;
+  return sample_of_lane(upto, 15);
+}
 
 // The number that lane i ^ J holds, without a way through LDS.
 template <int J>
@@ -370,25 +386,14 @@ __device__ __forceinline__ uint64_t sample_sort(uint64_t c, int n, uint64_t* s_s
 }
 
 // The first C (in order) at which the running sum of `measure` reaches target, 1 <=
-// target <= the sum over all.  visit(f) calls f(C, measure) for the thread's tokens, at(C) is
-// its measure again.  Bins over the range of the tokens' C tell which of them has it; a bin
-// of few tokens is sorted, another one is divided again.
+// target <= the sum over all, of tokens in lo .. hi.  visit(f) calls f(C, measure) for the
+// thread's tokens, measure_of(C) is its measure again.  Bins over lo .. hi tell which of them has it;
+// a bin of few tokens is sorted, another one is divided again.
 template <class Visit, class Measure>
-__device__ __forceinline__ uint64_t sample_select(Visit&& visit, Measure&& measure_of, uint64_t target, SampleShared& sh) {
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  uint64_t lo = ~0ull, hi = 0;
-  visit([&](uint64_t c, uint64_t) W4K_INLINE {
-    lo = c < lo ? c : lo;
-    hi = c > hi ? c : hi;
-  });
-  lo = sample_wave_least<32>(lo), hi = ~sample_wave_least<32>(~hi);
-  __syncthreads();
-  if (lane == 0) sh.bins[wave] = lo, sh.bins[kSampleWaves + wave] = hi;
-  __syncthreads();
-  for (int w = 0; w < kSampleWaves; ++w) {
-    lo = sh.bins[w] < lo ? sh.bins[w] : lo;
-    hi = sh.bins[kSampleWaves + w] > hi ? sh.bins[kSampleWaves + w] : hi;
-  }
+__device__ __forceinline__ uint64_t sample_select(Visit&& visit, Measure&& measure_of, uint64_t target, uint64_t lo,
+                                                  uint64_t hi, SampleShared& sh) {
+  constexpr int SCAN = 4, EACH = kSampleBins / (SCAN * kWave);      // waves that scan the bins, bins a thread
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   uint64_t base = 0;      // the sum in front of lo
   for (;;) {
     const uint64_t range = hi - lo;
@@ -402,14 +407,16 @@ __device__ __forceinline__ uint64_t sample_select(Visit&& visit, Measure&& measu
       if (c >= lo && c <= hi) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[(c - lo) >> shift]), measure);
     });
     __syncthreads();
-    const uint64_t v0 = sh.bins[2 * tid], v1 = sh.bins[2 * tid + 1];
-    uint64_t before;
-    sample_scan(v0 + v1, before, sh.waves);
+    uint64_t sum = 0, before;
+    if (wave < SCAN)
+      for (int i = 0; i < EACH; ++i) sum += sh.bins[EACH * tid + i];
+    sample_scan(sum, before, SCAN, sh);
     before += base;
-    if (before < target && before + v0 + v1 >= target) {      // one thread's
-      const bool second = before + v0 < target;
-      sh.found[0] = 2 * tid + second;
-      sh.found[1] = before + (second ? v0 : 0);
+    if (wave < SCAN && before < target && before + sum >= target) {      // one thread's
+      int at = EACH * tid;
+      while (before + sh.bins[at] < target) before += sh.bins[at++];
+      sh.found[0] = at;
+      sh.found[1] = before;
     }
     __syncthreads();
     lo += sh.found[0] << shift;
@@ -429,9 +436,9 @@ __device__ __forceinline__ uint64_t sample_select(Visit&& visit, Measure&& measu
     while (threads < n) threads <<= 1;
     const uint64_t c = sample_sort(tid < n ? sh.bins[tid] : ~0ull, threads, sh.bins + kSampleThreads);
     const uint64_t m = tid < n ? measure_of(c) : 0;
-    sample_scan(m, before, sh.waves);
+    sample_scan(m, before, threads / kWave, sh);
     before += base;
-    if (before < target && before + m >= target) sh.found[0] = c;
+    if (m && before < target && before + m >= target) sh.found[0] = c;
     __syncthreads();
     return sh.found[0];
   }
@@ -513,7 +520,7 @@ __global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs
     }
   };
   // Without limits a wave takes its own largest logit: it computes while others wait for their logits
-  // (all of them behind one barrier, the two times added up: 256 rows of 262144 71 us instead of @@).
+  // (behind one barrier for all, the loads' time and the sums' add up: 256 rows of 262144 71.5 us, else 70.2).
   const bool limited = sample_limited(p);
   if (!p.greedy && !limited) {
     double sum = 0.0;
@@ -650,7 +657,7 @@ __device__ __forceinline__ SampleCut sample_find_cut(const SampleArgs& a, int r,
     auto in_units = [&](double m) { return (uint64_t)__builtin_rint(__builtin_ldexp(m, kCutScale)); };
     units = sample_wave_scan(in_units(mass + s_part[b]));
     const uint64_t units_behind = sample_wave_scan(in_units(behind + s_part[kBuckets + b]));
-    counted = sample_wave_scan(count + sh.count[b]);
+    counted = sample_wave_scan((uint64_t)(count + sh.count[b]));
     if (lane == kWave - 1) sh.waves[0][wave] = units, sh.waves[1][wave] = counted, sh.waves[2][wave] = units_behind;
   }
   __syncthreads();
@@ -759,7 +766,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_collect_kernel(SampleArgs
     mine |= (below >= cut.lo && below <= cut.hi && sample_token<T>(chunk, x) < a.N ? 1u : 0u) << x;
   }
   if (__any(mine)) {
-    const uint32_t count = __builtin_popcount(mine), upto = (uint32_t)sample_wave_scan(count);
+    const uint32_t count = __builtin_popcount(mine), upto = sample_wave_scan(count);
     uint32_t slot = 0;
     if (lane == kWave - 1) slot = atomicAdd(&s_listed, upto);
     slot = (uint32_t)__builtin_amdgcn_readlane((int)slot, kWave - 1) + upto - count;
@@ -792,42 +799,104 @@ __global__ __launch_bounds__(kScanThreads) void sample_collect_kernel(SampleArgs
 // ---------------------------------------------------------------------------
 // draw
 // ---------------------------------------------------------------------------
+// What the launches before left of a row, in its workgroup's first wave.
+__device__ __forceinline__ void sample_begin(const SampleArgs& a, int r, SampleShared& sh) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const size_t at0 = (size_t)r * a.chunks;
+  // all loads at once: what is read one after the other costs a microsecond or two each
+  const SampleTops tops = sample_tops(a, r);
+  double mass[2];
+  uint32_t listed[2];
+  uint64_t kept[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const size_t c = at0 + min(lane + i * kWave, a.chunks - 1);
+    mass[i] = a.mass[c];
+    listed[i] = a.listed[c];
+    kept[i] = a.kept[c];
+  }
+  const SampleCut cut = a.cut[r];
+  const SampleRow p = sample_row(a, r);
+  const float top = sample_row_top(tops);
+  const bool special = p.greedy || !(top > -__builtin_inff()), limited = sample_limited(p);
+  if (special) {
+    // the first chunk that has a NaN, or the largest
+    int chunk = 0;
+#pragma unroll
+    for (int i = 1; i >= 0; --i) {
+      const float t = tops.top[i];
+      const uint64_t has = __ballot(lane + i * kWave < a.chunks && (top != top ? t != t : t == top));
+      if (has) chunk = i * kWave + __builtin_ctzll(has);
+    }
+    if (lane == 0) sh.picked = chunk, sh.few = ~0u;
+  } else if (!limited) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = lane + i * kWave;
+      const bool some = c < a.chunks && tops.top[i] > -__builtin_inff();
+      sh.chunk[c] = some ? (uint64_t)__builtin_rint(mass[i] * sample_weight(tops.top[i], top, p.inv_t, a.log2_scale)) : 0;
+    }
+  } else {
+    // (lists that a thread cannot hold its part of are left, and the row's logits are read instead)
+    bool over = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (lane + i * kWave >= a.chunks) listed[i] = 0, kept[i] = 0;
+      over |= listed[i] > (uint32_t)min(kListed, a.list_threads * kHeld);
+    }
+    const bool overflow = __any(over);
+    uint64_t base = 0;
+    uint32_t all = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = lane + i * kWave;
+      if (overflow || sample_few(p)) kept[i] = 0;
+      sh.chunk[c] = kept[i], sh.listed[c] = listed[i];
+      base += sample_of_lane(sample_wave_scan(kept[i]), kWave - 1);
+      const uint32_t upto = sample_wave_scan(listed[i]);
+      sh.place[c] = all + upto - listed[i];
+      all += sample_of_lane(upto, kWave - 1);
+    }
+    if (lane == 0) {
+      sh.base = base, sh.all_listed = all, sh.total = cut.total;
+      sh.overflow = overflow;
+      sh.alone = !overflow && cut.min_p_alone;
+      sh.k = p.k ? p.k - (overflow ? 0 : cut.before) : 0;
+      sh.sure = overflow ? 0 : cut.lo;
+      sh.top_p = p.top_p;
+      sh.least = p.min_p > 0.0f ? log((double)p.min_p) : -__builtin_inf();
+    }
+  }
+  if (lane == 0) {
+    sh.top = top, sh.inv_t = p.inv_t;
+    sh.special = special, sh.limited = limited;
+  }
+}
+
 template <class T>
 __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs a) {
   __shared__ SampleShared sh;
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const T* const row = static_cast<const T*>(a.logits) + r * a.stride;
   const size_t at0 = (size_t)r * a.chunks;
-  // What the launches before left, all at once: what is read one after the other costs a
-  // microsecond or two each.  `threads` threads a chunk for its listed tokens.
-  const SampleTops tops = sample_tops(a, r);
-  const int mine = min(tid, a.chunks - 1);
+  // `threads` threads a chunk for its listed tokens; the first of each is on its way from the start
   const int threads = a.list_threads;
   const int list_chunk = tid / threads, list_at = tid & (threads - 1);
-  const float mine_top = a.top[at0 + mine];
-  const double mine_mass = a.mass[at0 + mine];
-  uint32_t mine_listed = a.listed[at0 + mine];
-  uint64_t mine_kept = a.kept[at0 + mine];
-  const SampleCut cut = a.cut[r];
-  const float u = a.uniforms ? a.uniforms[r] : 0.0f;
   const uint2* const list = a.list + (at0 + min(list_chunk, a.chunks - 1)) * kListed + list_at;
   const uint2 first_entry = *list;
-  const SampleRow p = sample_row(a, r);
-  const float top = sample_row_top(tops);
-  if (p.greedy || !(top > -__builtin_inff())) {
-    // the first NaN, or the first of the largest: of the first chunk that has one
-    auto is = [&](float v) { return top != top ? v != v : v == top; };
-    if (tid == 0) sh.few = ~0u;
-    __syncthreads();
-    if (tid < a.chunks && is(mine_top)) atomicMin(&sh.few, (uint32_t)tid);
-    __syncthreads();
-    const int chunk = (int)min(sh.few, (uint32_t)a.chunks - 1);
-    __syncthreads();
-    if (tid == 0) sh.few = ~0u;
-    __syncthreads();
+  const float u = a.uniforms ? a.uniforms[r] : 0.0f;
+  if (wave == 0) sample_begin(a, r, sh);
+  __syncthreads();
+  const float top = sh.top;
+  const double inv_t = sh.inv_t;
+  if (sh.special) {
+    const int chunk = sh.picked;
     uint32_t at = ~0u;
-    for (int i = kChunk * chunk + tid; i < min(kChunk * (chunk + 1), a.N); i += kSampleThreads)
-      if (is(sample_load(row + i))) at = min(at, (uint32_t)i);
+    for (int i = kChunk * chunk + tid; i < min(kChunk * (chunk + 1), a.N); i += kSampleThreads) {
+      const float v = sample_load(row + i);
+      if (top != top ? v != v : v == top) at = min(at, (uint32_t)i);
+    }
     if (at != ~0u) atomicMin(&sh.few, at);
     __syncthreads();
     if (tid == 0) {
@@ -836,32 +905,23 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
     }
     return;
   }
-  auto weight = [&](float v) { return (uint64_t)__builtin_rint(sample_weight(v, top, p.inv_t, a.log2_scale)); };
+  auto weight = [&](float v) { return (uint64_t)__builtin_rint(sample_weight(v, top, inv_t, a.log2_scale)); };
   auto weight_of = [&](uint64_t c) { return weight(sample_logit(c)); };
-  uint64_t last = ~0ull;      // the last C that top_k and top_p keep
-  int sure = kBuckets;        // buckets in front of it are kept whole
-  const double least = p.min_p > 0.0f ? log((double)p.min_p) : -__builtin_inf();
-  const float scale = sample_bucket_scale(p.inv_t);
-  const int top_bucket = sample_bucket(top, scale);
+  const bool limited = sh.limited;
+  uint64_t last = ~0ull;      // the last C that is kept (0: no listed token is)
+  bool check_min_p = false;   // (but for min_p)
+  int sure = 0;               // buckets in front of it are kept whole
+  double least = 0.0;
   uint64_t before;
-  if (!sample_limited(p)) {
-    if (tid < a.chunks)
-      sh.chunk[tid] = mine_top > -__builtin_inff()
-                          ? (uint64_t)__builtin_rint(mine_mass * sample_weight(mine_top, top, p.inv_t, a.log2_scale))
-                          : 0;
-    __syncthreads();
-  } else {
-    if (tid >= a.chunks || sample_few(p)) mine_kept = 0;
-    if (tid >= a.chunks) mine_listed = 0;
-    // (lists that a thread cannot hold its part of are left, and the row's logits are read instead)
-    const bool overflow = __syncthreads_or(mine_listed > (uint32_t)min(kListed, threads * kHeld));
-    sure = overflow ? 0 : cut.lo;
-    if (overflow) mine_kept = 0;
-    if (tid < a.chunks) sh.chunk[tid] = mine_kept, sh.listed[tid] = mine_listed;
-    const uint64_t base = sample_scan(mine_kept, before, sh.waves);      // (and a barrier)
-    const bool others = overflow || !cut.min_p_alone;
-    const uint64_t all_listed = sample_scan(mine_listed, before, sh.waves);
-    if (tid < a.chunks) sh.place[tid] = (uint32_t)before;
+  if (limited) {
+    const bool overflow = sh.overflow, others = !sh.alone;
+    const int k = sh.k;
+    const float top_p = sh.top_p;
+    const uint64_t base = sh.base;
+    const uint32_t all_listed = sh.all_listed;
+    least = sh.least;
+    sure = sh.sure;
+    const bool min_p = least > -__builtin_inf();
     const int count = list_chunk < a.chunks ? (int)sh.listed[list_chunk] : 0;
     uint64_t c[kHeld];
     auto order = [&](uint2 e) { return sample_order(__uint_as_float(e.x), (int)e.y); };
@@ -872,34 +932,36 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
         if (list_at + e * threads < count) c[e] = order(e ? list[e * threads] : first_entry);
       }
     }
-    sh.bins[tid] = ~0ull;
-    __syncthreads();
     if (!overflow && all_listed <= kSorted) {
       // in order: the limits are numbers of tokens
       const int n = (int)all_listed;
+      int sorted = kWave;
+      while (sorted < n) sorted <<= 1;
 #pragma unroll
       for (int e = 0; e < kHeld; ++e)
         if (c[e] != ~0ull) sh.bins[sh.place[list_chunk] + list_at + e * threads] = c[e];
       __syncthreads();
-      int sorted = kWave;
-      while (sorted < n) sorted <<= 1;
-      const uint64_t mine_c = sample_sort(sh.bins[tid], sorted, sh.bins + kSampleThreads);
-      const float v = sample_logit(mine_c);
+      const uint64_t mine = sample_sort(tid < n ? sh.bins[tid] : ~0ull, sorted, sh.bins + kSampleThreads);
       bool kept = tid < n;
-      const uint64_t w = kept ? weight(v) : 0;
-      if (p.k && others) kept = kept && tid < p.k - cut.before;
-      if (p.top_p < 1.0f && others) {
-        const uint64_t sum = sample_scan(kept ? w : 0, before, sh.waves);
-        const uint64_t all = p.k ? base + sum : cut.total;
-        kept = kept && (base + before < (uint64_t)__builtin_ceil((double)p.top_p * (double)all) || base + before == 0);
+      uint64_t w = 0;
+      if (kept) {
+        w = weight_of(mine);
+        if (min_p) kept = sample_log_weight(sample_logit(mine), top, inv_t) >= least;
+      }
+      if (k && others) kept = kept && tid < k;
+      if (top_p < 1.0f && others) {
+        // (of what top_k keeps)
+        const uint64_t sum = sample_scan(!k || tid < k ? w : 0, before, sorted / kWave, sh);
+        const uint64_t all = k ? base + sum : sh.total;
+        kept = kept && (base + before < (uint64_t)__builtin_ceil((double)top_p * (double)all) || base + before == 0);
       }
       const int keep = __syncthreads_count(kept);
-      if (tid == keep - 1) sh.found[0] = mine_c;
-      kept = kept && sample_log_weight(v, top, p.inv_t) >= least;
-      if (kept) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk[(uint32_t)mine_c / kChunk]), w);
+      if (tid == keep - 1) sh.found[0] = mine;
+      if (kept) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk[(uint32_t)mine / kChunk]), w);
       __syncthreads();
       last = keep ? sh.found[0] : 0;
     } else {
+      check_min_p = min_p;
       uint64_t w[kHeld];
       if (!overflow) {
 #pragma unroll
@@ -918,23 +980,32 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
             if (c[e] != ~0ull) f(c[e], w[e]);
         }
       };
-      bool none = false;      // no listed token is kept
-      if (p.k && others) {
-        const int64_t k = p.k - (overflow ? 0 : cut.before);
-        // (fewer are listed where top_p ends in front of the k-th)
-        if ((overflow ? (int64_t)a.N : (int64_t)all_listed) >= k)
-          last = sample_select([&](auto&& f) W4K_INLINE { visit([&](uint64_t c, uint64_t) W4K_INLINE { f(c, 1); }); },
-                               [](uint64_t) { return (uint64_t)1; }, (uint64_t)k, sh);
+      // All of them lie between the logits that bound the buckets lo .. hi, with half a bucket more at both ends
+      // (far logits share the outermost buckets: there, anywhere).
+      uint64_t lo = 0, hi = ~0ull;
+      if (!overflow) {
+        const SampleCut cut = a.cut[r];
+        const float scale = sample_bucket_scale(inv_t);
+        const int top_bucket = sample_bucket(top, scale);
+        const float high = __int_as_float(top_bucket - cut.lo) + 1.0f, low = __int_as_float(top_bucket - cut.hi) - 1.0f;
+        if (high < 0x1.fffffep23f && low > 0x1p23f && cut.hi < kBuckets - 1) {
+          lo = sample_order(fminf((high - 0x1.8p23f) / scale, top), 0);
+          hi = sample_order((low - 0x1.8p23f) / scale, -1);
+        }
       }
-      if (p.top_p < 1.0f && others) {
+      // (fewer than k are listed where top_p ends in front of the k-th)
+      if (k && others && (overflow ? (int64_t)a.N : (int64_t)all_listed) >= k)
+        last = sample_select([&](auto&& f) W4K_INLINE { visit([&](uint64_t c, uint64_t) W4K_INLINE { f(c, 1); }); },
+                             [](uint64_t) { return (uint64_t)1; }, (uint64_t)k, lo, hi, sh);
+      if (top_p < 1.0f && others) {
         const uint64_t limit = last;
         uint64_t sum = 0;
         visit([&](uint64_t c, uint64_t w) W4K_INLINE { sum += c <= limit ? w : 0; });
-        sum = sample_scan(sum, before, sh.waves);
-        const uint64_t all = p.k || overflow ? base + sum : cut.total;
-        const uint64_t target = (uint64_t)__builtin_ceil((double)p.top_p * (double)all);
+        sum = sample_scan(sum, before, kSampleWaves, sh);
+        const uint64_t all = k || overflow ? base + sum : sh.total;
+        const uint64_t target = (uint64_t)__builtin_ceil((double)top_p * (double)all);
         if (target <= base && base > 0)
-          none = true;
+          last = 0;
         else if (target - base < sum)
           last = sample_select(
               [&](auto&& f) W4K_INLINE {
@@ -942,13 +1013,12 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
                   if (c <= limit) f(c, w);
                 });
               },
-              weight_of, target > base ? target - base : 1, sh);
+              weight_of, target > base ? target - base : 1, lo, hi, sh);
       }
-      if (none) last = 0;
       // the kept weights of each chunk: a wave's together, or those of the threads that hold a chunk's list
       // (additions of one token each to few sums would wait for each other)
       auto kept_weight = [&](uint64_t c, uint64_t w) W4K_INLINE {
-        return c <= last && sample_log_weight(sample_logit(c), top, p.inv_t) >= least ? w : 0;
+        return c <= last && (!min_p || sample_log_weight(sample_logit(c), top, inv_t) >= least) ? w : 0;
       };
       auto add = [&](int chunk, uint64_t sum) W4K_INLINE {
         if (sum) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk[chunk]), sum);
@@ -976,17 +1046,24 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
     }
   }
   // the chunk: the first whose running sum exceeds u * total, that is its whole part
-  uint64_t sum = tid < a.chunks ? sh.chunk[tid] : 0;
-  const uint64_t total = sample_scan(sum, before, sh.waves);
-  const double at = (double)u * (double)total;
-  uint64_t target = at > 0.0 ? at < 9e18 ? (uint64_t)at : ~0ull : 0;
-  target = target < total ? target : total - 1;
-  if (tid == 0) sh.found[0] = 0, sh.found[1] = 0;
+  if (wave == 0) {
+    uint64_t sum[2], upto[2], total = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      sum[i] = lane + i * kWave < a.chunks ? sh.chunk[lane + i * kWave] : 0;
+      upto[i] = total + sample_wave_scan(sum[i]);
+      total = sample_of_lane(upto[i], kWave - 1);
+    }
+    const double at = (double)u * (double)total;
+    uint64_t target = at > 0.0 ? at < 9e18 ? (uint64_t)at : ~0ull : 0;
+    target = target < total ? target : total - 1;
+    if (lane == 0) sh.picked = 0, sh.found[0] = 0, sh.all = total;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (upto[i] - sum[i] <= target && upto[i] > target) sh.picked = lane + i * kWave, sh.found[0] = target - (upto[i] - sum[i]);
+  }
   __syncthreads();
-  if (before <= target && before + sum > target) sh.found[0] = tid, sh.found[1] = target - before;
-  __syncthreads();
-  const int chunk = (int)sh.found[0];
-  const uint64_t into = sh.found[1];
+  const int chunk = sh.picked;
   const float chunk_top = a.top[at0 + chunk];      // (kept, as the chunk has a kept token)
   // its tokens, eight a thread
   constexpr int V = kChunk / kSampleThreads;
@@ -994,19 +1071,28 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
   float v[V];
   sample_load_row<V <= kPiece<T> ? V : kPiece<T>>(row, i0, a.N, v);
   if constexpr (V > kPiece<T>) sample_load_row<kPiece<T>>(row, i0 + kPiece<T>, a.N, v + kPiece<T>);
-  uint64_t w[V];
-  sum = 0;
+  const float scale = sample_bucket_scale(inv_t), last_v = sample_logit(last);
+  const int top_bucket = sample_bucket(top, scale), last_i = (int)(uint32_t)last;
+  const double to_log2 = inv_t * kLog2E;
+  uint64_t w[V], sum = 0;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const bool kept = sample_limited(p) ? sample_below(top_bucket, v[e], scale) < sure ||
-                                              (sample_order(v[e], i0 + e) <= last &&
-                                               sample_log_weight(v[e], top, p.inv_t) >= least)
-                                        : true;
-    w[e] = kept ? sample_units(sample_weight(v[e], chunk_top, p.inv_t, kChunkScale)) : 0;
+    bool kept = true;
+    if (limited) {
+      // (tokens of whole buckets come in front of every listed one)
+      kept = last ? v[e] > last_v || (v[e] == last_v && i0 + e <= last_i) : sample_below(top_bucket, v[e], scale) < sure;
+      if (check_min_p)
+        kept = kept && (sample_below(top_bucket, v[e], scale) < sure || sample_log_weight(v[e], top, inv_t) >= least);
+    }
+    w[e] = 0;
+    if (kept)
+      w[e] = sample_units(chunk_top == __builtin_inff()
+                              ? v[e] == chunk_top ? __builtin_ldexp(1.0, kChunkScale) : 0.0
+                              : sample_exp2(((double)v[e] - (double)chunk_top) * to_log2, kChunkScale));
     sum += w[e];
   }
-  const uint64_t in_chunk = sample_scan(sum, before, sh.waves);
-  target = (uint64_t)fmin((double)into / sample_weight(chunk_top, top, p.inv_t, a.log2_scale - kChunkScale), 0x1p63);
+  const uint64_t in_chunk = sample_scan(sum, before, kSampleWaves, sh);
+  uint64_t target = (uint64_t)fmin((double)sh.found[0] / sample_weight(chunk_top, top, inv_t, a.log2_scale - kChunkScale), 0x1p63);
   target = target < in_chunk ? target : in_chunk - 1;
   if (before <= target && before + sum > target) {
     int e = 0;
@@ -1018,7 +1104,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
     for (int i = 1; i < V; ++i) drawn = e == i ? v[i] : drawn;
     a.tokens[r] = i0 + e;
     // (of the weight itself: a small one's integer has few digits)
-    if (a.share) a.share[r] = (float)(sample_weight(drawn, top, p.inv_t, a.log2_scale) / (double)total);
+    if (a.share) a.share[r] = (float)(sample_weight(drawn, top, inv_t, a.log2_scale) / (double)sh.all);
   }
 }
 
@@ -1072,8 +1158,7 @@ void sample_launch(SampleArgs a, void* ws, hipStream_t st) {
     sample_places(a, (uintptr_t)ws, at_once);
     const dim3 grid(a.chunks, a.M);
     hipLaunchKernelGGL(sample_scan_kernel<T>, grid, dim3(kScanThreads), 0, st, a);
-    // (a workgroup for each CU at most: they find the buckets side by side)
-    if (limits && a.chunks * a.M <= 256) {
+    if (limits && a.chunks * a.M <= kCutAlone) {
       hipLaunchKernelGGL((sample_collect_kernel<T, true>), grid, dim3(kScanThreads), 0, st, a);
     } else if (limits) {
       hipLaunchKernelGGL(sample_cut_kernel, dim3(a.M), dim3(kScanThreads), 0, st, a);
