@@ -298,7 +298,7 @@ struct SampleShared {
   float top, top_p;
   double inv_t, least;
   int special, limited, overflow, alone, k, sure, picked;
-  uint64_t base, total, all;
+  uint64_t base, total, all, left;
   uint32_t all_listed;
 };
 
@@ -1057,10 +1057,10 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
     const double at = (double)u * (double)total;
     uint64_t target = at > 0.0 ? at < 9e18 ? (uint64_t)at : ~0ull : 0;
     target = target < total ? target : total - 1;
-    if (lane == 0) sh.picked = 0, sh.found[0] = 0, sh.all = total;
+    if (lane == 0) sh.picked = 0, sh.left = 0, sh.all = total;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (upto[i] - sum[i] <= target && upto[i] > target) sh.picked = lane + i * kWave, sh.found[0] = target - (upto[i] - sum[i]);
+      if (upto[i] - sum[i] <= target && upto[i] > target) sh.picked = lane + i * kWave, sh.left = target - (upto[i] - sum[i]);
   }
   __syncthreads();
   const int chunk = sh.picked;
@@ -1092,7 +1092,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
     sum += w[e];
   }
   const uint64_t in_chunk = sample_scan(sum, before, kSampleWaves, sh);
-  uint64_t target = (uint64_t)fmin((double)sh.found[0] / sample_weight(chunk_top, top, inv_t, a.log2_scale - kChunkScale), 0x1p63);
+  uint64_t target = (uint64_t)fmin((double)sh.left / sample_weight(chunk_top, top, inv_t, a.log2_scale - kChunkScale), 0x1p63);
   target = target < in_chunk ? target : in_chunk - 1;
   if (before <= target && before + sum > target) {
     int e = 0;
