@@ -236,10 +236,12 @@ w4a16_status_t w4a16_qk_norm_rope(const uint16_t* q, int64_t q_stride, const uin
   // the card; more where they share their token's sines.  Measured (us in a graph, for at least 2048 /
   // 8192 / 16384 waves): 4099 tokens of 20 heads of 128 with three axes 10.6 / 13.6 / 16.7, 1500 of
   // 40 8.8 / 11.9 / 11.8, 11801 of 40 48.0 / 47.5 / 46.7.
+  // Shares are made even (1500 of 40: 8.2 instead of 8.8).
   const int fulls = (a.heads + kWave * 8 / dim - 1) / (kWave * 8 / dim);
   const int64_t waves = (int64_t)tokens * fulls;
   a.span = waves <= kRopeFill ? 1 : (int)(waves / kRopeFill) < fulls ? (int)(waves / kRopeFill) : fulls;
   a.parts = (fulls + a.span - 1) / a.span;
+  a.span = (fulls + a.parts - 1) / a.parts;
   hipStream_t st = (hipStream_t)stream;
   switch (dim) {
     case 64: rope_launch<64>(a, flags, st); break;
