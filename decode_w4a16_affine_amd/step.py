@@ -275,6 +275,7 @@ def _logits(logits):
     if logits.dim() != 2:
         raise ValueError(f"logits must be 2-D [M, N], got {list(logits.shape)}")
     M, N = logits.shape
+    _int32("M, N", M, N)
     stride, unit = logits.stride()
     if M <= 1:
         stride = N                      # no second row: any valid stride

@@ -158,6 +158,8 @@ def test_sample_binding_refuses_bad_tensors():
             w4.w4a16_sample(x, f, None, None, None, None, tokens, share, ws)
     with pytest.raises(ValueError):
         w4.w4a16_sample_workspace_bytes(2 ** 33, 5)
+    with pytest.raises(ValueError, match="32 bits"):      # (its low 32 bits would be no rows)
+        w4.sample(torch.empty((2 ** 32, 0)))
 
 
 def test_sample_definition_by_hand():
