@@ -43,8 +43,8 @@ extern "C" {
  * sum to rot / 2, in order; NULL with one axis).
  *   q_weight, k_weight  bf16 [D];  inv_freq  fp32 [rot / 2];  positions  int32 [axes][T]
  * Squares are summed, factors applied and pairs turned in fp32; an angle is reduced to one
- * turn in fp64, exact to 2^-24 of a turn for every int32 position; one rounding to bf16
- * at the end.  H 0 (a layer that reads another's keys) and HQ 0 are allowed, as is rot 0
+ * turn in fp64, off by 2^-22 of a turn at most for every int32 position where frequencies
+ * are not above 1 (by 2^-25 for positions below 2^20); one rounding to bf16 at the end.  H 0 (a layer that reads another's keys) and HQ 0 are allowed, as is rot 0
  * (no rotation; inv_freq and positions may be NULL).
  * q_out may be q and k_out may be k (with the same stride); otherwise outputs do not
  * overlap inputs.
@@ -78,8 +78,9 @@ size_t w4a16_kv_attention_shared_workspace_bytes(int tokens, int requests, int m
  * max_new * HQ / H must not exceed 64: prompts' many rows read each entry once for many of
  * them in w4a16_kv_attention already (W4A16_ERR_UNSUPPORTED).
  * The arithmetic is w4a16_kv_attention's; the order of sums depends on the call's sizes
- * (tokens, requests, max_*) and s, never on chance.  max_shared, max_own <= 2^28; the other
- * limits and the alignment are w4a16_kv_attention's.
+ * (tokens, requests, max_*) and s, never on chance.  max_shared, max_own <= 2^28; a call whose
+ * chunks of own entries make more than 2^22 workgroups is refused (W4A16_ERR_SHAPE); the
+ * other limits and the alignment are w4a16_kv_attention's.
  */
 w4a16_status_t w4a16_kv_attention_shared(const uint16_t *q, int64_t q_stride, const w4a16_kv_cache_t *cache,
                                          const int32_t *block_table, int width, const int32_t *seq_lens,
@@ -88,7 +89,8 @@ w4a16_status_t w4a16_kv_attention_shared(const uint16_t *q, int64_t q_stride, co
                                          int max_own, int q_heads, void *workspace, size_t workspace_bytes,
                                          void *stream);
 
-/* Bytes of workspace w4a16_sample needs (0 for invalid arguments). */
+/* Bytes of workspace w4a16_sample needs (0 for invalid arguments): 10.3 KB for each 8192 logits of a row, 170 MB at most
+ * (more rows take turns). */
 size_t w4a16_sample_workspace_bytes(int M, int N);
 
 /*
