@@ -148,26 +148,27 @@ __device__ __forceinline__ float sample_logit(uint64_t c) {
 __device__ __forceinline__ double sample_log_weight(float v, float top, double inv_t) {
   return v == top ? 0.0 : ((double)v - (double)top) * inv_t;
 }
-// 2^t times 2^scale for t <= 0, below 2^-1000 as there.  2^t = 2^n 2^f with |f| <= 1/2, the latter as 1 + f q(f), q the
-// polynomial through (2^f - 1) / f at the nine Chebyshev points: off by 2^-44.6 of it.  n appears in the low bits
-// of a sum with 1.5 * 2^52 and is added to the exponent's: conversions to and from fp64, rint and ldexp take four
-// times as long as a sum (256 tempered rows of 262144: 70 us with them, 64 without).
-__device__ __forceinline__ double sample_exp2(double t, int scale) {
+typedef uint32_t sample_u32x2 __attribute__((ext_vector_type(2)));
+// (2^f - 1) / f for |f| <= 1/2: the polynomial through it at the nine Chebyshev points, which leaves 2^f off by
+// 2^-44.6 of it.
+struct SampleSeries {
+  double c[9] = {6.931471805599453e-01,  2.402265069581299e-01,  5.5504108664760424e-02,
+                 9.618129159402558e-03,  1.3333558179043112e-03, 1.5403455852453838e-04,
+                 1.525268684626772e-05, 1.3255224878668817e-06, 1.0203121063391729e-07};
+};
+// 2^t times 2^scale for t <= 0, below 2^-1000 as there.  2^t = 2^n 2^f with |f| <= 1/2.  n + scale appears in the low
+// bits of a sum with 1.5 * 2^52 and is added to the exponent's: conversions to and from fp64, rint and ldexp take
+// four times as long as a sum (256 tempered rows of 262144: 70 us with them, 64 without).
+__device__ __forceinline__ double sample_exp2(double t, int scale, const SampleSeries& series = SampleSeries{}) {
   t = fmax(t, -1000.0);
-  const double shifted = t + 0x1.8p52, f = t - (shifted - 0x1.8p52);
-  double y = 1.0203121063391729e-07;
-  y = __builtin_fma(y, f, 1.3255224878668817e-06);
-  y = __builtin_fma(y, f, 1.525268684626772e-05);
-  y = __builtin_fma(y, f, 1.5403455852453838e-04);
-  y = __builtin_fma(y, f, 1.3333558179043112e-03);
-  y = __builtin_fma(y, f, 9.618129159402558e-03);
-  y = __builtin_fma(y, f, 5.5504108664760424e-02);
-  y = __builtin_fma(y, f, 2.402265069581299e-01);
-  y = __builtin_fma(y, f, 6.931471805599453e-01);
+  const double to_int = 0x1.8p52 + (double)scale, shifted = t + to_int, f = t - (shifted - to_int);
+  double y = series.c[8];
+#pragma unroll
+  for (int i = 7; i >= 0; --i) y = __builtin_fma(y, f, series.c[i]);
   y = __builtin_fma(y, f, 1.0);
-  const uint64_t u = (uint64_t)__double_as_longlong(y);
-  const uint32_t n = (uint32_t)__double_as_longlong(shifted) + (uint32_t)scale;
-  return __longlong_as_double((long long)((uint64_t)((uint32_t)(u >> 32) + (n << 20)) << 32 | (uint32_t)u));
+  sample_u32x2 u = __builtin_bit_cast(sample_u32x2, y);
+  u[1] += (uint32_t)__double_as_longlong(shifted) << 20;
+  return __builtin_bit_cast(double, u);
 }
 constexpr double kLog2E = 1.4426950408889634074;
 // A weight times 2^log2_scale
@@ -503,18 +504,21 @@ __global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs
   // f(logit, weight times 2^scale), four at a time: more would take too many registers.  Where the
   // largest logit is moderate one fma gives the exponent, off by 2^-41 for all alike.
   const double inv_t = p.inv_t * kLog2E;
+  SampleSeries series;      // in scalar registers: otherwise each weight's instructions load them again
+#pragma unroll
+  for (double& c : series.c) asm("" : "+s"(c));
   auto weights = [&](int log2_scale, auto&& f) W4K_INLINE {
     const double away = -(double)top * inv_t;
     if (away < 4096.0 && away > -4096.0) {
 #pragma unroll
       for (int x = 0; x < kLane; ++x) {
-        f(v[x], sample_exp2(__builtin_fma((double)v[x], inv_t, away), log2_scale));
+        f(v[x], sample_exp2(__builtin_fma((double)v[x], inv_t, away), log2_scale, series));
         if (x % 4 == 3) __builtin_amdgcn_sched_barrier(0);
       }
     } else {
 #pragma unroll
       for (int x = 0; x < kLane; ++x) {
-        f(v[x], sample_weight(v[x], top, p.inv_t, log2_scale));
+        f(v[x], sample_exp2(sample_log_weight(v[x], top, p.inv_t) * kLog2E, log2_scale, series));
         if (x % 4 == 3) __builtin_amdgcn_sched_barrier(0);
       }
     }
