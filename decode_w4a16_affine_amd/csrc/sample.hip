@@ -7,12 +7,13 @@
 // only those buckets' tokens are looked at one by one.
 //
 // Launches.  scan: a workgroup reads a chunk of 8192 logits into registers; its largest
-// logit, and either the sum of its weights (rows without limits) or its histogram.
+// logit and its histogram, or (rows without limits) each wave's largest and sum of weights.
 // cut: a workgroup a row adds the chunks' histograms and finds the buckets lo .. hi that the
 // limits lie in.  collect: reads the logits again and lists the tokens of these buckets; where the
 // chunks are few each of its workgroups makes the cut for itself (see kCutAlone).  draw: a workgroup a row finds the
 // last kept token among the listed ones, adds the kept weights of each chunk, picks a
-// chunk and looks up the token in it.  A call without limits has scan and draw alone.  A row whose
+// chunk and looks up the token in it (without limits: a wave's 1024 logits).  A call without limits
+// has scan and draw alone.  A row whose
 // lists overflow (thousands of tokens of a chunk in one bucket: ties) is left to the
 // draw's workgroup, which finds the limits from the logits themselves.
 //
@@ -23,12 +24,12 @@
 // of which a row has up to 2^20.)
 //
 // What bounds it.  Many rows: the scan, at the rate of its fp64 weights or of memory, whichever is
-// slower (256 rows of 262144 fp32 without limits: 64 us for 268 MB, 4.2 TB/s, and 9 for the
-// draw; 48 rows of bf16 with top_p and min_p: 15.7 for 25 MB and every weight, cut 7.0,
-// collect 9.4, draw 19).  One row: the latency of the stages behind each other, each with two or
-// three trips to memory (262144 fp32, top_k and top_p: scan 4.0, collect with its cut 9.8, draw 8.8).
+// slower (256 rows of 262144 fp32 without limits: 57 us for 268 MB, 4.7 TB/s, and 7 for the
+// draw; of bf16 the same together 58; 48 rows of bf16 with top_p and min_p: 12.5 for 25 MB and every
+// weight, cut 7.0, collect 9.1, draw 19).  One row: the latency of the stages behind each other, each with two or
+// three trips to memory (262144 fp32, top_k and top_p: scan 4.0, collect with its cut 9.8, draw 8.6).
 // A draw's workgroup has a CU to itself and is bound by its own instructions: what one wave can do
-// it does alone, 11 us before instead of 8.8, and 25 instead of 19 for the 48.
+// it does alone, 11 us before instead of 8.6, and 25 instead of 19 for the 48.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -49,6 +50,7 @@ constexpr int kScanThreads = 512;
 constexpr int kScanWaves = kScanThreads / kWave;
 constexpr int kLane = 16;                             // logits a lane holds
 constexpr int kChunk = kScanThreads * kLane;          // and a workgroup
+constexpr int kSub = kWave * kLane;                    // a wave
 constexpr int kChunks = W4A16_SAMPLE_MAX_N / kChunk;
 constexpr int kBuckets = 256;
 constexpr float kBucketsPerUnit = 12.0f;              // of (logit / temperature)
@@ -66,7 +68,7 @@ constexpr int kBinScale = 36, kBinCount = 50;
 constexpr int kSorted = 1024;                         // listed tokens that are sorted at most
 constexpr int kHeld = 8;                              // listed tokens that a thread of the draw holds
 static_assert(kChunk == 1 << (62 - kChunkScale) && kChunk <= 1 << (kBinCount - kBinScale - 1), "sums fit");
-static_assert(kChunks <= kSampleThreads && kBuckets <= kScanThreads && kSorted == kSampleThreads, "a thread each");
+static_assert(kSub == kSampleThreads && kChunks * kScanWaves <= kSampleThreads && kBuckets <= kScanThreads && kSorted == kSampleThreads, "a thread each");
 
 struct SampleArgs {
   const void* logits;
@@ -80,9 +82,13 @@ struct SampleArgs {
   // of these rows (see sample_places)
   int chunks;
   int list_threads;    // of the draw, for each chunk's list: a power of two
+  // rows without limits: a wave's tokens of the scan (`subs` of 1024 a row)
+  int subs;
+  float* sub_top;      // [M][subs] largest logit, NaN if it has one
+  double* sub_mass;    // [M][subs] weights, of this one's
+  // others
   float* top;          // [M][chunks] largest logit of a chunk, NaN if it has one
-  double* mass;        // [M][chunks] rows without limits: weights, of a chunk's largest logit
-  uint64_t* kept;      // [M][chunks] others: weights of the buckets in front of lo, of a row's
+  uint64_t* kept;      // [M][chunks] weights of the buckets in front of lo, of a row's
   uint64_t* bins;      // [M][chunks][kBuckets] tokens and weights of a chunk's buckets, of its largest logit
   uint32_t* listed;    // [M][chunks] tokens in lo .. hi
   uint2* list;         // [M][chunks][kListed] these: logit, token
@@ -123,7 +129,9 @@ __device__ __forceinline__ SampleRow sample_row(const SampleArgs& a, int r) {
   p.greedy |= p.top_p <= 0.0f || p.min_p > 1.0f;
   return p;
 }
-__device__ __forceinline__ bool sample_limited(const SampleRow& p) { return p.k || p.top_p < 1.0f || p.min_p > 0.0f; }
+__device__ __forceinline__ bool sample_limited(const SampleRow& p) {
+  return !p.greedy && (p.k || p.top_p < 1.0f || p.min_p > 0.0f);
+}
 // Few tokens are kept at most: all in the buckets up to the k-th token's are listed, and the
 // scan counts without computing weights.
 __device__ __forceinline__ bool sample_few(const SampleRow& p) { return p.k && p.k <= kSmallK; }
@@ -298,9 +306,10 @@ struct SampleShared {
   // sixteen cycles for an instruction, one takes four
   float top, top_p;
   double inv_t, least;
-  int special, limited, overflow, alone, k, sure, picked;
+  int special, overflow, alone, k, sure, picked;
   uint64_t base, total, all, left;
   uint32_t all_listed;
+  float tops[kSampleWaves], sub_top;      // of rows without limits
 };
 
 // Sums over the block's first `waves` waves (the others only wait): of threads before this one, and of all.
@@ -484,13 +493,11 @@ template <class T>
 __global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs a) {
   __shared__ uint64_t s_bins[kBuckets];
   __shared__ float s_top[kScanWaves];
-  __shared__ double s_sum[kScanWaves];
   const int chunk = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const T* const row = static_cast<const T*>(a.logits) + r * a.stride;
   float v[kLane];
   sample_load_chunk(row, chunk, a.N, v);
   const SampleRow p = sample_row(a, r);
-  if (tid < kBuckets) s_bins[tid] = 0;
   const size_t at = (size_t)r * a.chunks + chunk;
   // the largest logit (fmaxf leaves NaN out)
   float top = -__builtin_inff();
@@ -518,25 +525,32 @@ __global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs
     } else {
 #pragma unroll
       for (int x = 0; x < kLane; ++x) {
-        f(v[x], sample_exp2(sample_log_weight(v[x], top, p.inv_t) * kLog2E, log2_scale, series));
+        float y = v[x];
+        asm("" : "+v"(y));      // (both sides' conversions in front of the branch would take all registers)
+        f(y, sample_exp2(sample_log_weight(y, top, p.inv_t) * kLog2E, log2_scale, series));
         if (x % 4 == 3) __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
-  // Without limits a wave takes its own largest logit: it computes while others wait for their logits
-  // (behind one barrier for all, the loads' time and the sums' add up: 256 rows of 262144 71.5 us, else 70.2).
-  const bool limited = sample_limited(p);
-  if (!p.greedy && !limited) {
+  // Without limits every wave is for itself: it computes while others wait for their logits, and nothing waits
+  // for the last of them (256 rows of 262144: 57 us, with a chunk's sums behind a barrier 65).
+  if (!sample_limited(p)) {
     double sum = 0.0;
-    if (top > -__builtin_inff()) weights(0, [&](float, double w) W4K_INLINE { sum += w; });
+    if (!p.greedy && top > -__builtin_inff()) weights(0, [&](float, double w) W4K_INLINE { sum += w; });
     sum = sample_wave_sum(sum);
-    if (lane == 0) s_sum[wave] = sum;
+    nan = __any(nan);
+    if (lane == 0) {
+      a.sub_top[at * kScanWaves + wave] = nan ? __builtin_nanf("") : top;
+      a.sub_mass[at * kScanWaves + wave] = sum;
+    }
+    return;
   }
+  if (tid < kBuckets) s_bins[tid] = 0;
   if (lane == 0) s_top[wave] = top;
   nan = __syncthreads_or(nan);
 #pragma unroll
   for (int w = 0; w < kScanWaves; ++w) top = fmaxf(top, s_top[w]);
-  if (!p.greedy && limited && !nan && top > -__builtin_inff()) {
+  if (!nan && top > -__builtin_inff()) {
     const float scale = sample_bucket_scale(p.inv_t);
     const int top_bucket = sample_bucket(top, scale);
     if (sample_few(p)) {
@@ -561,15 +575,8 @@ __global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs
       if (lane == kWave - 1 && rest) atomicAdd(reinterpret_cast<unsigned long long*>(&s_bins[kBuckets - 1]), rest);
     }
   }
-  if (limited) {
-    __syncthreads();
-    if (tid < kBuckets) a.bins[at * kBuckets + tid] = s_bins[tid];
-  } else if (wave == 0 && !p.greedy) {
-    const float t = s_top[lane % kScanWaves];
-    double sum = lane < kScanWaves && t > -__builtin_inff() ? s_sum[lane] * sample_weight(t, top, p.inv_t, 0) : 0.0;
-    sum = sample_wave_sum(sum);
-    if (lane == 0) a.mass[at] = sum;
-  }
+  __syncthreads();
+  if (tid < kBuckets) a.bins[at * kBuckets + tid] = s_bins[tid];
   if (tid == 0) a.top[at] = nan ? __builtin_nanf("") : top;
 }
 
@@ -721,7 +728,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_cut_kernel(SampleArgs a) 
   SampleCutLoads l;
   sample_cut_load(a, r, 0, l);
   const SampleRow p = sample_row(a, r);
-  if (p.greedy || !sample_limited(p)) return;
+  if (!sample_limited(p)) return;
   const float top = sample_row_top(tops);
   if (!(top > -__builtin_inff())) return;
   const SampleCut cut = sample_find_cut(a, r, p, tops, top, l, sh);
@@ -751,7 +758,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_collect_kernel(SampleArgs
   float v[kLane];
   sample_load_chunk(row, chunk, a.N, v);
   const SampleRow p = sample_row(a, r);
-  if (p.greedy || !sample_limited(p)) return;
+  if (!sample_limited(p)) return;
   const float top = sample_row_top(tops);
   if (!(top > -__builtin_inff())) return;
   if (tid == 0) s_listed = 0;
@@ -809,37 +816,27 @@ __device__ __forceinline__ void sample_begin(const SampleArgs& a, int r, SampleS
   const size_t at0 = (size_t)r * a.chunks;
   // all loads at once: what is read one after the other costs a microsecond or two each
   const SampleTops tops = sample_tops(a, r);
-  double mass[2];
   uint32_t listed[2];
   uint64_t kept[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const size_t c = at0 + min(lane + i * kWave, a.chunks - 1);
-    mass[i] = a.mass[c];
     listed[i] = a.listed[c];
     kept[i] = a.kept[c];
   }
   const SampleCut cut = a.cut[r];
   const SampleRow p = sample_row(a, r);
   const float top = sample_row_top(tops);
-  const bool special = p.greedy || !(top > -__builtin_inff()), limited = sample_limited(p);
+  const bool special = !(top > -__builtin_inff());
   if (special) {
-    // the first chunk that has a NaN, or the largest
+    // the first chunk that has a NaN
     int chunk = 0;
 #pragma unroll
     for (int i = 1; i >= 0; --i) {
-      const float t = tops.top[i];
-      const uint64_t has = __ballot(lane + i * kWave < a.chunks && (top != top ? t != t : t == top));
+      const uint64_t has = __ballot(lane + i * kWave < a.chunks && tops.top[i] != tops.top[i]);
       if (has) chunk = i * kWave + __builtin_ctzll(has);
     }
     if (lane == 0) sh.picked = chunk, sh.few = ~0u;
-  } else if (!limited) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = lane + i * kWave;
-      const bool some = c < a.chunks && tops.top[i] > -__builtin_inff();
-      sh.chunk[c] = some ? (uint64_t)__builtin_rint(mass[i] * sample_weight(tops.top[i], top, p.inv_t, a.log2_scale)) : 0;
-    }
   } else {
     // (lists that a thread cannot hold its part of are left, and the row's logits are read instead)
     bool over = false;
@@ -873,7 +870,71 @@ __device__ __forceinline__ void sample_begin(const SampleArgs& a, int r, SampleS
   }
   if (lane == 0) {
     sh.top = top, sh.inv_t = p.inv_t;
-    sh.special = special, sh.limited = limited;
+    sh.special = special;
+  }
+}
+
+// The token that has the rest of a target behind the tokens before it, of a piece of weights 2^-kChunkScale of its
+// largest logit's.
+__device__ __forceinline__ uint64_t sample_rest(uint64_t left, float piece_top, float top, double inv_t, int log2_scale,
+                                                uint64_t in_piece) {
+  const uint64_t target =
+      (uint64_t)fmin((double)left / sample_weight(piece_top, top, inv_t, log2_scale - kChunkScale), 0x1p63);
+  return target < in_piece ? target : in_piece - 1;
+}
+__device__ __forceinline__ double sample_piece_weight(float v, float piece_top, double to_log2) {
+  return piece_top == __builtin_inff() ? v == piece_top ? __builtin_ldexp(1.0, kChunkScale) : 0.0
+                                       : sample_exp2(((double)v - (double)piece_top) * to_log2, kChunkScale);
+}
+// Of the sum of weights the part in front of the drawn token: floor(u * total).
+__device__ __forceinline__ uint64_t sample_target(float u, uint64_t total) {
+  const double at = (double)u * (double)total;
+  const uint64_t target = at > 0.0 ? at < 9e18 ? (uint64_t)at : ~0ull : 0;
+  return target < total ? target : total - 1;
+}
+
+// A row without limits, or its largest logit.
+template <class T>
+__device__ __forceinline__ void sample_draw_free(const SampleArgs& a, int r, const SampleRow& p, const T* row, float u,
+                                                 float sub_top, double sub_mass, SampleShared& sh) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const float most = sample_wave_max(sub_top);
+  if (lane == 0) sh.tops[wave] = most;
+  if (tid == 0) sh.few = ~0u, sh.picked = kSampleThreads;
+  const bool nan = __syncthreads_or(sub_top != sub_top);
+  const float top = nan ? __builtin_nanf("") : sample_wave_max(sh.tops[lane % kSampleWaves]);
+  if (p.greedy || !(top > -__builtin_inff())) {
+    const uint64_t has = __ballot(nan ? sub_top != sub_top : sub_top == top);
+    if (has && lane == 0) atomicMin(&sh.picked, wave * kWave + __builtin_ctzll(has));
+    __syncthreads();
+    const int i = sh.picked * kSub + tid;
+    const float v = i < a.N ? sample_load(row + i) : -__builtin_inff();
+    const uint64_t here = __ballot(i < a.N && (nan ? v != v : v == top));
+    if (here && lane == 0) atomicMin(&sh.few, (uint32_t)(i + __builtin_ctzll(here)));
+    __syncthreads();
+    if (tid == 0) {
+      a.tokens[r] = top == -__builtin_inff() ? -1 : (int)sh.few;
+      if (a.share) a.share[r] = nan ? top : top == -__builtin_inff() ? 0.0f : 1.0f;
+    }
+    return;
+  }
+  const uint64_t sum = sub_top > -__builtin_inff()
+                           ? (uint64_t)__builtin_rint(sub_mass * sample_weight(sub_top, top, p.inv_t, a.log2_scale))
+                           : 0;
+  uint64_t before;
+  const uint64_t total = sample_scan(sum, before, kSampleWaves, sh), target = sample_target(u, total);
+  if (before <= target && before + sum > target) sh.picked = tid, sh.left = target - before, sh.sub_top = sub_top;
+  __syncthreads();
+  const int i = sh.picked * kSub + tid;
+  const float piece_top = sh.sub_top;
+  const float v = i < a.N ? sample_load(row + i) : -__builtin_inff();
+  const uint64_t w = sample_units(sample_piece_weight(v, piece_top, p.inv_t * kLog2E));
+  const uint64_t in_piece = sample_scan(w, before, kSampleWaves, sh);
+  const uint64_t rest = sample_rest(sh.left, piece_top, top, p.inv_t, a.log2_scale, in_piece);
+  if (before <= rest && before + w > rest) {
+    a.tokens[r] = i;
+    // (of the weight itself: a small one's integer has few digits)
+    if (a.share) a.share[r] = (float)(sample_weight(v, top, p.inv_t, a.log2_scale) / (double)total);
   }
 }
 
@@ -889,165 +950,172 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
   const int list_chunk = tid / threads, list_at = tid & (threads - 1);
   const uint2* const list = a.list + (at0 + min(list_chunk, a.chunks - 1)) * kListed + list_at;
   const uint2 first_entry = *list;
+  const size_t sub = (size_t)r * a.subs + min(tid, a.subs - 1);
+  const float sub_top = a.sub_top[sub];
+  const double sub_mass = a.sub_mass[sub];
   const float u = a.uniforms ? a.uniforms[r] : 0.0f;
+  if (const SampleRow p = sample_row(a, r); !sample_limited(p)) {
+    sample_draw_free(a, r, p, row, u, tid < a.subs ? sub_top : -__builtin_inff(), sub_mass, sh);
+    return;
+  }
   if (wave == 0) sample_begin(a, r, sh);
   __syncthreads();
   const float top = sh.top;
   const double inv_t = sh.inv_t;
   if (sh.special) {
-    const int chunk = sh.picked;
+    const bool none = top == -__builtin_inff();
     uint32_t at = ~0u;
-    for (int i = kChunk * chunk + tid; i < min(kChunk * (chunk + 1), a.N); i += kSampleThreads) {
-      const float v = sample_load(row + i);
-      if (top != top ? v != v : v == top) at = min(at, (uint32_t)i);
+    if (!none) {
+      const int chunk = sh.picked;
+      for (int i = kChunk * chunk + tid; i < min(kChunk * (chunk + 1), a.N); i += kSampleThreads) {
+        const float v = sample_load(row + i);
+        if (v != v) at = min(at, (uint32_t)i);
+      }
     }
     if (at != ~0u) atomicMin(&sh.few, at);
     __syncthreads();
     if (tid == 0) {
-      a.tokens[r] = top == -__builtin_inff() ? -1 : (int)sh.few;
-      if (a.share) a.share[r] = top != top ? top : top == -__builtin_inff() ? 0.0f : 1.0f;
+      a.tokens[r] = none ? -1 : (int)sh.few;
+      if (a.share) a.share[r] = none ? 0.0f : top;
     }
     return;
   }
   auto weight = [&](float v) { return (uint64_t)__builtin_rint(sample_weight(v, top, inv_t, a.log2_scale)); };
   auto weight_of = [&](uint64_t c) { return weight(sample_logit(c)); };
-  const bool limited = sh.limited;
   uint64_t last = ~0ull;      // the last C that is kept (0: no listed token is)
   bool check_min_p = false;   // (but for min_p)
   int sure = 0;               // buckets in front of it are kept whole
   double least = 0.0;
   uint64_t before;
-  if (limited) {
-    const bool overflow = sh.overflow, others = !sh.alone;
-    const int k = sh.k;
-    const float top_p = sh.top_p;
-    const uint64_t base = sh.base;
-    const uint32_t all_listed = sh.all_listed;
-    least = sh.least;
-    sure = sh.sure;
-    const bool min_p = least > -__builtin_inf();
-    const int count = list_chunk < a.chunks ? (int)sh.listed[list_chunk] : 0;
-    uint64_t c[kHeld];
-    auto order = [&](uint2 e) { return sample_order(__uint_as_float(e.x), (int)e.y); };
+  const bool overflow = sh.overflow, others = !sh.alone;
+  const int k = sh.k;
+  const float top_p = sh.top_p;
+  const uint64_t base = sh.base;
+  const uint32_t all_listed = sh.all_listed;
+  least = sh.least;
+  sure = sh.sure;
+  const bool min_p = least > -__builtin_inf();
+  const int count = list_chunk < a.chunks ? (int)sh.listed[list_chunk] : 0;
+  uint64_t c[kHeld];
+  auto order = [&](uint2 e) { return sample_order(__uint_as_float(e.x), (int)e.y); };
+  if (!overflow) {
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) {
+      c[e] = ~0ull;
+      if (list_at + e * threads < count) c[e] = order(e ? list[e * threads] : first_entry);
+    }
+  }
+  if (!overflow && all_listed <= kSorted) {
+    // in order: the limits are numbers of tokens
+    const int n = (int)all_listed;
+    int sorted = kWave;
+    while (sorted < n) sorted <<= 1;
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e)
+      if (c[e] != ~0ull) sh.bins[sh.place[list_chunk] + list_at + e * threads] = c[e];
+    __syncthreads();
+    const uint64_t mine = sample_sort(tid < n ? sh.bins[tid] : ~0ull, sorted, sh.bins + kSampleThreads);
+    bool kept = tid < n;
+    uint64_t w = 0;
+    if (kept) {
+      w = weight_of(mine);
+      if (min_p) kept = sample_log_weight(sample_logit(mine), top, inv_t) >= least;
+    }
+    if (k && others) kept = kept && tid < k;
+    if (top_p < 1.0f && others) {
+      // (of what top_k keeps)
+      const uint64_t sum = sample_scan(!k || tid < k ? w : 0, before, sorted / kWave, sh);
+      const uint64_t all = k ? base + sum : sh.total;
+      kept = kept && (base + before < (uint64_t)__builtin_ceil((double)top_p * (double)all) || base + before == 0);
+    }
+    const int keep = __syncthreads_count(kept);
+    if (tid == keep - 1) sh.found[0] = mine;
+    if (kept) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk[(uint32_t)mine / kChunk]), w);
+    __syncthreads();
+    last = keep ? sh.found[0] : 0;
+  } else {
+    check_min_p = min_p;
+    uint64_t w[kHeld];
     if (!overflow) {
 #pragma unroll
-      for (int e = 0; e < kHeld; ++e) {
-        c[e] = ~0ull;
-        if (list_at + e * threads < count) c[e] = order(e ? list[e * threads] : first_entry);
-      }
+      for (int e = 0; e < kHeld; ++e) w[e] = c[e] != ~0ull ? weight_of(c[e]) : 0;
     }
-    if (!overflow && all_listed <= kSorted) {
-      // in order: the limits are numbers of tokens
-      const int n = (int)all_listed;
-      int sorted = kWave;
-      while (sorted < n) sorted <<= 1;
-#pragma unroll
-      for (int e = 0; e < kHeld; ++e)
-        if (c[e] != ~0ull) sh.bins[sh.place[list_chunk] + list_at + e * threads] = c[e];
-      __syncthreads();
-      const uint64_t mine = sample_sort(tid < n ? sh.bins[tid] : ~0ull, sorted, sh.bins + kSampleThreads);
-      bool kept = tid < n;
-      uint64_t w = 0;
-      if (kept) {
-        w = weight_of(mine);
-        if (min_p) kept = sample_log_weight(sample_logit(mine), top, inv_t) >= least;
-      }
-      if (k && others) kept = kept && tid < k;
-      if (top_p < 1.0f && others) {
-        // (of what top_k keeps)
-        const uint64_t sum = sample_scan(!k || tid < k ? w : 0, before, sorted / kWave, sh);
-        const uint64_t all = k ? base + sum : sh.total;
-        kept = kept && (base + before < (uint64_t)__builtin_ceil((double)top_p * (double)all) || base + before == 0);
-      }
-      const int keep = __syncthreads_count(kept);
-      if (tid == keep - 1) sh.found[0] = mine;
-      if (kept) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk[(uint32_t)mine / kChunk]), w);
-      __syncthreads();
-      last = keep ? sh.found[0] : 0;
-    } else {
-      check_min_p = min_p;
-      uint64_t w[kHeld];
-      if (!overflow) {
-#pragma unroll
-        for (int e = 0; e < kHeld; ++e) w[e] = c[e] != ~0ull ? weight_of(c[e]) : 0;
-      }
-      // calls f(C, weight) for the thread's tokens
-      auto visit = [&](auto&& f) W4K_INLINE {
-        if (overflow) {
-          for (int i = tid; i < a.N; i += kSampleThreads) {
-            const float v = sample_load(row + i);
-            f(sample_order(v, i), weight(v));
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < kHeld; ++e)
-            if (c[e] != ~0ull) f(c[e], w[e]);
-        }
-      };
-      // All of them lie between the logits that bound the buckets lo .. hi, with half a bucket more at both ends
-      // (far logits share the outermost buckets: there, anywhere).
-      uint64_t lo = 0, hi = ~0ull;
-      if (!overflow) {
-        const SampleCut cut = a.cut[r];
-        const float scale = sample_bucket_scale(inv_t);
-        const int top_bucket = sample_bucket(top, scale);
-        const float high = __int_as_float(top_bucket - cut.lo) + 1.0f, low = __int_as_float(top_bucket - cut.hi) - 1.0f;
-        if (high < 0x1.fffffep23f && low > 0x1p23f && cut.hi < kBuckets - 1) {
-          lo = sample_order(fminf((high - 0x1.8p23f) / scale, top), 0);
-          hi = sample_order((low - 0x1.8p23f) / scale, -1);
-        }
-      }
-      // (fewer than k are listed where top_p ends in front of the k-th)
-      if (k && others && (overflow ? (int64_t)a.N : (int64_t)all_listed) >= k)
-        last = sample_select([&](auto&& f) W4K_INLINE { visit([&](uint64_t c, uint64_t) W4K_INLINE { f(c, 1); }); },
-                             [](uint64_t) { return (uint64_t)1; }, (uint64_t)k, lo, hi, sh);
-      if (top_p < 1.0f && others) {
-        const uint64_t limit = last;
-        uint64_t sum = 0;
-        visit([&](uint64_t c, uint64_t w) W4K_INLINE { sum += c <= limit ? w : 0; });
-        sum = sample_scan(sum, before, kSampleWaves, sh);
-        const uint64_t all = k || overflow ? base + sum : sh.total;
-        const uint64_t target = (uint64_t)__builtin_ceil((double)top_p * (double)all);
-        if (target <= base && base > 0)
-          last = 0;
-        else if (target - base < sum)
-          last = sample_select(
-              [&](auto&& f) W4K_INLINE {
-                visit([&](uint64_t c, uint64_t w) W4K_INLINE {
-                  if (c <= limit) f(c, w);
-                });
-              },
-              weight_of, target > base ? target - base : 1, lo, hi, sh);
-      }
-      // the kept weights of each chunk: a wave's together, or those of the threads that hold a chunk's list
-      // (additions of one token each to few sums would wait for each other)
-      auto kept_weight = [&](uint64_t c, uint64_t w) W4K_INLINE {
-        return c <= last && (!min_p || sample_log_weight(sample_logit(c), top, inv_t) >= least) ? w : 0;
-      };
-      auto add = [&](int chunk, uint64_t sum) W4K_INLINE {
-        if (sum) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk[chunk]), sum);
-      };
+    // calls f(C, weight) for the thread's tokens
+    auto visit = [&](auto&& f) W4K_INLINE {
       if (overflow) {
-        for (int i0 = 0; i0 < a.N; i0 += kChunk) {
-          uint64_t sum = 0;
-          for (int i = i0 + tid; i < min(i0 + kChunk, a.N); i += kSampleThreads) {
-            const float v = sample_load(row + i);
-            sum += kept_weight(sample_order(v, i), weight(v));
-          }
-          sum = sample_wave_scan(sum);
-          if (lane == kWave - 1) add(i0 / kChunk, sum);
+        for (int i = tid; i < a.N; i += kSampleThreads) {
+          const float v = sample_load(row + i);
+          f(sample_order(v, i), weight(v));
         }
       } else {
-        uint64_t sum = 0;
 #pragma unroll
-        for (int e = 0; e < kHeld; ++e) sum += c[e] != ~0ull ? kept_weight(c[e], w[e]) : 0;
-        sum = sample_wave_scan(sum);
-        const int part = min(threads, kWave);
-        const uint64_t earlier = __shfl((unsigned long long)sum, max(lane - part, 0));
-        if ((lane & (part - 1)) == part - 1 && list_chunk < a.chunks) add(list_chunk, sum - (lane >= part ? earlier : 0));
+        for (int e = 0; e < kHeld; ++e)
+          if (c[e] != ~0ull) f(c[e], w[e]);
       }
-      __syncthreads();
+    };
+    // All of them lie between the logits that bound the buckets lo .. hi, with half a bucket more at both ends
+    // (far logits share the outermost buckets: there, anywhere).
+    uint64_t lo = 0, hi = ~0ull;
+    if (!overflow) {
+      const SampleCut cut = a.cut[r];
+      const float scale = sample_bucket_scale(inv_t);
+      const int top_bucket = sample_bucket(top, scale);
+      const float high = __int_as_float(top_bucket - cut.lo) + 1.0f, low = __int_as_float(top_bucket - cut.hi) - 1.0f;
+      if (high < 0x1.fffffep23f && low > 0x1p23f && cut.hi < kBuckets - 1) {
+        lo = sample_order(fminf((high - 0x1.8p23f) / scale, top), 0);
+        hi = sample_order((low - 0x1.8p23f) / scale, -1);
+      }
     }
+    // (fewer than k are listed where top_p ends in front of the k-th)
+    if (k && others && (overflow ? (int64_t)a.N : (int64_t)all_listed) >= k)
+      last = sample_select([&](auto&& f) W4K_INLINE { visit([&](uint64_t c, uint64_t) W4K_INLINE { f(c, 1); }); },
+                           [](uint64_t) { return (uint64_t)1; }, (uint64_t)k, lo, hi, sh);
+    if (top_p < 1.0f && others) {
+      const uint64_t limit = last;
+      uint64_t sum = 0;
+      visit([&](uint64_t c, uint64_t w) W4K_INLINE { sum += c <= limit ? w : 0; });
+      sum = sample_scan(sum, before, kSampleWaves, sh);
+      const uint64_t all = k || overflow ? base + sum : sh.total;
+      const uint64_t target = (uint64_t)__builtin_ceil((double)top_p * (double)all);
+      if (target <= base && base > 0)
+        last = 0;
+      else if (target - base < sum)
+        last = sample_select(
+            [&](auto&& f) W4K_INLINE {
+              visit([&](uint64_t c, uint64_t w) W4K_INLINE {
+                if (c <= limit) f(c, w);
+              });
+            },
+            weight_of, target > base ? target - base : 1, lo, hi, sh);
+    }
+    // the kept weights of each chunk: a wave's together, or those of the threads that hold a chunk's list
+    // (additions of one token each to few sums would wait for each other)
+    auto kept_weight = [&](uint64_t c, uint64_t w) W4K_INLINE {
+      return c <= last && (!min_p || sample_log_weight(sample_logit(c), top, inv_t) >= least) ? w : 0;
+    };
+    auto add = [&](int chunk, uint64_t sum) W4K_INLINE {
+      if (sum) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk[chunk]), sum);
+    };
+    if (overflow) {
+      for (int i0 = 0; i0 < a.N; i0 += kChunk) {
+        uint64_t sum = 0;
+        for (int i = i0 + tid; i < min(i0 + kChunk, a.N); i += kSampleThreads) {
+          const float v = sample_load(row + i);
+          sum += kept_weight(sample_order(v, i), weight(v));
+        }
+        sum = sample_wave_scan(sum);
+        if (lane == kWave - 1) add(i0 / kChunk, sum);
+      }
+    } else {
+      uint64_t sum = 0;
+#pragma unroll
+      for (int e = 0; e < kHeld; ++e) sum += c[e] != ~0ull ? kept_weight(c[e], w[e]) : 0;
+      sum = sample_wave_scan(sum);
+      const int part = min(threads, kWave);
+      const uint64_t earlier = __shfl((unsigned long long)sum, max(lane - part, 0));
+      if ((lane & (part - 1)) == part - 1 && list_chunk < a.chunks) add(list_chunk, sum - (lane >= part ? earlier : 0));
+    }
+    __syncthreads();
   }
   // the chunk: the first whose running sum exceeds u * total, that is its whole part
   if (wave == 0) {
@@ -1058,9 +1126,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
       upto[i] = total + sample_wave_scan(sum[i]);
       total = sample_of_lane(upto[i], kWave - 1);
     }
-    const double at = (double)u * (double)total;
-    uint64_t target = at > 0.0 ? at < 9e18 ? (uint64_t)at : ~0ull : 0;
-    target = target < total ? target : total - 1;
+    const uint64_t target = sample_target(u, total);
     if (lane == 0) sh.picked = 0, sh.left = 0, sh.all = total;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -1081,23 +1147,16 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
   uint64_t w[V], sum = 0;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    bool kept = true;
-    if (limited) {
-      // (tokens of whole buckets come in front of every listed one)
-      kept = last ? v[e] > last_v || (v[e] == last_v && i0 + e <= last_i) : sample_below(top_bucket, v[e], scale) < sure;
-      if (check_min_p)
-        kept = kept && (sample_below(top_bucket, v[e], scale) < sure || sample_log_weight(v[e], top, inv_t) >= least);
-    }
+    // (tokens of whole buckets come in front of every listed one)
+    bool kept = last ? v[e] > last_v || (v[e] == last_v && i0 + e <= last_i) : sample_below(top_bucket, v[e], scale) < sure;
+    if (check_min_p)
+      kept = kept && (sample_below(top_bucket, v[e], scale) < sure || sample_log_weight(v[e], top, inv_t) >= least);
     w[e] = 0;
-    if (kept)
-      w[e] = sample_units(chunk_top == __builtin_inff()
-                              ? v[e] == chunk_top ? __builtin_ldexp(1.0, kChunkScale) : 0.0
-                              : sample_exp2(((double)v[e] - (double)chunk_top) * to_log2, kChunkScale));
+    if (kept) w[e] = sample_units(sample_piece_weight(v[e], chunk_top, to_log2));
     sum += w[e];
   }
   const uint64_t in_chunk = sample_scan(sum, before, kSampleWaves, sh);
-  uint64_t target = (uint64_t)fmin((double)sh.left / sample_weight(chunk_top, top, inv_t, a.log2_scale - kChunkScale), 0x1p63);
-  target = target < in_chunk ? target : in_chunk - 1;
+  const uint64_t target = sample_rest(sh.left, chunk_top, top, inv_t, a.log2_scale, in_chunk);
   if (before <= target && before + sum > target) {
     int e = 0;
 #pragma unroll
@@ -1107,7 +1166,6 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
 #pragma unroll
     for (int i = 1; i < V; ++i) drawn = e == i ? v[i] : drawn;
     a.tokens[r] = i0 + e;
-    // (of the weight itself: a small one's integer has few digits)
     if (a.share) a.share[r] = (float)(sample_weight(drawn, top, inv_t, a.log2_scale) / (double)sh.all);
   }
 }
@@ -1125,7 +1183,7 @@ __global__ __launch_bounds__(256) void sample_none_kernel(SampleArgs a) {
 
 int sample_chunks(int N) { return (N + kChunk - 1) / kChunk; }
 
-// Rows that go through the launches together: a chunk takes 10.3 KB of workspace.
+// Rows that go through the launches together: a chunk takes 10.4 KB of workspace.
 int sample_rows_at_once(int M, int N) {
   const int most = 16384 / sample_chunks(N);
   return M < most ? M : most;
@@ -1134,6 +1192,7 @@ int sample_rows_at_once(int M, int N) {
 // Places of `rows` rows' arrays in the workspace; the bytes they take.
 size_t sample_places(SampleArgs& a, uintptr_t ws, int rows) {
   a.chunks = sample_chunks(a.N);
+  a.subs = a.chunks * kScanWaves;
   a.list_threads = kSampleThreads;
   while (a.list_threads * a.chunks > kSampleThreads) a.list_threads >>= 1;
   const size_t n = (size_t)rows * a.chunks;
@@ -1144,10 +1203,11 @@ size_t sample_places(SampleArgs& a, uintptr_t ws, int rows) {
   };
   take(a.list, n * kListed);
   take(a.bins, n * kBuckets);
-  take(a.mass, n);
+  take(a.sub_mass, n * kScanWaves);
   take(a.kept, n);
   take(a.cut, rows);
   take(a.top, n);
+  take(a.sub_top, n * kScanWaves);
   take(a.listed, n);
   return at;
 }
