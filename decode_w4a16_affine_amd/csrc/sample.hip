@@ -356,13 +356,6 @@ __device__ __forceinline__ uint64_t sample_exchange(uint64_t c, bool up) {
   return (other < c) == (up == ((threadIdx.x & J) == 0)) ? other : c;
 }
 template <int J>
-__device__ __forceinline__ uint64_t sample_wave_least(uint64_t c) {
-  const uint64_t other = (uint64_t)sample_across<J>((uint32_t)(c >> 32)) << 32 | sample_across<J>((uint32_t)c);
-  c = other < c ? other : c;
-  if constexpr (J > 1) c = sample_wave_least<J / 2>(c);
-  return c;
-}
-template <int J>
 __device__ __forceinline__ uint64_t sample_merge(uint64_t c, bool up) {
   c = sample_exchange<J>(c, up);
   if constexpr (J > 1) c = sample_merge<J / 2>(c, up);
