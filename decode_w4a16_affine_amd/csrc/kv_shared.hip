@@ -17,6 +17,7 @@ constexpr int kSplitSteps = 768;     // of 128 entries and 32 rows
 constexpr int kOwnFill = 2048;       // workgroups of the requests' own entries
 constexpr int kSplitFill = 512;      // workgroups of the split form
 constexpr int kPartTiles = 4;        // tiles of a part at least
+constexpr int kOwnOfTile = 256;      // own entries that take as long as a tile of shared ones
 
 w4a16_status_t check_shared(const w4a16_kv_cache_t* cache, int tokens, int requests, int max_new, int max_shared,
                             int max_own, int q_heads) {
@@ -82,15 +83,20 @@ KvSharedArgs shared_args(const w4a16_kv_cache_t* cache, int tokens, int requests
     a.part = 1 << a.part_shift;
     a.parts = (max_shared + a.part - 1) >> a.part_shift;
   } else if (max_shared > 0) {
-    // Parts for a workgroup a CU, so that the requests' own run beside them (64 single tokens behind 8000 and
-    // up to 2000 of their own, 62 us; for two a CU 66), and for two where tiles are many (24 behind
-    // 100001: 87; for one 99), which eight waves of heads of 256 leave no room for.  Each
+    // Parts for a workgroup a CU, so that the requests' own run beside them, and for one in two where these take as
+    // long all the same: fewer partial results (64 single tokens behind 8000 and up to 2000 of their own, 512 entries
+    // a tile, for 2 / 1 / 0.5 a CU 66 / 58.7 / 54.5 us; 24 of them 31.4 for 1, 29.1 for 0.5; behind 30000, 136 a
+    // tile, 83 and 111; with up to 20 of their own 31 and 39).  Two where tiles are many (24 behind 100001: 87;
+    // for one 99), which eight waves of heads of 256 leave no room for.  Each
     // row and part costs D + 5 floats written and read again: four tiles at least (us, 2 / 3 / 4 / 6: 61
     // tokens of 16 requests behind 6000, 16 heads of 64 over 4, 28.0 / 27.0 / 24.5 / 25.7).
     const int tile_tokens = kv_tile_rows(cache->dim, cache->type) / a.group;
     const int64_t workgroups = (int64_t)((tokens + tile_tokens - 1) / tile_tokens) * cache->heads;
     const int64_t tiles = workgroups * (max_shared / kKvTile);
-    const int64_t fill = tiles > 256 * 32 && kv_tile_waves(cache->dim, cache->type) == 4 ? 512 : 256;
+    const int64_t own = (int64_t)requests * max_own * cache->heads;
+    const int64_t fill = own >= kOwnOfTile * tiles                                              ? 128
+                         : tiles > 256 * 32 && kv_tile_waves(cache->dim, cache->type) == 4 ? 512
+                                                                                           : 256;
     const int64_t wanted = std::min<int64_t>({fill / workgroups, max_shared / (kPartTiles * kKvTile), kKvMaxParts});
     const int64_t parts = wanted > 1 ? wanted : 1;
     a.part = (int)((max_shared + parts * kKvTile - 1) / (parts * kKvTile)) * kKvTile;
