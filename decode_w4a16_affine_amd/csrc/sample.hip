@@ -54,6 +54,10 @@ constexpr int kSub = kWave * kLane;                    // a wave
 constexpr int kChunks = W4A16_SAMPLE_MAX_N / kChunk;
 constexpr int kBuckets = 256;
 constexpr float kBucketsPerUnit = 12.0f;              // of (logit / temperature)
+// For lower temperatures buckets are not narrower than 1 / 18 of a logit, 14 logits for all of them: tokens that top_k
+// keeps lie that far apart whatever their weights (262144 normal logits of deviation 3, temperature 0.1, the
+// first 50: @@ us, with 1 / 120 @@).
+constexpr float kMaxInverse = 1.5f;
 // Up to a workgroup for each CU collect makes the cut itself, side by side, and a launch is saved (8 rows of 262144
 // with top_k and top_p 33.3 us in a graph, with a cut of its own 34.6; 16 rows 38.0 and 37.9, 24 43.6 and 41.5).
 constexpr int kCutAlone = 256;
@@ -99,8 +103,9 @@ struct SampleArgs {
 struct SampleCut {
   int lo, hi;          // buckets
   int before;          // tokens in front of lo
-  int min_p_alone;     // top_k and top_p end behind hi
+  int min_p_alone;     // top_k and top_p end behind hi: nothing is listed, `kept` is of all that min_p keeps
   uint64_t total;      // all weights, as kept (SampleArgs)
+  double least;        // (logit - largest) / temperature of min_p
 };
 
 // A row's parameters.
@@ -191,7 +196,7 @@ __device__ __forceinline__ uint64_t sample_units(double w) {
 // A logit's bucket counted from any fixed one; grows with the logit.  (A sum with 1.5 * 2^23 is rounded
 // to an integer; far logits share the outermost ones.)
 __device__ __forceinline__ float sample_bucket_scale(double inv_t) {
-  return fminf(kBucketsPerUnit * (float)inv_t, 0x1p100f);
+  return kBucketsPerUnit * fminf((float)inv_t, kMaxInverse);
 }
 __device__ __forceinline__ int sample_bucket(float v, float scale) {
   return __float_as_int(__builtin_amdgcn_fmed3f(__builtin_fmaf(v, scale, 0x1.8p23f), 0x1p23f, 0x1.fffffep23f));
@@ -254,6 +259,15 @@ __device__ __forceinline__ void sample_load_chunk(const T* row, int chunk, int N
   }
 }
 
+// Eight in a row, of a thread of the draw.
+constexpr int kDrawLane = kChunk / kSampleThreads;
+template <class T>
+__device__ __forceinline__ void sample_load_eight(const T* row, int i, int N, float (&v)[kDrawLane]) {
+  constexpr int V = kDrawLane <= kPiece<T> ? kDrawLane : kPiece<T>;
+#pragma unroll
+  for (int e = 0; e < kDrawLane; e += V) sample_load_row<V>(row, i + e, N, v + e);
+}
+
 // A wave's running sums: rows of 16 lanes by shifts within them, then their last lanes' to the rows behind.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ uint32_t sample_from_lane(uint32_t v) {
@@ -305,9 +319,10 @@ struct SampleShared {
   // what its first wave makes of the row, so that others do not: sixteen waves on four SIMDs take
   // sixteen cycles for an instruction, one takes four
   float top, top_p;
-  double inv_t, least;
-  int special, overflow, alone, k, sure, picked;
-  uint64_t base, total, all, left;
+  double inv_t;
+  int special, overflow, k, picked;
+  SampleCut cut;
+  uint64_t base, all, left;
   uint32_t all_listed;
   float tops[kSampleWaves], sub_top;      // of rows without limits
 };
@@ -389,8 +404,8 @@ __device__ __forceinline__ uint64_t sample_sort(uint64_t c, int n, uint64_t* s_s
 }
 
 // The first C (in order) at which the running sum of `measure` reaches target, 1 <=
-// target <= the sum over all, of tokens in lo .. hi.  visit(f) calls f(C, measure) for the
-// thread's tokens, measure_of(C) is its measure again.  Bins over lo .. hi tell which of them has it;
+// target <= the sum over all, of tokens in lo .. hi (others do not count).  visit(f) calls f(C, measure)
+// for the thread's tokens, measure_of(C) is measure() again.  Bins over lo .. hi tell which of them has it;
 // a bin of few tokens is sorted, another one is divided again.
 template <class Visit, class Measure>
 __device__ __forceinline__ uint64_t sample_select(Visit&& visit, Measure&& measure_of, uint64_t target, uint64_t lo,
@@ -406,8 +421,8 @@ __device__ __forceinline__ uint64_t sample_select(Visit&& visit, Measure&& measu
     sh.bins[tid] = 0, sh.bins[tid + kSampleThreads] = 0;
     if (tid == 0) sh.found[0] = 0, sh.found[1] = 0, sh.few = 0;
     __syncthreads();
-    visit([&](uint64_t c, uint64_t measure) W4K_INLINE {
-      if (c >= lo && c <= hi) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[(c - lo) >> shift]), measure);
+    visit([&](uint64_t c, auto&& measure) W4K_INLINE {
+      if (c >= lo && c <= hi) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[(c - lo) >> shift]), measure());
     });
     __syncthreads();
     uint64_t sum = 0, before;
@@ -427,7 +442,7 @@ __device__ __forceinline__ uint64_t sample_select(Visit&& visit, Measure&& measu
     base = sh.found[1];
     if (shift == 0) return lo;
     // the bin's tokens, in order, if they are few
-    visit([&](uint64_t c, uint64_t) W4K_INLINE {
+    visit([&](uint64_t c, auto&&) W4K_INLINE {
       if (c < lo || c > hi) return;
       const uint32_t at = atomicAdd(&sh.few, 1u);
       if (at < kSorted) sh.bins[at] = c;
@@ -611,8 +626,10 @@ __device__ __forceinline__ SampleCut sample_find_cut(const SampleArgs& a, int r,
   const int top_bucket = sample_bucket(top, scale);
   // the bucket of the least weight, by fp32 arithmetic on its edge
   int edge_at = kBuckets;
+  double least = -__builtin_inf();
   if (p.min_p > 0.0f) {
-    const float edge = (float)((double)top + log((double)p.min_p) * p.t);
+    least = log((double)p.min_p);
+    const float edge = (float)((double)top + least * p.t);
     edge_at = sample_below(top_bucket, fminf(fmaxf(edge, -3e38f), top), scale);
   }
   if (tid < kWave) {
@@ -689,8 +706,8 @@ __device__ __forceinline__ SampleCut sample_find_cut(const SampleArgs& a, int r,
     // Sums are exact to 2^-24 (2^-37 times 8192 for each of 128 chunks at worst, 2^-28 where errors
     // cancel), beside a total of at least 1: a border that near leaves both buckets open.  The weights
     // that top_k keeps end somewhere in its bucket.
-    const double least = p.k ? (k_at ? sh.mass[k_at - 1] : 0.0) : total, most = p.k ? sh.mass[k_at] : total;
-    first_of(upto + 0x1p-16 >= p.top_p * least, 1);
+    const double fewest = p.k ? (k_at ? sh.mass[k_at - 1] : 0.0) : total, most = p.k ? sh.mass[k_at] : total;
+    first_of(upto + 0x1p-16 >= p.top_p * fewest, 1);
     first_of(upto >= p.top_p * most + 0x1p-16, 2);
   }
   __syncthreads();
@@ -711,7 +728,7 @@ __device__ __forceinline__ SampleCut sample_find_cut(const SampleArgs& a, int r,
   }
   lo = max(lo, 0), hi = min(hi, kBuckets - 1);
   return SampleCut{lo, hi, lo ? (int)sh.count[lo - 1] : 0, min_p_alone,
-                   (uint64_t)__builtin_rint(__builtin_ldexp(total, a.log2_scale))};
+                   (uint64_t)__builtin_rint(__builtin_ldexp(total, a.log2_scale)), least};
 }
 
 __global__ __launch_bounds__(kScanThreads) void sample_cut_kernel(SampleArgs a) {
@@ -735,6 +752,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_collect_kernel(SampleArgs
   __shared__ std::conditional_t<CUT, SampleCutShared, Empty> sh;
   __shared__ uint32_t s_listed;
   __shared__ double s_sum[kScanWaves];
+  __shared__ uint64_t s_units[kScanWaves];
   const int chunk = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const T* const row = static_cast<const T*>(a.logits) + r * a.stride;
   const size_t at = (size_t)r * a.chunks + chunk;
@@ -769,7 +787,17 @@ __global__ __launch_bounds__(kScanThreads) void sample_collect_kernel(SampleArgs
     const int below = sample_below(top_bucket, v[x], scale);
     mine |= (below >= cut.lo && below <= cut.hi && sample_token<T>(chunk, x) < a.N ? 1u : 0u) << x;
   }
-  if (__any(mine)) {
+  uint64_t units = 0;      // min_p alone: the weights of these tokens that it keeps
+  if (cut.min_p_alone) {
+#pragma unroll
+    for (int x = 0; x < kLane; ++x) {
+      const double log_weight = sample_log_weight(v[x], top, p.inv_t);
+      if (mine >> x & 1 && log_weight >= cut.least)
+        units += (uint64_t)__builtin_rint(sample_exp2(log_weight * kLog2E, a.log2_scale));
+      if (x % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    }
+    units = sample_wave_scan(units);
+  } else if (__any(mine)) {
     const uint32_t count = __builtin_popcount(mine), upto = sample_wave_scan(count);
     uint32_t slot = 0;
     if (lane == kWave - 1) slot = atomicAdd(&s_listed, upto);
@@ -789,13 +817,14 @@ __global__ __launch_bounds__(kScanThreads) void sample_collect_kernel(SampleArgs
       tid + top_bucket - sample_bucket(own_top, scale) < cut.lo)
     sum = sample_bin_mass(own_bin);
   sum = sample_wave_sum(sum);
-  if (lane == 0) s_sum[wave] = sum;
+  if (lane == kWave - 1) s_sum[wave] = sum, s_units[wave] = units;
   __syncthreads();
   if (tid == 0) {
-    for (int w = 1; w < kScanWaves; ++w) sum += s_sum[w];
-    a.kept[at] = own_top > -__builtin_inff()
+    units = s_units[0];
+    for (int w = 1; w < kScanWaves; ++w) sum += s_sum[w], units += s_units[w];
+    a.kept[at] = units + (own_top > -__builtin_inff()
                      ? (uint64_t)__builtin_rint(sum * sample_weight(own_top, top, p.inv_t, a.log2_scale - kBinScale))
-                     : 0;
+                     : 0);
     a.listed[at] = s_listed;
   }
 }
@@ -833,32 +862,26 @@ __device__ __forceinline__ void sample_begin(const SampleArgs& a, int r, SampleS
   } else {
     // (lists that a thread cannot hold its part of are left, and the row's logits are read instead)
     bool over = false;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (lane + i * kWave >= a.chunks) listed[i] = 0, kept[i] = 0;
-      over |= listed[i] > (uint32_t)min(kListed, a.list_threads * kHeld);
-    }
-    const bool overflow = __any(over);
     uint64_t base = 0;
     uint32_t all = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int c = lane + i * kWave;
-      if (overflow || sample_few(p)) kept[i] = 0;
+      if (c >= a.chunks) listed[i] = 0, kept[i] = 0;
+      over |= listed[i] > (uint32_t)min(kListed, a.list_threads * kHeld);
+      if (sample_few(p)) kept[i] = 0;
       sh.chunk[c] = kept[i], sh.listed[c] = listed[i];
       base += sample_of_lane(sample_wave_scan(kept[i]), kWave - 1);
       const uint32_t upto = sample_wave_scan(listed[i]);
       sh.place[c] = all + upto - listed[i];
       all += sample_of_lane(upto, kWave - 1);
     }
+    const bool overflow = __any(over);
     if (lane == 0) {
-      sh.base = base, sh.all_listed = all, sh.total = cut.total;
+      sh.base = base, sh.all_listed = all, sh.cut = cut;
       sh.overflow = overflow;
-      sh.alone = !overflow && cut.min_p_alone;
-      sh.k = p.k ? p.k - (overflow ? 0 : cut.before) : 0;
-      sh.sure = overflow ? 0 : cut.lo;
+      sh.k = p.k ? p.k - cut.before : 0;
       sh.top_p = p.top_p;
-      sh.least = p.min_p > 0.0f ? log((double)p.min_p) : -__builtin_inf();
     }
   }
   if (lane == 0) {
@@ -975,19 +998,18 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
   }
   auto weight = [&](float v) { return (uint64_t)__builtin_rint(sample_weight(v, top, inv_t, a.log2_scale)); };
   auto weight_of = [&](uint64_t c) { return weight(sample_logit(c)); };
-  uint64_t last = ~0ull;      // the last C that is kept (0: no listed token is)
-  bool check_min_p = false;   // (but for min_p)
-  int sure = 0;               // buckets in front of it are kept whole
-  double least = 0.0;
+  uint64_t last = sample_order(-__builtin_inff(), W4A16_SAMPLE_MAX_N);      // the last C that is kept (0: no listed token is)
   uint64_t before;
-  const bool overflow = sh.overflow, others = !sh.alone;
+  const bool overflow = sh.overflow;
   const int k = sh.k;
   const float top_p = sh.top_p;
   const uint64_t base = sh.base;
   const uint32_t all_listed = sh.all_listed;
-  least = sh.least;
-  sure = sh.sure;
-  const bool min_p = least > -__builtin_inf();
+  const SampleCut cut = sh.cut;
+  const float scale = sample_bucket_scale(inv_t);
+  const int top_bucket = sample_bucket(top, scale);
+  const bool min_p = cut.least > -__builtin_inf();
+  bool check_min_p = min_p;      // (behind last it need not be)
   const int count = list_chunk < a.chunks ? (int)sh.listed[list_chunk] : 0;
   uint64_t c[kHeld];
   auto order = [&](uint2 e) { return sample_order(__uint_as_float(e.x), (int)e.y); };
@@ -998,7 +1020,9 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
       if (list_at + e * threads < count) c[e] = order(e ? list[e * threads] : first_entry);
     }
   }
-  if (!overflow && all_listed <= kSorted) {
+  if (cut.min_p_alone) {
+    // nothing is listed
+  } else if (!overflow && all_listed <= kSorted) {
     // in order: the limits are numbers of tokens
     const int n = (int)all_listed;
     int sorted = kWave;
@@ -1008,17 +1032,18 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
       if (c[e] != ~0ull) sh.bins[sh.place[list_chunk] + list_at + e * threads] = c[e];
     __syncthreads();
     const uint64_t mine = sample_sort(tid < n ? sh.bins[tid] : ~0ull, sorted, sh.bins + kSampleThreads);
+    check_min_p = false;
     bool kept = tid < n;
     uint64_t w = 0;
     if (kept) {
       w = weight_of(mine);
-      if (min_p) kept = sample_log_weight(sample_logit(mine), top, inv_t) >= least;
+      if (min_p) kept = sample_log_weight(sample_logit(mine), top, inv_t) >= cut.least;
     }
-    if (k && others) kept = kept && tid < k;
-    if (top_p < 1.0f && others) {
+    if (k) kept = kept && tid < k;
+    if (top_p < 1.0f) {
       // (of what top_k keeps)
       const uint64_t sum = sample_scan(!k || tid < k ? w : 0, before, sorted / kWave, sh);
-      const uint64_t all = k ? base + sum : sh.total;
+      const uint64_t all = k ? base + sum : cut.total;
       kept = kept && (base + before < (uint64_t)__builtin_ceil((double)top_p * (double)all) || base + before == 0);
     }
     const int keep = __syncthreads_count(kept);
@@ -1027,77 +1052,76 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
     __syncthreads();
     last = keep ? sh.found[0] : 0;
   } else {
-    check_min_p = min_p;
     uint64_t w[kHeld];
     if (!overflow) {
 #pragma unroll
       for (int e = 0; e < kHeld; ++e) w[e] = c[e] != ~0ull ? weight_of(c[e]) : 0;
     }
-    // calls f(C, weight) for the thread's tokens
+    // calls f(C, its weight as a function) for the thread's tokens of a chunk
+    auto visit_chunk = [&](int chunk, auto&& f) W4K_INLINE {
+      float v[kDrawLane];
+      const int i0 = chunk * kChunk + tid * kDrawLane;
+      sample_load_eight(row, i0, a.N, v);
+#pragma unroll
+      for (int e = 0; e < kDrawLane; ++e) {
+        const int b = sample_below(top_bucket, v[e], scale);
+        if (b >= cut.lo && b <= cut.hi && i0 + e < a.N)
+          f(sample_order(v[e], i0 + e), [&]() W4K_INLINE { return weight(v[e]); });
+      }
+    };
+    // ... of the row
     auto visit = [&](auto&& f) W4K_INLINE {
       if (overflow) {
-        for (int i = tid; i < a.N; i += kSampleThreads) {
-          const float v = sample_load(row + i);
-          f(sample_order(v, i), weight(v));
-        }
+        for (int i = 0; i < a.chunks; ++i)
+          if (sh.listed[i]) visit_chunk(i, f);
       } else {
 #pragma unroll
         for (int e = 0; e < kHeld; ++e)
-          if (c[e] != ~0ull) f(c[e], w[e]);
+          if (c[e] != ~0ull) f(c[e], [&]() W4K_INLINE { return w[e]; });
       }
     };
     // All of them lie between the logits that bound the buckets lo .. hi, with half a bucket more at both ends
     // (far logits share the outermost buckets: there, anywhere).
     uint64_t lo = 0, hi = ~0ull;
-    if (!overflow) {
-      const SampleCut cut = a.cut[r];
-      const float scale = sample_bucket_scale(inv_t);
-      const int top_bucket = sample_bucket(top, scale);
-      const float high = __int_as_float(top_bucket - cut.lo) + 1.0f, low = __int_as_float(top_bucket - cut.hi) - 1.0f;
-      if (high < 0x1.fffffep23f && low > 0x1p23f && cut.hi < kBuckets - 1) {
-        lo = sample_order(fminf((high - 0x1.8p23f) / scale, top), 0);
-        hi = sample_order((low - 0x1.8p23f) / scale, -1);
-      }
+    const float high = __int_as_float(top_bucket - cut.lo) + 1.0f, low = __int_as_float(top_bucket - cut.hi) - 1.0f;
+    if (high < 0x1.fffffep23f && low > 0x1p23f && cut.hi < kBuckets - 1) {
+      lo = sample_order(fminf((high - 0x1.8p23f) / scale, top), 0);
+      hi = sample_order((low - 0x1.8p23f) / scale, -1);
     }
     // (fewer than k are listed where top_p ends in front of the k-th)
-    if (k && others && (overflow ? (int64_t)a.N : (int64_t)all_listed) >= k)
-      last = sample_select([&](auto&& f) W4K_INLINE { visit([&](uint64_t c, uint64_t) W4K_INLINE { f(c, 1); }); },
-                           [](uint64_t) { return (uint64_t)1; }, (uint64_t)k, lo, hi, sh);
-    if (top_p < 1.0f && others) {
+    if (k && all_listed >= (uint32_t)k)
+      last = sample_select(
+          [&](auto&& f) W4K_INLINE {
+            visit([&](uint64_t c, auto&&) W4K_INLINE { f(c, []() W4K_INLINE { return (uint64_t)1; }); });
+          },
+          [](uint64_t) { return (uint64_t)1; }, (uint64_t)k, lo, hi, sh);
+    if (top_p < 1.0f) {
       const uint64_t limit = last;
       uint64_t sum = 0;
-      visit([&](uint64_t c, uint64_t w) W4K_INLINE { sum += c <= limit ? w : 0; });
+      visit([&](uint64_t c, auto&& w) W4K_INLINE { sum += c <= limit ? w() : 0; });
       sum = sample_scan(sum, before, kSampleWaves, sh);
-      const uint64_t all = k || overflow ? base + sum : sh.total;
+      const uint64_t all = k ? base + sum : cut.total;
       const uint64_t target = (uint64_t)__builtin_ceil((double)top_p * (double)all);
       if (target <= base && base > 0)
         last = 0;
       else if (target - base < sum)
-        last = sample_select(
-            [&](auto&& f) W4K_INLINE {
-              visit([&](uint64_t c, uint64_t w) W4K_INLINE {
-                if (c <= limit) f(c, w);
-              });
-            },
-            weight_of, target > base ? target - base : 1, lo, hi, sh);
+        last = sample_select(visit, weight_of, target > base ? target - base : 1, lo, min(hi, limit), sh);
     }
     // the kept weights of each chunk: a wave's together, or those of the threads that hold a chunk's list
     // (additions of one token each to few sums would wait for each other)
     auto kept_weight = [&](uint64_t c, uint64_t w) W4K_INLINE {
-      return c <= last && (!min_p || sample_log_weight(sample_logit(c), top, inv_t) >= least) ? w : 0;
+      return c <= last && (!min_p || sample_log_weight(sample_logit(c), top, inv_t) >= cut.least) ? w : 0;
     };
     auto add = [&](int chunk, uint64_t sum) W4K_INLINE {
       if (sum) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk[chunk]), sum);
     };
     if (overflow) {
-      for (int i0 = 0; i0 < a.N; i0 += kChunk) {
+      for (int i = 0; i < a.chunks; ++i) {
+        if (!sh.listed[i]) continue;
         uint64_t sum = 0;
-        for (int i = i0 + tid; i < min(i0 + kChunk, a.N); i += kSampleThreads) {
-          const float v = sample_load(row + i);
-          sum += kept_weight(sample_order(v, i), weight(v));
-        }
+        visit_chunk(i, [&](uint64_t c, auto&& w) W4K_INLINE { sum += c <= last ? kept_weight(c, w()) : 0; });
         sum = sample_wave_scan(sum);
-        if (lane == kWave - 1) add(i0 / kChunk, sum);
+        if (lane == kWave - 1) add(i, sum);
       }
     } else {
       uint64_t sum = 0;
@@ -1129,21 +1153,20 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
   const int chunk = sh.picked;
   const float chunk_top = a.top[at0 + chunk];      // (kept, as the chunk has a kept token)
   // its tokens, eight a thread
-  constexpr int V = kChunk / kSampleThreads;
+  constexpr int V = kDrawLane;
   const int i0 = chunk * kChunk + tid * V;
   float v[V];
-  sample_load_row<V <= kPiece<T> ? V : kPiece<T>>(row, i0, a.N, v);
-  if constexpr (V > kPiece<T>) sample_load_row<kPiece<T>>(row, i0 + kPiece<T>, a.N, v + kPiece<T>);
-  const float scale = sample_bucket_scale(inv_t), last_v = sample_logit(last);
-  const int top_bucket = sample_bucket(top, scale), last_i = (int)(uint32_t)last;
+  sample_load_eight(row, i0, a.N, v);
+  const float last_v = sample_logit(last);
+  const int last_i = (int)(uint32_t)last;
   const double to_log2 = inv_t * kLog2E;
   uint64_t w[V], sum = 0;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     // (tokens of whole buckets come in front of every listed one)
-    bool kept = last ? v[e] > last_v || (v[e] == last_v && i0 + e <= last_i) : sample_below(top_bucket, v[e], scale) < sure;
+    bool kept = last ? v[e] > last_v || (v[e] == last_v && i0 + e <= last_i) : sample_below(top_bucket, v[e], scale) < cut.lo;
     if (check_min_p)
-      kept = kept && (sample_below(top_bucket, v[e], scale) < sure || sample_log_weight(v[e], top, inv_t) >= least);
+      kept = kept && (sample_below(top_bucket, v[e], scale) < cut.lo || sample_log_weight(v[e], top, inv_t) >= cut.least);
     w[e] = 0;
     if (kept) w[e] = sample_units(sample_piece_weight(v[e], chunk_top, to_log2));
     sum += w[e];

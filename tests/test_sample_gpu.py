@@ -117,6 +117,21 @@ def test_rows_that_ask_for_different_things(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N", [(3, 9001), (3, 200001), (1, 1 << 20)])
+@pytest.mark.parametrize("spread,temperature,limits", [
+    (0.1, 1.0, dict(top_p=0.95)), (0.5, 1.0, dict(top_p=0.5)), (1.0, 3.0, dict(top_p=0.99)), (3.0, 0.1, dict(top_k=50)),
+    (3.0, 0.1, dict(top_k=1000)), (3.0, 0.05, dict(top_k=3000, top_p=0.9)), (6.0, 0.02, dict(top_p=0.99, min_p=1e-9)),
+    (0.3, 1.0, dict(min_p=0.2)), (0.1, 1.0, dict(min_p=0.9, top_k=8000)), (0.01, 2.0, dict(top_k=100, top_p=0.7)),
+    (0.3, 1.0, dict(top_k=7000, top_p=0.6, min_p=0.4)), (0.0, 1.0, dict(top_k=5000, top_p=0.35))])
+def test_flat_and_steep_rows(dtype, M, N, spread, temperature, limits):
+    """Thousands of tokens of nearly the same weight, and weights that vanish long before a limit is reached."""
+    say("sample flat or steep", dtype, M, N, spread, temperature, limits)
+    rng = np.random.default_rng(N + int(100 * spread))
+    Problem(rng.normal(size=(M, N)) * spread, dtype, rng.random(M), temperature=[temperature] * M,
+            **{k: [v] * M for k, v in limits.items()}).check()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("N", [5, 700, 20000])
 def test_equal_logits(dtype, N):
     """Ties everywhere: limits cut between equal tokens by their index."""
