@@ -14,8 +14,8 @@
 // last kept token among the listed ones, adds the kept weights of each chunk, picks a
 // chunk and looks up the token in it (without limits: a wave's 1024 logits).  A call without limits
 // has scan and draw alone.  A row whose
-// lists overflow (thousands of tokens of a chunk in one bucket: ties) is left to the
-// draw's workgroup, which finds the limits from the logits themselves.
+// chunks list thousands of tokens (flat rows, ties) is gone through by waves, a chunk each, from the lists or, where
+// a list is too short, from the logits.
 //
 // Weights exp((logit - largest) / temperature) are computed in fp64 and added as integers of
 // 2^-e (e = 62 - log2 N for a row: its sum stays below 2^63), or in a fixed order: sums do not
@@ -56,12 +56,12 @@ constexpr int kBuckets = 256;
 constexpr float kBucketsPerUnit = 12.0f;              // of (logit / temperature)
 // For lower temperatures buckets are not narrower than 1 / 18 of a logit, 14 logits for all of them: tokens that top_k
 // keeps lie that far apart whatever their weights (262144 normal logits of deviation 3, temperature 0.1, the
-// first 50: @@ us, with 1 / 120 @@).
+// first 50: 22 us, with 1 / 120 159).
 constexpr float kMaxInverse = 1.5f;
 // Up to a workgroup for each CU collect makes the cut itself, side by side, and a launch is saved (8 rows of 262144
 // with top_k and top_p 33.3 us in a graph, with a cut of its own 34.6; 16 rows 38.0 and 37.9, 24 43.6 and 41.5).
 constexpr int kCutAlone = 256;
-constexpr int kListed = 1024;                         // tokens of a chunk that are listed at most
+constexpr int kListed = 2048;                         // tokens of a chunk that are listed at most
 constexpr int kSmallK = 512;                          // limits of so few tokens need no weights from the scan
 constexpr int kCutScale = 42;                         // sums of a row's buckets (2^20 weights below 2^63)
 constexpr int kChunkScale = 49;                       // a chunk's weights are multiples of 2^-49 (8192 of them below 2^63)
@@ -320,7 +320,7 @@ struct SampleShared {
   // sixteen cycles for an instruction, one takes four
   float top, top_p;
   double inv_t;
-  int special, overflow, k, picked;
+  int special, far, k, picked;
   SampleCut cut;
   uint64_t base, all, left;
   uint32_t all_listed;
@@ -403,13 +403,13 @@ __device__ __forceinline__ uint64_t sample_sort(uint64_t c, int n, uint64_t* s_s
   return c;
 }
 
-// The first C (in order) at which the running sum of `measure` reaches target, 1 <=
-// target <= the sum over all, of tokens in lo .. hi (others do not count).  visit(f) calls f(C, measure)
+// The first C (in order) at which the running sum of `measure` reaches target >= 1, of tokens in lo .. hi
+// (others do not count); `otherwise` if it does not.  visit(f) calls f(C, measure)
 // for the thread's tokens, measure_of(C) is measure() again.  Bins over lo .. hi tell which of them has it;
 // a bin of few tokens is sorted, another one is divided again.
 template <class Visit, class Measure>
 __device__ __forceinline__ uint64_t sample_select(Visit&& visit, Measure&& measure_of, uint64_t target, uint64_t lo,
-                                                  uint64_t hi, SampleShared& sh) {
+                                                  uint64_t hi, uint64_t otherwise, SampleShared& sh) {
   constexpr int SCAN = 4, EACH = kSampleBins / (SCAN * kWave);      // waves that scan the bins, bins a thread
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   uint64_t base = 0;      // the sum in front of lo
@@ -428,7 +428,8 @@ __device__ __forceinline__ uint64_t sample_select(Visit&& visit, Measure&& measu
     uint64_t sum = 0, before;
     if (wave < SCAN)
       for (int i = 0; i < EACH; ++i) sum += sh.bins[EACH * tid + i];
-    sample_scan(sum, before, SCAN, sh);
+    const uint64_t all = sample_scan(sum, before, SCAN, sh);
+    if (base + all < target) return otherwise;
     before += base;
     if (wave < SCAN && before < target && before + sum >= target) {      // one thread's
       int at = EACH * tid;
@@ -860,7 +861,6 @@ __device__ __forceinline__ void sample_begin(const SampleArgs& a, int r, SampleS
     }
     if (lane == 0) sh.picked = chunk, sh.few = ~0u;
   } else {
-    // (lists that a thread cannot hold its part of are left, and the row's logits are read instead)
     bool over = false;
     uint64_t base = 0;
     uint32_t all = 0;
@@ -876,10 +876,10 @@ __device__ __forceinline__ void sample_begin(const SampleArgs& a, int r, SampleS
       sh.place[c] = all + upto - listed[i];
       all += sample_of_lane(upto, kWave - 1);
     }
-    const bool overflow = __any(over);
+    const bool far = __any(over);
     if (lane == 0) {
       sh.base = base, sh.all_listed = all, sh.cut = cut;
-      sh.overflow = overflow;
+      sh.far = far;
       sh.k = p.k ? p.k - cut.before : 0;
       sh.top_p = p.top_p;
     }
@@ -1000,7 +1000,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
   auto weight_of = [&](uint64_t c) { return weight(sample_logit(c)); };
   uint64_t last = sample_order(-__builtin_inff(), W4A16_SAMPLE_MAX_N);      // the last C that is kept (0: no listed token is)
   uint64_t before;
-  const bool overflow = sh.overflow;
+  const bool far = sh.far;      // some chunk lists more than its threads hold
   const int k = sh.k;
   const float top_p = sh.top_p;
   const uint64_t base = sh.base;
@@ -1013,7 +1013,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
   const int count = list_chunk < a.chunks ? (int)sh.listed[list_chunk] : 0;
   uint64_t c[kHeld];
   auto order = [&](uint2 e) { return sample_order(__uint_as_float(e.x), (int)e.y); };
-  if (!overflow) {
+  if (!far) {
 #pragma unroll
     for (int e = 0; e < kHeld; ++e) {
       c[e] = ~0ull;
@@ -1022,7 +1022,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
   }
   if (cut.min_p_alone) {
     // nothing is listed
-  } else if (!overflow && all_listed <= kSorted) {
+  } else if (!far && all_listed <= kSorted) {
     // in order: the limits are numbers of tokens
     const int n = (int)all_listed;
     int sorted = kWave;
@@ -1053,27 +1053,33 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
     last = keep ? sh.found[0] : 0;
   } else {
     uint64_t w[kHeld];
-    if (!overflow) {
+    if (!far) {
 #pragma unroll
       for (int e = 0; e < kHeld; ++e) w[e] = c[e] != ~0ull ? weight_of(c[e]) : 0;
     }
-    // calls f(C, its weight as a function) for the thread's tokens of a chunk
+    // calls f(C, its weight as a function) for the thread's tokens of a chunk, a wave's: those listed, or (of a chunk that has
+    // more of them than its list holds) those in lo .. hi
     auto visit_chunk = [&](int chunk, auto&& f) W4K_INLINE {
-      float v[kDrawLane];
-      const int i0 = chunk * kChunk + tid * kDrawLane;
-      sample_load_eight(row, i0, a.N, v);
-#pragma unroll
-      for (int e = 0; e < kDrawLane; ++e) {
-        const int b = sample_below(top_bucket, v[e], scale);
-        if (b >= cut.lo && b <= cut.hi && i0 + e < a.N)
-          f(sample_order(v[e], i0 + e), [&]() W4K_INLINE { return weight(v[e]); });
+      const int n = (int)sh.listed[chunk];
+      if (n <= kListed) {
+        const uint2* const from = a.list + (at0 + chunk) * kListed;
+        for (int i = lane; i < n; i += kWave) {
+          const uint2 entry = from[i];
+          const float v = __uint_as_float(entry.x);
+          f(sample_order(v, (int)entry.y), [&]() W4K_INLINE { return weight(v); });
+        }
+      } else {
+        for (int i = chunk * kChunk + lane; i < min((chunk + 1) * kChunk, a.N); i += kWave) {
+          const float v = sample_load(row + i);
+          const int b = sample_below(top_bucket, v, scale);
+          if (b >= cut.lo && b <= cut.hi) f(sample_order(v, i), [&]() W4K_INLINE { return weight(v); });
+        }
       }
     };
     // ... of the row
     auto visit = [&](auto&& f) W4K_INLINE {
-      if (overflow) {
-        for (int i = 0; i < a.chunks; ++i)
-          if (sh.listed[i]) visit_chunk(i, f);
+      if (far) {
+        for (int i = wave; i < a.chunks; i += kSampleWaves) visit_chunk(i, f);
       } else {
 #pragma unroll
         for (int e = 0; e < kHeld; ++e)
@@ -1094,34 +1100,32 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
           [&](auto&& f) W4K_INLINE {
             visit([&](uint64_t c, auto&&) W4K_INLINE { f(c, []() W4K_INLINE { return (uint64_t)1; }); });
           },
-          [](uint64_t) { return (uint64_t)1; }, (uint64_t)k, lo, hi, sh);
+          [](uint64_t) { return (uint64_t)1; }, (uint64_t)k, lo, hi, last, sh);
     if (top_p < 1.0f) {
       const uint64_t limit = last;
-      uint64_t sum = 0;
-      visit([&](uint64_t c, auto&& w) W4K_INLINE { sum += c <= limit ? w() : 0; });
-      sum = sample_scan(sum, before, kSampleWaves, sh);
-      const uint64_t all = k ? base + sum : cut.total;
+      uint64_t all = cut.total;
+      if (k) {
+        uint64_t sum = 0;
+        visit([&](uint64_t c, auto&& w) W4K_INLINE { sum += c <= limit ? w() : 0; });
+        all = base + sample_scan(sum, before, kSampleWaves, sh);
+      }
       const uint64_t target = (uint64_t)__builtin_ceil((double)top_p * (double)all);
       if (target <= base && base > 0)
         last = 0;
-      else if (target - base < sum)
-        last = sample_select(visit, weight_of, target > base ? target - base : 1, lo, min(hi, limit), sh);
+      else
+        last = sample_select(visit, weight_of, target > base ? target - base : 1, lo, min(hi, limit), limit, sh);
     }
-    // the kept weights of each chunk: a wave's together, or those of the threads that hold a chunk's list
+    // the kept weights of each chunk, by its wave or the threads that hold its list
     // (additions of one token each to few sums would wait for each other)
     auto kept_weight = [&](uint64_t c, uint64_t w) W4K_INLINE {
       return c <= last && (!min_p || sample_log_weight(sample_logit(c), top, inv_t) >= cut.least) ? w : 0;
     };
-    auto add = [&](int chunk, uint64_t sum) W4K_INLINE {
-      if (sum) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk[chunk]), sum);
-    };
-    if (overflow) {
-      for (int i = 0; i < a.chunks; ++i) {
-        if (!sh.listed[i]) continue;
+    if (far) {
+      for (int i = wave; i < a.chunks; i += kSampleWaves) {
         uint64_t sum = 0;
         visit_chunk(i, [&](uint64_t c, auto&& w) W4K_INLINE { sum += c <= last ? kept_weight(c, w()) : 0; });
         sum = sample_wave_scan(sum);
-        if (lane == kWave - 1) add(i, sum);
+        if (lane == kWave - 1) sh.chunk[i] += sum;
       }
     } else {
       uint64_t sum = 0;
@@ -1130,7 +1134,9 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
       sum = sample_wave_scan(sum);
       const int part = min(threads, kWave);
       const uint64_t earlier = __shfl((unsigned long long)sum, max(lane - part, 0));
-      if ((lane & (part - 1)) == part - 1 && list_chunk < a.chunks) add(list_chunk, sum - (lane >= part ? earlier : 0));
+      sum -= lane >= part ? earlier : 0;
+      if ((lane & (part - 1)) == part - 1 && list_chunk < a.chunks && sum)
+        atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk[list_chunk]), sum);
     }
     __syncthreads();
   }
@@ -1199,9 +1205,9 @@ __global__ __launch_bounds__(256) void sample_none_kernel(SampleArgs a) {
 
 int sample_chunks(int N) { return (N + kChunk - 1) / kChunk; }
 
-// Rows that go through the launches together: a chunk takes 10.4 KB of workspace.
+// Rows that go through the launches together: a chunk takes 18.5 KB of workspace.
 int sample_rows_at_once(int M, int N) {
-  const int most = 16384 / sample_chunks(N);
+  const int most = 8192 / sample_chunks(N);
   return M < most ? M : most;
 }
 

@@ -89,7 +89,7 @@ w4a16_status_t w4a16_kv_attention_shared(const uint16_t *q, int64_t q_stride, co
                                          int max_own, int q_heads, void *workspace, size_t workspace_bytes,
                                          void *stream);
 
-/* Bytes of workspace w4a16_sample needs (0 for invalid arguments): 10.4 KB for each 8192 logits of a row, 170 MB at most
+/* Bytes of workspace w4a16_sample needs (0 for invalid arguments): 18.5 KB for each 8192 logits of a row, 152 MB at most
  * (more rows take turns). */
 size_t w4a16_sample_workspace_bytes(int M, int N);
 

@@ -139,7 +139,7 @@ def test_sample_refuses_bad_arguments(L):
     assert sample(M=0) == OK and sample(M=0, x=None, tokens=None, ws=None, ws_bytes=0) == OK
     # rows go through in turns of 16384 chunks of 8192 tokens
     ws = L.w4a16_sample_workspace_bytes
-    assert ws(65536, 2 ** 20) == ws(128, 2 ** 20) < 200 << 20 and ws(65536, 1) == ws(16384, 1) > ws(16383, 1)
+    assert ws(65536, 2 ** 20) == ws(64, 2 ** 20) < 200 << 20 and ws(65536, 1) == ws(8192, 1) > ws(8191, 1)
     assert ws(0, 5) == 0 and ws(5, 0) == 0
     assert L.w4a16_sample_workspace_bytes(-1, 5) == 0 and L.w4a16_sample_workspace_bytes(5, 2 ** 20 + 1) == 0
 
