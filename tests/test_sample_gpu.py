@@ -132,6 +132,22 @@ def test_flat_and_steep_rows(dtype, M, N, spread, temperature, limits):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N", [9001, 150001])
+@pytest.mark.parametrize("value", [-np.inf, "lowest", -1e4, -25.0])
+def test_rows_masked_but_for_a_few(dtype, N, value):
+    """A grammar's mask: limits that are not reached before the masked tokens, which have no weight or (-25) a small one."""
+    say("sample masked", dtype, N, value)
+    rng = np.random.default_rng(N)
+    M = 6
+    x = np.full((M, N), float(torch.finfo(dtype).min) if value == "lowest" else value)
+    for r in range(M):
+        at = rng.integers(0, N, size=[1, 3, 30, 200, 1500, 4000][r])
+        x[r, at] = 3 * rng.normal(size=len(at))
+    Problem(x, dtype, rng.random(M), temperature=[1.0, 0.2, 1.0, 0.8, 1.3, 0.6], top_k=[50, 1000, 400, 1000, 5000, 6000],
+            top_p=[1.0, 0.9, 1.0, 0.9999999, 1.0, 0.95], min_p=[0.0, 0.0, 1e-30, 0.0, 0.0, 0.01]).check()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("N", [5, 700, 20000])
 def test_equal_logits(dtype, N):
     """Ties everywhere: limits cut between equal tokens by their index."""
