@@ -17,6 +17,7 @@ constexpr int kSplitSteps = 768;     // of 128 entries and 32 rows
 constexpr int kOwnFill = 2048;       // workgroups of the requests' own entries
 constexpr int kSplitFill = 512;      // workgroups of the split form
 constexpr int kPartTiles = 4;        // tiles of a part at least
+constexpr int kPartFill = 48;        // workgroups of fewer tiles, if there are fewer
 constexpr int kOwnOfTile = 256;      // own entries that take as long as a tile of shared ones
 
 w4a16_status_t check_shared(const w4a16_kv_cache_t* cache, int tokens, int requests, int max_new, int max_shared,
@@ -89,7 +90,9 @@ KvSharedArgs shared_args(const w4a16_kv_cache_t* cache, int tokens, int requests
     // tile, 83 and 111; with up to 20 of their own 31 and 39).  Two where tiles are many (24 behind 100001: 87;
     // for one 99), which eight waves of heads of 256 leave no room for.  Each
     // row and part costs D + 5 floats written and read again: four tiles at least (us, 2 / 3 / 4 / 6: 61
-    // tokens of 16 requests behind 6000, 16 heads of 64 over 4, 28.0 / 27.0 / 24.5 / 25.7).
+    // tokens of 16 requests behind 6000, 16 heads of 64 over 4, 28.0 / 27.0 / 24.5 / 25.7), fewer where that
+    // makes less than 48 workgroups (64 tokens behind 500, 10 heads of 256 over 2, 1 / 2 / 8 tiles 23.9 / 25.0
+    // / 35.6; behind 4000 37.7 / 32.0 and 33.7 for 4).
     const int tile_tokens = kv_tile_rows(cache->dim, cache->type) / a.group;
     const int64_t workgroups = (int64_t)((tokens + tile_tokens - 1) / tile_tokens) * cache->heads;
     const int64_t tiles = workgroups * (max_shared / kKvTile);
@@ -97,7 +100,9 @@ KvSharedArgs shared_args(const w4a16_kv_cache_t* cache, int tokens, int requests
     const int64_t fill = own >= kOwnOfTile * tiles                                              ? 128
                          : tiles > 256 * 32 && kv_tile_waves(cache->dim, cache->type) == 4 ? 512
                                                                                            : 256;
-    const int64_t wanted = std::min<int64_t>({fill / workgroups, max_shared / (kPartTiles * kKvTile), kKvMaxParts});
+    const int64_t few = std::min<int64_t>(kPartFill / workgroups, (max_shared + kKvTile - 1) / kKvTile);
+    const int64_t wanted =
+        std::min<int64_t>({fill / workgroups, std::max<int64_t>(max_shared / (kPartTiles * kKvTile), few), kKvMaxParts});
     const int64_t parts = wanted > 1 ? wanted : 1;
     a.part = (int)((max_shared + parts * kKvTile - 1) / (parts * kKvTile)) * kKvTile;
     a.parts = (max_shared + a.part - 1) / a.part;

@@ -71,7 +71,8 @@ size_t w4a16_kv_attention_shared_workspace_bytes(int tokens, int requests, int m
  * request lies in page
  *   block_table[0][j / P] for j < s,   block_table[r][j / P] from there on,
  * so the shared entries are read once for all requests (those columns of the other rows are
- * not looked at).  s need not end a page.  Rows, positions and masks are those of
+ * not looked at).  s need not end a page.  (Partial results are joined for that: from some 500
+ * shared entries on it is the faster call.)  Rows, positions and masks are those of
  * w4a16_kv_attention: the row at position pos attends entries 0 .. pos (also where pos < s).
  * max_new bounds the requests' new tokens, max_own their entries from s on (entries from
  * s + max_own on are unread); rows past max_new stay unwritten.
