@@ -74,6 +74,13 @@ constexpr int kHeld = 8;                              // listed tokens that a th
 static_assert(kChunk == 1 << (62 - kChunkScale) && kChunk <= 1 << (kBinCount - kBinScale - 1), "sums fit");
 static_assert(kSub == kSampleThreads && kChunks * kScanWaves <= kSampleThreads && kBuckets <= kScanThreads && kSorted == kSampleThreads, "a thread each");
 
+// (2^f - 1) / f for |f| <= 1/2: the polynomial through it at the nine Chebyshev points, which leaves 2^f off by
+// 2^-44.6 of it.
+struct SampleSeries {
+  double c[9] = {6.931471805599453e-01,  2.402265069581299e-01,  5.5504108664760424e-02,
+                 9.618129159402558e-03,  1.3333558179043112e-03, 1.5403455852453838e-04,
+                 1.525268684626772e-05, 1.3255224878668817e-06, 1.0203121063391729e-07};
+};
 struct SampleArgs {
   const void* logits;
   int64_t stride;
@@ -97,6 +104,7 @@ struct SampleArgs {
   uint32_t* listed;    // [M][chunks] tokens in lo .. hi
   uint2* list;         // [M][chunks][kListed] these: logit, token
   struct SampleCut* cut;      // [M]
+  SampleSeries series;        // for the scan: literals would be loaded anew for each weight
 };
 
 // Where a row's limits lie.
@@ -162,13 +170,6 @@ __device__ __forceinline__ double sample_log_weight(float v, float top, double i
   return v == top ? 0.0 : ((double)v - (double)top) * inv_t;
 }
 typedef uint32_t sample_u32x2 __attribute__((ext_vector_type(2)));
-// (2^f - 1) / f for |f| <= 1/2: the polynomial through it at the nine Chebyshev points, which leaves 2^f off by
-// 2^-44.6 of it.
-struct SampleSeries {
-  double c[9] = {6.931471805599453e-01,  2.402265069581299e-01,  5.5504108664760424e-02,
-                 9.618129159402558e-03,  1.3333558179043112e-03, 1.5403455852453838e-04,
-                 1.525268684626772e-05, 1.3255224878668817e-06, 1.0203121063391729e-07};
-};
 // 2^t times 2^scale for t <= 0, below 2^-1000 as there.  2^t = 2^n 2^f with |f| <= 1/2.  n + scale appears in the low
 // bits of a sum with 1.5 * 2^52 and is added to the exponent's: conversions to and from fp64, rint and ldexp take
 // four times as long as a sum (256 tempered rows of 262144: 70 us with them, 64 without).
@@ -536,15 +537,12 @@ __global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs
   // f(logit, weight times 2^scale), four at a time: more would take too many registers.  Where the
   // largest logit is moderate one fma gives the exponent, off by 2^-41 for all alike.
   const double inv_t = p.inv_t * kLog2E;
-  SampleSeries series;      // in scalar registers: otherwise each weight's instructions load them again
-#pragma unroll
-  for (double& c : series.c) asm("" : "+s"(c));
   auto weights = [&](int log2_scale, auto&& f) W4K_INLINE {
     const double away = -(double)top * inv_t;
     if (away < 4096.0 && away > -4096.0) {
 #pragma unroll
       for (int x = 0; x < kLane; ++x) {
-        f(v[x], sample_exp2(__builtin_fma((double)v[x], inv_t, away), log2_scale, series));
+        f(v[x], sample_exp2(__builtin_fma((double)v[x], inv_t, away), log2_scale, a.series));
         if (x % 4 == 3) __builtin_amdgcn_sched_barrier(0);
       }
     } else {
@@ -552,7 +550,7 @@ __global__ __launch_bounds__(kScanThreads, 8) void sample_scan_kernel(SampleArgs
       for (int x = 0; x < kLane; ++x) {
         float y = v[x];
         asm("" : "+v"(y));      // (both sides' conversions in front of the branch would take all registers)
-        f(y, sample_exp2(sample_log_weight(y, top, p.inv_t) * kLog2E, log2_scale, series));
+        f(y, sample_exp2(sample_log_weight(y, top, p.inv_t) * kLog2E, log2_scale, a.series));
         if (x % 4 == 3) __builtin_amdgcn_sched_barrier(0);
       }
     }
