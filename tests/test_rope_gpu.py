@@ -58,7 +58,7 @@ def close(got, want):
 SHAPES = [  # T, HQ, H, D, rot
     (1, 1, 1, 64, 64), (1, 10, 2, 256, 256), (2, 5, 1, 128, 128), (3, 32, 8, 128, 64), (7, 7, 7, 64, 16), (5, 3, 1, 256, 8),
     (63, 9, 3, 128, 120), (65, 16, 4, 64, 32), (33, 8, 2, 256, 64), (1, 64, 1, 64, 56), (1030, 32, 8, 128, 128),
-    (4099, 4, 1, 64, 64), (2050, 10, 2, 256, 128), (9001, 1, 1, 128, 128),
+    (4099, 4, 1, 64, 64), (2050, 10, 2, 256, 128), (9001, 1, 1, 128, 128), (1500, 40, 3, 64, 64), (2, 20001, 9999, 64, 64),
 ]
 
 

@@ -210,6 +210,26 @@ def test_infinities_nan_and_masked_rows(dtype, N):
     assert (Problem(x, dtype, None).check()[[1, 3]] == [0, N // 3]).all()
 
 
+@pytest.mark.parametrize("M,N,params", [(8200, 9, True), (8200, 9, False), (300, 260001, False), (65536, 1, True)])
+def test_rows_that_take_turns(M, N, params):
+    """More rows than go through the launches together; a few of each turn's ends are looked at."""
+    say("sample turns", M, N, params)
+    rng = np.random.default_rng(M)
+    x = torch.from_numpy(rng.normal(size=(min(M, 512), N)).astype(np.float32)).cuda()
+    x = x.repeat(-(-M // len(x)), 1)[:M].contiguous()
+    u, t = rng.random(M).astype(np.float32), rng.uniform(0.3, 2, M).astype(np.float32)
+    k = rng.integers(0, 9, M) if params else None
+    tokens, share = w4.sample(x, f32(u), f32(t), None if k is None else i32(k), f32(t / 2) if params else None)
+    turn = 8192 // -(-N // 8192)
+    for r in sorted({0, 1, turn - 1, turn, turn + 1, M // 2, M - 2, M - 1} & set(range(M))):
+        p = Problem(x[r:r + 1].cpu(), torch.float32, u[r:r + 1], t[r:r + 1], None if k is None else k[r:r + 1],
+                    t[r:r + 1] / 2 if params else None)
+        assert int(tokens[r]) == p.want()[0][0], r
+        one, part = w4.sample(*p.args())
+        assert int(one[0]) == int(tokens[r]) and float(part[0]) == float(share[r])
+    assert ((tokens >= 0) & (tokens < N)).all()
+
+
 def test_shares_follow_the_distribution():
     """Uniforms spread evenly over [0, 1) give each token as often as its weight says (within one)."""
     say("sample frequencies")

@@ -91,6 +91,9 @@ FORMS = [
     ("large pages", 1, 4, 128, 256, [800, 700], [1, 4], 600),
     ("parts", 1, 2, 64, 16, [3001, 3010], [1, 1], 2990),
     ("parts of large heads", 1, 5, 256, 128, [1700, 1650], [1, 2], 1640),
+    ("parts of a tile", 1, 5, 256, 64, [520] * 40, [1] * 40, 500),
+    ("parts beside long own entries", 4, 2, 64, 32, [900 + i for i in range(70)], [1] * 70, 330),
+    ("parts of many tiles", 8, 4, 64, 128, [4004 + i % 3 for i in range(34)], [1] * 34, 4000),
     ("empty requests", 2, 4, 128, 32, [90, 0, 95, 0, 100], [0, 0, 1, 0, 1], 70),
     ("positions among the shared entries", 1, 4, 64, 16, [200, 50, 3, 120], [1, 4, 5, 2], 150),
     ("rows before the first entry", 1, 2, 64, 16, [40, 1, 3], [1, 3, 5], 30),
