@@ -3,19 +3,20 @@
 // With C = (falling logit, rising index) as one 64-bit number every limit is "the tokens up
 // to some C": top_k's is the C of the k-th token, top_p's that of the first token at which
 // the running sum of weights reaches its share.  So nothing is sorted: a histogram over
-// buckets of logits (1 / 12 of a temperature wide) tells which buckets the limits lie in, and
+// buckets of logits (1 / 12 of a temperature or 1 / 18 wide) tells which buckets the limits lie in, and
 // only those buckets' tokens are looked at one by one.
 //
 // Launches.  scan: a workgroup reads a chunk of 8192 logits into registers; its largest
 // logit and its histogram, or (rows without limits) each wave's largest and sum of weights.
 // cut: a workgroup a row adds the chunks' histograms and finds the buckets lo .. hi that the
-// limits lie in.  collect: reads the logits again and lists the tokens of these buckets; where the
-// chunks are few each of its workgroups makes the cut for itself (see kCutAlone).  draw: a workgroup a row finds the
-// last kept token among the listed ones, adds the kept weights of each chunk, picks a
-// chunk and looks up the token in it (without limits: a wave's 1024 logits).  A call without limits
-// has scan and draw alone.  A row whose
-// chunks list thousands of tokens (flat rows, ties) is gone through by waves, a chunk each, from the lists or, where
-// a list is too short, from the logits.
+// limits lie in.  collect: reads the logits again and lists the tokens of these buckets; where
+// the chunks are few each of its workgroups makes the cut for itself (kCutAlone), and
+// where min_p is the first limit it adds up what that keeps and lists nothing.  draw: a
+// workgroup a row finds the last kept token among the listed ones, adds the kept weights of
+// each chunk, picks a chunk and looks up the token in it (without limits: a wave's 1024
+// logits).  A call without limits has scan and draw alone.  A row whose chunks list
+// thousands of tokens (flat rows, ties) is gone through by waves, a chunk each, from the lists
+// or, where a list is too short, from the logits.
 //
 // Weights exp((logit - largest) / temperature) are computed in fp64 and added as integers of
 // 2^-e (e = 62 - log2 N for a row: its sum stays below 2^63), or in a fixed order: sums do not
@@ -26,10 +27,10 @@
 // What bounds it.  Many rows: the scan, at the rate of its fp64 weights or of memory, whichever is
 // slower (256 rows of 262144 fp32 without limits: 57 us for 268 MB, 4.7 TB/s, and 7 for the
 // draw; of bf16 the same together 58; 48 rows of bf16 with top_p and min_p: 12.5 for 25 MB and every
-// weight, cut 7.0, collect 9.1, draw 19).  One row: the latency of the stages behind each other, each with two or
-// three trips to memory (262144 fp32, top_k and top_p: scan 4.0, collect with its cut 9.8, draw 8.6).
+// weight, cut 7.0, collect 9.8, draw 18).  One row: the latency of the stages behind each other, each with two or
+// three trips to memory (262144 fp32, top_k and top_p: scan 4.0, collect with its cut 9.8, draw 8.3).
 // A draw's workgroup has a CU to itself and is bound by its own instructions: what one wave can do
-// it does alone, 11 us before instead of 8.6, and 25 instead of 19 for the 48.
+// it does alone, 11 us before instead of 8.3, and 25 instead of 18 for the 48.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -72,7 +73,9 @@ constexpr int kBinScale = 36, kBinCount = 50;
 constexpr int kSorted = 1024;                         // listed tokens that are sorted at most
 constexpr int kHeld = 8;                              // listed tokens that a thread of the draw holds
 static_assert(kChunk == 1 << (62 - kChunkScale) && kChunk <= 1 << (kBinCount - kBinScale - 1), "sums fit");
-static_assert(kSub == kSampleThreads && kChunks * kScanWaves <= kSampleThreads && kBuckets <= kScanThreads && kSorted == kSampleThreads, "a thread each");
+static_assert(kSub == kSampleThreads && kChunks * kScanWaves <= kSampleThreads && kBuckets <= kScanThreads &&
+                  kSorted == kSampleThreads,
+              "a thread each");
 
 // (2^f - 1) / f for |f| <= 1/2: the polynomial through it at the nine Chebyshev points, which leaves 2^f off by
 // 2^-44.6 of it.
@@ -1076,8 +1079,8 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
 #pragma unroll
       for (int e = 0; e < kHeld; ++e) w[e] = c[e] != ~0ull ? weight_of(c[e]) : 0;
     }
-    // calls f(C, its weight as a function) for the thread's tokens of a chunk, a wave's: those listed, or (of a chunk that has
-    // more of them than its list holds) those in lo .. hi
+    // calls f(C, its weight as a function) for the thread's tokens of a chunk, a wave's: those listed, or (of a chunk
+    // that has more of them than its list holds) those in lo .. hi
     auto visit_chunk = [&](int chunk, auto&& f) W4K_INLINE {
       const int n = (int)sh.listed[chunk];
       constexpr int AHEAD = 4;      // loads on their way
