@@ -173,11 +173,14 @@ __device__ __forceinline__ double sample_log_weight(float v, float top, double i
   return v == top ? 0.0 : ((double)v - (double)top) * inv_t;
 }
 typedef uint32_t sample_u32x2 __attribute__((ext_vector_type(2)));
-// 2^t times 2^scale for t <= 0, below 2^-1000 as there.  2^t = 2^n 2^f with |f| <= 1/2.  n + scale appears in the low
-// bits of a sum with 1.5 * 2^52 and is added to the exponent's: conversions to and from fp64, rint and ldexp take
-// four times as long as a sum (256 tempered rows of 262144: 70 us with them, 64 without).
+// 2^(t + scale) for t <= 0 and |scale| <= 62, a result below 2^-1000 as 2^-1000.  2^t = 2^n 2^f with |f| <= 1/2.
+// n + scale appears in the low bits of a sum with 1.5 * 2^52 and is added to the exponent's: conversions to and from
+// fp64, rint and ldexp take four times as long as a sum (256 tempered rows of 262144: 70 us with them, 64 without).
+// That holds while the result is a normal number, so it is n + scale that -1000 bounds.  (With n alone bounded, the
+// -36 of a chunk's factor carried the exponent past its end for chunks 684 temperatures below the row's largest
+// logit: 2^-1036 came out as -2^1012.)
 __device__ __forceinline__ double sample_exp2(double t, int scale, const SampleSeries& series = SampleSeries{}) {
-  t = fmax(t, -1000.0);
+  t = fmax(t, -1000.0 - (double)scale);
   const double to_int = 0x1.8p52 + (double)scale, shifted = t + to_int, f = t - (shifted - to_int);
   double y = series.c[8];
 #pragma unroll

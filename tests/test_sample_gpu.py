@@ -303,3 +303,38 @@ def test_captured_and_on_two_streams():
         assert torch.equal(tokens, want) and torch.equal(got, want) and torch.equal(share, part)
     p.x, p.u, p.top_k = args[0].cpu().double().numpy(), args[1].cpu().numpy(), args[3].cpu().numpy()
     assert tokens.cpu().tolist() == [t for t, _ in p.want()]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N", [(5, 262144), (10, 262144), (1, 1 << 20), (5, 24576)])
+@pytest.mark.parametrize("temperature", [1.0, 0.01])
+def test_far_masks_beside_a_tail_that_counts(dtype, M, N, temperature):
+    """One token on top, 8192 others masked by a finite value far below it, the rest 21.5 temperatures below it, and a
+    top_p that cuts through these.
+
+    The tail's weight w is held to half of 2^-e, e = 62 - log2(N): N tokens move the border of top_p, and the drawn token
+    along the tail, by half of N 2^-e / w each, beside a token for either border's rounding.  The sum of kept weights is
+    off by that many tokens."""
+    say("sample far masks", dtype, M, N, temperature)
+    far = [-690.0, -1000.0, -1e4, None, -7000.0]
+    x = np.full((M, N), -21.5 * temperature)
+    x[:, :8192] = -np.inf
+    x[:, 100] = 0.0
+    for r in range(M):
+        piece = 1 + r % (N // 8192 - 1)
+        x[r, 8192 * piece:8192 * (piece + 1)] = float(torch.finfo(dtype).min) if far[r % 5] is None else far[r % 5] * temperature
+    tail = (N - 16384) * np.exp(-21.5)
+    u = np.array([0.0, 1.0, 1.0 / (1.0 + 0.2 * tail), 0.5, 1.0 - 2.0 ** -24] * 2)[:M]
+    p = Problem(x, dtype, u, temperature=[temperature] * M, top_p=[(1.0 + 0.5 * tail) / (1.0 + tail)] * M)
+    level = p.x[:, 8192:].max()      # the tail's logit
+    w = np.exp(level / float(p.floats[0][0]))
+    off = N * 2.0 ** ((N - 1).bit_length() - 62)
+    tokens, share = (t.cpu().numpy() for t in w4.sample(*p.args()))
+    for r, (token, part) in enumerate(p.want()):
+        if token == 100:
+            assert tokens[r] == 100, (r, tokens[r], share[r], part)
+        else:
+            place = np.flatnonzero(p.x[r] == level)
+            assert p.x[r, tokens[r]] == level, (r, tokens[r], token, share[r], part)
+            assert abs(np.searchsorted(place, tokens[r]) - np.searchsorted(place, token)) <= off / w + 2, (r, tokens[r], token)
+        assert abs(share[r] - part) <= (ref.F32_STEP + off + 3 * w) * part, (r, share[r], part)
