@@ -65,6 +65,15 @@ __device__ __forceinline__ float rope_sum(float v) {
   return v;
 }
 
+// 1 / sqrt(v).  The instruction takes a subnormal v (rows below 2^-63) for 0: TINY brings small ones up by an even power
+// of two.  An eps of kRopeTiny or more leaves none, and in its kernels the question would cost 1 to 2%.
+constexpr float kRopeTiny = 0x1p-100f;
+template <bool TINY>
+__device__ __forceinline__ float rope_rsq(float v) {
+  const bool small = TINY && v < kRopeTiny;
+  return __builtin_amdgcn_rsqf(small ? v * 0x1p64f : v) * (small ? 0x1p32f : 1.0f);
+}
+
 __device__ __forceinline__ rope_f32x4 rope_f32(uint2 u) {
   return rope_f32x4{bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y)};
 }
@@ -72,7 +81,9 @@ __device__ __forceinline__ uint2 rope_bf16(rope_f32x4 v) {
   return __builtin_bit_cast(uint2, __builtin_convertvector(v, rope_bf16x4));
 }
 
-template <int D, bool NORM, bool PAIRS>
+// NORM: kRopeNormTiny with an eps below kRopeTiny.
+constexpr int kRopeNorm = 1, kRopeNormTiny = 2;
+template <int D, int NORM, bool PAIRS>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
   constexpr int L = D / 8, HEADS = kWave / L;
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -96,7 +107,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
   uint2 next[2];
   load(first + lane / L, next);
   rope_f32x4 factor[2][2];      // of queries and keys
-  if constexpr (NORM) {
+  if constexpr (NORM != 0) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint16_t* p = i ? a.kw : a.qw;
@@ -127,13 +138,13 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
     rope_f32x4 x[2] = {rope_f32(next[0]), rope_f32(next[1])};
     if (h0 + HEADS < last) load(h + HEADS, next);
     const bool is_q = h < a.q_heads;
-    if constexpr (NORM) {
+    if constexpr (NORM != 0) {
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum = __builtin_fmaf(x[j][e], x[j][e], sum);
-      const float r = __builtin_amdgcn_rsqf(rope_sum<L>(sum) * (1.0f / D) + a.eps);
+      const float r = rope_rsq<NORM == kRopeNormTiny>(rope_sum<L>(sum) * (1.0f / D) + a.eps);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -169,10 +180,14 @@ void rope_launch(const RopeArgs& a, int flags, hipStream_t st) {
                        dim3(kRopeThreads), 0, st, a);
   };
   const bool pairs = flags & W4A16_ROPE_INTERLEAVED;
-  if (flags & W4A16_ROPE_NORM)
-    pairs ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+  auto with_pairs = [&](auto norm) { pairs ? go(norm, std::true_type{}) : go(norm, std::false_type{}); };
+  using std::integral_constant;
+  if (!(flags & W4A16_ROPE_NORM))
+    with_pairs(integral_constant<int, 0>{});
+  else if (a.eps >= kRopeTiny)
+    with_pairs(integral_constant<int, kRopeNorm>{});
   else
-    pairs ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
+    with_pairs(integral_constant<int, kRopeNormTiny>{});
 }
 
 bool rope_stride(int64_t stride, int64_t row) { return stride >= row && stride % 8 == 0 && stride <= (1LL << 40); }

@@ -42,10 +42,12 @@ extern "C" {
  * axis whose section pair i lies in (sections: a HOST array of `axes` pair counts that
  * sum to rot / 2, in order; NULL with one axis).
  *   q_weight, k_weight  bf16 [D];  inv_freq  fp32 [rot / 2];  positions  int32 [axes][T]
- * Squares are summed, factors applied and pairs turned in fp32; an angle is reduced to one
+ * Squares are summed, factors applied and pairs turned in fp32 (subnormal means and sums
+ * count; a head whose squares' sum is beyond fp32 becomes 0); an angle is reduced to one
  * turn in fp64, off by 2^-22 of a turn at most for every int32 position where frequencies
- * are not above 1 (by 2^-25 for positions below 2^20); one rounding to bf16 at the end.  H 0 (a layer that reads another's keys) and HQ 0 are allowed, as is rot 0
- * (no rotation; inv_freq and positions may be NULL).
+ * are not above 1 (by 2^-25 for positions below 2^20); one rounding to bf16 at the end.
+ * H 0 (a layer that reads another's keys) and HQ 0 are allowed, as is rot 0 (no rotation;
+ * inv_freq and positions may be NULL).
  * q_out may be q and k_out may be k (with the same stride); otherwise outputs do not
  * overlap inputs.
  * D 64, 128 or 256; rot a multiple of 8, at most D; T <= 2^20; HQ, H <= 2^16.

@@ -194,3 +194,23 @@ def test_captured_and_on_another_stream():
         side.synchronize()
         assert torch.equal(other[0], q) and torch.equal(other[1], k)
     close(out[0], p.want(p.q, p.weights[0]))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("exponent", [-60, -63, -64, -66])
+def test_rows_whose_mean_square_is_subnormal(D, exponent):
+    """eps 0: the mean square lies below fp32's least normal number, 2^-126, and is still what the row is divided by.
+
+    Elements' squares are multiples of 2^-149 there, each off by 2^-150: beside a mean of 2^(2 exponent) or more that is
+    2^(-150 - 2 exponent) of it, for the sum and again for the mean, halved by the root.  (2^-18 at worst.)"""
+    say("rope subnormal", D, exponent)
+    rng = np.random.default_rng(D - exponent)
+    p = Problem(17, 5, 4, 2, D, D // 2)
+    for x in (p.q, p.k):
+        signs = torch.from_numpy(rng.choice([-1.0, 1.0], size=tuple(x.shape)) * rng.uniform(1, 2, size=tuple(x.shape)))
+        x.copy_((signs * 2.0 ** exponent).to(torch.bfloat16))
+    q, k = w4.qk_norm_rope(p.q, p.k, *p.weights, **p.args(), eps=0.0)
+    for got, x, w in ((q, p.q, p.weights[0]), (k, p.k, p.weights[1])):
+        y, bound = p.want(x, w, eps=0.0)
+        size = bound / (32 * ref.F32_STEP)
+        close(got, (y, bound + size * 2.0 ** (-150 - 2 * exponent)))
