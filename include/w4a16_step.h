@@ -118,7 +118,12 @@ size_t w4a16_sample_workspace_bytes(int M, int N);
  * drawn; a row of nothing else gives token -1 and share 0.  With a logit of +infinity only
  * those of +infinity have weight.  A row with a NaN gives its first NaN and share NaN.
  * Sums of weights are of integers, or in a fixed order: the same call gives the same tokens.
- * (A weight counts to 2^-62 N of the largest: tokens of less may be passed over, also as "the last kept one".)
+ * A weight counts in them to 2^-49 of the row's largest, or to 2^-62 N where that is more
+ * (tokens of less may be passed over, also as "the last kept one").  In rows with top_p, min_p or
+ * a top_k above 512 the kept weights far in front of a limit, and the sum that top_p is a share
+ * of, count to 2^-37 of the largest among 8192 neighbours: sums are off by N 2^-37 of the
+ * largest weight at most (2^-17 for 2^20 tokens), and so are top_p's limit, the place that u
+ * gives, and share.
  * workspace: w4a16_sample_workspace_bytes(M, N) bytes, not initialised.
  * M <= W4A16_SAMPLE_MAX_ROWS, N <= W4A16_SAMPLE_MAX_N.  N 0: tokens -1, shares 0.
  * Alignment: logits by their type (rows need no more), fp32 and int32 arrays 4, workspace 16.

@@ -338,3 +338,22 @@ def test_far_masks_beside_a_tail_that_counts(dtype, M, N, temperature):
             assert p.x[r, tokens[r]] == level, (r, tokens[r], token, share[r], part)
             assert abs(np.searchsorted(place, tokens[r]) - np.searchsorted(place, token)) <= off / w + 2, (r, tokens[r], token)
         assert abs(share[r] - part) <= (ref.F32_STEP + off + 3 * w) * part, (r, share[r], part)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N", [1000, 8192, 100003, 1 << 20])
+@pytest.mark.parametrize("log2_weight", [-36.9, -37.5])
+@pytest.mark.parametrize("limits", [dict(), dict(top_k=400), dict(top_p=1 - 2.0 ** -24), dict(min_p=1e-30), dict(top_k=1 << 20, min_p=1e-30)])
+def test_small_weights_among_large_ones_count_as_the_header_says(dtype, N, log2_weight, limits):
+    """One token of 8192 on top, the rest near half of the 2^-36 that sums with limits hold weights to: sums are off by
+    N 2^-37 then, and by N times half of 2^-49 or 2^-62 N otherwise."""
+    say("sample small weights", dtype, N, log2_weight, limits)
+    x = np.full((3, N), log2_weight * np.log(2.0))
+    x[:, ::8192] = 0.0
+    p = Problem(x, dtype, [0.0, 0.3, 0.9], **{k: [v] * 3 for k, v in limits.items()})
+    tokens, share = (t.cpu().numpy() for t in w4.sample(*p.args()))
+    coarse = limits and limits.get("top_k") != 400
+    off = N * (2.0 ** -37 if coarse else max(2.0 ** -50, 2.0 ** ((N - 1).bit_length() - 63)))
+    for r, (token, part) in enumerate(p.want()):
+        assert tokens[r] == token, (r, tokens[r], token)
+        assert abs(share[r] - part) <= (ref.F32_STEP + off * part) * part, (r, share[r], part)      # (part: 1 / the sum)
