@@ -357,3 +357,21 @@ def test_small_weights_among_large_ones_count_as_the_header_says(dtype, N, log2_
     for r, (token, part) in enumerate(p.want()):
         assert tokens[r] == token, (r, tokens[r], token)
         assert abs(share[r] - part) <= (ref.F32_STEP + off * part) * part, (r, share[r], part)      # (part: 1 / the sum)
+
+
+def test_tokens_and_shares_beside_a_calls_rows_stay_as_they_were():
+    """Rows in the middle of wider arrays, with a workspace larger than asked for."""
+    say("sample guards")
+    x, u, rng = rows(17, 4, 30000)
+    limited = dict(top_p=[0.9, 1.0, 0.5, 0.99], top_k=[0, 40, 0, 3000], min_p=[0.0, 0.0, 0.02, 0.0])
+    for params in (limited, {}):
+        p = Problem(x, torch.float32, u, temperature=[1.0, 0.7, 0.0, 1.3], **params)
+        ws = torch.full((w4.w4a16_sample_workspace_bytes(4, 30000) + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+        tokens = torch.full((6,), -7, dtype=torch.int32, device="cuda")
+        share = torch.full((6,), -7.0, device="cuda")
+        w4.w4a16_sample(*p.args(), tokens[1:5], share[1:5], ws)
+        want = p.want()
+        assert tokens.cpu().tolist() == [-7, *(t for t, _ in want), -7]
+        assert share[0] == -7 and share[5] == -7 and (ws[-64:] == 0xFF).all()
+        off = ref.F32_STEP + 30000 * 2.0 ** (15 - 63) + 2.0 ** -50
+        assert all(abs(float(share[1 + r]) - part) <= off * part for r, (_, part) in enumerate(want))
