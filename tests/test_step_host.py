@@ -254,3 +254,12 @@ def test_shared_entries_by_hand():
     table = np.array([[3, 1, 7], [9, 4, 5]])
     assert ref.entry_table(table, [5, 6], 2, 3, 2).tolist() == [[6, 7, 2, 3, 14, -1], [6, 7, 2, 9, 10, -1]]
     assert ref.entry_table(table, [5, 2], 2, 0, 9).tolist() == [[6, 7, 2, 3, 14], [18, 19, 8, 9, 10]]
+
+
+@pytest.mark.parametrize("N", [1, 8192, 8193, 100003, 262144, 1 << 20])
+def test_sampling_takes_turns_of_8192_chunks(L, N):
+    """A chunk is 8192 logits: no more rows than 8192 chunks hold have workspace, whatever a call's rows."""
+    ws = L.w4a16_sample_workspace_bytes
+    turn = 8192 // -(-N // 8192)
+    assert ws(turn - 1, N) < ws(turn, N) == ws(turn + 1, N) == ws(65536, N)
+    assert ws(turn, N) < 153 * 10 ** 6
