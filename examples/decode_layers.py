@@ -1,7 +1,7 @@
 """Prompt, decode and verify steps of a small stack of W4 layers over the paged 8-bit cache.
 
     python examples/decode_layers.py [--layers 4] [--kind int8|fp8] [--steps 16] [--candidates 3]
-        [--rope-base 10000] [--share 640] [--temperature 0.8 [--top-k 50] [--top-p 0.95] [--min-p 0.02]]
+        [--rope-base 10000] [--share 2048 [--share-from 2048]] [--temperature 0.8 [--top-k 50] [--top-p 0.95] [--min-p 0.02]]
 
 Every weight product, the cache and its attention, the rotation and the sampling
 are the library's; torch allocates, normalises the hidden rows (root mean square, no
@@ -13,8 +13,8 @@ to verify), and its bookkeeping (w4a16_kv_plan) is made once for all layers:
   plan -> per layer: q/k/v products -> (head norms, positions rotated in) -> append -> attention
        -> o product -> MLP -> LM head -> largest logits, or tokens drawn from them
 
-Requests that begin with the same tokens can share their pages (Stack.share): steps of few
-tokens a request then read these once for all of them.
+Requests that begin with the same tokens can share their pages (Stack.share): from some 2000 of
+them on, steps of few tokens a request read these once for all requests (w4a16_kv_attention_shared).
 """
 from __future__ import annotations
 
@@ -99,7 +99,7 @@ class Stack:
     """Layers with a paged cache for `requests` requests of at most max_len tokens."""
 
     def __init__(self, layers=2, hidden=2560, ffn=10240, q_heads=10, kv_heads=2, dim=256, vocab=4096, requests=4,
-                 max_len=2048, page=64, kind="int8", window=0, seed=0, rope_base=None):
+                 max_len=2048, page=64, kind="int8", window=0, seed=0, rope_base=None, share_from=2048):
         self.embedding = Weights(vocab, hidden, seed + 100)      # tied: gathered rows in, LM head out
         self.layers = [Layer(hidden, ffn, q_heads, kv_heads, dim, seed + 1000 * (i + 1)) for i in range(layers)]
         self.heads, self.dim, self.page, self.max_len, self.window = (q_heads, kv_heads), dim, page, max_len, window
@@ -113,6 +113,9 @@ class Stack:
         self.inv_freq = None if rope_base is None else rope_base ** (-torch.arange(0, dim, 2) / dim).float().cuda()
         self.shared = 0                                          # entries that all requests begin with
         self.shared_len = torch.zeros((1,), dtype=torch.int32, device="cuda")
+        # fewer shared entries are read by each request for itself: joining partial results takes longer (4 requests, 10
+        # heads of 256 over 2: behind 512 entries 10.7 us instead of 9.1, 2048 12.1 and 12.5, 16384 23 instead of 28)
+        self.share_from = share_from
 
     def step(self, tokens, counts):
         """tokens [T]: counts[r] of each request, in request order.  (logits' argmax [T], final hidden rows [T, hidden])"""
@@ -147,7 +150,7 @@ class Stack:
 
     def attention(self, q, cache, seq, start, most):
         rows = most * (self.heads[0] // self.heads[1])
-        if self.shared and not self.window and rows <= 64:
+        if self.shared and self.shared >= self.share_from and not self.window and rows <= 64:
             return w4.kv_attention_shared(q, *cache, self.table, seq, start, self.shared_len, most, max_shared=self.shared,
                                           max_own=self.max_len - self.shared)
         return w4.kv_attention(q, *cache, self.table, seq, start, most, max_len=self.max_len, window=self.window)
@@ -203,13 +206,14 @@ def main():
     ap.add_argument("--candidates", type=int, default=3)
     ap.add_argument("--rope-base", type=float, help="norm queries and keys and rotate positions in, with this base")
     ap.add_argument("--share", type=int, default=0, help="tokens that all requests begin with (whole pages of 64)")
+    ap.add_argument("--share-from", type=int, default=2048, help="shared tokens from which steps read them once for all")
     ap.add_argument("--temperature", type=float, default=0.0, help="draw tokens (0: take the largest logits)")
     ap.add_argument("--top-k", type=int, default=0)
     ap.add_argument("--top-p", type=float, default=1.0)
     ap.add_argument("--min-p", type=float, default=0.0)
     a = ap.parse_args()
     prompts = [700, 64, 333, 5]
-    stack = Stack(layers=a.layers, kind=a.kind, rope_base=a.rope_base)
+    stack = Stack(layers=a.layers, kind=a.kind, rope_base=a.rope_base, max_len=2048 + a.share, share_from=a.share_from)
     generator = torch.Generator().manual_seed(1)
     if a.share:
         stack.share(torch.randint(0, 4096, (a.share,), dtype=torch.int32, generator=torch.Generator().manual_seed(2)).cuda())

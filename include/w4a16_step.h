@@ -73,9 +73,12 @@ size_t w4a16_kv_attention_shared_workspace_bytes(int tokens, int requests, int m
  * request lies in page
  *   block_table[0][j / P] for j < s,   block_table[r][j / P] from there on,
  * so the shared entries are read once for all requests (those columns of the other rows are
- * not looked at).  s need not end a page.  (Partial results are joined for that: from some 500
- * shared entries on it is the faster call.)  Rows, positions and masks are those of
- * w4a16_kv_attention: the row at position pos attends entries 0 .. pos (also where pos < s).
+ * not looked at).  s need not end a page.  Partial results are joined for that, which takes
+ * longer where shared entries are few: w4a16_kv_attention is faster behind some hundreds of
+ * them, by up to a factor of two; from 2000 of them on, 4000 in batches of some 32 requests with
+ * heads of 256, this call is as fast or faster, by up to a factor of the requests.
+ * Rows, positions and masks are those of w4a16_kv_attention: the row at position pos attends
+ * entries 0 .. pos (also where pos < s).
  * max_new bounds the requests' new tokens, max_own their entries from s on (entries from
  * s + max_own on are unread); rows past max_new stay unwritten.
  * max_new * HQ / H must not exceed 64: prompts' many rows read each entry once for many of

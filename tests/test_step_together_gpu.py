@@ -154,3 +154,31 @@ def test_the_example_stack_with_all_of_them(kind):
     assert diff < 0.04
     with pytest.raises(ValueError, match="share"):
         s.share(prompt)
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+def test_the_example_stack_reads_shared_entries_by_their_number(kind, monkeypatch):
+    """From share_from shared entries on by one call for all requests, else each for itself; the hidden rows are the same
+    (to the bound above)."""
+    import decode_layers as ex
+
+    say("example, share_from", kind)
+    g = torch.Generator().manual_seed(9)
+    prompt, own = (torch.randint(0, 1024, (n,), dtype=torch.int32, generator=g).cuda() for n in (64, 9))
+    calls = []
+    call = w4.kv_attention_shared
+    monkeypatch.setattr(w4, "kv_attention_shared", lambda *a, **k: (calls.append(1), call(*a, **k))[1])
+    rows = []
+    for share_from, made in ((64, 4), (0, 4), (65, 0)):
+        s = ex.Stack(layers=2, ffn=2560, vocab=1024, requests=3, max_len=128, page=32, kind=kind, rope_base=10000.0,
+                     share_from=share_from)
+        s.share(prompt)
+        calls.clear()
+        _, h = s.step(own, [5, 3, 1])
+        _, h1 = s.step(own[:3], [1, 1, 1])
+        assert len(calls) == made
+        rows.append(torch.cat([h, h1]).float())
+    assert torch.equal(rows[0], rows[1])
+    diff = float((rows[0] - rows[2]).norm() / rows[2].norm())
+    print("relative difference", diff)
+    assert diff < 0.04
