@@ -57,9 +57,9 @@ KvSharedArgs shared_args(const w4a16_kv_cache_t* cache, int tokens, int requests
   const int rows = a.split_tokens * a.group;
   a.row_groups = rows <= 16 ? 1 : (rows + 31) / 32;
   // Chunks of a request's own entries, which may begin inside one: of one step while the workgroups
-  // are few.  Measured (us in a graph, at most 512 / 1024 / 2048 / 4096): 64 requests with up to 2000 of
-  // their own 60.8 / 60.5 / 60.0 / 62.0, 24 37.6 / 32.1 / 31.3 / 35.5, 16 with up to 8000 59.6 / 50.4 /
-  // 49.6 / 50.2.
+  // are few.  Measured behind 8000, 32 heads of 128 over 8 (us in a graph, at most 512 / 1024 / 2048 / 4096): 64
+  // requests with up to 2000 of their own 56.2 / 56.2 / 55.4 / 59.9, 24 33.0 / 32.0 / 32.4 / 36.3, 16 with up to
+  // 8000 58.1 / 49.5 / 48.3 / 50.0.
   const int64_t own_groups = (int64_t)requests * cache->heads * a.row_groups;
   a.chunk_shift = 7;
   auto in_chunks = [&](int64_t n) { return (n + (1LL << a.chunk_shift) - 1) >> a.chunk_shift; };
@@ -67,17 +67,17 @@ KvSharedArgs shared_args(const w4a16_kv_cache_t* cache, int tokens, int requests
   a.chunks = max_own > 0 ? (int)in_chunks(max_own) + 1 : 0;
   // The form over the shared entries.  The split form's workgroup has 32 rows and a step of 128
   // entries, short ones side by side; the tile form converts an entry once for 128 rows.  The
-  // split form takes 64 rows, or more while its steps are few.  Measured (us in a graph, split / tile):
-  // 70 rows of 256 over 2 heads behind 1000 entries 12.2 / 26.2, 4000 15.8 / 25.2, 12000 25.3 / 29.1,
-  // 50000 53.5 / 42.9; 120 of 64 over 4 behind 1000 10.9 / 15.8, 8000 17.3 / 16.7; 96 of 128 over 8
-  // behind 8000 29.9 / 31.6, 100001 172 / 91; 250 of 256 over 2 behind 4000 28.5 / 25.7.
+  // split form takes 64 rows, or more (up to 128) while its steps are few.  Measured (us in a graph, split / tile):
+  // 70 rows of 256 over 2 heads behind 1000 entries 13.3 / 16.6, 4000 16.0 / 21.8, 12000 24.3 / 26.6,
+  // 50000 50.7 / 44.3; 120 of 64 over 4 behind 1000 10.6 / 12.7, 8000 14.5 / 16.4; 96 of 128 over 8
+  // behind 8000 22.3 / 24.7, 100001 149 / 73.
   a.part = kKvTile;
   const int rows_shared = tokens <= kWave ? tokens * a.group : kKvMaxSharedRows + 1;
   const int64_t groups = (int64_t)cache->heads * ((rows_shared + 31) / 32);
   if (max_shared > 0 && (rows_shared <= kKvSplitRows || (rows_shared <= kKvMaxSharedRows &&
                                                          groups * ((max_shared + 127) / 128) <= kSplitSteps))) {
     // Chunks of one step while their workgroups are fewer than the card holds (us, 256 / 512 / 1024 at most):
-    // 16 rows behind 100001, 8 heads of 128, 61.0 / 55.7 / 61.6; 64 behind 8000 29.9 / 31.0 / 39.6.
+    // 16 rows behind 100001, 8 heads of 128, 54.7 / 43.7 / 52.7; 64 behind 8000 18.4 / 20.0 / 24.8.
     a.part_shift = 7;
     while ((max_shared - 1) >> a.part_shift >= kKvMaxParts || groups * (max_shared >> a.part_shift) > kSplitFill)
       ++a.part_shift;
@@ -85,14 +85,14 @@ KvSharedArgs shared_args(const w4a16_kv_cache_t* cache, int tokens, int requests
     a.parts = (max_shared + a.part - 1) >> a.part_shift;
   } else if (max_shared > 0) {
     // Parts for a workgroup a CU, so that the requests' own run beside them, and for one in two where these take as
-    // long all the same: fewer partial results (64 single tokens behind 8000 and up to 2000 of their own, 512 entries
-    // a tile, for 2 / 1 / 0.5 a CU 66 / 58.7 / 54.5 us; 24 of them 31.4 for 1, 29.1 for 0.5; behind 30000, 136 a
-    // tile, 83 and 111; with up to 20 of their own 31 and 39).  Two where tiles are many (24 behind 100001: 87;
-    // for one 99), which eight waves of heads of 256 leave no room for.  Each
-    // row and part costs D + 5 floats written and read again: four tiles at least (us, 2 / 3 / 4 / 6: 61
-    // tokens of 16 requests behind 6000, 16 heads of 64 over 4, 28.0 / 27.0 / 24.5 / 25.7), fewer where that
-    // makes less than 48 workgroups (64 tokens behind 500, 10 heads of 256 over 2, 1 / 2 / 8 tiles 23.9 / 25.0
-    // / 35.6; behind 4000 37.7 / 32.0 and 33.7 for 4).
+    // long all the same: fewer partial results (32 heads of 128 over 8, 2 / 1 / 0.5 a CU in us: 64 single tokens
+    // behind 8000 and up to 2000 of their own, 512 entries a tile, 65 / 61 / 55.5; 24 of them 35 / 35 / 32.4; 64 behind
+    // 30000, 136 a tile, 90 / 79.5 / 107; behind 8000 with up to 20 of their own 40.5 / 36.7 / 41).  Two where tiles
+    // are many (24 behind 100001 75 / 90 / 164), which eight waves of heads of 256 leave no room for.  Each
+    // row and part costs D + 5 floats written and read again: four tiles at least (us, 2 / 3 / 4 / 6: 64
+    // tokens of 16 requests behind 6000, 16 heads of 64 over 4, 18.8 / 18.0 / 18.2 / 19.8), fewer where that
+    // makes less than 48 workgroups (64 tokens behind 500, 10 heads of 256 over 2, 18.4 instead of 27.3; behind 4000,
+    // where they are more, parts of one tile gain nothing: 26.5 and 26.0).
     const int tile_tokens = kv_tile_rows(cache->dim, cache->type) / a.group;
     const int64_t workgroups = (int64_t)((tokens + tile_tokens - 1) / tile_tokens) * cache->heads;
     const int64_t tiles = workgroups * (max_shared / kKvTile);

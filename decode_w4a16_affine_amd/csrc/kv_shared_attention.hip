@@ -7,11 +7,11 @@
 // form; kv_shared_join_kernel adds the parts of each row.
 //
 // Bound and measured (in a graph).  64 single tokens, 32 heads of 128 over 8, E4M3, behind 8000
-// shared and up to 2000 own entries, 148 MB: 53.5 us, of which the join takes 5.6 (14 MB of
+// shared and up to 2000 own entries, 148 MB: 52 us, of which the join takes 5.7 (14 MB of
 // partial results written and read again).  The tiles' registers leave the own entries' workgroups two a
 // CU where three stream better: in launches of their own the tiles took 26 and the others 32.
-// (w4a16_kv_attention reads 1.2 GB for that.)  24 behind 100001, int8, 229 MB: 87 us; 96 of a
-// tile's 128 rows, a quarter of the units idle.  8 behind 1501, 10 heads of 256 over 2: 12.6 us.
+// (w4a16_kv_attention reads 1.2 GB for that.)  24 behind 100001, int8, 229 MB: 80 us; 96 of a
+// tile's 128 rows, a quarter of the units idle.  8 behind 1501, 10 heads of 256 over 2: 12.4 us.
 #include "kv_attn_split.hpp"
 #include "kv_attn_tile.hpp"
 #include "kv_device.hpp"

@@ -14,8 +14,8 @@
 // fraction's sine and cosine in fp32.
 //
 // Bound and measured: rows read and written once.  11801 tokens of 40 heads of 128,
-// 242 MB: 48 us, 5.0 TB/s (a copy of 2 GiB: 4.9); 4099 of 20 with positions of
-// three axes, 42 MB: 10.6 us, 4.0 TB/s.  A step of 48 tokens takes 3.2 us: one launch and
+// 242 MB: 47 us, 5.2 TB/s (a copy of 2 GiB: 4.9); 4099 of 20 with positions of
+// three axes, 42 MB: 10.5 us, 4.0 TB/s.  A step of 48 tokens takes 3.2 us in a graph: one launch and
 // two loads that wait for each other (positions and rows).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
