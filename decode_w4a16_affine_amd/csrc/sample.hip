@@ -70,6 +70,7 @@ constexpr int kChunkScale = 49;                       // a chunk's weights are m
 // are found with a margin for that, and what a weight is off by, 2^-37 of the largest, divides among the tokens'
 // borders: one in 10^6 rows or fewer would draw a neighbour.
 constexpr int kBinScale = 36, kBinCount = 50;
+constexpr double kBinUnit = 0x1p-36;
 constexpr int kSorted = 1024;                         // listed tokens that are sorted at most
 constexpr int kHeld = 8;                              // listed tokens that a thread of the draw holds
 static_assert(kChunk == 1 << (62 - kChunkScale) && kChunk <= 1 << (kBinCount - kBinScale - 1), "sums fit");
@@ -173,14 +174,15 @@ __device__ __forceinline__ double sample_log_weight(float v, float top, double i
   return v == top ? 0.0 : ((double)v - (double)top) * inv_t;
 }
 typedef uint32_t sample_u32x2 __attribute__((ext_vector_type(2)));
-// 2^(t + scale) for t <= 0 and |scale| <= 62, a result below 2^-1000 as 2^-1000.  2^t = 2^n 2^f with |f| <= 1/2.
-// n + scale appears in the low bits of a sum with 1.5 * 2^52 and is added to the exponent's: conversions to and from
-// fp64, rint and ldexp take four times as long as a sum (256 tempered rows of 262144: 70 us with them, 64 without).
-// That holds while the result is a normal number, so it is n + scale that -1000 bounds.  (With n alone bounded, the
-// -36 of a chunk's factor carried the exponent past its end for chunks 684 temperatures below the row's largest
-// logit: 2^-1036 came out as -2^1012.)
+// 2^(t + scale) for t <= 0, below t = -1000 as there.  2^t = 2^n 2^f with |f| <= 1/2.  n + scale appears in the low
+// bits of a sum with 1.5 * 2^52 and is added to the exponent's: conversions to and from fp64, rint and ldexp take
+// four times as long as a sum (256 tempered rows of 262144: 70 us with them, 64 without).  It holds for normal results,
+// so for scales from kLeastScale on.  (Further down the exponent is carried past its end: 2^-1036 came out as -2^1012
+// where a chunk's factor had the scale -36 and a chunk lay 684 temperatures below the row's largest logit.)
+constexpr int kLeastScale = -21;
+static_assert(62 - 20 - kChunkScale >= kLeastScale && W4A16_SAMPLE_MAX_N == 1 << 20, "log2_scale - kChunkScale");
 __device__ __forceinline__ double sample_exp2(double t, int scale, const SampleSeries& series = SampleSeries{}) {
-  t = fmax(t, -1000.0 - (double)scale);
+  t = fmax(t, -1000.0);
   const double to_int = 0x1.8p52 + (double)scale, shifted = t + to_int, f = t - (shifted - to_int);
   double y = series.c[8];
 #pragma unroll
@@ -660,7 +662,7 @@ __device__ __forceinline__ SampleCut sample_find_cut(const SampleArgs& a, int r,
       if (c >= a.chunks) break;
       // (a chunk of -infinity alone has no weights; its tokens lie in the last bucket)
       const float t = tops.top[i];
-      sh.factor[c] = t > -__builtin_inff() ? sample_weight(t, top, p.inv_t, -kBinScale) : 0.0;
+      sh.factor[c] = t > -__builtin_inff() ? sample_weight(t, top, p.inv_t, 0) * kBinUnit : 0.0;
       sh.shift[c] = t > -__builtin_inff() ? min(top_bucket - sample_bucket(t, scale), kBuckets) : kBuckets;
     }
   }
