@@ -315,7 +315,7 @@ def _sample(rows, logits, uniforms, temperature, top_k, top_p, min_p, tokens, sh
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None, eps: float = 1e-6,
                  weight_offset: float = 0.0, norm: bool = True, interleaved: bool = False, sections=None, stream=None):
     """(q_out, k_out), dense and new (see w4a16_qk_norm_rope)."""
-    if stream is not None:
+    if stream is not None and not (q is None and k is None):
         with _current(stream, k if q is None else q):
             return qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, weight_offset, norm, interleaved,
                                 sections)

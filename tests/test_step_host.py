@@ -263,3 +263,9 @@ def test_sampling_takes_turns_of_8192_chunks(L, N):
     turn = 8192 // -(-N // 8192)
     assert ws(turn - 1, N) < ws(turn, N) == ws(turn + 1, N) == ws(65536, N)
     assert ws(turn, N) < 153 * 10 ** 6
+
+
+def test_rope_without_queries_and_keys_is_refused_on_a_stream_too():
+    for stream in (None, 0):
+        with pytest.raises(ValueError, match="both None"):
+            w4.qk_norm_rope(None, None, stream=stream)
